@@ -230,11 +230,7 @@ def prepare(c, seed):
         s.block_table = table.cuda()
         s.old = torch.tensor(old, dtype=torch.int32, device="cuda")
         s.lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
-        s.codes, s.scales = [], []
-        for pack in (_pack_k, _pack_v):
-            nibbles, scale = _quantise(_normal(gen, (n_pages, H_kv, page, d), bf))
-            s.codes.append(pack(nibbles))
-            s.scales.append(scale)
+        s.codes, s.scales = _full_cache(c, [_normal(gen, (n_pages, H_kv, page, d), bf) for _ in range(2)])
         if c["op"] == "cache":
             s.k_new, s.v_new = (_normal(gen, (B, H_kv, c["new"], d), bf) for _ in range(2))
             s.k, s.v = (torch.empty((B, H_kv, max(lens), d), dtype=bf, device="cuda") for _ in range(2))
@@ -341,33 +337,51 @@ def _quantise(x):
     return (code + 8).to(torch.uint8).flatten(-2), scale
 
 
-# Order of the nibbles in a token's row: K as 32-bit words (t, g) of the eight values
-# 32 g + 8 t + 0..7, t outermost; V as 16-bit words (t, g) of the four values 32 g + 4 t + 0..3.
-def _pack(n, inner):
-    n = n.unflatten(-1, (-1, 32 // inner, inner)).transpose(-2, -3).flatten(-3)
-    return n[..., 0::2] | (n[..., 1::2] << 4)
+# Where a token's bytes (of two neighbouring values) and scales lie within its page, [page, d / 2]
+# and [page, d / 32]: K in token rows of 32-bit words (t, group) of eight values, V in tiles of 16
+# tokens of 16-bit words (half, g, pair, token of the pair, group) of four values, V's scales with
+# two tokens side by side.
+def _places(c, which):
+    page, d = c["page"], c["d"]
+    groups = d // 32
+    slot = torch.arange(page, device="cuda")[:, None]
+    e = torch.arange(0, d, 2, device="cuda")[None]
+    group = torch.arange(groups, device="cuda")[None]
+    if which == 0:
+        return slot * (d // 2) + 4 * (e % 32 // 8 * groups + e // 32) + e % 8 // 2, slot * groups + group
+    half, k = slot % 16 // 8, slot % 8
+    word = (((half * 8 + e % 32 // 4) * 4 + k // 2) * 2 + k % 2) * groups + e // 32
+    return slot // 16 * (8 * d) + 2 * word + e % 4 // 2, slot // 2 * (2 * groups) + 2 * group + slot % 2
 
 
-def _unpack(codes, inner):
-    n = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
-    return n.unflatten(-1, (32 // inner, -1, inner)).transpose(-2, -3).flatten(-3)
+def _store(codes, scales, nibbles, scale, places, page, slot):
+    """Tokens [..., H_kv, d] and [..., H_kv, d / 32] into their pages' places."""
+    for array, place, x in zip((codes, scales), places, _halves(nibbles, scale)):
+        array.flatten(2)[page[..., None], :, place[slot]] = x.transpose(-1, -2)
 
 
-def _pack_k(n):
-    return _pack(n, 8)
+def _full_cache(c, x):
+    """Codes and scales of pages that hold x [n_pages, H_kv, page, d], K's then V's."""
+    out = []
+    for which in range(2):
+        for data, place in zip(_halves(*_quantise(x[which])), _places(c, which)):
+            order = torch.argsort(place.flatten())
+            out.append(data.flatten(2)[..., order].view_as(data))
+    return out[0::2], out[1::2]
 
 
-def _pack_v(n):
-    return _pack(n, 4)
+def _halves(nibbles, scale):
+    return nibbles[..., 0::2] | (nibbles[..., 1::2] << 4), scale
 
 
 def _values(s, which):
     """The cached K (0) or V (1) of every request, [B, H_kv, positions, d] in float32."""
     c = s.c
     table = s.block_table.clamp(min=0).long()
-    code = _unpack(s.codes[which][table], (8, 4)[which]).transpose(1, 2).flatten(2, 3)
-    scale = s.scales[which][table].transpose(1, 2).flatten(2, 3).float()
-    x = (code.float() - 8).unflatten(-1, (-1, 32)) * scale[..., None]
+    byte, scale = (a[which].flatten(2)[table][..., place.flatten()].unflatten(-1, place.shape).transpose(
+        1, 2).flatten(2, 3) for a, place in zip((s.codes, s.scales), _places(c, which)))
+    code = torch.stack([byte & 15, byte >> 4], -1).flatten(-2)
+    x = (code.float() - 8).unflatten(-1, (-1, 32)) * scale.float()[..., None]
     return x.view(c["B"], c["H_kv"], -1, c["d"])
 
 
@@ -377,9 +391,8 @@ def _plain_cache(s):
     page = torch.gather(s.block_table.long(), 1, pos // c["page"])
     out = {}
     for which, (x, name) in enumerate(((s.k_new, "k"), (s.v_new, "v"))):
-        nibbles, scale = _quantise(x)
-        s.codes[which][page, :, pos % c["page"]] = (_pack_k, _pack_v)[which](nibbles).transpose(1, 2)
-        s.scales[which][page, :, pos % c["page"]] = scale.transpose(1, 2)
+        nibbles, scale = _quantise(x.transpose(1, 2))
+        _store(s.codes[which], s.scales[which], nibbles, scale, _places(c, which), page, pos % c["page"])
         n = s.k.shape[2]
         seen = torch.arange(n, device="cuda") < s.lengths[:, None]
         y = _values(s, which)[:, :, :n] * seen[:, None, :, None]
@@ -526,17 +539,22 @@ def _exact_window(s, c):
 
 
 def _exact_tokens(s, c, which, b, n):
-    """The first n cached tokens of request b, [H_kv, n, d], decoded value by value's place."""
+    """The first n cached tokens of request b, [H_kv, n, d]: each value's nibble and scale by place."""
     d, page = c["d"], c["page"]
-    e = torch.arange(d)
-    per = 8 if which == 0 else 4                      # values of one word
-    word = (e % 32) // per * (d // 32) + e // 32      # its place in the row
-    nib = word * per + e % per
-    rows = s.block_table[b, :-(-n // page)].long()
-    byte = s.codes[which][rows][..., (nib // 2).cuda()].long()
-    code = (byte >> ((nib % 2) * 4).cuda()) % 16 - 8
-    x = code.double() * s.scales[which][rows].double().repeat_interleave(32, -1)
-    return x.transpose(0, 1).reshape(c["H_kv"], -1, d)[:, :n]
+    i, e = torch.arange(n)[:, None], torch.arange(d)[None]
+    k = i % page
+    if which == 0:  # nibble of a page
+        nibble = k * d + (e % 32 // 8) * (d // 4) + (e // 32) * 8 + e % 8
+        scale = k * (d // 32) + e // 32
+    else:
+        nibble = (k // 16) * 16 * d + (k % 16 // 8) * 8 * d + (e % 32 // 4) * d + (k % 8) * (d // 8) \
+            + (e // 32) * 4 + e % 4
+        scale = (k // 2) * (d // 16) + (e // 32) * 2 + k % 2
+    rows = s.block_table[b, torch.arange(n, device="cuda") // page].long()[:, None]
+    byte = s.codes[which].flatten(2)[rows, :, (nibble // 2).cuda()].long()  # [n, d, H_kv]
+    code = (byte >> (4 * (nibble % 2)).cuda()[..., None]) % 16 - 8
+    x = code.double() * s.scales[which].flatten(2)[rows, :, scale.cuda()].double()
+    return x.permute(2, 0, 1)
 
 
 def _exact_cache(s, c):
