@@ -7,6 +7,7 @@
 
 #include "../../include/fa.h"
 #include "internal.h"
+#include "layer_ops.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -69,6 +70,12 @@ __global__ void wait_selftest_kernel(DevCtl ctl) {
 
 }  // namespace
 
+bool device_ctl(DevCtl* ctl, int* err) {
+    ctl->status = status_word(err);
+    ctl->wait_ns = g_wait_ns.load();
+    return ctl->status != nullptr;
+}
+
 cudaError_t launch_wait_selftest(DevCtl ctl, cudaStream_t s) {
     wait_selftest_kernel<<<1, 32, 0, s>>>(ctl);
     return cudaGetLastError();
@@ -87,6 +94,7 @@ __attribute__((visibility("default"))) const char* fa_status_string(int status) 
         case FA_ERR_UNSUPPORTED: return "FA_ERR_UNSUPPORTED";
         case FA_ERR_CUDA: return "FA_ERR_CUDA";
         case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT";
+        case FA_ERR_DEVICE_INDEX: return "FA_ERR_DEVICE_INDEX";
         default: return "FA_ERR_UNKNOWN";
     }
 }

@@ -1,0 +1,692 @@
+// kv4_decode.cu -- attention of the newest tokens of each request over its paged 4-bit
+// cache (kv4.cuh): the serving form of the attention call, with its window and sinks.
+//
+// For the N_q newest tokens i of request b (positions lengths[b] - N_q + i) and a K/V head's
+// group of G = H / H_kv query heads: softmax over the visible tokens of scale q . k, times v,
+// with one pass over the codes and the running maximum and sum of each row.
+//
+// Bound by memory: a cached token is d / 2 + d / 16 bytes of K and of V, read once for all
+// rows of its group; nothing else grows with the length.  What that leaves to arrange:
+//   * Tensor work.  mma.m16n8k16 with the 16 cache tokens as the M side and the (up to 8)
+//     query rows as N: S^T = K Q^T and O^T = V^T P^T.  Eight rows then fill the instruction,
+//     where rows on the M side would leave half of it empty.  tcgen05's smallest M is 64 and
+//     its operands come from shared memory: the codes would have to be expanded into it, 4
+//     times their bytes, which costs more than the whole multiplication here.
+//   * Expanding codes.  (word >> 4 i) & 0x000F000F | 0x43004300 is two bf16 values 128 + u:
+//     under one integer operation a value.  The offset 136 = 128 + 8 costs nothing for K, whose
+//     accumulators start at -136 sum_d q_d of each group of 32; for V it is one packed
+//     subtraction (exact) per two values.  (Adding up P in a further product, with A = -136 in
+//     one group's rows and 0 elsewhere, is cheaper, but 0 * NaN would carry a NaN scale from
+//     its own group's outputs into the others'.)  Scales: K's multiply the group's accumulators
+//     in float; V's multiply P.  P is rounded to bf16 for the product and again with a
+//     scale, each by at most 2^-8 of its value and without a common sign; the row sum, and
+//     with it lse, adds the unrounded P.
+//   * S^T to P^T.  The accumulator layout of S^T transposed is the operand layout of P^T:
+//     one movmatrix per 8 x 8 block.
+//   * Copies.  Each warp runs its own ring of 16-token tiles, filled by bulk copies (four
+//     contiguous pieces a tile, a tile never crossing a page), no barrier between warps.
+//   * Splitting.  The units of 64 tokens of all requests and heads form one list that is cut
+//     evenly over the resident CTAs, whatever the lengths are: a CTA's share may cover several
+//     requests or a part of one.  Whole requests are written at once; parts go to the
+//     workspace, and decode_join_kernel adds them.  The cut depends on the lengths alone, so
+//     results do not change from call to call.
+#include <atomic>
+#include <cmath>
+
+#include "kv4.cuh"
+#include "layer_ops.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnitTiles = kWarps;  // tiles of 16 tokens in a unit: one per warp
+constexpr int kStages = 3;
+constexpr float kTau = 8.0f;        // lazy rescale: the reference moves by more than this (log2)
+constexpr int kMaxCtas = 1024;
+
+template <int D>
+struct TileCfg {
+    static constexpr int kCodes = kTileTokens * D / 2;       // bytes of K or V codes
+    static constexpr int kScales = kTileTokens * (D / 32) * 2;
+    static constexpr int kOffV = kCodes;
+    static constexpr int kOffKs = 2 * kCodes;
+    static constexpr int kOffVs = 2 * kCodes + kScales;
+    static constexpr int kBytes = 2 * (kCodes + kScales);
+};
+
+// Tiles of 16 tokens that a request's queries read between them: `sink` tiles from the first
+// token on, then tiles [start, end).
+struct Reach {
+    int len, sink, start, n_tiles, n_units;
+};
+
+__device__ __forceinline__ Reach reach_of(const DecodeArgs& a, long long b) {
+    Reach r;
+    r.len = a.lengths[b];
+    const long long cap = static_cast<long long>(a.cache.max_blocks) << a.cache.page_log2;
+    if (r.len < 0 || r.len > cap) {
+        atomicCAS(a.ctl.status, kDevOk, kDevIndex);
+        r.len = r.len < 0 ? 0 : static_cast<int>(cap);
+    }
+    int lo = 0;
+    if (a.window > 0) lo = max(0, static_cast<int>(max(-1ll, static_cast<long long>(r.len) - a.N_q + 1 - a.window)));
+    r.sink = (min(a.sinks, lo) + kTileTokens - 1) / kTileTokens;
+    r.start = max(r.sink, lo / kTileTokens);
+    const int end = (r.len + kTileTokens - 1) / kTileTokens;
+    r.n_tiles = r.sink + max(0, end - r.start);
+    if (r.len == 0) r.n_tiles = 0;
+    r.n_units = (r.n_tiles + kUnitTiles - 1) / kUnitTiles;
+    return r;
+}
+
+// Workspace: prefix sums of the requests' units, then per CTA two parts (its first and its
+// last entry), each ROWS x (D + 2) floats: O unnormalised, then m and l.
+struct Work {
+    long long* prefix;  // [B + 1]
+    float* parts;
+};
+__host__ __device__ inline size_t prefix_bytes(int B) {
+    return (static_cast<size_t>(B) + 1 + 1) / 2 * 2 * sizeof(long long);
+}
+
+__device__ __forceinline__ long long share_start(long long total, int ctas, int c) { return total * c / ctas; }
+// The CTA whose share holds unit u.
+__device__ __forceinline__ int owner_of(long long total, int ctas, long long u) {
+    return static_cast<int>(((u + 1) * ctas - 1) / total);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// nibble i of both halves of w as bf16 pair 128 + u
+__device__ __forceinline__ uint32_t expand(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// N neighbouring words (1, 2 or 4) as one load
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// NT: tiles of 8 query rows that share the expanded codes (1 or 2).
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+    decode_kv4_kernel(const __grid_constant__ DecodeArgs a, const Work work, const int row_tiles) {
+    using T = TileCfg<D>;
+    constexpr int G = D / 32;      // groups of 32 values
+    constexpr int ROWS = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];  // rings, then the warps' results
+    __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+    __shared__ long long s_sum[kWarps];
+    __shared__ long long s_found[2];  // request of the first unit, units before it
+    __shared__ volatile int abort_flag;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    uint8_t* const ring = smem + warp * kStages * T::kBytes;
+    float* const results = reinterpret_cast<float*>(smem + kWarps * kStages * T::kBytes);
+    const uint64_t lim = a.ctl.wait_ns;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
+    fence_barrier_init();
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // units before each request: a scan over the batch, a run of requests per thread
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += reach_of(a, b).n_units;
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, per_head = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        per_head += s_sum[w];
+    }
+    const int entries = a.cache.H_kv * row_tiles;  // per request
+    const long long total = per_head * entries;
+    const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x);
+    if (blockIdx.x == 0) {  // for the join
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            work.prefix[b] = at;
+            at += reach_of(a, b).n_units;
+        }
+        if (b1 == a.B && b0 < b1) work.prefix[a.B] = at;
+    }
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    const long long u_begin = share_start(total, ctas, blockIdx.x), u_end = share_start(total, ctas, blockIdx.x + 1);
+    if (u_begin >= before * entries && u_begin < (before + mine) * entries) {
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            const int n = reach_of(a, b).n_units;
+            if (u_begin < (at + n) * entries) {
+                s_found[0] = b;
+                s_found[1] = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    int b = static_cast<int>(s_found[0]);
+    long long b_first = s_found[1] * entries;  // first unit of request b
+
+    const int rows_all = a.H / a.cache.H_kv * a.N_q;  // query rows of a K/V head
+    int tile_no = 0;                                  // tiles this warp has consumed, over all entries
+    bool ok = true;
+    for (long long u = u_begin; u < u_end;) {
+        const Reach R = reach_of(a, b);
+        if (R.n_units == 0) {
+            ++b;
+            continue;
+        }
+        const long long rel = u - b_first;
+        const int entry = static_cast<int>(rel / R.n_units), k0 = static_cast<int>(rel % R.n_units);
+        const int take = static_cast<int>(min(static_cast<long long>(R.n_units - k0), u_end - u));
+        const int kv = entry / row_tiles, row0 = (entry % row_tiles) * ROWS;
+        const bool whole = k0 == 0 && take == R.n_units;
+        const bool is_first = u == u_begin;
+
+        // this warp's tiles: list indexes x0, x0 + kWarps, ... below x1
+        const int x0 = k0 * kUnitTiles + warp, x1 = min(R.n_tiles, (k0 + take) * kUnitTiles);
+        const int n_mine = x0 < x1 ? (x1 - x0 + kWarps - 1) / kWarps : 0;
+        auto token_of = [&](int i) {
+            const int x = x0 + i * kWarps;
+            return kTileTokens * (x < R.sink ? x : R.start + x - R.sink);
+        };
+        auto page_at = [&](int i) {  // lane 0; -1: none
+            if (i >= n_mine) return -1;
+            const int p = __ldg(a.cache.table + static_cast<long long>(b) * a.cache.max_blocks + (token_of(i) >> a.cache.page_log2));
+            if (p < 0 || p >= a.cache.n_pages) {
+                atomicCAS(a.ctl.status, kDevOk, kDevIndex);
+                return -1;
+            }
+            return p;
+        };
+        // lane 0 fills a stage with tile i; a tile without a page is not copied
+        auto issue = [&](int i, int page) {
+            const int s = (tile_no + i) % kStages;
+            const uint32_t bar = smem_u32(&bars[warp][s]);
+            if (page < 0) {
+                mbar_arrive(bar);
+                return;
+            }
+            const uint32_t dst = smem_u32(ring + s * T::kBytes);
+            const int slot = token_of(i) & ((1 << a.cache.page_log2) - 1);
+            const size_t row = ((static_cast<size_t>(page) * a.cache.H_kv + kv) << a.cache.page_log2) + slot;
+            mbar_arrive_expect_tx(bar, T::kBytes);
+            bulk_load(dst, a.cache.codes[0] + row * (D / 2), T::kCodes, bar);
+            bulk_load(dst + T::kOffV, a.cache.codes[1] + row * (D / 2), T::kCodes, bar);
+            bulk_load(dst + T::kOffKs, a.cache.scales[0] + row * G, T::kScales, bar);
+            bulk_load(dst + T::kOffVs, a.cache.scales[1] + row * G, T::kScales, bar);
+        };
+        // pages of the tiles in flight: bit i % 32 of `have` says whether tile i has one
+        uint32_t have = 0;
+        int next_page = -1;
+        int issued = tile_no + min(n_mine, kStages);
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < kStages; ++i)
+                if (i < n_mine) {
+                    const int p = page_at(i);
+                    have |= (p >= 0 ? 1u : 0u) << i;
+                    issue(i, p);
+                }
+            next_page = page_at(kStages);
+        }
+
+        // Q^T fragments, in the order of d that a lane's K words have, and -136 sum q by group
+        uint32_t qf[NT][D / 16][2];
+        float q0[NT][G][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = row0 + 8 * n + g;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                               ((static_cast<size_t>(b) * a.H + static_cast<size_t>(kv) * (a.H / a.cache.H_kv)) * a.N_q + r) * D);
+#pragma unroll
+            for (int c = 0; c < G; ++c) {
+                // values 32 c + 8 t + 0..7 of row g: pairs (i, i + 4)
+                const uint4 w = r < rows_all ? __ldg(src + 4 * c + t) : make_uint4(0, 0, 0, 0);
+                qf[n][2 * c][0] = __byte_perm(w.x, w.z, 0x5410);
+                qf[n][2 * c][1] = __byte_perm(w.x, w.z, 0x7632);
+                qf[n][2 * c + 1][0] = __byte_perm(w.y, w.w, 0x5410);
+                qf[n][2 * c + 1][1] = __byte_perm(w.y, w.w, 0x7632);
+                float sum = (bf_lo(w.x) + bf_hi(w.x)) + (bf_lo(w.y) + bf_hi(w.y)) + ((bf_lo(w.z) + bf_hi(w.z)) +
+                            (bf_lo(w.w) + bf_hi(w.w)));
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                // from row g's lanes to those of columns 2t, 2t + 1
+                q0[n][c][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t);
+                q0[n][c][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+            }
+        }
+        // positions of the rows of this lane's columns
+        int last[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) last[n][e] = R.len - a.N_q + (row0 + 8 * n + 2 * t + e) % a.N_q;
+
+        float o[NT][G][2][4];   // O^T: rows 32 c + 4 g + {0, 1 | 2, 3}, columns 2t, 2t + 1
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < G; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[n][c][i / 4][i % 4] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+            }
+        }
+
+        for (int i = 0; i < n_mine; ++i) {
+            const int s = (tile_no + i) % kStages;
+            const bool filled = mbar_wait(smem_u32(&bars[warp][s]), ((tile_no + i) / kStages) & 1, lim, &abort_flag);
+            if (!__all_sync(0xffffffffu, filled)) {
+                ok = false;
+                break;
+            }
+            const bool there = __shfl_sync(0xffffffffu, have, 0) >> (i & 31) & 1u;
+            const uint8_t* st = ring + s * T::kBytes;
+            const int tok = token_of(i);
+            // S^T of 16 tokens
+            float x[NT][4];
+            {
+                uint32_t kw[2][G], ks[2][G / 2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    load_words(st + (g + 8 * r) * (D / 2) + t * (D / 8), kw[r]);
+                    load_words(st + T::kOffKs + (g + 8 * r) * (D / 16), ks[r]);
+                }
+#pragma unroll
+                for (int c = 0; c < G; ++c) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) f[h][r] = expand(kw[r & 1][c], 2 * h + r / 2);
+                    const float s0 = (c & 1) ? bf_hi(ks[0][c / 2]) : bf_lo(ks[0][c / 2]);
+                    const float s1 = (c & 1) ? bf_hi(ks[1][c / 2]) : bf_lo(ks[1][c / 2]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float init[4] = {q0[n][c][0], q0[n][c][1], q0[n][c][0], q0[n][c][1]};
+                        float acc[4];
+                        mma_bf16(acc, f[0], qf[n][2 * c][0], qf[n][2 * c][1], init);
+                        mma_bf16(acc, f[1], qf[n][2 * c + 1][0], qf[n][2 * c + 1][1], acc);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[n][e] = c == 0 ? acc[e] * (e < 2 ? s0 : s1) : fmaf(acc[e], e < 2 ? s0 : s1, x[n][e]);
+                    }
+                }
+            }
+            // scores in log2 units; hidden tokens by selection, whatever their bytes hold
+            const bool edge = !there || tok + kTileTokens - 1 > R.len - a.N_q ||
+                              (a.window > 0 && tok <= R.len - 1 - a.window && tok + kTileTokens > a.sinks);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n][e] *= a.c_log2;
+                    if (edge) {
+                        const int j = tok + g + (e < 2 ? 0 : 8), i_pos = last[n][e & 1];
+                        const bool seen = there && j <= i_pos &&
+                                          (a.window == 0 || static_cast<long long>(j) + a.window > i_pos || j < a.sinks);
+                        if (!seen) x[n][e] = -INFINITY;
+                    }
+                }
+            // the rows' reference maxima, moved only when a score passes one by more than kTau
+            bool over = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) over |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + kTau;
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(x[n][e], x[n][e + 2]);
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        if (top > m[n][e]) {
+                            const float alpha = ex2_approx(m[n][e] - top);  // 0 from -inf
+                            m[n][e] = top;
+                            l[n][e] *= alpha;
+#pragma unroll
+                            for (int c = 0; c < G; ++c)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    o[n][c][h][e] *= alpha;
+                                    o[n][c][h][e + 2] *= alpha;
+                                }
+                        }
+                    }
+            }
+            // P^T as the operand of the second product
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                    const float p0 = ex2_approx(x[n][2 * h] - r0), p1 = ex2_approx(x[n][2 * h + 1] - r1);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    pf[n][h] = transpose8x8(pack_bf16x2(p0, p1));
+                }
+            // O^T += V^T (P s)^T
+            {
+                uint32_t vw[2][G], vs[2][G];  // codes: the first token's G / 2 words, then the second's
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    load_words(st + T::kOffV + (r * 32 + lane) * (D / 8), vw[r]);
+                    load_words(st + T::kOffVs + (r * 4 + t) * (D / 8), vs[r]);
+                }
+#pragma unroll
+                for (int c = 0; c < G; ++c) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        // 16-bit words of this lane's two tokens side by side
+                        const uint32_t w = __byte_perm(vw[r][c / 2], vw[r][G / 2 + c / 2], (c & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[e / 2][2 * r + (e & 1)] = sub_bf16x2(expand(w, e), 0x43084308u);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t ps[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            ps[r] = mul_bf16x2(pf[n][r], vs[r][c]);
+                            if (edge) {  // a hidden token's scale may be anything
+                                if ((pf[n][r] & 0x0000FFFFu) == 0) ps[r] &= 0xFFFF0000u;
+                                if ((pf[n][r] & 0xFFFF0000u) == 0) ps[r] &= 0x0000FFFFu;
+                            }
+                        }
+                        mma_bf16(o[n][c][0], f[0], ps[0], ps[1], o[n][c][0]);
+                        mma_bf16(o[n][c][1], f[1], ps[0], ps[1], o[n][c][1]);
+                    }
+                }
+            }
+            // the stage has been read by every lane: refill it
+            __syncwarp();
+            issued = tile_no + min(n_mine, i + 1 + kStages);
+            if (lane == 0) {
+                const int i2 = i + kStages;
+                if (i2 < n_mine) {
+                    const uint32_t bit = 1u << (i2 & 31);
+                    have = next_page >= 0 ? have | bit : have & ~bit;
+                    issue(i2, next_page);
+                    next_page = page_at(i2 + 1);
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            abort_flag = 1;
+            atomicCAS(a.ctl.status, kDevOk, kDevTimeout);
+            // this warp's copies in flight land before its shared memory goes away: the newest
+            // tile of every stage, of those issued
+            const volatile int never = 0;
+            for (int x = max(0, issued - kStages); x < issued; ++x)
+                mbar_wait(smem_u32(&bars[warp][x % kStages]), (x / kStages) & 1, kDrainWaitNs, &never);
+        }
+        tile_no += n_mine;
+
+        // the warps' states side by side, then one sum per value
+        constexpr int kRowFloats = D + 2;
+        float* mine_r = results + warp * ROWS * kRowFloats;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[n][e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                float* row = mine_r + (8 * n + 2 * t + e) * kRowFloats;
+                if (g == 0) {
+                    row[D] = m[n][e];
+                    row[D + 1] = sum;
+                }
+#pragma unroll
+                for (int c = 0; c < G; ++c) {
+                    row[32 * c + 4 * g] = o[n][c][0][e];
+                    row[32 * c + 4 * g + 1] = o[n][c][0][e + 2];
+                    row[32 * c + 4 * g + 2] = o[n][c][1][e];
+                    row[32 * c + 4 * g + 3] = o[n][c][1][e + 2];
+                }
+            }
+        if (__syncthreads_or(ok ? 0 : 1)) break;  // a wait ran out in one of the warps
+        for (int x = threadIdx.x; x < ROWS * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), c4 = 4 * (x % (D / 4));
+            if (row0 + r >= rows_all) continue;
+            float mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, results[(w * ROWS + r) * kRowFloats + D]);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float* row = results + (w * ROWS + r) * kRowFloats;
+                const float f = ex2_approx(row[D] - ref);
+                sum = fmaf(f, row[D + 1], sum);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(f, row[c4 + e], acc[e]);
+            }
+            if (whole) {
+                const size_t out = (static_cast<size_t>(b) * a.H + static_cast<size_t>(kv) * (a.H / a.cache.H_kv)) * a.N_q + row0 + r;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + out * D + c4) =
+                    make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+                if (c4 == 0 && a.lse != nullptr)
+                    a.lse[out] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.69314718055994530942f;
+            } else {
+                float* part = work.parts + (static_cast<size_t>(2 * blockIdx.x + (is_first ? 0 : 1)) * ROWS + r) * kRowFloats;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[c4 + e] = acc[e];
+                if (c4 == 0) {
+                    part[D] = mm;
+                    part[D + 1] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        u += take;
+        if (u == b_first + static_cast<long long>(R.n_units) * entries) {
+            b_first = u;
+            ++b;
+        }
+    }
+}
+
+// One block per query row: adds the parts of requests that were cut, and writes the rows of
+// requests without tokens.
+template <int D>
+__global__ void __launch_bounds__(256)
+    decode_join_kernel(const __grid_constant__ DecodeArgs a, const Work work, const int row_tiles, const int rows_tile,
+                       const int ctas_main) {
+    constexpr int kRowFloats = D + 2;
+    __shared__ float s_w[2 * 256];
+    __shared__ float s_o[8][D];
+    __shared__ float s_red[2][8];
+    griddep_wait();
+    const int row = blockIdx.x;  // of B * H * N_q
+    const int G = a.H / a.cache.H_kv;
+    const int per_b = a.H * a.N_q, per_kv = G * a.N_q;
+    const int b = row / per_b, kv = row % per_b / per_kv, r = row % per_kv;
+    const int entries = a.cache.H_kv * row_tiles, entry = kv * row_tiles + r / rows_tile;
+    const long long p0 = work.prefix[b], p1 = work.prefix[b + 1];
+    const long long n = p1 - p0, total = work.prefix[a.B] * entries;
+    if (n == 0) {
+        for (int x = threadIdx.x; x < D; x += blockDim.x) static_cast<uint16_t*>(a.o)[static_cast<size_t>(row) * D + x] = 0;
+        if (threadIdx.x == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
+        return;
+    }
+    const int ctas = static_cast<int>(total < ctas_main ? total : ctas_main);
+    const long long u0 = p0 * entries + entry * n, u1 = u0 + n;
+    const int c0 = owner_of(total, ctas, u0), c1 = owner_of(total, ctas, u1 - 1);
+    if (c0 == c1) {
+        return;  // written whole by its CTA
+    }
+    const int parts = c1 - c0 + 1;
+    const bool first_of_c0 = share_start(total, ctas, c0) == u0;
+    const int rt = r % rows_tile;
+    auto part_at = [&](int i) {
+        const int slot = 2 * (c0 + i) + (i == 0 && !first_of_c0 ? 1 : 0);
+        return work.parts + (static_cast<size_t>(slot) * rows_tile + rt) * kRowFloats;
+    };
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // the row's maximum over its parts
+    float mm = -INFINITY;
+    for (int i = threadIdx.x; i < parts; i += blockDim.x) mm = fmaxf(mm, part_at(i)[D]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+    if (lane == 0) s_red[0][warp] = mm;
+    __syncthreads();
+    mm = s_red[0][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) mm = fmaxf(mm, s_red[0][w]);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < parts; i += blockDim.x) {
+        const float* p = part_at(i);
+        const float f = ex2_approx(p[D] - ref);
+        if (i < 512) s_w[i] = f;
+        sum = fmaf(f, p[D + 1], sum);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += s_red[1][w];
+    // warps take parts in turn, a lane D / 32 neighbouring values
+    constexpr int V = D / 32;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < parts; i += 8) {
+        const float* p = part_at(i);
+        const float f = i < 512 ? s_w[i] : ex2_approx(p[D] - ref);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(p + lane * V + e);
+            acc[e] = fmaf(f, x.x, acc[e]);
+            acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            x += s_o[w][2 * threadIdx.x];
+            y += s_o[w][2 * threadIdx.x + 1];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        reinterpret_cast<uint32_t*>(a.o)[static_cast<size_t>(row) * (D / 2) + threadIdx.x] = pack_bf16x2(x * inv, y * inv);
+        if (threadIdx.x == 0 && a.lse != nullptr)
+            a.lse[row] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.69314718055994530942f;
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch_impl(const DecodeArgs& a, cudaStream_t s) {
+    constexpr int kSmem = kWarps * (kStages * TileCfg<D>::kBytes + 8 * NT * (D + 2) * static_cast<int>(sizeof(float)));
+    // CTAs that are resident together, per device; asked once
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int ctas = dev < 64 ? resident[dev].load() : 0;
+    if (ctas == 0) {
+        int sms = 0, per_sm = 0;
+        e = cudaFuncSetAttribute(decode_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kv4_kernel<D, NT>, kThreads, kSmem);
+        if (e != cudaSuccess) return e;
+        ctas = sms * (per_sm < 1 ? 1 : per_sm);
+        if (ctas > kMaxCtas) ctas = kMaxCtas;
+        if (dev < 64) resident[dev].store(ctas);
+    }
+    const int rows = a.H / a.cache.H_kv * a.N_q;
+    const int row_tiles = (rows + 8 * NT - 1) / (8 * NT);
+    // no more CTAs than units that the tables could hold
+    const long long most_units = (((static_cast<long long>(a.cache.max_blocks) << a.cache.page_log2) + 63) / 64) *
+                                 a.B * a.cache.H_kv * row_tiles;
+    const long long grid = ctas < most_units ? ctas : most_units;
+    Work w;
+    w.prefix = static_cast<long long*>(a.workspace);
+    w.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + prefix_bytes(a.B));
+    e = launch_pdl(decode_kv4_kernel<D, NT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a, w,
+                   row_tiles);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(decode_join_kernel<D>, dim3(static_cast<unsigned>(a.B * a.H * a.N_q)), dim3(256), 0, s, a, w,
+                      row_tiles, 8 * NT, static_cast<int>(grid));
+}
+
+}  // namespace
+
+size_t decode_kv4_workspace_bytes(int B, int H, int H_kv, int N_q, int d) {
+    const int rows = H / H_kv * N_q;
+    return prefix_bytes(B) + static_cast<size_t>(2 * kMaxCtas) * (rows <= 8 ? 8 : 16) * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_decode_kv4(const DecodeArgs& a, int d, cudaStream_t s) {
+    const int rows = a.H / a.cache.H_kv * a.N_q;
+    if (d == 64) return rows <= 8 ? launch_impl<64, 1>(a, s) : launch_impl<64, 2>(a, s);
+    return rows <= 8 ? launch_impl<128, 1>(a, s) : launch_impl<128, 2>(a, s);
+}
+
+}  // namespace fa

@@ -52,7 +52,9 @@ typedef enum {
     FA_ERR_INVALID_ARG = 1,     /* null/misaligned pointer, N < 1, B/H < 1, bad dtype */
     FA_ERR_UNSUPPORTED = 2,     /* valid request this build does not implement      */
     FA_ERR_CUDA = 3,            /* a CUDA runtime/driver call or launch failed      */
-    FA_ERR_DEVICE_TIMEOUT = 4   /* a kernel's bounded wait ran out (device-side)    */
+    FA_ERR_DEVICE_TIMEOUT = 4,  /* a kernel's bounded wait ran out (device-side)    */
+    FA_ERR_DEVICE_INDEX = 5     /* a page, position or length outside the 4-bit cache
+                                   (device-side; the access was left out)           */
 } fa_status;
 
 /*
@@ -279,12 +281,136 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
                    const void* dO, void* dq, void* dk, void* dv, int B, int H, int N, int d,
                    float scale, int causal, int dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A layer's work around the attention call.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Norm and rotation of the query and key heads, from a layer's projections to the
+ * operands of the attention calls in one pass.  For each head row x of Q or K at
+ * position t, with that operand's weights w:
+ *     y = w o x / sqrt(mean(x^2) + eps),
+ *     (y_a, y_b) -> (y_a cos A - y_b sin A,  y_b cos A + y_a sin A),  A = t inv_freq[p],
+ * for the rot / 2 pairs p of its first `rot` elements: (a, b) = (p, p + rot / 2), or with
+ * `interleaved` (2 p, 2 p + 1).  V is moved only.
+ *
+ *   qkv       : [B][N][H + 2 H_kv][d] of `dtype`: a token's query heads, then its key heads,
+ *               then its value heads (the one tensor here that is not [B][H][N][d]).
+ *   q_weight, k_weight : [d] float32, or NULL (ones).
+ *   positions : [B][N] int32 (negative ones turn backwards), or NULL: the index in the
+ *               sequence.
+ *   inv_freq  : HOST array of rot / 2 finite doubles, radians per position; read before the
+ *               call returns.  May be NULL if rot is 0.  Angles are exact to 2^-24 of a turn
+ *               at every int32 position.
+ *   q, k, v   : [B][H][N][d] and twice [B][H_kv][N][d] of `dtype`, written; they must not
+ *               overlap qkv.
+ *   d : 64 or 128.  rot : a multiple of 16, 0 to d.  eps : finite, >= 0.
+ *   dtype : FA_BF16 or FA_F32 (arithmetic in float32 either way).
+ * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, B, H, H_kv, N < 1, bad rot, eps,
+ * frequencies or dtype), FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, B*N
+ * beyond 2^31 - 1), FA_ERR_CUDA (launch failure).
+ */
+int fa_qk_norm_rope(const void* qkv, const float* q_weight, const float* k_weight,
+                    const int* positions, const double* inv_freq, void* q, void* k, void* v, int B,
+                    int H, int H_kv, int N, int d, int rot, int interleaved, float eps, int dtype,
+                    void* stream);
+
+/*
+ * Gradient of fa_qk_norm_rope.  With g the incoming row turned back by its angles and
+ * r = (mean(x^2) + eps)^(-1/2):
+ *     dx = r (w g - r^2 x mean(w g x)),    dw = sum over all rows of g r x.
+ *
+ *   dq, dk, dv : gradients of q, k, v, in their layouts, read only.
+ *   dqkv       : gradient of qkv, in its layout, written.
+ *   dq_weight, dk_weight : [d] float32, written (the sum over all rows), or NULL if not
+ *                wanted.  The sums have a fixed order: the same bits every time.
+ *   workspace  : at least fa_qk_norm_rope_bwd_workspace_size() bytes of device memory; NULL
+ *                with 0 bytes is accepted when neither weight gradient is wanted.  Calls that
+ *                overlap in time must not share one.
+ *   Other arguments as fa_qk_norm_rope; nothing of the forward is needed.
+ * Errors: as fa_qk_norm_rope; FA_ERR_INVALID_ARG also for a workspace that is too small.
+ */
+int fa_qk_norm_rope_bwd(const void* qkv, const float* q_weight, const float* k_weight,
+                        const int* positions, const double* inv_freq, const void* dq,
+                        const void* dk, const void* dv, void* dqkv, float* dq_weight,
+                        float* dk_weight, void* workspace, size_t workspace_bytes, int B, int H,
+                        int H_kv, int N, int d, int rot, int interleaved, float eps, int dtype,
+                        void* stream);
+/* Bytes for any call with these sizes; 0 for sizes that the call refuses. */
+size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int H_kv, int N, int d);
+
+/*
+ * A paged K/V cache in 4 bits.  32 neighbouring values of a head share one scale
+ * s = bf16(max|x| / 7); a value is held as the nearest integer to x / s (ties to even) in
+ * -7 .. 7, as the nibble code + 8.  A group of zeros has s = 0; a group that holds an
+ * infinity or a NaN has a NaN scale and reads back as NaN.  4.5 bits a value.
+ *
+ *   k_codes, v_codes   : [n_pages][H_kv][page][d / 2] bytes.
+ *   k_scales, v_scales : [n_pages][H_kv][page][d / 32] bfloat16.
+ * These are sizes; within a page the nibbles lie in the order in which the decode kernel
+ * reads them (kv4.cuh), so that only these functions and code written to that order
+ * address single values.  Zero-initialised pages are valid.
+ *   block_table        : [B][max_blocks] int32: token i of request b is token i % page of
+ *                        page block_table[b][i / page].  Entries past a request's tokens are
+ *                        not read.
+ *   page : 16, 32, 64, 128 or 256 tokens.   d : 64 or 128.
+ * A page, position or length outside the cache that a kernel meets is left out (not written;
+ * read as zeros; hidden from attention) and recorded as FA_ERR_DEVICE_INDEX.
+ */
+
+/*
+ * Store rows of K and V: row i of request b becomes its token first[b] + i, for
+ * i < count[b] (count NULL: all N).  Two rows of one call must not name the same token.
+ *   k, v  : [B][H_kv][N][d] bfloat16, read only.
+ *   first : [B] int32, device: tokens that the requests had before.   count : [B] int32 or NULL.
+ * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, sizes < 1, bad page),
+ * FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, max_blocks * page beyond
+ * 2^31 - 1), FA_ERR_CUDA.
+ */
+int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes,
+                  void* v_scales, const int* block_table, const int* first, const int* count, int B,
+                  int H_kv, int N, int d, int page, int n_pages, int max_blocks, void* stream);
+
+/*
+ * Read tokens 0 .. N - 1 of every request back as bfloat16 rows [B][H_kv][N][d] (code * s,
+ * rounded to nearest even): the dense prefix that a chunked prompt attends to, for
+ * fa_fwd_kv_shard.  Rows from lengths[b] on are written as zeros.  Errors: as fa_kv4_append.
+ */
+int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes,
+                const void* v_scales, const int* block_table, const int* lengths, void* k, void* v,
+                int B, int H_kv, int N, int d, int page, int n_pages, int max_blocks, void* stream);
+
+/*
+ * Attention of the N_q newest tokens of every request over the cache (their own keys and
+ * values stored before the call): query i of request b is at position
+ * p = lengths[b] - N_q + i and sees token j iff j <= p and, for window > 0,
+ * (j > p - window or j < n_sink).  window = 0: every j <= p.  Query head h reads K/V head
+ * h / (H / H_kv).  A query at a negative position (a request shorter than N_q, or empty) sees
+ * nothing: O = 0, lse = -inf.
+ *
+ *   q, o  : [B][H][N_q][d] bfloat16.   lse : [B][H][N_q] float32, or NULL.
+ *   lengths : [B] int32, device.
+ *   workspace : at least fa_decode_kv4_workspace_size() bytes; its contents on entry do not
+ *           matter.  Calls that overlap in time must not share one.
+ * The work is divided by the lengths that the kernel reads, so that a captured call follows
+ * them; the result depends on the inputs and the device alone.
+ * Errors: as fa_kv4_append; FA_ERR_INVALID_ARG also for H % H_kv != 0, a scale that is not
+ * finite, window < 0, n_sink < 0, or a workspace that is too small.
+ */
+int fa_decode_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                  const void* v_scales, const int* block_table, const int* lengths, void* o,
+                  float* lse, void* workspace, size_t workspace_bytes, int B, int H, int H_kv,
+                  int N_q, int d, int page, int n_pages, int max_blocks, float scale, int window,
+                  int n_sink, void* stream);
+/* 0 for sizes that the call refuses. */
+size_t fa_decode_kv4_workspace_size(int B, int H, int H_kv, int N_q, int d);
+
 /*
  * Synchronise `stream`, then return and clear the current device's status
  * word: FA_OK, or the first device-side error recorded since the last call
  * (FA_ERR_DEVICE_TIMEOUT when a kernel's bounded wait ran out; that kernel
- * returned early and its outputs are undefined).  FA_ERR_CUDA if the
- * synchronisation itself failed.
+ * returned early and its outputs are undefined.  FA_ERR_DEVICE_INDEX: see the
+ * 4-bit cache).  FA_ERR_CUDA if the synchronisation itself failed.
  */
 int fa_last_device_error(void* stream);
 
