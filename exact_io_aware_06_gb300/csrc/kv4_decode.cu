@@ -18,13 +18,12 @@
 //     subtraction (exact) per two values.  (Adding up P in a further product, with A = -136 in
 //     one group's rows and 0 elsewhere, is cheaper, but 0 * NaN would carry a NaN scale from
 //     its own group's outputs into the others'.)  Scales: K's multiply the group's accumulators
-//     in float; V's multiply P.  P is rounded to bf16 for the product and again with a
-//     scale, each by at most 2^-8 of its value and without a common sign; the row sum, and
-//     with it lse, adds the unrounded P.
+//     in float; V's multiply P in float, and the product is rounded to bf16 once, by at most
+//     2^-8 of its value.  The row sum, and with it lse, adds the unrounded P.
 //   * S^T to P^T.  The accumulator layout of S^T transposed is the operand layout of P^T:
 //     one movmatrix per 8 x 8 block.
-//   * Copies.  Each warp runs its own ring of 16-token tiles, filled by bulk copies (four
-//     contiguous pieces a tile, a tile never crossing a page), no barrier between warps.
+//   * Copies.  Each warp runs its own ring of 16-token tiles, filled by 16-byte asynchronous
+//     copies of its lanes (a tile never crosses a page); no barrier between warps.
 //   * Splitting.  The units of 64 tokens of all requests and heads form one list that is cut
 //     evenly over the resident CTAs, whatever the lengths are: a CTA's share may cover several
 //     requests or a part of one.  Whole requests are written at once; parts go to the
@@ -43,7 +42,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnitTiles = kWarps;  // tiles of 16 tokens in a unit: one per warp
-constexpr int kStages = 3;
+constexpr int kStages = 4;         // ring of tiles per warp
 constexpr float kTau = 8.0f;        // lazy rescale: the reference moves by more than this (log2)
 constexpr int kMaxCtas = 1024;
 
@@ -113,10 +112,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 // nibble i of both halves of w as bf16 pair 128 + u
 __device__ __forceinline__ uint32_t expand(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -146,24 +143,17 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 
 // NT: tiles of 8 query rows that share the expanded codes (1 or 2).
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
     decode_kv4_kernel(const __grid_constant__ DecodeArgs a, const Work work, const int row_tiles) {
     using T = TileCfg<D>;
     constexpr int G = D / 32;      // groups of 32 values
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];  // rings, then the warps' results
-    __shared__ __align__(8) uint64_t bars[kWarps][kStages];
     __shared__ long long s_sum[kWarps];
     __shared__ long long s_found[2];  // request of the first unit, units before it
-    __shared__ volatile int abort_flag;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     uint8_t* const ring = smem + warp * kStages * T::kBytes;
     float* const results = reinterpret_cast<float*>(smem + kWarps * kStages * T::kBytes);
-    const uint64_t lim = a.ctl.wait_ns;
-    if (threadIdx.x == 0) abort_flag = 0;
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
-    fence_barrier_init();
     griddep_wait();
     griddep_launch_dependents();
 
@@ -215,9 +205,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     int b = static_cast<int>(s_found[0]);
     long long b_first = s_found[1] * entries;  // first unit of request b
 
+    const uint32_t half_sel = (g & 1) ? 0x3244u : 0x1044u;  // this token's half of a pair's word, as a float
     const int rows_all = a.H / a.cache.H_kv * a.N_q;  // query rows of a K/V head
-    int tile_no = 0;                                  // tiles this warp has consumed, over all entries
-    bool ok = true;
     for (long long u = u_begin; u < u_end;) {
         const Reach R = reach_of(a, b);
         if (R.n_units == 0) {
@@ -238,46 +227,44 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
             const int x = x0 + i * kWarps;
             return kTileTokens * (x < R.sink ? x : R.start + x - R.sink);
         };
-        auto page_at = [&](int i) {  // lane 0; -1: none
+        auto page_at = [&](int i) {  // -1: none
             if (i >= n_mine) return -1;
             const int p = __ldg(a.cache.table + static_cast<long long>(b) * a.cache.max_blocks + (token_of(i) >> a.cache.page_log2));
             if (p < 0 || p >= a.cache.n_pages) {
-                atomicCAS(a.ctl.status, kDevOk, kDevIndex);
+                if (lane == 0) atomicCAS(a.ctl.status, kDevOk, kDevIndex);
                 return -1;
             }
             return p;
         };
-        // lane 0 fills a stage with tile i; a tile without a page is not copied
+        // the lanes' copies of tile i into its stage; a tile without a page is not copied
         auto issue = [&](int i, int page) {
-            const int s = (tile_no + i) % kStages;
-            const uint32_t bar = smem_u32(&bars[warp][s]);
-            if (page < 0) {
-                mbar_arrive(bar);
-                return;
-            }
-            const uint32_t dst = smem_u32(ring + s * T::kBytes);
-            const int slot = token_of(i) & ((1 << a.cache.page_log2) - 1);
-            const size_t row = ((static_cast<size_t>(page) * a.cache.H_kv + kv) << a.cache.page_log2) + slot;
-            mbar_arrive_expect_tx(bar, T::kBytes);
-            bulk_load(dst, a.cache.codes[0] + row * (D / 2), T::kCodes, bar);
-            bulk_load(dst + T::kOffV, a.cache.codes[1] + row * (D / 2), T::kCodes, bar);
-            bulk_load(dst + T::kOffKs, a.cache.scales[0] + row * G, T::kScales, bar);
-            bulk_load(dst + T::kOffVs, a.cache.scales[1] + row * G, T::kScales, bar);
-        };
-        // pages of the tiles in flight: bit i % 32 of `have` says whether tile i has one
-        uint32_t have = 0;
-        int next_page = -1;
-        int issued = tile_no + min(n_mine, kStages);
-        if (lane == 0) {
+            if (page >= 0) {
+                const uint32_t dst = smem_u32(ring + (i % kStages) * T::kBytes);
+                const int slot = token_of(i) & ((1 << a.cache.page_log2) - 1);
+                const size_t row = ((static_cast<size_t>(page) * a.cache.H_kv + kv) << a.cache.page_log2) + slot;
+                const uint8_t* kc = a.cache.codes[0] + row * (D / 2);
+                const uint8_t* vc = a.cache.codes[1] + row * (D / 2);
 #pragma unroll
-            for (int i = 0; i < kStages; ++i)
-                if (i < n_mine) {
-                    const int p = page_at(i);
-                    have |= (p >= 0 ? 1u : 0u) << i;
-                    issue(i, p);
+                for (int x = 0; x < T::kCodes; x += 512) {
+                    cp_async16(dst + x + lane * 16, kc + x + lane * 16);
+                    cp_async16(dst + T::kOffV + x + lane * 16, vc + x + lane * 16);
                 }
-            next_page = page_at(kStages);
+                constexpr int kPieces = T::kScales / 16;
+                if (lane < 2 * kPieces) {
+                    const uint16_t* src = a.cache.scales[lane >= kPieces] + row * G;
+                    cp_async16(dst + T::kOffKs + lane * 16, src + (lane % kPieces) * 8);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        uint32_t have = 0;  // bit i % 32: tile i has a page (of the tiles in the ring)
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            const int p = page_at(i);
+            have |= (p >= 0 ? 1u : 0u) << i;
+            issue(i, p);
         }
+        int next_page = page_at(kStages - 1);
 
         // Q^T fragments, in the order of d that a lane's K words have, and -136 sum q by group
         uint32_t qf[NT][D / 16][2];
@@ -327,14 +314,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         }
 
         for (int i = 0; i < n_mine; ++i) {
-            const int s = (tile_no + i) % kStages;
-            const bool filled = mbar_wait(smem_u32(&bars[warp][s]), ((tile_no + i) / kStages) & 1, lim, &abort_flag);
-            if (!__all_sync(0xffffffffu, filled)) {
-                ok = false;
-                break;
+            // the stage of tile i - 1, which every lane has read, takes tile i + kStages - 1
+            {
+                const int i2 = i + kStages - 1;
+                const uint32_t bit = 1u << (i2 & 31);
+                have = next_page >= 0 ? have | bit : have & ~bit;
+                issue(i2, next_page);
+                next_page = page_at(i2 + 1);
             }
-            const bool there = __shfl_sync(0xffffffffu, have, 0) >> (i & 31) & 1u;
-            const uint8_t* st = ring + s * T::kBytes;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
+            const bool there = have >> (i & 31) & 1u;
+            const uint8_t* st = ring + (i % kStages) * T::kBytes;
             const int tok = token_of(i);
             // S^T of 16 tokens
             float x[NT][4];
@@ -409,25 +400,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
                         }
                     }
             }
-            // P^T as the operand of the second product
-            uint32_t pf[NT][2];
+            // P, rows of tokens g and g + 8
+            float p[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-                    const float p0 = ex2_approx(x[n][2 * h] - r0), p1 = ex2_approx(x[n][2 * h + 1] - r1);
-                    l[n][0] += p0;
-                    l[n][1] += p1;
-                    pf[n][h] = transpose8x8(pack_bf16x2(p0, p1));
+                for (int e = 0; e < 4; ++e) {
+                    p[n][e] = ex2_approx(x[n][e] - (e & 1 ? r1 : r0));
+                    l[n][e & 1] += p[n][e];
                 }
+            }
             // O^T += V^T (P s)^T
             {
-                uint32_t vw[2][G], vs[2][G];  // codes: the first token's G / 2 words, then the second's
+                uint32_t vw[2][G];  // codes: the first token's G / 2 words, then the second's
+                uint32_t vs[2][G];  // scales of token pairs g / 2, 4 + g / 2
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     load_words(st + T::kOffV + (r * 32 + lane) * (D / 8), vw[r]);
-                    load_words(st + T::kOffVs + (r * 4 + t) * (D / 8), vs[r]);
+                    load_words(st + T::kOffVs + (r * 4 + g / 2) * (D / 8), vs[r]);
                 }
 #pragma unroll
                 for (int c = 0; c < G; ++c) {
@@ -441,43 +432,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
+                        // P times the group's scale, transposed into the operand of the second product
                         uint32_t ps[2];
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            ps[r] = mul_bf16x2(pf[n][r], vs[r][c]);
+                            const float s = __uint_as_float(__byte_perm(vs[r][c], 0u, half_sel));
+                            float y0 = p[n][2 * r] * s, y1 = p[n][2 * r + 1] * s;
                             if (edge) {  // a hidden token's scale may be anything
-                                if ((pf[n][r] & 0x0000FFFFu) == 0) ps[r] &= 0xFFFF0000u;
-                                if ((pf[n][r] & 0xFFFF0000u) == 0) ps[r] &= 0x0000FFFFu;
+                                if (x[n][2 * r] == -INFINITY) y0 = 0.f;
+                                if (x[n][2 * r + 1] == -INFINITY) y1 = 0.f;
                             }
+                            ps[r] = transpose8x8(pack_bf16x2(y0, y1));
                         }
                         mma_bf16(o[n][c][0], f[0], ps[0], ps[1], o[n][c][0]);
                         mma_bf16(o[n][c][1], f[1], ps[0], ps[1], o[n][c][1]);
                     }
                 }
             }
-            // the stage has been read by every lane: refill it
-            __syncwarp();
-            issued = tile_no + min(n_mine, i + 1 + kStages);
-            if (lane == 0) {
-                const int i2 = i + kStages;
-                if (i2 < n_mine) {
-                    const uint32_t bit = 1u << (i2 & 31);
-                    have = next_page >= 0 ? have | bit : have & ~bit;
-                    issue(i2, next_page);
-                    next_page = page_at(i2 + 1);
-                }
-            }
+            __syncwarp();  // every lane has read the stage
         }
-        if (!ok && lane == 0) {
-            abort_flag = 1;
-            atomicCAS(a.ctl.status, kDevOk, kDevTimeout);
-            // this warp's copies in flight land before its shared memory goes away: the newest
-            // tile of every stage, of those issued
-            const volatile int never = 0;
-            for (int x = max(0, issued - kStages); x < issued; ++x)
-                mbar_wait(smem_u32(&bars[warp][x % kStages]), (x / kStages) & 1, kDrainWaitNs, &never);
-        }
-        tile_no += n_mine;
 
         // the warps' states side by side, then one sum per value
         constexpr int kRowFloats = D + 2;
@@ -502,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
                     row[32 * c + 4 * g + 3] = o[n][c][1][e + 2];
                 }
             }
-        if (__syncthreads_or(ok ? 0 : 1)) break;  // a wait ran out in one of the warps
+        __syncthreads();
         for (int x = threadIdx.x; x < ROWS * (D / 4); x += kThreads) {
             const int r = x / (D / 4), c4 = 4 * (x % (D / 4));
             if (row0 + r >= rows_all) continue;
