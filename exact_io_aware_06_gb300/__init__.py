@@ -19,7 +19,7 @@ __all__ = [
     "fa_bwd_workspace_size", "fa_bwd_noalloc", "fa_last_device_error", "fa_set_wait_timeout_ns",
     "fa_selftest_wait_timeout", "fa_status_string", "attention_forward", "attention_backward",
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
-    "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_decode_kv4_workspace_size",
+    "fa_fwd_window", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_decode_kv4_workspace_size",
     "rope_frequencies", "kv4_cache",
 ]
 
@@ -78,6 +78,8 @@ def lib():
         L.fa_qk_norm_rope_bwd.restype = i
         L.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i] * 5
         L.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+        L.fa_fwd_window.argtypes = [vp] * 5 + [i] * 5 + [f, i, i, i, vp]
+        L.fa_fwd_window.restype = i
         L.fa_kv4_append.argtypes = [vp] * 9 + [i] * 7 + [vp]
         L.fa_kv4_append.restype = i
         L.fa_kv4_read.argtypes = [vp] * 8 + [i] * 7 + [vp]
@@ -317,6 +319,20 @@ def fa_qk_norm_rope_bwd(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv
         _maybe("dq_weight", torch.float32, (d,), dq_weight),
         _maybe("dk_weight", torch.float32, (d,), dk_weight), _ptr(workspace), ws_bytes, B, H, H_kv, N, d,
         rot, int(bool(interleaved)), float(eps), code, _stream(stream)), "fa_qk_norm_rope_bwd")
+
+
+def fa_fwd_window(q, k, v, o, lse, scale, window, n_sink, dtype=FA_BF16, stream=None):
+    """Forward under a causal window of `window` keys and the first n_sink keys: q, o
+    [B, H, N, d], k, v [B, H_kv, N, d] bfloat16; lse [B, H, N] or None."""
+    import torch
+    B, H, N, d = _shape(q)
+    H_kv = _shape(k)[1]
+    t = torch.bfloat16
+    _check(lib().fa_fwd_window(_dense("q", t, (B, H, N, d), q), _dense("k", t, (B, H_kv, N, d), k),
+                               _dense("v", t, (B, H_kv, N, d), v), _dense("o", t, (B, H, N, d), o),
+                               _maybe("lse", torch.float32, (B, H, N), lse), B, H, H_kv, N, d,
+                               float(scale), int(window), int(n_sink), int(dtype), _stream(stream)),
+           "fa_fwd_window")
 
 
 def kv4_cache(n_pages, H_kv, page, d, device="cuda"):

@@ -92,6 +92,17 @@ int decode_sizes(int B, int H, int H_kv, int N_q, int d) {
     return FA_OK;
 }
 
+// Sizes and parameters of the windowed attention, forward and backward.
+int window_args(const void* q, const void* k, const void* v, const void* o, int B, int H, int H_kv, int N, int d,
+                float scale, int window, int n_sink, int dtype) {
+    if (!pointers_ok(q, k, v, o)) return FA_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || N < 1 || H_kv < 1 || H % H_kv != 0) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || window < 1 || n_sink < 0) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_F32 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_BF16 || (d != 64 && d != 128) || !sizes_supported(B, H, N)) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -136,6 +147,19 @@ FA_API int fa_qk_norm_rope_bwd(const void* qkv, const float* q_weight, const flo
     float* const dw[2] = {dq_weight, dk_weight};
     return from_cuda(
         launch_qk_norm_rope_bwd(a, dw, d, dtype == FA_F32, interleaved ? 1 : 0, static_cast<cudaStream_t>(stream)));
+}
+
+FA_API int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv,
+                         int N, int d, float scale, int window, int n_sink, int dtype, void* stream) {
+    if (!optional_ok(lse)) return FA_ERR_INVALID_ARG;
+    const int rc = window_args(q, k, v, o, B, H, H_kv, N, d, scale, window, n_sink, dtype);
+    if (rc != FA_OK) return rc;
+    DevCtl ctl;
+    int err = FA_OK;
+    if (!device_ctl(&ctl, &err)) return err;
+    const int e = launch_fwd_window(q, k, v, o, lse, B, H, H_kv, N, d, scale * 1.4426950408889634f, window, n_sink, ctl,
+                                    static_cast<cudaStream_t>(stream));
+    return e == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
 FA_API int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes, void* v_scales,

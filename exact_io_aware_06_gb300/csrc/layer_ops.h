@@ -69,6 +69,10 @@ struct DecodeArgs {
 size_t decode_kv4_workspace_bytes(int B, int H, int H_kv, int N_q, int d);
 cudaError_t launch_decode_kv4(const DecodeArgs& a, int d, cudaStream_t s);
 
+// Forward under a causal window of `window` keys and the first `sinks` keys: bf16, d in {64, 128}.
+int launch_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv, int N,
+                      int d, float c_log2, int window, int sinks, DevCtl ctl, cudaStream_t s);
+
 constexpr int kDevIndex = 5;  // == FA_ERR_DEVICE_INDEX: a page or length outside the cache
 
 }  // namespace fa

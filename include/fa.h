@@ -340,6 +340,22 @@ int fa_qk_norm_rope_bwd(const void* qkv, const float* q_weight, const float* k_w
 size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int H_kv, int N, int d);
 
 /*
+ * Forward under a causal sliding window with sinks: query i sees key j iff j <= i and
+ * (j > i - window or j < n_sink), the `window` newest keys (its own among them) and the
+ * first n_sink ones.  O, lse and the grouping of heads as fa_fwd_gqa; only key blocks that
+ * hold a visible key are read.
+ *
+ *   q, o : [B][H][N][d] bfloat16;  k, v : [B][H_kv][N][d] bfloat16;  lse : [B][H][N] float32,
+ *   or NULL.   window >= 1 (N or more: plain causal), n_sink >= 0.   dtype : FA_BF16.
+ * K and V are read in blocks of 128 keys: a NaN or an infinity in V reaches every query whose
+ * blocks hold it (0 * NaN), hidden or not, as in fa_fwd.
+ * Errors: as fa_fwd_gqa; FA_ERR_INVALID_ARG also for window < 1 or n_sink < 0.
+ */
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
+                  int H_kv, int N, int d, float scale, int window, int n_sink, int dtype,
+                  void* stream);
+
+/*
  * A paged K/V cache in 4 bits.  32 neighbouring values of a head share one scale
  * s = bf16(max|x| / 7); a value is held as the nearest integer to x / s (ties to even) in
  * -7 .. 7, as the nibble code + 8.  A group of zeros has s = 0; a group that holds an

@@ -1,0 +1,143 @@
+"""Attention under a causal sliding window with sinks, forward and backward, against float64.
+
+Forward tolerance, with w the softmax weights and A = sum w |v|: P is rounded to bfloat16 (2^-8
+of each weight; the row sum is not, so o moves by at most 2^-8 A), o is rounded (2^-8 |o|), and
+float32 scores and sums add under 1e-5 (1 + max |score|) of A.  lse: 1e-5 (1 + max |score|)."""
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_06_gb300 as fa
+import plain64
+from gpu_util import check_status, ensure_built, f64, scale_for
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def rand(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g)).to(torch.bfloat16).cuda()
+
+
+def inputs(B, H, H_kv, N, d, seed=0):
+    return (rand((B, H, N, d), seed), rand((B, H_kv, N, d), seed + 1), rand((B, H_kv, N, d), seed + 2),
+            rand((B, H, N, d), seed + 3))
+
+
+def forward(q, k, v, scale, window, n_sink):
+    o = torch.full_like(q, float("nan"))
+    lse = torch.full(q.shape[:3], float("nan"), device="cuda")
+    fa.fa_fwd_window(q, k, v, o, lse, scale, window, n_sink)
+    check_status()
+    return o, lse
+
+
+def check_forward(q, k, v, o, lse, scale, window, n_sink, heads=None):
+    B, H, N, d = q.shape
+    seen = plain64.window_mask(N, N, 0, window, n_sink)
+    q, k, v, o, lse = (f64(t) for t in (q, k, v, o, lse))
+    for b in range(B):
+        for h in range(H) if heads is None else heads:
+            kv = h // (H // k.shape[1])
+            ref, ref_lse, P = plain64.attention(q[b, h], k[b, kv], v[b, kv], scale, seen)
+            A = P @ np.abs(v[b, kv])
+            top = 1e-5 * (1 + np.abs(scale) * np.abs(q[b, h] @ k[b, kv].T).max(-1))
+            tol = 2.0 ** -8 * (A + np.abs(ref)) + top[:, None] * A
+            err = np.abs(o[b, h] - ref)
+            assert np.isfinite(o[b, h]).all() and (err <= tol).all(), (b, h, float((err / tol).max()))
+            dl = np.abs(lse[b, h] - ref_lse)
+            assert (dl <= top).all(), (b, h, float((dl / top).max()))
+
+
+WINDOWS = [(1, 0), (1, 1), (2, 4), (7, 0), (64, 4), (127, 1), (128, 0), (128, 32), (129, 33), (200, 4), (256, 130),
+           (300, 4), (5000, 0), (2 ** 31 - 1, 7), (40, 2 ** 31 - 1)]
+
+
+@pytest.mark.parametrize("window,n_sink", WINDOWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_windows(window, n_sink, d):
+    q, k, v, _ = inputs(1, 2, 1, 700, d)
+    o, lse = forward(q, k, v, scale_for(d), window, n_sink)
+    check_forward(q, k, v, o, lse, scale_for(d), window, n_sink)
+
+
+@pytest.mark.parametrize("N", [1, 2, 31, 127, 128, 129, 255, 256, 257, 384, 385, 513])
+@pytest.mark.parametrize("window,n_sink", [(100, 4), (130, 0), (33, 40)])
+def test_forward_lengths(N, window, n_sink):
+    q, k, v, _ = inputs(2, 3, 1, N, 64, seed=N)
+    o, lse = forward(q, k, v, 0.125, window, n_sink)
+    check_forward(q, k, v, o, lse, 0.125, window, n_sink)
+
+
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (6, 3), (8, 2), (7, 1)])
+def test_forward_heads_many_items(H, H_kv):
+    # more items than SMs: every CTA carries its barriers from item to item
+    q, k, v, _ = inputs(16, H, H_kv, 1500, 64, seed=7)
+    o, lse = forward(q, k, v, 0.125, 150, 4)
+    check_forward(q[::5], k[::5], v[::5], o[::5], lse[::5], 0.125, 150, 4)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
+def test_forward_scales(scale):
+    q, k, v, _ = inputs(1, 2, 2, 400, 64, seed=3)
+    o, lse = forward(q, k, v, scale, 150, 3)
+    check_forward(q, k, v, o, lse, scale, 150, 3)
+
+
+def test_forward_growing_scores():
+    N, d = 600, 64
+    unit = rand((d,), 3).float()
+    k = (torch.arange(N, device="cuda")[:, None] / 40 * unit).to(torch.bfloat16)[None, None].contiguous()
+    q = unit.to(torch.bfloat16).expand(1, 1, N, d).contiguous()
+    v = rand((1, 1, N, d), 4)
+    o, lse = forward(q, k, v, 0.125, 200, 20)
+    check_forward(q, k, v, o, lse, 0.125, 200, 20)
+
+
+def test_forward_is_causal_attention_when_the_window_covers_everything():
+    q, k, v, _ = inputs(1, 4, 2, 1100, 128, seed=5)
+    o, lse = forward(q, k, v, scale_for(128), 1100, 0)
+    o2, lse2 = fa.attention_forward(q, k, v, causal=True)
+    # the same arithmetic per row up to the order of blocks: both within the forward's bound
+    check_forward(q, k, v, o2, lse2, scale_for(128), 1100, 0)
+    assert (f64(lse) - f64(lse2)).max() < 1e-5
+
+
+def test_forward_repeats_bit_for_bit_and_without_lse():
+    q, k, v, _ = inputs(3, 8, 2, 2000, 128, seed=9)
+    o, lse = forward(q, k, v, scale_for(128), 333, 4)
+    o2 = torch.empty_like(q)
+    fa.fa_fwd_window(q, k, v, o2, None, scale_for(128), 333, 4)
+    assert torch.equal(o, o2)
+
+
+def test_forward_large_offsets():
+    # K/V beyond 2^31 bytes from the base
+    B, H, N, d = 70, 8, 16384, 128
+    q = torch.zeros((B, H, N, d), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.zeros_like(q), torch.zeros_like(q)
+    small = inputs(1, 1, 1, N, d, seed=11)
+    q[-1, -1], k[-1, -1], v[-1, -1] = (t[0, 0] for t in small[:3])
+    o, lse = forward(q, k, v, scale_for(d), 200, 4)
+    o1, lse1 = forward(*small[:3], scale_for(d), 200, 4)
+    assert torch.equal(o[-1, -1], o1[0, 0]) and torch.equal(lse[-1, -1], lse1[0, 0])
+    assert (o[0] == 0).all()
+
+
+def test_forward_short_wait_limit_reports_and_recovers():
+    q, k, v, _ = inputs(4, 16, 16, 2048, 128, seed=13)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    try:
+        fa.fa_set_wait_timeout_ns(300)
+        for _ in range(3):
+            fa.fa_fwd_window(q, k, v, o, lse, scale_for(128), 500, 4)
+            assert fa.fa_last_device_error() in (fa.FA_OK, fa.FA_ERR_DEVICE_TIMEOUT)
+    finally:
+        fa.fa_set_wait_timeout_ns(0)
+    o, lse = forward(q, k, v, scale_for(128), 500, 4)
+    check_forward(q[:1], k[:1], v[:1], o[:1], lse[:1], scale_for(128), 500, 4, heads=[0, 15])

@@ -60,6 +60,23 @@ def test_norm_rope_bwd_refusals(L, change, status):
                                  a["H_kv"], a["N"], a["d"], a["rot"], 0, a["eps"], a["dtype"], None) == status
 
 
+WINDOW = dict(q=P, k=P, v=P, o=P, lse=None, B=1, H=4, H_kv=2, N=128, d=64, scale=0.1, window=16, sinks=4,
+              dtype=1)
+WINDOW_BAD = [
+    (dict(q=None), 1), (dict(k=MIS), 1), (dict(v=None), 1), (dict(o=None), 1), (dict(lse=MIS), 1),
+    (dict(B=0), 1), (dict(H=0), 1), (dict(H_kv=0), 1), (dict(H_kv=3), 1), (dict(N=0), 1),
+    (dict(scale=NAN), 1), (dict(scale=INF), 1), (dict(window=0), 1), (dict(window=-5), 1),
+    (dict(sinks=-1), 1), (dict(dtype=2), 1), (dict(dtype=0), 2), (dict(d=96), 2), (dict(d=256), 2),
+    (dict(N=(1 << 24) + 1), 2), (dict(B=1 << 12, H=1 << 13), 2), (dict(B=1 << 8, H=1 << 8, N=1 << 22), 2)]
+
+
+@pytest.mark.parametrize("change,status", WINDOW_BAD)
+def test_window_forward_refusals(L, change, status):
+    a = dict(WINDOW, **change)
+    assert L.fa_fwd_window(a["q"], a["k"], a["v"], a["o"], a["lse"], a["B"], a["H"], a["H_kv"], a["N"], a["d"],
+                           a["scale"], a["window"], a["sinks"], a["dtype"], None) == status
+
+
 CACHE = dict(kc=P, ks=P, vc=P, vs=P, table=P, B=2, H_kv=2, N=4, d=64, page=16, n_pages=8, max_blocks=4)
 CACHE_BAD = [
     (dict(kc=None), 1), (dict(ks=MIS), 1), (dict(vc=None), 1), (dict(vs=MIS), 1), (dict(table=None), 1),
