@@ -19,7 +19,7 @@ __all__ = [
     "fa_bwd_workspace_size", "fa_bwd_noalloc", "fa_last_device_error", "fa_set_wait_timeout_ns",
     "fa_selftest_wait_timeout", "fa_status_string", "attention_forward", "attention_backward",
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
-    "fa_fwd_window", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_decode_kv4_workspace_size",
+    "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_workspace_size", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_decode_kv4_workspace_size",
     "rope_frequencies", "kv4_cache",
 ]
 
@@ -80,6 +80,10 @@ def lib():
         L.fa_qk_norm_rope_bwd_workspace_size.restype = sz
         L.fa_fwd_window.argtypes = [vp] * 5 + [i] * 5 + [f, i, i, i, vp]
         L.fa_fwd_window.restype = i
+        L.fa_bwd_window.argtypes = [vp] * 10 + [sz] + [i] * 5 + [f, i, i, i, vp]
+        L.fa_bwd_window.restype = i
+        L.fa_bwd_window_workspace_size.argtypes = [i] * 7
+        L.fa_bwd_window_workspace_size.restype = sz
         L.fa_kv4_append.argtypes = [vp] * 9 + [i] * 7 + [vp]
         L.fa_kv4_append.restype = i
         L.fa_kv4_read.argtypes = [vp] * 8 + [i] * 7 + [vp]
@@ -333,6 +337,28 @@ def fa_fwd_window(q, k, v, o, lse, scale, window, n_sink, dtype=FA_BF16, stream=
                                _maybe("lse", torch.float32, (B, H, N), lse), B, H, H_kv, N, d,
                                float(scale), int(window), int(n_sink), int(dtype), _stream(stream)),
            "fa_fwd_window")
+
+
+def fa_bwd_window_workspace_size(B, H, H_kv, N, d, window, n_sink):
+    return int(lib().fa_bwd_window_workspace_size(int(B), int(H), int(H_kv), int(N), int(d), int(window),
+                                                  int(n_sink)))
+
+
+def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_sink, dtype=FA_BF16,
+                  stream=None):
+    """dq, dk, dv <- backward of fa_fwd_window, from its o and lse."""
+    import torch
+    B, H, N, d = _shape(q)
+    H_kv = _shape(k)[1]
+    t, rows, kv_rows = torch.bfloat16, (B, H, N, d), (B, H_kv, N, d)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().fa_bwd_window(_dense("q", t, rows, q), _dense("k", t, kv_rows, k),
+                               _dense("v", t, kv_rows, v), _dense("o", t, rows, o),
+                               _dense("lse", torch.float32, (B, H, N), lse), _dense("do", t, rows, do),
+                               _dense("dq", t, rows, dq), _dense("dk", t, kv_rows, dk),
+                               _dense("dv", t, kv_rows, dv), workspace.data_ptr(), ws_bytes, B, H, H_kv,
+                               N, d, float(scale), int(window), int(n_sink), int(dtype),
+                               _stream(stream)), "fa_bwd_window")
 
 
 def kv4_cache(n_pages, H_kv, page, d, device="cuda"):

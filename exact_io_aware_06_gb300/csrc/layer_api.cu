@@ -93,9 +93,7 @@ int decode_sizes(int B, int H, int H_kv, int N_q, int d) {
 }
 
 // Sizes and parameters of the windowed attention, forward and backward.
-int window_args(const void* q, const void* k, const void* v, const void* o, int B, int H, int H_kv, int N, int d,
-                float scale, int window, int n_sink, int dtype) {
-    if (!pointers_ok(q, k, v, o)) return FA_ERR_INVALID_ARG;
+int window_args(int B, int H, int H_kv, int N, int d, float scale, int window, int n_sink, int dtype) {
     if (B < 1 || H < 1 || N < 1 || H_kv < 1 || H % H_kv != 0) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || window < 1 || n_sink < 0) return FA_ERR_INVALID_ARG;
     if (dtype != FA_F32 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
@@ -151,14 +149,34 @@ FA_API int fa_qk_norm_rope_bwd(const void* qkv, const float* q_weight, const flo
 
 FA_API int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv,
                          int N, int d, float scale, int window, int n_sink, int dtype, void* stream) {
-    if (!optional_ok(lse)) return FA_ERR_INVALID_ARG;
-    const int rc = window_args(q, k, v, o, B, H, H_kv, N, d, scale, window, n_sink, dtype);
+    if (!pointers_ok(q, k, v, o) || !optional_ok(lse)) return FA_ERR_INVALID_ARG;
+    const int rc = window_args(B, H, H_kv, N, d, scale, window, n_sink, dtype);
     if (rc != FA_OK) return rc;
     DevCtl ctl;
     int err = FA_OK;
     if (!device_ctl(&ctl, &err)) return err;
     const int e = launch_fwd_window(q, k, v, o, lse, B, H, H_kv, N, d, scale * 1.4426950408889634f, window, n_sink, ctl,
                                     static_cast<cudaStream_t>(stream));
+    return e == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+FA_API size_t fa_bwd_window_workspace_size(int B, int H, int H_kv, int N, int d, int window, int n_sink) {
+    return window_args(B, H, H_kv, N, d, 1.f, window, n_sink, FA_BF16) == FA_OK
+               ? bwd_window_workspace_bytes(B, H, H_kv, N, d, window, n_sink) : 0;
+}
+
+FA_API int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                         void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int B, int H, int H_kv,
+                         int N, int d, float scale, int window, int n_sink, int dtype, void* stream) {
+    if (!pointers_ok(q, k, v, o, lse, dO, dq, dk, dv, workspace)) return FA_ERR_INVALID_ARG;
+    const int rc = window_args(B, H, H_kv, N, d, scale, window, n_sink, dtype);
+    if (rc != FA_OK) return rc;
+    if (workspace_bytes < bwd_window_workspace_bytes(B, H, H_kv, N, d, window, n_sink)) return FA_ERR_INVALID_ARG;
+    DevCtl ctl;
+    int err = FA_OK;
+    if (!device_ctl(&ctl, &err)) return err;
+    const int e = launch_bwd_window(q, k, v, o, lse, dO, dq, dk, dv, workspace, B, H, H_kv, N, d, scale, window, n_sink,
+                                    ctl, static_cast<cudaStream_t>(stream));
     return e == 0 ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -73,6 +73,22 @@ cudaError_t launch_decode_kv4(const DecodeArgs& a, int d, cudaStream_t s);
 int launch_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv, int N,
                       int d, float c_log2, int window, int sinks, DevCtl ctl, cudaStream_t s);
 
+// The windowed backward's deal: key block j meets query blocks j .. j + reach; the first
+// n_part blocks (those with sinks and more query blocks after that) leave the rest to
+// `pieces` pieces of `per` query blocks.
+struct WinSplit {
+    int window, sinks, reach, n_part, per, pieces;
+};
+WinSplit win_split(int B, int H_kv, int N, int window, int sinks);
+size_t bwd_window_workspace_bytes(int B, int H, int H_kv, int N, int d, int window, int sinks);
+int launch_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                      void* dq, void* dk, void* dv, void* workspace, int B, int H, int H_kv, int N, int d, float scale,
+                      int window, int sinks, DevCtl ctl, cudaStream_t s);
+// dQ for d = 128, from the workspace's negated rows.
+int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2,
+                         const float* ws_ndelta, void* dq, int B, int H, int H_kv, int N, float scale,
+                         const WinSplit& sp, DevCtl ctl, cudaStream_t s);
+
 constexpr int kDevIndex = 5;  // == FA_ERR_DEVICE_INDEX: a page or length outside the cache
 
 }  // namespace fa

@@ -356,6 +356,25 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
                   void* stream);
 
 /*
+ * Backward of fa_fwd_window, by recomputation from its lse, as fa_bwd_gqa over the pairs that
+ * the forward saw.
+ *   o, lse      : from fa_fwd_window with the same window and n_sink.
+ *   dq          : [B][H][N][d];  dk, dv : [B][H_kv][N][d] bfloat16, written.
+ *   workspace   : at least fa_bwd_window_workspace_size() bytes; its contents on entry do not
+ *                 matter.  Calls that overlap in time must not share one.
+ * dk and dv (and at d = 128 dq) have the same bits every time; at d = 64 dq is summed with
+ * float32 atomics in the workspace, in the order in which key blocks finish, as in fa_bwd.
+ * Errors: as fa_fwd_window; FA_ERR_INVALID_ARG also for a null lse and a workspace that is
+ * too small.
+ */
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                  const void* dO, void* dq, void* dk, void* dv, void* workspace,
+                  size_t workspace_bytes, int B, int H, int H_kv, int N, int d, float scale,
+                  int window, int n_sink, int dtype, void* stream);
+/* 0 for sizes that the call refuses. */
+size_t fa_bwd_window_workspace_size(int B, int H, int H_kv, int N, int d, int window, int n_sink);
+
+/*
  * A paged K/V cache in 4 bits.  32 neighbouring values of a head share one scale
  * s = bf16(max|x| / 7); a value is held as the nearest integer to x / s (ties to even) in
  * -7 .. 7, as the nibble code + 8.  A group of zeros has s = 0; a group that holds an

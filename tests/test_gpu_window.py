@@ -2,7 +2,13 @@
 
 Forward tolerance, with w the softmax weights and A = sum w |v|: P is rounded to bfloat16 (2^-8
 of each weight; the row sum is not, so o moves by at most 2^-8 A), o is rounded (2^-8 |o|), and
-float32 scores and sums add under 1e-5 (1 + max |score|) of A.  lse: 1e-5 (1 + max |score|)."""
+float32 scores and sums add under 1e-5 (1 + max |score|) of A.  lse: 1e-5 (1 + max |score|).
+
+Backward tolerance, with t = 1e-5 (1 + max |score|) for the recomputed P: dV takes P in bfloat16
+(2^-8 P^T |dO|); dS = P (dP - delta) has P in fp16 (2^-11 of dS, and 2^-25 of |dP - delta| below its
+normal range), is rounded to bfloat16 (2^-8), and delta = dO . o takes the o that the forward rounded:
+its error is |dO| . (o's tolerance).  Each gradient adds its own rounding, 2^-8 of the value.  Group
+sums add up."""
 import numpy as np
 import pytest
 import torch
@@ -141,3 +147,157 @@ def test_forward_short_wait_limit_reports_and_recovers():
         fa.fa_set_wait_timeout_ns(0)
     o, lse = forward(q, k, v, scale_for(128), 500, 4)
     check_forward(q[:1], k[:1], v[:1], o[:1], lse[:1], scale_for(128), 500, 4, heads=[0, 15])
+
+
+# ---------------------------------------------------------------- backward
+def backward(q, k, v, o, lse, do, scale, window, n_sink, ws=None):
+    B, H, N, d = q.shape
+    out = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+    if ws is None:
+        n = fa.fa_bwd_window_workspace_size(B, H, k.shape[1], N, d, window, n_sink)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    fa.fa_bwd_window(q, k, v, o, lse, do, *out, ws, scale, window, n_sink)
+    check_status()
+    return out
+
+
+def check_backward(q, k, v, do, grads, scale, window, n_sink, kv_heads=None):
+    B, H, N, d = q.shape
+    H_kv = k.shape[1]
+    G = H // H_kv
+    seen = plain64.window_mask(N, N, 0, window, n_sink)
+    q, k, v, do = (f64(t) for t in (q, k, v, do))
+    got = [f64(t) for t in grads]
+    assert all(np.isfinite(g).all() for g in got)
+    a = abs(scale)
+    for b in range(B):
+        for kv in range(H_kv) if kv_heads is None else kv_heads:
+            K, V = k[b, kv], v[b, kv]
+            aK, aV = np.abs(K), np.abs(V)
+            ref_dk, ref_dv, tol_dk, tol_dv = (np.zeros((N, d)) for _ in range(4))
+            for h in range(kv * G, kv * G + G):
+                Q, dO = q[b, h], do[b, h]
+                aQ, adO = np.abs(Q), np.abs(dO)
+                o, _, P = plain64.attention(Q, K, V, scale, seen)
+                t = 1e-5 * (1 + np.where(seen, a * np.abs(Q @ K.T), 0).max(-1, keepdims=True))
+                dP = dO @ V.T
+                diff = dP - (dO * o).sum(-1, keepdims=True)
+                A = P @ aV
+                d_delta = (adO * (2.0 ** -8 * (A + np.abs(o)) + t * A)).sum(-1, keepdims=True)
+                e_P = P * t + seen * 2.0 ** -25
+                e_dS = (2.0 ** -8 + 2.0 ** -11) * np.abs(P * diff) + P * d_delta + e_P * np.abs(diff) \
+                    + 1e-6 * P * (adO @ aV.T)
+                dS = P * diff
+                rq, tq = scale * dS @ K, a * e_dS @ aK
+                err = np.abs(got[0][b, h] - rq)
+                tq += 2.0 ** -8 * np.abs(rq) + 1e-6 * a * np.abs(dS) @ aK + 1e-37
+                assert (err <= tq).all(), ("dq", b, h, float((err / tq).max()))
+                ref_dk += scale * dS.T @ Q
+                ref_dv += P.T @ dO
+                tol_dk += a * e_dS.T @ aQ + 1e-6 * a * np.abs(dS).T @ aQ
+                tol_dv += (2.0 ** -8 * P + P * t + 1e-6 * P).T @ adO
+            for name, g, r, tol in (("dk", got[1], ref_dk, tol_dk), ("dv", got[2], ref_dv, tol_dv)):
+                tol = tol + 2.0 ** -8 * np.abs(r) + 1e-37
+                err = np.abs(g[b, kv] - r)
+                assert (err <= tol).all(), (name, b, kv, float((err / tol).max()))
+
+
+def step(B, H, H_kv, N, d, window, n_sink, scale=None, seed=0, kv_heads=None):
+    q, k, v, do = inputs(B, H, H_kv, N, d, seed)
+    scale = scale_for(d) if scale is None else scale
+    o, lse = forward(q, k, v, scale, window, n_sink)
+    grads = backward(q, k, v, o, lse, do, scale, window, n_sink)
+    check_backward(q, k, v, do, grads, scale, window, n_sink, kv_heads)
+    return (q, k, v, o, lse, do), grads
+
+
+@pytest.mark.parametrize("window,n_sink", WINDOWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_windows(window, n_sink, d):
+    step(1, 2, 1, 700, d, window, n_sink)
+
+
+@pytest.mark.parametrize("N", [1, 2, 127, 128, 129, 256, 385, 513])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_lengths(N, d):
+    step(2, 3, 1, N, d, 100, 4, seed=N)
+    step(2, 2, 2, N, d, 33, 40, seed=N)
+
+
+@pytest.mark.parametrize("H,H_kv,d", [(6, 3, 64), (8, 1, 64), (8, 2, 128), (3, 3, 128)])
+def test_backward_heads_many_items_and_pieces(H, H_kv, d):
+    # more items than SMs; sinks in two blocks, whose later query blocks are dealt in pieces
+    step(9, H, H_kv, 1700, d, 150, 140, kv_heads=[0])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_long_with_few_heads(d):
+    # one K/V head: the sink block's later query blocks in many pieces, the last one short
+    step(1, 2, 1, 5000, d, 130, 4)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+def test_backward_scales(scale):
+    step(1, 2, 2, 400, 64, 150, 3, scale=scale)
+    step(1, 2, 2, 400, 128, 150, 3, scale=scale)
+
+
+def test_backward_is_causal_backward_when_the_window_covers_everything():
+    (q, k, v, o, lse, do), grads = step(1, 4, 2, 900, 128, 900, 0, seed=5)
+    o2, lse2 = fa.attention_forward(q, k, v, causal=True)
+    grads2 = fa.attention_backward(q, k, v, o2, lse2, do, causal=True)
+    for g, r in zip(grads, grads2):
+        assert np.abs(f64(g) - f64(r)).max() <= 5e-2
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_repeats_on_a_used_workspace(d):
+    (q, k, v, o, lse, do), grads = step(2, 4, 2, 1500, d, 200, 4, seed=9)
+    n = fa.fa_bwd_window_workspace_size(2, 4, 2, 1500, d, 200, 4)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        again = backward(q, k, v, o, lse, do, scale_for(d), 200, 4, ws)
+        assert torch.equal(again[1], grads[1]) and torch.equal(again[2], grads[2])
+        if d == 128:
+            assert torch.equal(again[0], grads[0])
+        else:  # float32 sums in another order, then one rounding
+            assert ((again[0].float() - grads[0].float()).abs() <= 2.0 ** -7 * grads[0].float().abs() + 1e-4).all()
+
+
+def test_training_step_in_a_graph():
+    # forward and backward captured together, replayed on new inputs in the same buffers
+    B, H, H_kv, N, d, window, n_sink = 2, 4, 2, 600, 64, 130, 4
+    q, k, v, do = inputs(B, H, H_kv, N, d)
+    o, lse = torch.empty_like(q), torch.empty((B, H, N), device="cuda")
+    out = [torch.empty_like(t) for t in (q, k, v)]
+    ws = torch.empty(fa.fa_bwd_window_workspace_size(B, H, H_kv, N, d, window, n_sink), dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_window(q, k, v, o, lse, 0.125, window, n_sink)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fa_fwd_window(q, k, v, o, lse, 0.125, window, n_sink)
+        fa.fa_bwd_window(q, k, v, o, lse, do, *out, ws, 0.125, window, n_sink)
+    for seed in (20, 30):
+        for t, new in zip((q, k, v, do), inputs(B, H, H_kv, N, d, seed)):
+            t.copy_(new)
+        graph.replay()
+        check_status()
+        check_forward(q, k, v, o, lse, 0.125, window, n_sink)
+        check_backward(q, k, v, do, out, 0.125, window, n_sink)
+
+
+def test_backward_short_wait_limit_reports_and_recovers():
+    for d in (64, 128):
+        q, k, v, do = inputs(2, 16, 16, 2048, d, seed=13)
+        o, lse = forward(q, k, v, scale_for(d), 500, 4)
+        out = [torch.empty_like(t) for t in (q, k, v)]
+        ws = torch.empty(fa.fa_bwd_window_workspace_size(2, 16, 16, 2048, d, 500, 4), dtype=torch.uint8, device="cuda")
+        try:
+            fa.fa_set_wait_timeout_ns(300)
+            for _ in range(3):
+                fa.fa_bwd_window(q, k, v, o, lse, do, *out, ws, scale_for(d), 500, 4)
+                assert fa.fa_last_device_error() in (fa.FA_OK, fa.FA_ERR_DEVICE_TIMEOUT)
+        finally:
+            fa.fa_set_wait_timeout_ns(0)
+        grads = backward(q, k, v, o, lse, do, scale_for(d), 500, 4, ws)
+        check_backward(q[:1], k[:1], v[:1], do[:1], [g[:1] for g in grads], scale_for(d), 500, 4, kv_heads=[0, 15])

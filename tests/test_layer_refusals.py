@@ -77,6 +77,31 @@ def test_window_forward_refusals(L, change, status):
                            a["scale"], a["window"], a["sinks"], a["dtype"], None) == status
 
 
+@pytest.mark.parametrize("change,status", WINDOW_BAD + [
+    (dict(lse=None), 1), (dict(do=MIS), 1), (dict(dq=None), 1), (dict(dk=MIS), 1), (dict(dv=None), 1),
+    (dict(ws=None), 1), (dict(ws=MIS), 1), (dict(short=4), 1)])
+def test_window_backward_refusals(L, change, status):
+    a = dict(WINDOW, lse=P, do=P, dq=P, dk=P, dv=P, ws=P, short=0)
+    a.update(change)
+    n = fa.fa_bwd_window_workspace_size(*(a[x] for x in ("B", "H", "H_kv", "N", "d", "window", "sinks")))
+    assert L.fa_bwd_window(a["q"], a["k"], a["v"], a["o"], a["lse"], a["do"], a["dq"], a["dk"], a["dv"], a["ws"],
+                           n - a["short"] if n else 0, a["B"], a["H"], a["H_kv"], a["N"], a["d"], a["scale"],
+                           a["window"], a["sinks"], a["dtype"], None) == status
+
+
+def test_window_workspace(L):
+    # delta, lse and the dQ accumulator as the plain backward's; nothing more without sinks, or
+    # where the window covers the sequence; a sink block's parts otherwise
+    rows = fa.fa_bwd_workspace_size(2, 4, 4096, 64)
+    size = fa.fa_bwd_window_workspace_size
+    assert size(2, 4, 2, 4096, 64, 512, 0) == rows
+    assert size(2, 4, 2, 4096, 64, 4096, 100) == rows
+    # 32 query blocks, 5 of them in reach: 27 later ones in pieces of 5 blocks, and the near part
+    assert size(2, 4, 2, 4096, 64, 512, 4) == rows + 2 * 2 * (6 + 1) * 2 * 128 * 64 * 4
+    assert size(1, 4, 3, 4096, 64, 512, 4) == 0
+    assert size(1, 4, 2, 4096, 64, 0, 4) == 0
+
+
 CACHE = dict(kc=P, ks=P, vc=P, vs=P, table=P, B=2, H_kv=2, N=4, d=64, page=16, n_pages=8, max_blocks=4)
 CACHE_BAD = [
     (dict(kc=None), 1), (dict(ks=MIS), 1), (dict(vc=None), 1), (dict(vs=MIS), 1), (dict(table=None), 1),
