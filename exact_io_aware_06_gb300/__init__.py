@@ -18,10 +18,24 @@ __all__ = [
     "fa_fwd_fp8_per_head", "fa_fwd_fp8_per_block", "fa_bwd",
     "fa_bwd_workspace_size", "fa_bwd_noalloc", "fa_last_device_error", "fa_set_wait_timeout_ns",
     "fa_selftest_wait_timeout", "fa_status_string", "attention_forward", "attention_backward",
-    "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
-    "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_workspace_size", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_decode_kv4_workspace_size",
-    "rope_frequencies", "kv4_cache",
 ]
+
+# the layer around the attention call (_layer.py, loaded on first use)
+_LAYER = (
+    "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_fwd_window",
+    "fa_bwd_window", "fa_bwd_window_workspace_size", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
+    "fa_decode_kv4_workspace_size", "rope_frequencies", "kv4_cache",
+)
+__all__ += _LAYER
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import _layer
+    globals().update({n: getattr(_layer, n) for n in _LAYER})
+    return globals()[name]
+
 
 FA_F32, FA_BF16, FA_E4M3 = 0, 1, 2
 FA_OK = 0
@@ -241,193 +255,6 @@ def fa_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, scale, causal, dtype, stream
     _check(lib().fa_bwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do),
                                 _ptr(dq), _ptr(dk), _ptr(dv), B, H, N, d, float(scale),
                                 int(bool(causal)), int(dtype), _stream(stream)), "fa_bwd_noalloc")
-
-
-# ---------------------------------------------------------------- the layer around the call
-def _dense(what, dtype, shape, t):
-    """Device pointer of a contiguous tensor of this dtype and shape on the current device."""
-    import torch
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous {dtype} {list(shape)} expected, got {t.dtype} "
-                         f"{list(t.shape)}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what}: a tensor on the current CUDA device expected, got {t.device}")
-    return t.data_ptr()
-
-
-def _maybe(what, dtype, shape, t):
-    return None if t is None else _dense(what, dtype, shape, t)
-
-
-def _float_code(t):
-    import torch
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"float32 or bfloat16 expected, got {t.dtype}")
-    return FA_F32 if t.dtype == torch.float32 else FA_BF16
-
-
-def _norm_rope_head(qkv, q_like, k_like, q_weight, k_weight, positions, inv_freq):
-    """What fa_qk_norm_rope and its gradient have in common: pointers and sizes."""
-    import torch
-    code = _float_code(qkv)
-    B, H, N, d = _shape(q_like)
-    H_kv = _shape(k_like)[1]
-    rot = 0
-    if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq: a contiguous float64 tensor on the host (rope_frequencies)")
-        rot = 2 * inv_freq.numel()
-    head = (_dense("qkv", qkv.dtype, (B, N, H + 2 * H_kv, d), qkv),
-            _maybe("q_weight", torch.float32, (d,), q_weight),
-            _maybe("k_weight", torch.float32, (d,), k_weight),
-            _maybe("positions", torch.int32, (B, N), positions),
-            inv_freq.data_ptr() if rot else None)
-    return code, (B, H, H_kv, N, d), rot, head
-
-
-def rope_frequencies(rot, base=10000.0):
-    """The rotation's rot / 2 frequencies base^(-2 p / rot), radians per position (float64, host)."""
-    import torch
-    return float(base) ** (-torch.arange(rot // 2, dtype=torch.float64) * 2 / rot)
-
-
-def fa_qk_norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, eps, interleaved=False,
-                    stream=None):
-    """q [B, H, N, d], k, v [B, H_kv, N, d] <- norm and rotation of qkv [B, N, H + 2 H_kv, d].
-    q_weight, k_weight (float32 [d]), positions (int32 [B, N]) and inv_freq (float64 host tensor
-    of rot / 2) may be None: ones, the index in the sequence, no rotation."""
-    code, (B, H, H_kv, N, d), rot, head = _norm_rope_head(qkv, q, k, q_weight, k_weight, positions,
-                                                          inv_freq)
-    t = qkv.dtype
-    _check(lib().fa_qk_norm_rope(*head, _dense("q", t, (B, H, N, d), q), _dense("k", t, (B, H_kv, N, d), k),
-                                 _dense("v", t, (B, H_kv, N, d), v), B, H, H_kv, N, d, rot,
-                                 int(bool(interleaved)), float(eps), code, _stream(stream)),
-           "fa_qk_norm_rope")
-
-
-def fa_qk_norm_rope_bwd_workspace_size(B, H, H_kv, N, d):
-    return int(lib().fa_qk_norm_rope_bwd_workspace_size(int(B), int(H), int(H_kv), int(N), int(d)))
-
-
-def fa_qk_norm_rope_bwd(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv, dqkv, dq_weight,
-                        dk_weight, workspace, eps, interleaved=False, stream=None):
-    """dqkv and (float32 [d], or None) dq_weight, dk_weight <- gradient of fa_qk_norm_rope."""
-    import torch
-    code, (B, H, H_kv, N, d), rot, head = _norm_rope_head(qkv, dq, dk, q_weight, k_weight, positions,
-                                                          inv_freq)
-    t = qkv.dtype
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().fa_qk_norm_rope_bwd(
-        *head, _dense("dq", t, (B, H, N, d), dq), _dense("dk", t, (B, H_kv, N, d), dk),
-        _dense("dv", t, (B, H_kv, N, d), dv), _dense("dqkv", t, (B, N, H + 2 * H_kv, d), dqkv),
-        _maybe("dq_weight", torch.float32, (d,), dq_weight),
-        _maybe("dk_weight", torch.float32, (d,), dk_weight), _ptr(workspace), ws_bytes, B, H, H_kv, N, d,
-        rot, int(bool(interleaved)), float(eps), code, _stream(stream)), "fa_qk_norm_rope_bwd")
-
-
-def fa_fwd_window(q, k, v, o, lse, scale, window, n_sink, dtype=FA_BF16, stream=None):
-    """Forward under a causal window of `window` keys and the first n_sink keys: q, o
-    [B, H, N, d], k, v [B, H_kv, N, d] bfloat16; lse [B, H, N] or None."""
-    import torch
-    B, H, N, d = _shape(q)
-    H_kv = _shape(k)[1]
-    t = torch.bfloat16
-    _check(lib().fa_fwd_window(_dense("q", t, (B, H, N, d), q), _dense("k", t, (B, H_kv, N, d), k),
-                               _dense("v", t, (B, H_kv, N, d), v), _dense("o", t, (B, H, N, d), o),
-                               _maybe("lse", torch.float32, (B, H, N), lse), B, H, H_kv, N, d,
-                               float(scale), int(window), int(n_sink), int(dtype), _stream(stream)),
-           "fa_fwd_window")
-
-
-def fa_bwd_window_workspace_size(B, H, H_kv, N, d, window, n_sink):
-    return int(lib().fa_bwd_window_workspace_size(int(B), int(H), int(H_kv), int(N), int(d), int(window),
-                                                  int(n_sink)))
-
-
-def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_sink, dtype=FA_BF16,
-                  stream=None):
-    """dq, dk, dv <- backward of fa_fwd_window, from its o and lse."""
-    import torch
-    B, H, N, d = _shape(q)
-    H_kv = _shape(k)[1]
-    t, rows, kv_rows = torch.bfloat16, (B, H, N, d), (B, H_kv, N, d)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().fa_bwd_window(_dense("q", t, rows, q), _dense("k", t, kv_rows, k),
-                               _dense("v", t, kv_rows, v), _dense("o", t, rows, o),
-                               _dense("lse", torch.float32, (B, H, N), lse), _dense("do", t, rows, do),
-                               _dense("dq", t, rows, dq), _dense("dk", t, kv_rows, dk),
-                               _dense("dv", t, kv_rows, dv), workspace.data_ptr(), ws_bytes, B, H, H_kv,
-                               N, d, float(scale), int(window), int(n_sink), int(dtype),
-                               _stream(stream)), "fa_bwd_window")
-
-
-def kv4_cache(n_pages, H_kv, page, d, device="cuda"):
-    """Zeroed arrays of a 4-bit cache: k_codes, k_scales, v_codes, v_scales."""
-    import torch
-    codes = [torch.zeros((n_pages, H_kv, page, d // 2), dtype=torch.uint8, device=device) for _ in "kv"]
-    scales = [torch.zeros((n_pages, H_kv, page, d // 32), dtype=torch.bfloat16, device=device) for _ in "kv"]
-    return codes[0], scales[0], codes[1], scales[1]
-
-
-def _cache_args(k_codes, k_scales, v_codes, v_scales, block_table, B, d):
-    import torch
-    if k_codes.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("4-bit cache: codes [n_pages, H_kv, page, d / 2], block_table [B, max_blocks]")
-    n_pages, H_kv, page = (int(x) for x in k_codes.shape[:3])
-    codes, scales = (n_pages, H_kv, page, d // 2), (n_pages, H_kv, page, d // 32)
-    max_blocks = int(block_table.shape[1])
-    return ((_dense("k_codes", torch.uint8, codes, k_codes),
-             _dense("k_scales", torch.bfloat16, scales, k_scales),
-             _dense("v_codes", torch.uint8, codes, v_codes),
-             _dense("v_scales", torch.bfloat16, scales, v_scales),
-             _dense("block_table", torch.int32, (B, max_blocks), block_table)), H_kv,
-            (page, n_pages, max_blocks))
-
-
-def fa_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, block_table, first, count=None,
-                  stream=None):
-    """Store k, v (bfloat16 [B, H_kv, N, d]) in the cache as tokens first[b] + 0 .. count[b] - 1
-    (int32 [B]; count None: N)."""
-    import torch
-    B, H_kv, N, d = _shape(k)
-    cache, heads, sizes = _cache_args(k_codes, k_scales, v_codes, v_scales, block_table, B, d)
-    rows = (B, heads, N, d)
-    _check(lib().fa_kv4_append(_dense("k", torch.bfloat16, rows, k), _dense("v", torch.bfloat16, rows, v),
-                               *cache, _dense("first", torch.int32, (B,), first),
-                               _maybe("count", torch.int32, (B,), count), B, H_kv, N, d, *sizes,
-                               _stream(stream)), "fa_kv4_append")
-
-
-def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, block_table, lengths, k, v, stream=None):
-    """k, v (bfloat16 [B, H_kv, N, d]) <- the cache's first N tokens of every request; rows from
-    lengths[b] (int32 [B]) on are zeros."""
-    import torch
-    B, H_kv, N, d = _shape(k)
-    cache, heads, sizes = _cache_args(k_codes, k_scales, v_codes, v_scales, block_table, B, d)
-    rows = (B, heads, N, d)
-    _check(lib().fa_kv4_read(*cache, _dense("lengths", torch.int32, (B,), lengths),
-                             _dense("k", torch.bfloat16, rows, k), _dense("v", torch.bfloat16, rows, v),
-                             B, H_kv, N, d, *sizes, _stream(stream)), "fa_kv4_read")
-
-
-def fa_decode_kv4_workspace_size(B, H, H_kv, N_q, d):
-    return int(lib().fa_decode_kv4_workspace_size(int(B), int(H), int(H_kv), int(N_q), int(d)))
-
-
-def fa_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, lengths, o, lse, workspace,
-                  scale, window=0, n_sink=0, stream=None):
-    """o (and lse, may be None) <- attention of the newest N_q tokens of every request, q
-    [B, H, N_q, d], over the 4-bit cache; lengths int32 [B]; window 0: all earlier tokens."""
-    import torch
-    B, H, N_q, d = _shape(q)
-    cache, H_kv, sizes = _cache_args(k_codes, k_scales, v_codes, v_scales, block_table, B, d)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib().fa_decode_kv4(_dense("q", torch.bfloat16, (B, H, N_q, d), q), *cache,
-                               _dense("lengths", torch.int32, (B,), lengths),
-                               _dense("o", torch.bfloat16, (B, H, N_q, d), o),
-                               _maybe("lse", torch.float32, (B, H, N_q), lse), workspace.data_ptr(),
-                               ws_bytes, B, H, H_kv, N_q, d, *sizes, float(scale), int(window),
-                               int(n_sink), _stream(stream)), "fa_decode_kv4")
 
 
 def fa_last_device_error(stream=None):

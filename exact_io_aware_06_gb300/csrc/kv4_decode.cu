@@ -12,10 +12,12 @@
 //     where rows on the M side would leave half of it empty.  tcgen05's smallest M is 64 and
 //     its operands come from shared memory: the codes would have to be expanded into it, 4
 //     times their bytes, which costs more than the whole multiplication here.
-//   * Expanding codes.  (word >> 4 i) & 0x000F000F | 0x43004300 is two bf16 values 128 + u:
-//     under one integer operation a value.  The offset 136 = 128 + 8 costs nothing for K, whose
-//     accumulators start at -136 sum_d q_d of each group of 32; for V it is one packed
-//     subtraction (exact) per two values.  (Adding up P in a further product, with A = -136 in
+//   * Expanding codes, which the integer pipe bounds before memory does.  K meets Q in fp16:
+//     word & 0x000F000F and word & 0x00F000F0 are pairs of the subnormals u 2^-24 and 16 u 2^-24
+//     as they stand, five operations for eight values; Q is scaled to fit (exactly), and the
+//     codes' offset 8 costs nothing: the accumulators start at -8 sum_d q_d of each group of 32.
+//     V meets P s, whose range only bf16 holds: (word >> 4 i) & 0x000F000F | 0x43004300 is a
+//     pair of 128 + u, and one packed subtraction (exact) makes it u - 8.  (Adding up P in a further product, with A = -136 in
 //     one group's rows and 0 elsewhere, is cheaper, but 0 * NaN would carry a NaN scale from
 //     its own group's outputs into the others'.)  Scales: K's multiply the group's accumulators
 //     in float; V's multiply P in float, and the product is rounded to bf16 once, by at most
@@ -24,7 +26,7 @@
 //     one movmatrix per 8 x 8 block.
 //   * Copies.  Each warp runs its own ring of 16-token tiles, filled by 16-byte asynchronous
 //     copies of its lanes (a tile never crosses a page); no barrier between warps.
-//   * Splitting.  The units of 64 tokens of all requests and heads form one list that is cut
+//   * Splitting.  The units of 128 tokens of all requests and heads form one list that is cut
 //     evenly over the resident CTAs, whatever the lengths are: a CTA's share may cover several
 //     requests or a part of one.  Whole requests are written at once; parts go to the
 //     workspace, and decode_join_kernel adds them.  The cut depends on the lengths alone, so
@@ -41,8 +43,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnitTiles = kWarps;  // tiles of 16 tokens in a unit: one per warp
-constexpr int kStages = 4;         // ring of tiles per warp
+constexpr int kTiles = 2;                      // tiles of 16 tokens that a warp works on together
+constexpr int kUnitTiles = kWarps * kTiles;    // tiles of a unit
+constexpr int kStages = 3;                     // ring of such steps per warp
+constexpr int kNowhere = 0x7fffff00;           // the "token" of a tile that is not there: hidden to every row
 constexpr float kTau = 8.0f;        // lazy rescale: the reference moves by more than this (log2)
 constexpr int kMaxCtas = 1024;
 
@@ -105,6 +109,19 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -112,6 +129,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 // nibble i of both halves of w as bf16 pair 128 + u
 __device__ __forceinline__ uint32_t expand(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
+// nibbles 0 (u) and 1 (16 u) of both halves of w as fp16 pairs, times 2^-24: subnormals
+__device__ __forceinline__ uint32_t tiny(uint32_t w, int i) { return w & (i ? 0x00F000F0u : 0x000F000Fu); }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -143,17 +162,17 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 
 // NT: tiles of 8 query rows that share the expanded codes (1 or 2).
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     decode_kv4_kernel(const __grid_constant__ DecodeArgs a, const Work work, const int row_tiles) {
     using T = TileCfg<D>;
     constexpr int G = D / 32;      // groups of 32 values
     constexpr int ROWS = 8 * NT;
-    extern __shared__ __align__(128) uint8_t smem[];  // rings, then the warps' results
+    extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings; at an entry's end their results
     __shared__ long long s_sum[kWarps];
     __shared__ long long s_found[2];  // request of the first unit, units before it
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    uint8_t* const ring = smem + warp * kStages * T::kBytes;
-    float* const results = reinterpret_cast<float*>(smem + kWarps * kStages * T::kBytes);
+    uint8_t* const ring = smem + warp * (kStages * kTiles * T::kBytes);
+    float* const results = reinterpret_cast<float*>(smem);
     griddep_wait();
     griddep_launch_dependents();
 
@@ -220,76 +239,108 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
         const bool whole = k0 == 0 && take == R.n_units;
         const bool is_first = u == u_begin;
 
-        // this warp's tiles: list indexes x0, x0 + kWarps, ... below x1
-        const int x0 = k0 * kUnitTiles + warp, x1 = min(R.n_tiles, (k0 + take) * kUnitTiles);
-        const int n_mine = x0 < x1 ? (x1 - x0 + kWarps - 1) / kWarps : 0;
-        auto token_of = [&](int i) {
-            const int x = x0 + i * kWarps;
-            return kTileTokens * (x < R.sink ? x : R.start + x - R.sink);
-        };
-        auto page_at = [&](int i) {  // -1: none
-            if (i >= n_mine) return -1;
-            const int p = __ldg(a.cache.table + static_cast<long long>(b) * a.cache.max_blocks + (token_of(i) >> a.cache.page_log2));
-            if (p < 0 || p >= a.cache.n_pages) {
-                if (lane == 0) atomicCAS(a.ctl.status, kDevOk, kDevIndex);
-                return -1;
+        // this warp's tiles: kTiles neighbours in every unit of the list [8 k0, 8 (k0 + take))
+        const int x0 = k0 * kUnitTiles + warp * kTiles, x1 = min(R.n_tiles, (k0 + take) * kUnitTiles);
+        const int n_mine = x0 < x1 ? (x1 - x0 + kUnitTiles - 1) / kUnitTiles : 0;  // steps
+        const int shift = R.start - R.sink;
+        const int* table = a.cache.table + static_cast<long long>(b) * a.cache.max_blocks;
+        const int page_mask = (1 << a.cache.page_log2) - 1;
+        const size_t head_row = static_cast<size_t>(kv) << a.cache.page_log2;
+        const size_t page_rows = static_cast<size_t>(a.cache.H_kv) << a.cache.page_log2;
+        const uint8_t* k_src = a.cache.codes[0] + head_row * (D / 2) + lane * 16;
+        const uint8_t* v_src = a.cache.codes[1] + head_row * (D / 2) + lane * 16;
+        constexpr int kPieces = T::kScales / 16;  // lanes below kPieces copy K's scales, the next ones V's
+        const uint8_t* s_src = reinterpret_cast<const uint8_t*>(a.cache.scales[lane >= kPieces ? 1 : 0]) +
+                               head_row * (D / 16) + (lane % kPieces) * 16;
+        // first token and page of tile j of step i; kNowhere where there is none
+        auto place = [&](int i, int j, int& tok, int& page) {
+            const int x = x0 + i * kUnitTiles + j;
+            tok = kNowhere;
+            page = -1;
+            if (x >= x1) return;
+            const int t0 = kTileTokens * (x < R.sink ? x : x + shift);
+            page = __ldg(table + (t0 >> a.cache.page_log2));
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages)) {
+                tok = t0;
+            } else if (lane == 0) {
+                atomicCAS(a.ctl.status, kDevOk, kDevIndex);
             }
-            return p;
         };
-        // the lanes' copies of tile i into its stage; a tile without a page is not copied
-        auto issue = [&](int i, int page) {
-            if (page >= 0) {
-                const uint32_t dst = smem_u32(ring + (i % kStages) * T::kBytes);
-                const int slot = token_of(i) & ((1 << a.cache.page_log2) - 1);
-                const size_t row = ((static_cast<size_t>(page) * a.cache.H_kv + kv) << a.cache.page_log2) + slot;
-                const uint8_t* kc = a.cache.codes[0] + row * (D / 2);
-                const uint8_t* vc = a.cache.codes[1] + row * (D / 2);
+        // the lanes' copies of a tile; one that is not there is not copied
+        auto copy = [&](uint32_t dst, int tok, int page) {
+            if (tok == kNowhere) return;
+            const size_t row = page * page_rows + (tok & page_mask);
+            const uint8_t* ks = k_src + row * (D / 2);
+            const uint8_t* vs = v_src + row * (D / 2);
 #pragma unroll
-                for (int x = 0; x < T::kCodes; x += 512) {
-                    cp_async16(dst + x + lane * 16, kc + x + lane * 16);
-                    cp_async16(dst + T::kOffV + x + lane * 16, vc + x + lane * 16);
-                }
-                constexpr int kPieces = T::kScales / 16;
-                if (lane < 2 * kPieces) {
-                    const uint16_t* src = a.cache.scales[lane >= kPieces] + row * G;
-                    cp_async16(dst + T::kOffKs + lane * 16, src + (lane % kPieces) * 8);
-                }
+            for (int x = 0; x < T::kCodes; x += 512) {
+                cp_async16(dst + x + lane * 16, ks + x);
+                cp_async16(dst + T::kOffV + x + lane * 16, vs + x);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (lane < 2 * kPieces) cp_async16(dst + T::kOffKs + lane * 16, s_src + row * (D / 16));
         };
-        uint32_t have = 0;  // bit i % 32: tile i has a page (of the tiles in the ring)
+        const uint32_t ring0 = smem_u32(ring);
+        int toks[kStages][kTiles], next_tok[kTiles], next_page[kTiles];  // toks[s]: the s-th step from here on
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            const int p = page_at(i);
-            have |= (p >= 0 ? 1u : 0u) << i;
-            issue(i, p);
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                int page;
+                place(i, j, toks[i][j], page);
+                copy(ring0 + (i * kTiles + j) * T::kBytes, toks[i][j], page);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        int next_page = page_at(kStages - 1);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) place(kStages - 1, j, next_tok[j], next_page[j]);
+        int stage = 0, fill = kStages - 1;  // ring positions of this step and of the one to be fetched
 
-        // Q^T fragments, in the order of d that a lane's K words have, and -136 sum q by group
+        // Q^T fragments in fp16, in the order of d that a lane's K words have.  A row is scaled by
+        // a power of two to below 2^14 (back in c_row), so that its bf16 values are exact down to
+        // 2^-28 of the largest, and where K's nibble comes as 16 u, q is divided by 16.
         uint32_t qf[NT][D / 16][2];
-        float q0[NT][G][2];
+        float q0[NT][G][2];  // -8 sum of q by group, times 2^-24: what takes the codes' 8 out
+        float c_row[NT][2];  // scale * log2(e) * 2^24 over the rows' factors
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = row0 + 8 * n + g;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
                                ((static_cast<size_t>(b) * a.H + static_cast<size_t>(kv) * (a.H / a.cache.H_kv)) * a.N_q + r) * D);
+            uint4 w[G];
+            uint32_t top = 0;  // largest magnitude, as bits
 #pragma unroll
             for (int c = 0; c < G; ++c) {
-                // values 32 c + 8 t + 0..7 of row g: pairs (i, i + 4)
-                const uint4 w = r < rows_all ? __ldg(src + 4 * c + t) : make_uint4(0, 0, 0, 0);
-                qf[n][2 * c][0] = __byte_perm(w.x, w.z, 0x5410);
-                qf[n][2 * c][1] = __byte_perm(w.x, w.z, 0x7632);
-                qf[n][2 * c + 1][0] = __byte_perm(w.y, w.w, 0x5410);
-                qf[n][2 * c + 1][1] = __byte_perm(w.y, w.w, 0x7632);
-                float sum = (bf_lo(w.x) + bf_hi(w.x)) + (bf_lo(w.y) + bf_hi(w.y)) + ((bf_lo(w.z) + bf_hi(w.z)) +
-                            (bf_lo(w.w) + bf_hi(w.w)));
+                w[c] = r < rows_all ? __ldg(src + 4 * c + t) : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(13 - exponent), kept within float's normal range (a row of zeros or subnormals
+            // stays small; infinities and NaN stay what they are)
+            const int ex = static_cast<int>(top >> 7) - 127;
+            const int up = min(max(13 - ex, -100), 100);
+            const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            const float back = a.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * 0x1p24f;
+#pragma unroll
+            for (int c = 0; c < G; ++c) {
+                // values 32 c + 8 t + 0..7 of row g: pairs (i, i + 4) for nibble i
+                const float q[8] = {bf_lo(w[c].x) * f, bf_hi(w[c].x) * f, bf_lo(w[c].y) * f, bf_hi(w[c].y) * f,
+                                    bf_lo(w[c].z) * f, bf_hi(w[c].z) * f, bf_lo(w[c].w) * f, bf_hi(w[c].w) * f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    qf[n][2 * c + i / 2][i % 2] = (i & 1) ? pack_f16x2(q[i] * 0.0625f, q[i + 4] * 0.0625f)
+                                                          : pack_f16x2(q[i], q[i + 4]);
+                float sum = ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 // from row g's lanes to those of columns 2t, 2t + 1
-                q0[n][c][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t);
-                q0[n][c][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                q0[n][c][0] = -0x1p-21f * __shfl_sync(0xffffffffu, sum, 8 * t);
+                q0[n][c][1] = -0x1p-21f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
             }
+            c_row[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+            c_row[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
         }
         // positions of the rows of this lane's columns
         int last[NT][2];
@@ -297,9 +348,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) last[n][e] = R.len - a.N_q + (row0 + 8 * n + 2 * t + e) % a.N_q;
+        // a tile from token `tok` on is seen whole by every row if it ends by the first row's
+        // position, and starts inside the last row's window or ends among the sinks
+        const int whole_to = R.len - a.N_q - (kTileTokens - 1);
+        const int whole_from = a.window > 0 ? R.len - a.window : 0;
 
         float o[NT][G][2][4];   // O^T: rows 32 c + 4 g + {0, 1 | 2, 3}, columns 2t, 2t + 1
-        float m[NT][2], l[NT][2];
+        float m[NT][2], ref[NT][2], l[NT][2];  // reference maximum; the same or 0 for -inf; sum
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -309,32 +364,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m[n][e] = -INFINITY;
-                l[n][e] = 0.f;
+                ref[n][e] = l[n][e] = 0.f;
             }
         }
 
         for (int i = 0; i < n_mine; ++i) {
-            // the stage of tile i - 1, which every lane has read, takes tile i + kStages - 1
-            {
-                const int i2 = i + kStages - 1;
-                const uint32_t bit = 1u << (i2 & 31);
-                have = next_page >= 0 ? have | bit : have & ~bit;
-                issue(i2, next_page);
-                next_page = page_at(i2 + 1);
+            // the ring position that step i - 1 has left, which every lane has read, takes step
+            // i + kStages - 1
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                copy(ring0 + (fill * kTiles + j) * T::kBytes, next_tok[j], next_page[j]);
+                toks[kStages - 1][j] = next_tok[j];
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) place(i + kStages, j, next_tok[j], next_page[j]);
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
-            const bool there = have >> (i & 31) & 1u;
-            const uint8_t* st = ring + (i % kStages) * T::kBytes;
-            const int tok = token_of(i);
-            // S^T of 16 tokens
-            float x[NT][4];
-            {
+            const uint8_t* st = ring + stage * (kTiles * T::kBytes);
+            // S^T of the tiles' tokens, in log2 units; hidden tokens by selection, whatever their
+            // bytes hold
+            float x[kTiles][NT][4];
+            bool edge[kTiles];
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                const uint8_t* sj = st + j * T::kBytes;
+                const int tok = toks[0][j];
                 uint32_t kw[2][G], ks[2][G / 2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    load_words(st + (g + 8 * r) * (D / 2) + t * (D / 8), kw[r]);
-                    load_words(st + T::kOffKs + (g + 8 * r) * (D / 16), ks[r]);
+                    load_words(sj + (g + 8 * r) * (D / 2) + t * (D / 8), kw[r]);
+                    load_words(sj + T::kOffKs + (g + 8 * r) * (D / 16), ks[r]);
                 }
 #pragma unroll
                 for (int c = 0; c < G; ++c) {
@@ -342,53 +402,59 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) f[h][r] = expand(kw[r & 1][c], 2 * h + r / 2);
+                        for (int r = 0; r < 4; ++r) f[h][r] = tiny(h ? kw[r & 1][c] >> 8 : kw[r & 1][c], r / 2);
                     const float s0 = (c & 1) ? bf_hi(ks[0][c / 2]) : bf_lo(ks[0][c / 2]);
                     const float s1 = (c & 1) ? bf_hi(ks[1][c / 2]) : bf_lo(ks[1][c / 2]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const float init[4] = {q0[n][c][0], q0[n][c][1], q0[n][c][0], q0[n][c][1]};
                         float acc[4];
-                        mma_bf16(acc, f[0], qf[n][2 * c][0], qf[n][2 * c][1], init);
-                        mma_bf16(acc, f[1], qf[n][2 * c + 1][0], qf[n][2 * c + 1][1], acc);
+                        mma_f16(acc, f[0], qf[n][2 * c][0], qf[n][2 * c][1], init);
+                        mma_f16(acc, f[1], qf[n][2 * c + 1][0], qf[n][2 * c + 1][1], acc);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            x[n][e] = c == 0 ? acc[e] * (e < 2 ? s0 : s1) : fmaf(acc[e], e < 2 ? s0 : s1, x[n][e]);
+                            x[j][n][e] = c == 0 ? acc[e] * (e < 2 ? s0 : s1) : fmaf(acc[e], e < 2 ? s0 : s1, x[j][n][e]);
                     }
+                }
+                edge[j] = tok > whole_to || (tok < whole_from && tok + kTileTokens > a.sinks);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[j][n][e] *= c_row[n][e & 1];
+                if (edge[j]) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = tok + g + (e < 2 ? 0 : 8), i_pos = last[n][e & 1];
+                            const bool seen = key <= i_pos && (a.window == 0 || key > i_pos - a.window || key < a.sinks);
+                            if (!seen) x[j][n][e] = -INFINITY;
+                        }
                 }
             }
-            // scores in log2 units; hidden tokens by selection, whatever their bytes hold
-            const bool edge = !there || tok + kTileTokens - 1 > R.len - a.N_q ||
-                              (a.window > 0 && tok <= R.len - 1 - a.window && tok + kTileTokens > a.sinks);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[n][e] *= a.c_log2;
-                    if (edge) {
-                        const int j = tok + g + (e < 2 ? 0 : 8), i_pos = last[n][e & 1];
-                        const bool seen = there && j <= i_pos &&
-                                          (a.window == 0 || static_cast<long long>(j) + a.window > i_pos || j < a.sinks);
-                        if (!seen) x[n][e] = -INFINITY;
-                    }
-                }
             // the rows' reference maxima, moved only when a score passes one by more than kTau
+            float top[NT][2];
             bool over = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) over |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + kTau;
+                for (int e = 0; e < 2; ++e) {
+                    top[n][e] = fmaxf(x[0][n][e], x[0][n][e + 2]);
+#pragma unroll
+                    for (int j = 1; j < kTiles; ++j) top[n][e] = fmaxf(top[n][e], fmaxf(x[j][n][e], x[j][n][e + 2]));
+                    over |= top[n][e] > m[n][e] + kTau;
+                }
             if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(x[n][e], x[n][e + 2]);
+                        float v = top[n][e];
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                        if (top > m[n][e]) {
-                            const float alpha = ex2_approx(m[n][e] - top);  // 0 from -inf
-                            m[n][e] = top;
+                        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                        if (v > m[n][e]) {
+                            const float alpha = ex2_approx(m[n][e] - v);  // 0 from -inf
+                            m[n][e] = ref[n][e] = v;
                             l[n][e] *= alpha;
 #pragma unroll
                             for (int c = 0; c < G; ++c)
@@ -400,25 +466,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
                         }
                     }
             }
-            // P, rows of tokens g and g + 8
-            float p[NT][4];
+            // P, rows of tokens g and g + 8, and O^T += V^T (P s)^T
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+            for (int j = 0; j < kTiles; ++j) {
+                const uint8_t* sj = st + j * T::kBytes;
+                float p[NT][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[n][e] = ex2_approx(x[n][e] - (e & 1 ? r1 : r0));
-                    l[n][e & 1] += p[n][e];
-                }
-            }
-            // O^T += V^T (P s)^T
-            {
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[n][e] = ex2_approx(x[j][n][e] - ref[n][e & 1]);
+                        l[n][e & 1] += p[n][e];
+                    }
                 uint32_t vw[2][G];  // codes: the first token's G / 2 words, then the second's
                 uint32_t vs[2][G];  // scales of token pairs g / 2, 4 + g / 2
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    load_words(st + T::kOffV + (r * 32 + lane) * (D / 8), vw[r]);
-                    load_words(st + T::kOffVs + (r * 4 + g / 2) * (D / 8), vs[r]);
+                    load_words(sj + T::kOffV + (r * 32 + lane) * (D / 8), vw[r]);
+                    load_words(sj + T::kOffVs + (r * 4 + g / 2) * (D / 8), vs[r]);
                 }
 #pragma unroll
                 for (int c = 0; c < G; ++c) {
@@ -438,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
                         for (int r = 0; r < 2; ++r) {
                             const float s = __uint_as_float(__byte_perm(vs[r][c], 0u, half_sel));
                             float y0 = p[n][2 * r] * s, y1 = p[n][2 * r + 1] * s;
-                            if (edge) {  // a hidden token's scale may be anything
-                                if (x[n][2 * r] == -INFINITY) y0 = 0.f;
-                                if (x[n][2 * r + 1] == -INFINITY) y1 = 0.f;
+                            if (edge[j]) {  // a hidden token's scale may be anything
+                                if (x[j][n][2 * r] == -INFINITY) y0 = 0.f;
+                                if (x[j][n][2 * r + 1] == -INFINITY) y1 = 0.f;
                             }
                             ps[r] = transpose8x8(pack_bf16x2(y0, y1));
                         }
@@ -449,9 +514,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
                     }
                 }
             }
-            __syncwarp();  // every lane has read the stage
+            __syncwarp();  // every lane has read the step
+            fill = stage;
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+#pragma unroll
+            for (int s = 0; s < kStages - 1; ++s)
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) toks[s][j] = toks[s + 1][j];
         }
 
+        __syncthreads();  // the results take the rings' place
         // the warps' states side by side, then one sum per value
         constexpr int kRowFloats = D + 2;
         float* mine_r = results + warp * ROWS * kRowFloats;
@@ -615,7 +687,9 @@ __global__ void __launch_bounds__(256)
 
 template <int D, int NT>
 cudaError_t launch_impl(const DecodeArgs& a, cudaStream_t s) {
-    constexpr int kSmem = kWarps * (kStages * TileCfg<D>::kBytes + 8 * NT * (D + 2) * static_cast<int>(sizeof(float)));
+    constexpr int kRings = kWarps * kStages * kTiles * TileCfg<D>::kBytes;
+    constexpr int kResults = kWarps * 8 * NT * (D + 2) * static_cast<int>(sizeof(float));
+    constexpr int kSmem = kRings > kResults ? kRings : kResults;
     // CTAs that are resident together, per device; asked once
     static std::atomic<int> resident[64];
     int dev = 0;
@@ -636,7 +710,7 @@ cudaError_t launch_impl(const DecodeArgs& a, cudaStream_t s) {
     const int rows = a.H / a.cache.H_kv * a.N_q;
     const int row_tiles = (rows + 8 * NT - 1) / (8 * NT);
     // no more CTAs than units that the tables could hold
-    const long long most_units = (((static_cast<long long>(a.cache.max_blocks) << a.cache.page_log2) + 63) / 64) *
+    const long long most_units = ((static_cast<long long>(a.cache.max_blocks) << a.cache.page_log2) / (16 * kUnitTiles) + 1) *
                                  a.B * a.cache.H_kv * row_tiles;
     const long long grid = ctas < most_units ? ctas : most_units;
     Work w;

@@ -58,7 +58,7 @@ int norm_rope_args(NormRopeArgs* a, const void* qkv, const float* qw, const floa
     a->heads[1] = a->heads[2] = H_kv;
     a->N = N;
     a->rot = rot;
-    a->tokens = static_cast<long long>(B) * N;
+    a->tokens = static_cast<uint32_t>(B) * N;
     a->eps = eps;
     return FA_OK;
 }
@@ -187,7 +187,7 @@ FA_API int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_sc
     Kv4Cache c;
     const int rc = cache_args(&c, k_codes, k_scales, v_codes, v_scales, block_table, B, H_kv, d, page, n_pages, max_blocks);
     if (rc != FA_OK) return rc;
-    if (!sizes_supported(B, H_kv, N)) return FA_ERR_UNSUPPORTED;
+    if (!sizes_supported(B, H_kv, N) || static_cast<int64_t>(B) * H_kv * N > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
     DevCtl ctl;
     int err = FA_OK;
     if (!device_ctl(&ctl, &err)) return err;
@@ -201,7 +201,7 @@ FA_API int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_
     Kv4Cache c;
     const int rc = cache_args(&c, k_codes, k_scales, v_codes, v_scales, block_table, B, H_kv, d, page, n_pages, max_blocks);
     if (rc != FA_OK) return rc;
-    if (!sizes_supported(B, H_kv, N)) return FA_ERR_UNSUPPORTED;
+    if (!sizes_supported(B, H_kv, N) || static_cast<int64_t>(B) * H_kv * N > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
     DevCtl ctl;
     int err = FA_OK;
     if (!device_ctl(&ctl, &err)) return err;

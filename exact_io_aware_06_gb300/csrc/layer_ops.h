@@ -2,12 +2,42 @@
 // rotation of Q and K, windowed attention with sinks, and the 4-bit K/V cache.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace fa {
 
 // The current device's status word and wait limit; false with *err set on failure.
 bool device_ctl(DevCtl* ctl, int* err);
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; asked once per
+// kernel and device (`done`: one bit per device, of the kernel's own).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit & done.load()) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
+// n / d for n < 2^31 by a multiplication: with l = ceil(log2 d) and mul = 2^32 (2^l - d) / d + 1,
+// (n + (n mul >> 32)) >> l, whose sum stays below 2^32.
+struct Div {
+    uint32_t d, mul, shift;
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
+inline Div make_div(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return {d, static_cast<uint32_t>((((1ull << l) - d) << 32) / d + 1), l};
+}
 
 // Angle of position t in rotation pair p, in turns: frac(t * f[p] / 2^64).
 struct RopeFreq {
@@ -24,7 +54,7 @@ struct NormRopeArgs {
     float* part;            // backward: [grid][2][d] partial weight gradients
     int heads[3];           // H, H_kv, H_kv
     int N, rot;
-    long long tokens;       // B * N
+    uint32_t tokens;        // B * N, below 2^31
     float eps;
     RopeFreq freq;
 };

@@ -20,7 +20,7 @@
 // (t = 10^6: errors of 0.06 rad); a table would be read again by every token.  f_p / (2 pi)
 // is held as a 64-bit fraction instead, and t times it modulo 2^64 is an integer product
 // that drops whole turns exactly: the error is t 2^-65 turns, plus one float rounding.
-#include <cuda_bf16.h>
+#include <atomic>
 
 #include "layer_ops.h"
 #include "ptx.cuh"
@@ -103,7 +103,7 @@ __device__ __forceinline__ void rotate(float (&x)[8], const float (&c)[8], const
     for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], c[e], o[e] * s[e]);
 }
 
-// What a warp has of its token: the factors of its lane's eight elements.
+// The factors of this lane's eight elements at position t; `tab` is the warp's own.
 template <int D, bool INTER>
 __device__ __forceinline__ void token_angles(const NormRopeArgs& a, int t, float2* tab, int lane, float (&c)[8],
                                              float (&s)[8], int& mate) {
@@ -121,94 +121,134 @@ __device__ __forceinline__ void token_angles(const NormRopeArgs& a, int t, float
     __syncwarp();
     mate = lane;
     if (!INTER && e0 < a.rot) mate = e0 < half ? lane + half / 8 : lane - half / 8;
+    const bool turned = e0 < a.rot;  // rot is a multiple of 16: all eight elements, or none
+    const bool first = e0 < half;
+    const float2* f = tab + (INTER ? e0 / 2 : first ? e0 : e0 - half);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
-        if (e0 + e < a.rot) {
-            const bool first = INTER ? (e & 1) == 0 : e0 < half;
-            const float2 f = tab[INTER ? (e0 + e) / 2 : (e0 + e) % half];
-            c[e] = f.x;
-            s[e] = first ? -f.y : f.y;
-        }
+        const float2 v = turned ? f[INTER ? e / 2 : e] : make_float2(1.f, 0.f);
+        c[e] = v.x;
+        s[e] = (INTER ? (e & 1) == 0 : first) ? -v.y : v.y;
     }
 }
 
-// A warp's work: passes [p0, p1) of token tk, a pass being 32 / (D / 8) neighbouring heads
-// of Q, K or V.  Items count chunks of `per` passes, all tokens of a chunk together.
+// A warp's work: passes [p0, p1) of a token, a pass being 32 / (D / 8) neighbouring heads of
+// Q, K or V.  Items count chunks of `per` passes, all tokens of a chunk together.
 struct Split {
     int first[4];     // first pass of Q, K, V, and the end
     int per;          // passes per item
     int chunks;       // items per token
+    Div by_tokens, by_n;
 };
 
+// A warp's place in its work: some passes of a token, from `pa` on.
+struct Place {
+    uint32_t it, tk, b;
+    int n, pa, p1, pos;
+    bool fresh;  // the first passes of the token
+};
+__device__ __forceinline__ Place place_at(const NormRopeArgs& a, const Split& sp, uint32_t it, uint32_t items) {
+    Place p;
+    p.it = it;
+    p.fresh = true;
+    if (it < items) {
+        const uint32_t chunk = sp.by_tokens.of(it);
+        p.tk = it - chunk * a.tokens;
+        p.pa = static_cast<int>(chunk) * sp.per;
+        p.p1 = min(p.pa + sp.per, sp.first[3]);
+        p.b = sp.by_n.of(p.tk);
+        p.n = static_cast<int>(p.tk - p.b * sp.by_n.d);
+        p.pos = a.pos ? __ldg(a.pos + p.tk) : p.n;
+    }
+    return p;
+}
+// Pass p: 0, 1 or 2 for Q, K or V, and this lane's head there.
+struct Pass {
+    int seg, h, heads, before;
+};
+template <int HEADS>
+__device__ __forceinline__ Pass pass_at(const NormRopeArgs& a, const Split& sp, int p, int grp) {
+    Pass x;
+    x.seg = (p >= sp.first[1]) + (p >= sp.first[2]);
+    const int first = x.seg == 0 ? 0 : x.seg == 1 ? sp.first[1] : sp.first[2];
+    x.h = (p - first) * HEADS + grp;
+    x.heads = x.seg == 0 ? a.heads[0] : a.heads[1];
+    x.before = x.seg == 0 ? 0 : x.seg == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
+    return x;
+}
+
+// The loads of the next passes (of this token or the warp's next one) are in flight while
+// these are worked on: a warp that waited for each batch reached 52% of the copy rate.
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(kThreads)
-    qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const Split sp) {
+__global__ void __launch_bounds__(kThreads, 2)
+    qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Split sp) {
     constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
-    constexpr int kAhead = F32 ? 2 : 4;  // passes whose loads are in flight together
+    constexpr int kAhead = F32 ? 2 : 4;  // passes of a batch
     __shared__ float2 tab[kWarps][D / 2];
+    __shared__ __align__(16) float w[2][D];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int grp = lane / kLanes, e0 = 8 * (lane % kLanes);
-    const int all_heads = a.heads[0] + a.heads[1] + a.heads[2];
-    float w[2][8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
+    const int all_heads = a.heads[0] + 2 * a.heads[1];
     griddep_wait();
     griddep_launch_dependents();
+    const uint32_t items = a.tokens * sp.chunks, step = gridDim.x * kWarps;
+    auto load = [&](const Place& at, Raw<F32>(&raw)[kAhead]) {
+        const size_t in0 = static_cast<size_t>(at.tk) * all_heads * D + e0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (a.weight[i] != nullptr)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[i][e] = a.weight[i][e0 + e];
-
-    const long long items = a.tokens * sp.chunks;
-    const long long step = static_cast<long long>(gridDim.x) * kWarps;
-    for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items; it += step) {
-        const long long tk = it % a.tokens;
-        const int p0 = static_cast<int>(it / a.tokens) * sp.per;
-        const int p1 = min(p0 + sp.per, sp.first[3]);
-        const long long b = tk / a.N;
-        const int n = static_cast<int>(tk % a.N);
-        float c[8], s[8];
-        int mate = lane;
-        if (p0 < sp.first[2]) token_angles<D, INTER>(a, a.pos ? a.pos[tk] : n, tab[warp], lane, c, s, mate);
-        const size_t in0 = static_cast<size_t>(tk) * all_heads * D + e0;
-        for (int pa = p0; pa < p1; pa += kAhead) {
-            Raw<F32> raw[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int p = pa + u;
-                const int seg = (p >= sp.first[1]) + (p >= sp.first[2]);
-                const int h = (p - sp.first[seg]) * kHeads + grp;
-                const int before = seg == 0 ? 0 : seg == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
-                raw[u] = load8<F32>(a.qkv, in0 + static_cast<size_t>(before + h) * D, p < p1 && h < a.heads[seg]);
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int p = pa + u;
-                if (p >= p1) break;
-                const int seg = (p >= sp.first[1]) + (p >= sp.first[2]);
-                const int h = (p - sp.first[seg]) * kHeads + grp;
-                const int nh = a.heads[seg];
-                if (seg < 2) {
-                    float x[8];
-                    unpack<F32>(raw[u], x);
-                    float sq = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-                    const float r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + a.eps);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= r * (seg ? w[1][e] : w[0][e]);
-                    if (a.rot) rotate<INTER>(x, c, s, mate);
-                    raw[u] = pack<F32>(x);
-                }
-                if (h < nh)
-                    store8<F32>(a.out[seg], ((static_cast<size_t>(b) * nh + h) * a.N + n) * D + e0, raw[u]);
-            }
+        for (int u = 0; u < kAhead; ++u) {
+            const Pass x = pass_at<kHeads>(a, sp, at.pa + u, grp);
+            raw[u] = load8<F32>(a.qkv, in0 + static_cast<size_t>(x.before + x.h) * D, at.pa + u < at.p1 && x.h < x.heads);
         }
+    };
+    Place at = place_at(a, sp, blockIdx.x * kWarps + warp, items);
+    Raw<F32> raw[kAhead];
+    if (at.it < items) load(at, raw);
+    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+        const float* src = x < D ? a.weight[0] : a.weight[1];
+        w[x / D][x % D] = src ? src[x % D] : 1.f;
+    }
+    __syncthreads();
+
+    float c[8], s[8];
+    int mate = lane;
+    while (at.it < items) {
+        Place next = at;
+        next.pa += kAhead;
+        next.fresh = false;
+        if (next.pa >= at.p1) next = place_at(a, sp, at.it + step, items);
+        Raw<F32> ahead[kAhead];
+        if (next.it < items) load(next, ahead);
+        if (at.fresh && at.pa < sp.first[2]) token_angles<D, INTER>(a, at.pos, tab[warp], lane, c, s, mate);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (at.pa + u >= at.p1) break;
+            const Pass ps = pass_at<kHeads>(a, sp, at.pa + u, grp);
+            if (ps.seg < 2) {
+                float x[8];
+                unpack<F32>(raw[u], x);
+                float sq = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+                const float r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + a.eps);
+                const float4* w4 = reinterpret_cast<const float4*>(&w[ps.seg][e0]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 v = w4[i];
+                    x[4 * i] *= r * v.x;
+                    x[4 * i + 1] *= r * v.y;
+                    x[4 * i + 2] *= r * v.z;
+                    x[4 * i + 3] *= r * v.w;
+                }
+                if (a.rot) rotate<INTER>(x, c, s, mate);
+                raw[u] = pack<F32>(x);
+            }
+            if (ps.h < ps.heads)
+                store8<F32>(ps.seg == 0 ? a.out[0] : ps.seg == 1 ? a.out[1] : a.out[2],
+                            ((static_cast<size_t>(at.b) * ps.heads + ps.h) * a.N + at.n) * D + e0, raw[u]);
+        }
+        at = next;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
     }
 }
 
@@ -216,95 +256,102 @@ __global__ void __launch_bounds__(kThreads)
 // block's warps are then added in order and written as one partial row per block, and
 // dweight_sum_kernel adds the blocks in order: no atomics, the same bits every time.
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(kThreads)
-    qk_norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, const Split sp) {
+__global__ void __launch_bounds__(kThreads, 2)
+    qk_norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Split sp) {
     constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
-    constexpr int kAhead = 2;
+    constexpr int kAhead = F32 ? 1 : 2;
     __shared__ float2 tab[kWarps][D / 2];
+    __shared__ __align__(16) float w[2][D];
     __shared__ float sums[kWarps][2][D];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int grp = lane / kLanes, e0 = 8 * (lane % kLanes);
-    const int all_heads = a.heads[0] + a.heads[1] + a.heads[2];
-    float w[2][8], dw[2][8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[i][e] = 1.f;
-            dw[i][e] = 0.f;
-        }
+    const int all_heads = a.heads[0] + 2 * a.heads[1];
     griddep_wait();
     griddep_launch_dependents();
+    const uint32_t items = a.tokens * sp.chunks, step = gridDim.x * kWarps;
+    auto load = [&](const Place& at, Raw<F32>(&rx)[kAhead], Raw<F32>(&rg)[kAhead]) {
+        const size_t in0 = static_cast<size_t>(at.tk) * all_heads * D + e0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (a.weight[i] != nullptr)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[i][e] = a.weight[i][e0 + e];
+        for (int u = 0; u < kAhead; ++u) {
+            const Pass x = pass_at<kHeads>(a, sp, at.pa + u, grp);
+            const bool valid = at.pa + u < at.p1 && x.h < x.heads;
+            rx[u] = load8<F32>(a.qkv, in0 + static_cast<size_t>(x.before + x.h) * D, valid && x.seg < 2);
+            rg[u] = load8<F32>(x.seg == 0 ? a.grad[0] : x.seg == 1 ? a.grad[1] : a.grad[2],
+                               ((static_cast<size_t>(at.b) * x.heads + x.h) * a.N + at.n) * D + e0, valid);
+        }
+    };
+    Place at = place_at(a, sp, blockIdx.x * kWarps + warp, items);
+    Raw<F32> rx[kAhead], rg[kAhead];
+    if (at.it < items) load(at, rx, rg);
+    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+        const float* src = x < D ? a.weight[0] : a.weight[1];
+        w[x / D][x % D] = src ? src[x % D] : 1.f;
+    }
+    __syncthreads();
 
-    const long long items = a.tokens * sp.chunks;
-    const long long step = static_cast<long long>(gridDim.x) * kWarps;
-    for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items; it += step) {
-        const long long tk = it % a.tokens;
-        const int p0 = static_cast<int>(it / a.tokens) * sp.per;
-        const int p1 = min(p0 + sp.per, sp.first[3]);
-        const long long b = tk / a.N;
-        const int n = static_cast<int>(tk % a.N);
-        float c[8], s[8];
-        int mate = lane;
-        if (p0 < sp.first[2]) {
+    float c[8], s[8], dw[2][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
+    int mate = lane;
+    while (at.it < items) {
+        Place next = at;
+        next.pa += kAhead;
+        next.fresh = false;
+        if (next.pa >= at.p1) next = place_at(a, sp, at.it + step, items);
+        Raw<F32> nx[kAhead], ng[kAhead];
+        if (next.it < items) load(next, nx, ng);
+        if (at.fresh && at.pa < sp.first[2]) {
             // turned back: the opposite angle
-            token_angles<D, INTER>(a, a.pos ? a.pos[tk] : n, tab[warp], lane, c, s, mate);
+            token_angles<D, INTER>(a, at.pos, tab[warp], lane, c, s, mate);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = -s[e];
         }
-        const size_t in0 = static_cast<size_t>(tk) * all_heads * D + e0;
-        for (int pa = p0; pa < p1; pa += kAhead) {
-            Raw<F32> rx[kAhead], rg[kAhead];
+        const size_t in0 = static_cast<size_t>(at.tk) * all_heads * D + e0;
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int p = pa + u;
-                const int seg = (p >= sp.first[1]) + (p >= sp.first[2]);
-                const int h = (p - sp.first[seg]) * kHeads + grp;
-                const int nh = a.heads[seg];
-                const bool valid = p < p1 && h < nh;
-                const int before = seg == 0 ? 0 : a.heads[0];
-                rx[u] = load8<F32>(a.qkv, in0 + static_cast<size_t>(before + h) * D, valid && seg < 2);
-                rg[u] = load8<F32>(a.grad[seg], ((static_cast<size_t>(b) * nh + h) * a.N + n) * D + e0, valid);
-            }
+        for (int u = 0; u < kAhead; ++u) {
+            if (at.pa + u >= at.p1) break;
+            const Pass ps = pass_at<kHeads>(a, sp, at.pa + u, grp);
+            if (ps.seg < 2) {
+                float x[8], g[8], wg[8];
+                unpack<F32>(rx[u], x);
+                unpack<F32>(rg[u], g);
+                if (a.rot) rotate<INTER>(g, c, s, mate);
+                const float4* w4 = reinterpret_cast<const float4*>(&w[ps.seg][e0]);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int p = pa + u;
-                if (p >= p1) break;
-                const int seg = (p >= sp.first[1]) + (p >= sp.first[2]);
-                const int h = (p - sp.first[seg]) * kHeads + grp;
-                const int before = seg == 0 ? 0 : seg == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
-                if (seg < 2) {
-                    float x[8], g[8];
-                    unpack<F32>(rx[u], x);
-                    unpack<F32>(rg[u], g);
-                    if (a.rot) rotate<INTER>(g, c, s, mate);
-                    float sq = 0.f, dot = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        sq = fmaf(x[e], x[e], sq);
-                        dot = fmaf(g[e] * (seg ? w[1][e] : w[0][e]), x[e], dot);
-                    }
-                    const float r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + a.eps);
-                    const float m = row_sum<kLanes>(dot) * (1.f / D) * r * r;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // rows of heads past the end are zeros: they add nothing
-                        const float t = g[e] * (r * x[e]);
-                        if (seg)
-                            dw[1][e] += t;
-                        else
-                            dw[0][e] += t;
-                        x[e] = r * fmaf(-m, x[e], g[e] * (seg ? w[1][e] : w[0][e]));
-                    }
-                    rg[u] = pack<F32>(x);
+                for (int i = 0; i < 2; ++i) {
+                    const float4 v = w4[i];
+                    wg[4 * i] = v.x * g[4 * i];
+                    wg[4 * i + 1] = v.y * g[4 * i + 1];
+                    wg[4 * i + 2] = v.z * g[4 * i + 2];
+                    wg[4 * i + 3] = v.w * g[4 * i + 3];
                 }
-                if (h < a.heads[seg]) store8<F32>(a.dqkv, in0 + static_cast<size_t>(before + h) * D, rg[u]);
+                float sq = 0.f, dot = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sq = fmaf(x[e], x[e], sq);
+                    dot = fmaf(wg[e], x[e], dot);
+                }
+                const float r = rsqrtf(row_sum<kLanes>(sq) * (1.f / D) + a.eps);
+                const float m = row_sum<kLanes>(dot) * (1.f / D) * r * r;
+                // rows of heads past the end are zeros: they add nothing
+                if (ps.seg == 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dw[0][e] = fmaf(g[e], r * x[e], dw[0][e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dw[1][e] = fmaf(g[e], r * x[e], dw[1][e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = r * fmaf(-m, x[e], wg[e]);
+                rg[u] = pack<F32>(x);
             }
+            if (ps.h < ps.heads) store8<F32>(a.dqkv, in0 + static_cast<size_t>(ps.before + ps.h) * D, rg[u]);
+        }
+        at = next;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            rx[u] = nx[u];
+            rg[u] = ng[u];
         }
     }
     if (a.part == nullptr) return;
@@ -348,13 +395,6 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-int sm_count() {
-    int sms = 152, dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 // Passes of Q, K and V, and how many a warp takes: all of a token's where there are tokens
 // enough to fill the GPU (the angles are then computed once per token), fewer where there
 // are not (one token of 40 heads: a warp per pass).
@@ -363,40 +403,60 @@ Split split_passes(const NormRopeArgs& a, int d, int sms) {
     Split sp;
     sp.first[0] = 0;
     for (int i = 0; i < 3; ++i) sp.first[i + 1] = sp.first[i] + (a.heads[i] + per_pass - 1) / per_pass;
-    const long long passes = a.tokens * sp.first[3];
+    const long long passes = static_cast<long long>(a.tokens) * sp.first[3];
     const long long target = static_cast<long long>(sms) * 32;
     const long long per = (passes + target - 1) / target;
     sp.per = static_cast<int>(per < sp.first[3] ? per : sp.first[3]);
     sp.chunks = (sp.first[3] + sp.per - 1) / sp.per;
+    sp.by_tokens = make_div(a.tokens);
+    sp.by_n = make_div(a.N);
     return sp;
+}
+
+// CTAs of a kernel that are resident together on the current device, asked once per device.
+template <typename K>
+cudaError_t resident_ctas(K kernel, std::atomic<int> (&known)[64], int* sms, int* ctas) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    *ctas = dev < 64 ? known[dev].load() : 0;
+    if (*ctas == 0) {
+        int per_sm = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        *ctas = *sms * (per_sm < 1 ? 1 : per_sm);
+        if (dev < 64) known[dev].store(*ctas);
+    }
+    return cudaSuccess;
 }
 
 template <int D, bool F32, bool INTER>
 cudaError_t launch_fwd(const NormRopeArgs& a, cudaStream_t s) {
-    const int sms = sm_count();
+    static std::atomic<int> known[64];
+    int sms = 0, cap = 0;
+    const cudaError_t e = resident_ctas(qk_norm_rope_kernel<D, F32, INTER>, known, &sms, &cap);
+    if (e != cudaSuccess) return e;
     const Split sp = split_passes(a, D, sms);
-    const long long blocks = (a.tokens * sp.chunks + kWarps - 1) / kWarps;
-    const long long cap = static_cast<long long>(sms) * 32;
+    const long long blocks = (static_cast<long long>(a.tokens) * sp.chunks + kWarps - 1) / kWarps;
     return launch_pdl(qk_norm_rope_kernel<D, F32, INTER>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
                       dim3(kThreads), 0, s, a, sp);
 }
 
 template <int D, bool F32, bool INTER>
 cudaError_t launch_bwd(NormRopeArgs a, float* const (&dweight)[2], cudaStream_t s) {
-    const int sms = sm_count();
+    static std::atomic<int> known[64];
+    int sms = 0, cap = 0;
+    const cudaError_t e = resident_ctas(qk_norm_rope_bwd_kernel<D, F32, INTER>, known, &sms, &cap);
+    if (e != cudaSuccess) return e;
     const Split sp = split_passes(a, D, sms);
     const bool want = dweight[0] != nullptr || dweight[1] != nullptr;
     if (!want) a.part = nullptr;
-    int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per_sm, qk_norm_rope_bwd_kernel<D, F32, INTER>, kThreads, 0);
-    if (e != cudaSuccess) return e;
-    const long long blocks = (a.tokens * sp.chunks + kWarps - 1) / kWarps;
-    long long cap = static_cast<long long>(sms) * (per_sm < 1 ? 1 : per_sm);
+    const long long blocks = (static_cast<long long>(a.tokens) * sp.chunks + kWarps - 1) / kWarps;
     if (cap > kBwdMaxBlocks) cap = kBwdMaxBlocks;
     const int grid = static_cast<int>(blocks < cap ? blocks : cap);
-    e = launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER>, dim3(grid), dim3(kThreads), 0, s, a, sp);
-    if (e != cudaSuccess || !want) return e;
+    const cudaError_t e2 = launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER>, dim3(grid), dim3(kThreads), 0, s, a, sp);
+    if (e2 != cudaSuccess || !want) return e2;
     return launch_pdl(dweight_sum_kernel<D>, dim3(2 * D / 8), dim3(256), 0, s, a.part, grid, dweight[0],
                       dweight[1]);
 }

@@ -330,8 +330,8 @@ int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void
     if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, 128, N, BH_kv, 64, kBlk);
     if (rc == 0) rc = make_map_3d(&tdo, dO, dt, 2, 128, N, BH, 64, kBlk);
     if (rc != 0) return rc;
-    cudaError_t e = cudaFuncSetAttribute(win_bwd_dq_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmemAlloc);
+    static std::atomic<uint64_t> smem_done;
+    const cudaError_t e = allow_smem(win_bwd_dq_kernel<128>, C::kSmemAlloc, smem_done);
     if (e != cudaSuccess) return static_cast<int>(e);
     DqArgs a;
     a.ws_nlse2 = ws_nlse2;

@@ -1017,7 +1017,8 @@ int launch_bwd_impl(const void* q, const void* k, const void* v, const void* o, 
     if (rc == 0 && C::kFusedDQ) rc = make_map_3d(&tdk, dk, dt, 2, D, N, BH_kv, 64, kBlk);
     if (rc == 0 && C::kFusedDQ) rc = make_map_3d(&tdv, dv, dt, 2, D, N, BH_kv, 64, kBlk);
     if (rc != 0) return rc;
-    e = cudaFuncSetAttribute(win_bwd_main_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
+    static std::atomic<uint64_t> smem_done;
+    e = allow_smem(win_bwd_main_kernel<D>, C::kSmemAlloc, smem_done);
     if (e != cudaSuccess) return static_cast<int>(e);
     BwdArgs a;
     a.ws_delta = ws_delta;

@@ -560,8 +560,8 @@ int launch_impl(const void* q, const void* k, const void* v, void* o, float* lse
     int dev = 0, sms = 152;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(win_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
+    static std::atomic<uint64_t> smem_done;
+    if (e == cudaSuccess) e = allow_smem(win_fwd_kernel<D>, C::kSmemAlloc, smem_done);
     if (e != cudaSuccess) return static_cast<int>(e);
     WinArgs a;
     a.o = o;

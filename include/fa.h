@@ -399,8 +399,8 @@ size_t fa_bwd_window_workspace_size(int B, int H, int H_kv, int N, int d, int wi
  *   k, v  : [B][H_kv][N][d] bfloat16, read only.
  *   first : [B] int32, device: tokens that the requests had before.   count : [B] int32 or NULL.
  * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, sizes < 1, bad page),
- * FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, max_blocks * page beyond
- * 2^31 - 1), FA_ERR_CUDA.
+ * FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, max_blocks * page or B*H_kv*N
+ * beyond 2^31 - 1), FA_ERR_CUDA.
  */
 int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes,
                   void* v_scales, const int* block_table, const int* first, const int* count, int B,
@@ -423,7 +423,9 @@ int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes,
  * h / (H / H_kv).  A query at a negative position (a request shorter than N_q, or empty) sees
  * nothing: O = 0, lse = -inf.
  *
- *   q, o  : [B][H][N_q][d] bfloat16.   lse : [B][H][N_q] float32, or NULL.
+ *   q, o  : [B][H][N_q][d] bfloat16.   lse : [B][H][N_q] float32, or NULL.  The scores take
+ *           q to 2^-28 of its row's largest magnitude, which has to lie between 2^-85 and
+ *           2^115 (or be 0).
  *   lengths : [B] int32, device.
  *   workspace : at least fa_decode_kv4_workspace_size() bytes; its contents on entry do not
  *           matter.  Calls that overlap in time must not share one.
