@@ -12,7 +12,8 @@ from . import FA_BF16, FA_F32, _check, lib
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _current_device = torch.cuda.current_device
-_current_stream = torch.cuda.current_stream
+# the current stream's handle without the Stream object around it (2.9 us of a 13 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _dense(what, t, dtype, shape, device):
@@ -29,9 +30,9 @@ def _sizes(what, t):
     return t.shape
 
 
-def _handle(stream):
+def _handle(stream, device):
     if stream is None:
-        return _current_stream().cuda_stream
+        return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -75,9 +76,9 @@ def fa_qk_norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, eps, 
     """q [B, H, N, d], k, v [B, H_kv, N, d] <- norm and rotation of qkv [B, N, H + 2 H_kv, d].
     q_weight, k_weight (float32 [d]), positions (int32 [B, N]) and inv_freq (float64 host tensor
     of rot / 2) may be None: ones, the index in the sequence, no rotation."""
-    pointers, sizes, code = _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v,
-                                       _current_device())
-    _check(lib().fa_qk_norm_rope(*pointers, *sizes, bool(interleaved), eps, code, _handle(stream)),
+    device = _current_device()
+    pointers, sizes, code = _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, device)
+    _check(lib().fa_qk_norm_rope(*pointers, *sizes, bool(interleaved), eps, code, _handle(stream, device)),
            "fa_qk_norm_rope")
 
 
@@ -97,7 +98,7 @@ def fa_qk_norm_rope_bwd(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv
         *pointers, _dense("dqkv", dqkv, qkv.dtype, qkv.shape, device),
         None if dq_weight is None else _dense("dq_weight", dq_weight, _F32, (d,), device),
         None if dk_weight is None else _dense("dk_weight", dk_weight, _F32, (d,), device), space, nbytes,
-        *sizes, bool(interleaved), eps, code, _handle(stream)), "fa_qk_norm_rope_bwd")
+        *sizes, bool(interleaved), eps, code, _handle(stream, device)), "fa_qk_norm_rope_bwd")
 
 
 # ---------------------------------------------------------------- windowed attention
@@ -111,7 +112,7 @@ def fa_fwd_window(q, k, v, o, lse, scale, window, n_sink, dtype=FA_BF16, stream=
     _check(lib().fa_fwd_window(_dense("q", q, _BF16, rows, device), _dense("k", k, _BF16, kv_rows, device),
                                _dense("v", v, _BF16, kv_rows, device), _dense("o", o, _BF16, rows, device),
                                None if lse is None else _dense("lse", lse, _F32, (B, H, N), device), B, H,
-                               H_kv, N, d, scale, window, n_sink, dtype, _handle(stream)), "fa_fwd_window")
+                               H_kv, N, d, scale, window, n_sink, dtype, _handle(stream, device)), "fa_fwd_window")
 
 
 def fa_bwd_window_workspace_size(B, H, H_kv, N, d, window, n_sink):
@@ -131,7 +132,7 @@ def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_s
         _dense("lse", lse, _F32, (B, H, N), device), _dense("do", do, _BF16, rows, device),
         _dense("dq", dq, _BF16, rows, device), _dense("dk", dk, _BF16, kv_rows, device),
         _dense("dv", dv, _BF16, kv_rows, device), *_space(workspace, device), B, H, H_kv, N, d, scale,
-        window, n_sink, dtype, _handle(stream)), "fa_bwd_window")
+        window, n_sink, dtype, _handle(stream, device)), "fa_bwd_window")
 
 
 # ---------------------------------------------------------------- the 4-bit cache
@@ -166,7 +167,7 @@ def fa_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, block_table, first
     _check(lib().fa_kv4_append(_dense("k", k, _BF16, rows, device), _dense("v", v, _BF16, rows, device), *cache,
                                _dense("first", first, _I32, (B,), device),
                                None if count is None else _dense("count", count, _I32, (B,), device), B, H_kv,
-                               N, d, *pages, _handle(stream)), "fa_kv4_append")
+                               N, d, *pages, _handle(stream, device)), "fa_kv4_append")
 
 
 def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, block_table, lengths, k, v, stream=None):
@@ -177,7 +178,7 @@ def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, block_table, lengths, k, v
     cache, pages = _cache(k_codes, k_scales, v_codes, v_scales, block_table, B, H_kv, d, device)
     _check(lib().fa_kv4_read(*cache, _dense("lengths", lengths, _I32, (B,), device),
                              _dense("k", k, _BF16, rows, device), _dense("v", v, _BF16, rows, device), B, H_kv,
-                             N, d, *pages, _handle(stream)), "fa_kv4_read")
+                             N, d, *pages, _handle(stream, device)), "fa_kv4_read")
 
 
 def fa_decode_kv4_workspace_size(B, H, H_kv, N_q, d):
@@ -196,4 +197,4 @@ def fa_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, lengths,
                                _dense("o", o, _BF16, rows, device),
                                None if lse is None else _dense("lse", lse, _F32, (B, H, N_q), device),
                                *_space(workspace, device), B, H, k_codes.shape[1], N_q, d, *pages, scale,
-                               window, n_sink, _handle(stream)), "fa_decode_kv4")
+                               window, n_sink, _handle(stream, device)), "fa_decode_kv4")
