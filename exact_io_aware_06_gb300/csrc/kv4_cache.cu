@@ -3,8 +3,9 @@
 //
 // Both are bound by memory: 2 d bytes of bf16 against 9 d / 16 of codes and scales per row.
 // d / 8 lanes hold a row, eight values (16 bytes of bf16) each, four lanes a group of 32 whose
-// maximum is two shuffles.  A thread takes kRows rows, the loads of all of them before the work on
-// the first: the way to a row's bytes (request, its first token, its page) is three dependent loads.
+// maximum is two shuffles.  A thread takes a row of K and the same row of V: the way to their
+// bytes (request, its first token, its page: three dependent loads) is gone once for both.
+// Instructions bound these kernels next to memory, hence the arithmetic below.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -45,11 +46,17 @@ __device__ __forceinline__ float bf16_at(uint32_t w, int i) {
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float s) {
     float q[8];
     if (s >= 0x1p-120f) {
-        const float inv = __frcp_rn(s);
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = __fadd_rn(__fadd_rn(bf16_at(w[i / 2], i & 1) * inv, 3072.f), -3072.f);
-            q[i] = __fadd_rn(__fadd_rn(t, 12582912.f), -12582912.f);  // nearest integer, halves to even
+        for (int i = 0; i < 4; ++i) {
+            float2 t = __fmul2_rn(make_float2(bf16_at(w[i], 0), bf16_at(w[i], 1)), inv2);
+            t = __fadd2_rn(__fadd2_rn(t, make_float2(3072.f, 3072.f)), make_float2(-3072.f, -3072.f));
+            // the nearest integer, halves to even
+            t = __fadd2_rn(__fadd2_rn(t, make_float2(12582912.f, 12582912.f)), make_float2(-12582912.f, -12582912.f));
+            q[2 * i] = t.x;
+            q[2 * i + 1] = t.y;
         }
     } else {
 #pragma unroll
@@ -77,8 +84,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-constexpr int kRows = 2;  // rows per thread whose loads are in flight together
-
 // Where a row is: request, head and the index among the request's rows.
 struct Row {
     uint32_t b, h, n;
@@ -97,57 +102,53 @@ __global__ void __launch_bounds__(kThreads)
     kv4_append_kernel(const Kv4Cache c, const uint4* __restrict__ k, const uint4* __restrict__ v,
                       const int* __restrict__ first, const int* __restrict__ count, const Div by_n, const Div by_heads,
                       uint32_t rows, DevCtl ctl) {
-    constexpr int kLanes = D / 8, kStep = kThreads / kLanes;
+    constexpr int kLanes = D / 8;
     const int j = threadIdx.x % kLanes;  // this lane's eight values: 8 j ..
     const int grp = j / 4, t = j % 4;
-    const int which = blockIdx.y;        // K or V
-    const uint4* src = which ? v : k;
-    const uint32_t row0 = blockIdx.x * (kRows * kStep) + threadIdx.x / kLanes;
+    const uint32_t row = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     griddep_wait();
     griddep_launch_dependents();
-    uint4 raw[kRows];
-    int page[kRows], pos[kRows], head[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const uint32_t row = row0 + u * kStep;
-        raw[u] = row < rows ? __ldcs(src + static_cast<size_t>(row) * kLanes + j) : make_uint4(0, 0, 0, 0);
-        page[u] = -1;
-        if (row < rows) {
-            const Row r = row_at(row, by_n, by_heads);
-            head[u] = r.h;
-            if (count == nullptr || static_cast<int>(r.n) < count[r.b]) {
-                const long long at = static_cast<long long>(first[r.b]) + r.n;
-                pos[u] = at < 0 || at > 0x7fffffff ? -1 : static_cast<int>(at);
-                page[u] = page_of(c, ctl, r.b, pos[u]);
-            }
+    uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    int page = -1, pos = 0, head = 0;
+    if (row < rows) {
+        const size_t at = static_cast<size_t>(row) * kLanes + j;
+        raw[0] = __ldcs(k + at);
+        raw[1] = __ldcs(v + at);
+        const Row r = row_at(row, by_n, by_heads);
+        head = r.h;
+        if (count == nullptr || static_cast<int>(r.n) < count[r.b]) {
+            const long long p = static_cast<long long>(first[r.b]) + r.n;
+            pos = p < 0 || p > 0x7fffffff ? -1 : static_cast<int>(p);
+            page = page_of(c, ctl, r.b, pos);
         }
     }
+    uint32_t word[2], sbits[2];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         // the largest magnitude as bits: ordered as integers, infinities and NaN above all else
         uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
                                 __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = max(top & 0xFFFFu, top >> 16);
-        if (page[u] < 0) continue;  // all lanes of the row
         const bool finite = top < 0x7F80u;
-        const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(top << 16), 7.f)));
-        const uint32_t word = finite && s > 0.f ? codes_of(w, s) : 0x88888888u;
-        const uint16_t sbits = finite ? static_cast<uint16_t>(__float_as_uint(s) >> 16) : 0x7FC0u;
-        const int slot = pos[u] & ((1 << c.page_log2) - 1);
-        const size_t base = (static_cast<size_t>(page[u]) * c.H_kv + head[u]) << c.page_log2;  // in tokens
-        if (which == 0) {
-            *reinterpret_cast<uint32_t*>(c.codes[0] + (base + slot) * (D / 2) + kv4_k_word(D, t, grp)) = word;
-            if (t == 0) c.scales[0][(base + slot) * (D / 32) + grp] = sbits;
-        } else {
-            uint8_t* dst = c.codes[1] + base * (D / 2);
-            *reinterpret_cast<uint16_t*>(dst + kv4_v_half(D, slot, 2 * t, grp)) = static_cast<uint16_t>(word);
-            *reinterpret_cast<uint16_t*>(dst + kv4_v_half(D, slot, 2 * t + 1, grp)) =
-                static_cast<uint16_t>(word >> 16);
-            if (t == 0) c.scales[1][base * (D / 32) + kv4_v_scale(D, slot, grp)] = sbits;
-        }
+        // max / 7 has the binary period 001, so no max of 8 bits comes near a tie of bf16: the
+        // product with 1/7 rounds as the quotient does
+        const float s = __bfloat162float(__float2bfloat16_rn(__uint_as_float(top << 16) * (1.f / 7.f)));
+        word[i] = finite && s > 0.f ? codes_of(w, s) : 0x88888888u;
+        sbits[i] = finite ? __float_as_uint(s) >> 16 : 0x7FC0u;
+    }
+    if (page < 0) return;
+    const int slot = pos & ((1 << c.page_log2) - 1);
+    const size_t base = (static_cast<size_t>(page) * c.H_kv + head) << c.page_log2;  // in tokens
+    *reinterpret_cast<uint32_t*>(c.codes[0] + (base + slot) * (D / 2) + kv4_k_word(D, t, grp)) = word[0];
+    uint8_t* dst = c.codes[1] + base * (D / 2) + kv4_v_half(D, slot, 2 * t, grp);
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(word[1]);
+    *reinterpret_cast<uint16_t*>(dst + kv4_v_half(D, 0, 1, 0)) = static_cast<uint16_t>(word[1] >> 16);
+    if (t == 0) {
+        c.scales[0][(base + slot) * (D / 32) + grp] = static_cast<uint16_t>(sbits[0]);
+        c.scales[1][base * (D / 32) + kv4_v_scale(D, slot, grp)] = static_cast<uint16_t>(sbits[1]);
     }
 }
 
@@ -155,68 +156,46 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_read_kernel(const Kv4Cache c, const int* __restrict__ lengths, uint4* __restrict__ k,
                     uint4* __restrict__ v, const Div by_n, const Div by_heads, uint32_t rows, DevCtl ctl) {
-    constexpr int kLanes = D / 8, kStep = kThreads / kLanes;
+    constexpr int kLanes = D / 8;
     const int j = threadIdx.x % kLanes;
     const int grp = j / 4, t = j % 4;
-    const int which = blockIdx.y;
-    uint4* dst = which ? v : k;
-    const uint32_t row0 = blockIdx.x * (kRows * kStep) + threadIdx.x / kLanes;
+    const uint32_t row = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     griddep_wait();
     griddep_launch_dependents();
-    int page[kRows];
-    uint32_t word[kRows], sbits[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const uint32_t row = row0 + u * kStep;
-        page[u] = -1;
-        if (row < rows) {
-            const Row r = row_at(row, by_n, by_heads);
-            if (static_cast<int>(r.n) < lengths[r.b]) page[u] = page_of(c, ctl, r.b, r.n);
-        }
+    if (row >= rows) return;
+    const Row r = row_at(row, by_n, by_heads);
+    const int page = static_cast<int>(r.n) < lengths[r.b] ? page_of(c, ctl, r.b, r.n) : -1;
+    const size_t at = static_cast<size_t>(row) * kLanes + j;
+    if (page < 0) {
+        k[at] = v[at] = make_uint4(0, 0, 0, 0);
+        return;
     }
+    const int slot = r.n & ((1 << c.page_log2) - 1);
+    const size_t base = (static_cast<size_t>(page) * c.H_kv + r.h) << c.page_log2;
+    const uint8_t* src = c.codes[1] + base * (D / 2) + kv4_v_half(D, slot, 2 * t, grp);
+    const uint32_t word[2] = {
+        *reinterpret_cast<const uint32_t*>(c.codes[0] + (base + slot) * (D / 2) + kv4_k_word(D, t, grp)),
+        *reinterpret_cast<const uint16_t*>(src) |
+            static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + kv4_v_half(D, 0, 1, 0))) << 16};
+    const uint32_t scale[2] = {c.scales[0][(base + slot) * (D / 32) + grp],
+                               c.scales[1][base * (D / 32) + kv4_v_scale(D, slot, grp)]};
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const uint32_t row = row0 + u * kStep;
-        if (page[u] < 0) {
-            word[u] = 0x88888888u;
-            sbits[u] = 0;
-            continue;
-        }
-        const Row r = row_at(row, by_n, by_heads);
-        const int slot = r.n & ((1 << c.page_log2) - 1);
-        const size_t base = (static_cast<size_t>(page[u]) * c.H_kv + r.h) << c.page_log2;
-        if (which == 0) {
-            word[u] = __ldcs(reinterpret_cast<const uint32_t*>(c.codes[0] + (base + slot) * (D / 2) +
-                                                               kv4_k_word(D, t, grp)));
-            sbits[u] = c.scales[0][(base + slot) * (D / 32) + grp];
-        } else {
-            const uint8_t* src = c.codes[1] + base * (D / 2);
-            word[u] = *reinterpret_cast<const uint16_t*>(src + kv4_v_half(D, slot, 2 * t, grp));
-            word[u] |= static_cast<uint32_t>(
-                           *reinterpret_cast<const uint16_t*>(src + kv4_v_half(D, slot, 2 * t + 1, grp))) << 16;
-            sbits[u] = c.scales[1][base * (D / 32) + kv4_v_scale(D, slot, grp)];
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const uint32_t row = row0 + u * kStep;
-        if (row >= rows) break;
-        // pairs of values i and i + 4 as 128 + code + 8, less 136 (exact), times the scale: the
+    for (int i = 0; i < 2; ++i) {
+        // pairs of values m and m + 4 as 128 + code + 8, less 136 (exact), times the scale: the
         // product of 4 and 8 bits, rounded once
-        const uint32_t s2 = sbits[u] | sbits[u] << 16;
+        const uint32_t s2 = scale[i] | scale[i] << 16;
         uint32_t e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            e[i] = mul_bf16x2(sub_bf16x2(((word[u] >> (4 * i)) & 0x000F000Fu) | 0x43004300u, 0x43084308u), s2);
-        const uint4 o = make_uint4(__byte_perm(e[0], e[1], 0x5410), __byte_perm(e[2], e[3], 0x5410),
-                                   __byte_perm(e[0], e[1], 0x7632), __byte_perm(e[2], e[3], 0x7632));
-        dst[static_cast<size_t>(row) * kLanes + j] = page[u] < 0 ? make_uint4(0, 0, 0, 0) : o;
+        for (int m = 0; m < 4; ++m)
+            e[m] = mul_bf16x2(sub_bf16x2(((word[i] >> (4 * m)) & 0x000F000Fu) | 0x43004300u, 0x43084308u), s2);
+        (i ? v : k)[at] = make_uint4(__byte_perm(e[0], e[1], 0x5410), __byte_perm(e[2], e[3], 0x5410),
+                                     __byte_perm(e[0], e[1], 0x7632), __byte_perm(e[2], e[3], 0x7632));
     }
 }
 
 dim3 grid_of(uint32_t rows, int lanes) {
-    const uint32_t per = kRows * kThreads / lanes;
-    return dim3((rows + per - 1) / per, 2);
+    const uint32_t per = kThreads / lanes;
+    return dim3((rows + per - 1) / per);
 }
 
 }  // namespace
