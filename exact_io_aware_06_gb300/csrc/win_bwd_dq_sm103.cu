@@ -4,20 +4,22 @@
 //     dS_ij = P_ij o (dP_ij - delta_i),  dQ_i = scale * sum_j dS_ij K_j.
 // dQ_i accumulates in TMEM over the sweep and is written once as bf16: no atomics.
 //
-// Three products of 128 x 128 x 128 per pair of blocks, 24 MMAs.  The plain backward's dQ kernel
-// writes dS over S, so that the next scores wait for this block's dS and dQ: 3850 cycles a
-// pair.  Here dS has two TMEM buffers of its own, and the tensor core goes on with the next
-// block's S and dP as soon as the dS warps have taken this block's into registers:
-//   * MMA thread, for the pairs g = 0, 1, .. of all its items: S and dP of g + 1, then
-//     dQ += dS_g K_g.  A pair's sp_full thereby says that dQ of the pair before the last is
-//     done, whose dS buffer the dS warps then write.
+// Three products of 128 x 128 x 128 per pair of blocks, 24 MMAs: 1614 cycles of the tensor pipe.
+// The plain backward's dQ kernel writes dS over S, so that the next scores wait for this block's
+// dS and dQ: 3850 cycles a pair.  Here:
+//   * dS has two TMEM buffers of its own, and the tensor core goes on with the next block's S
+//     and dP as soon as the dS warps have taken this block's into registers.
+//   * Two issuing threads, S and dP in one, dQ in the other: a single thread issues S and dP of
+//     pair g + 1 (1034 cycles), then waits for dS of g and issues dQ (1100), 2970 cycles a pair.
 //   * K is read twice, up to two pairs apart: its ring is three deep, V's two (with Q and dO
 //     224 KB).
 //   * Persistent, one CTA per SM, items from the last query blocks to the first: the next
-//     item's Q, dO and first S, dP are under way while this one ends.
+//     item's Q, dO and first S, dP are under way while this one ends, and a warpgroup of its
+//     own writes dQ (its rows' 16-byte stores took 3000 cycles of the dS warps' time per item).
 //
-// Warp 0 TMA, warp 1 MMA, warps 4-7 and 8-11 one query row per thread, for keys 0-63 / 64-127
-// of block j.  TMEM: S 0-127, dP 128-255, dQ 256-383, dS (bf16) 384-447 and 448-511.
+// Warp 0 TMA, warps 1 and 2 MMA, warps 4-7 and 8-11 one query row per thread, for keys 0-63 /
+// 64-127 of block j, warps 12-15 write dQ.  TMEM: S 0-127, dP 128-255, dQ 256-383, dS (bf16)
+// 384-447 and 448-511.
 #include <cmath>
 
 #include "layer_ops.h"
@@ -29,7 +31,7 @@ namespace {
 
 constexpr int kBlk = 128;
 constexpr int kD = 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kKStages = 3, kVStages = 2;
 constexpr int kTile = kBlk * kD * 2;
 constexpr int kOffQ = 0, kOffDO = kTile, kOffK = 2 * kTile, kOffV = kOffK + kKStages * kTile;
@@ -57,8 +59,9 @@ struct DqBars {
     uint64_t q_full, q_free;
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t sp_full, sp_free;  // S, dP written; read by the dS warps
-    uint64_t ds_full[2];        // one per dS buffer: a waiter cannot fall two phases behind
-    uint64_t all_done, drain;
+    uint64_t ds_full[2], ds_empty[2];  // one per dS buffer: a waiter cannot fall two phases behind
+    uint64_t all_done, dq_read;        // an item's dQ complete; read out of TMEM
+    uint64_t drain, drain2;
 };
 
 __device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* abort_flag) {
@@ -121,8 +124,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bars.sp_free), 256);
         mbar_init(smem_u32(&bars.ds_full[0]), 256);
         mbar_init(smem_u32(&bars.ds_full[1]), 256);
+        mbar_init(smem_u32(&bars.ds_empty[0]), 1);
+        mbar_init(smem_u32(&bars.ds_empty[1]), 1);
         mbar_init(smem_u32(&bars.all_done), 1);
+        mbar_init(smem_u32(&bars.dq_read), 128);
         mbar_init(smem_u32(&bars.drain), 1);
+        mbar_init(smem_u32(&bars.drain2), 1);
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -140,9 +147,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    // 384 threads x 168 registers at launch: 128 * 120 + 256 * 184 <= 384 * 168
+    // 512 threads x 128 registers at launch: 72 + 2 * 160 + 120 = 4 * 128
     if (warp < 4) {
-        regs_dec<120>();
+        regs_dec<72>();
         if (warp == 0) {
             // ============================================================ producer
             if (lane == 0) {
@@ -164,16 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++n;
                     for (int j = 0; j < I.n_kv; ++j, ++g) {
                         const int sk = g % kKStages, sv = g % kVStages, row = I.block(j) * kBlk;
-                        if (g >= kKStages &&
-                            !mbar_wait(smem_u32(&bars.k_empty[sk]), ((g / kKStages) & 1) ^ 1, lim, &abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t kf = smem_u32(&bars.k_full[sk]);
-                        mbar_arrive_expect_tx(kf, kTile);
-                        for (int c = 0; c < 2; ++c)
-                            tma_load_3d(sb + kOffK + sk * kTile + c * 16384, &tm_k, kf, 64 * c, row, I.bh_kv);
-                        gk = g + 1;
+                        // V's slot is free once dP of g - 2 is done, K's after dQ of g - 3, issued later
                         if (g >= kVStages &&
                             !mbar_wait(smem_u32(&bars.v_empty[sv]), ((g / kVStages) & 1) ^ 1, lim, &abort_flag)) {
                             ok = false;
@@ -184,6 +182,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 2; ++c)
                             tma_load_3d(sb + kOffV + sv * kTile + c * 16384, &tm_v, vf, 64 * c, row, I.bh_kv);
                         gv = g + 1;
+                        if (g >= kKStages &&
+                            !mbar_wait(smem_u32(&bars.k_empty[sk]), ((g / kKStages) & 1) ^ 1, lim, &abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t kf = smem_u32(&bars.k_full[sk]);
+                        mbar_arrive_expect_tx(kf, kTile);
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_3d(sb + kOffK + sk * kTile + c * 16384, &tm_k, kf, 64 * c, row, I.bh_kv);
+                        gk = g + 1;
                     }
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
@@ -202,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t kStage16 = kTile >> 4;
                 const uint32_t q_lo = sdesc_sw128_lo(sb + kOffQ, 16), do_lo = sdesc_sw128_lo(sb + kOffDO, 16);
                 const uint32_t k_lo = sdesc_sw128_lo(sb + kOffK, 16), v_lo = sdesc_sw128_lo(sb + kOffV, 16);
-                const uint32_t k_mn = sdesc_sw128_lo(sb + kOffK, 16384);
                 // S = Q K_j^T and dP = dO V_j^T of pair g (both operands K-major along d)
                 auto issue_sp = [&](int g, int item, bool first, bool last) -> bool {
                     const int sk = g % kKStages, sv = g % kVStages;
@@ -233,26 +240,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (last) mma_commit(smem_u32(&bars.q_free));
                     return true;
                 };
-                int g = 0, item = 0;  // this pair, its item's number
+                int g = 0, item = 0;
                 bool ok = true;
-                int x = item_x(0), k = 0;
-                if (x < args.n_items) ok = issue_sp(0, 0, true, item_at(x).n_kv == 1);
-                while (ok && x < args.n_items) {
+                for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k), ++item) {
                     const int n_kv = item_at(x).n_kv;
-                    const int xn = item_x(k + 1);
-                    const bool more = xn < args.n_items;
-                    const int n_next = more ? item_at(xn).n_kv : 0;
+                    for (int j = 0; j < n_kv && ok; ++j, ++g) ok = issue_sp(g, item, j == 0, j + 1 == n_kv);
+                }
+                if (!ok) record_timeout(args.ctl, &abort_flag);
+                mma_commit(smem_u32(&bars.drain));
+                const volatile int never = 0;
+                mbar_wait(smem_u32(&bars.drain), 0, kDrainWaitNs, &never);
+            }
+        } else if (warp == 2) {
+            // ============================================================ dQ issuer
+            // Its MMAs read dS (TMEM) and K and write dQ: nothing that the other thread's write.
+            if (lane == 0) {
+                constexpr uint32_t kDescHi = sdesc_sw128_hi(1024);
+                const uint32_t k_mn = sdesc_sw128_lo(sb + kOffK, 16384);
+                int g = 0, item = 0;
+                bool ok = true;
+                for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k), ++item) {
+                    const int n_kv = item_at(x).n_kv;
                     for (int j = 0; j < n_kv; ++j, ++g) {
-                        // the pair after this one: of this item, or the next one's first
-                        if (j + 1 < n_kv)
-                            ok = issue_sp(g + 1, item, false, j + 2 == n_kv);
-                        else if (more)
-                            ok = issue_sp(g + 1, item + 1, true, n_next == 1);
+                        const int sk = g % kKStages;
+                        ok = mbar_wait(smem_u32(&bars.k_full[sk]), (g / kKStages) & 1, lim, &abort_flag);
+                        // the last item's dQ has been read out
+                        if (ok && j == 0 && item > 0)
+                            ok = mbar_wait(smem_u32(&bars.dq_read), (item - 1) & 1, lim, &abort_flag);
                         if (ok) ok = mbar_wait(smem_u32(&bars.ds_full[g & 1]), (g >> 1) & 1, lim, &abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         // dQ += dS_j K_j: A = dS from TMEM (queries x keys), B = K_j MN-major
-                        const uint32_t km = k_mn + (g % kKStages) * kStage16, ds = tmem + kColDS + 64 * (g & 1);
+                        const uint32_t km = k_mn + sk * (kTile >> 4), ds = tmem + kColDS + 64 * (g & 1);
 #pragma unroll
                         for (int kk = 0; kk < kBlk / 16; ++kk) {
                             if (kk == 0)
@@ -260,22 +279,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else
                                 mma_ts_w<false, 1>(tmem + kColDQ, ds + 8 * kk, km + 128 * kk, kDescHi, kIdescDQ);
                         }
-                        mma_commit(smem_u32(&bars.k_empty[g % kKStages]));
+                        mma_commit(smem_u32(&bars.ds_empty[g & 1]));
+                        mma_commit(smem_u32(&bars.k_empty[sk]));  // S of this pair read K before dS was made
                         if (j + 1 == n_kv) mma_commit(smem_u32(&bars.all_done));
                     }
-                    ++item;
-                    x = xn;
-                    ++k;
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
-                mma_commit(smem_u32(&bars.drain));
+                mma_commit(smem_u32(&bars.drain2));
                 const volatile int never = 0;
-                mbar_wait(smem_u32(&bars.drain), 0, kDrainWaitNs, &never);
+                mbar_wait(smem_u32(&bars.drain2), 0, kDrainWaitNs, &never);
             }
         }
-        // warps 2-3 have no role
-    } else {
-        regs_inc<184>();
+        // warp 3 has no role
+    } else if (warp < 12) {
+        regs_inc<160>();
         // ================================================================ dS warpgroups
         const int half = (warp - 4) / 4;  // keys 64*half .. 64*half+63 of each block
         const int wq = warp % 4;
@@ -283,12 +300,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float2 c2 = make_float2(args.c_log2, args.c_log2);
         bool ok = true;
-        int g = 0, item = 0;
-        for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k), ++item) {
+        int g = 0;
+        // an item's row values, loaded one item ahead; padded rows exist up to Np
+        auto row_at = [&](int x) {
+            const Item I = item_at(x);
+            return static_cast<size_t>(I.bh) * Np + I.qb * kBlk + row;
+        };
+        float next_nl = 0.f, next_nd = 0.f;
+        if (item_x(0) < args.n_items) {
+            next_nl = args.ws_nlse2[row_at(item_x(0))];
+            next_nd = args.ws_ndelta[row_at(item_x(0))];
+        }
+        for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k)) {
             const Item I = item_at(x);
             const int qrow = I.qb * kBlk + row;
-            const size_t srow = static_cast<size_t>(I.bh) * Np + qrow;  // padded rows exist up to Np
-            const float nl = args.ws_nlse2[srow], nd = args.ws_ndelta[srow];
+            const float nl = next_nl, nd = next_nd;
+            if (item_x(k + 1) < args.n_items) {
+                next_nl = args.ws_nlse2[row_at(item_x(k + 1))];
+                next_nd = args.ws_ndelta[row_at(item_x(k + 1))];
+            }
             const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
             for (int j = 0; j < I.n_kv; ++j, ++g) {
                 ok = mbar_wait(smem_u32(&bars.sp_full), g & 1, lim, &abort_flag);
@@ -332,39 +362,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 ds = __fmul2_rn(p, d);
                     pk[i] = pack_bf16x2(ds.x, ds.y);
                 }
-                // buffer g % 2: dQ of pair g - 2 was issued before these scores
+                if (g >= 2) {  // dQ of pair g - 2 has read this buffer
+                    ok = mbar_wait(smem_u32(&bars.ds_empty[g & 1]), ((g >> 1) & 1) ^ 1, lim, &abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 tmem_st32(lb + kColDS + 64 * (g & 1) + 32 * half, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.ds_full[g & 1]));
             }
-            if (ok) {
-                ok = mbar_wait(smem_u32(&bars.all_done), item & 1, lim, &abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-            }
+        }
+        if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
+    } else {
+        regs_dec<120>();
+        // ================================================================ dQ out
+        const int wq = warp % 4;
+        const int row = wq * 32 + lane;
+        const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const float sc = args.scale;
+        bool ok = true;
+        int item = 0;
+        for (int k = 0, x = item_x(0); x < args.n_items; x = item_x(++k), ++item) {
+            const Item I = item_at(x);
+            const int qrow = I.qb * kBlk + row;
+            ok = mbar_wait(smem_u32(&bars.all_done), item & 1, lim, &abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            // this half's 64 columns of its row: dQ = scale * accumulator.  Read before these warps
-            // hand over the next item's first dS, which lets its dQ overwrite the accumulator.
-            const float sc = args.scale;
-            uint16_t* out = static_cast<uint16_t*>(args.dq) + (static_cast<size_t>(I.bh) * N + qrow) * kD;
+            uint32_t w[kD / 2];  // dQ = scale * accumulator, as bf16 pairs
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int col = half * 64 + 32 * h;
+            for (int h = 0; h < kD / 32; ++h) {
                 uint32_t r[32];
-                tmem_ld32(lb + kColDQ + col, r);
-                if (qrow < N) {
-                    uint4* o4 = reinterpret_cast<uint4*>(out + col);
+                tmem_ld32(lb + kColDQ + 32 * h, r);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o4[i] = make_uint4(
-                            pack_bf16x2(__uint_as_float(r[8 * i]) * sc, __uint_as_float(r[8 * i + 1]) * sc),
-                            pack_bf16x2(__uint_as_float(r[8 * i + 2]) * sc, __uint_as_float(r[8 * i + 3]) * sc),
-                            pack_bf16x2(__uint_as_float(r[8 * i + 4]) * sc, __uint_as_float(r[8 * i + 5]) * sc),
-                            pack_bf16x2(__uint_as_float(r[8 * i + 6]) * sc, __uint_as_float(r[8 * i + 7]) * sc));
-                }
+                for (int i = 0; i < 16; ++i)
+                    w[16 * h + i] = pack_bf16x2(__uint_as_float(r[2 * i]) * sc, __uint_as_float(r[2 * i + 1]) * sc);
             }
             tc_fence_before();
+            mbar_arrive(smem_u32(&bars.dq_read));
+            if (qrow < N) {
+                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.dq) +
+                                                      (static_cast<size_t>(I.bh) * N + qrow) * kD);
+#pragma unroll
+                for (int i = 0; i < kD / 8; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
     }
