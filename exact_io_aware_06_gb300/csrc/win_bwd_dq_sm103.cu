@@ -15,7 +15,7 @@
 //     224 KB).
 //   * Persistent, one CTA per SM, items from the last query blocks to the first: the next
 //     item's Q, dO and first S, dP are under way while this one ends, and a warpgroup of its
-//     own writes dQ (its rows' 16-byte stores took 3000 cycles of the dS warps' time per item).
+//     own writes dQ (which took 3000 cycles of the dS warps' time per item).
 //
 // Warp 0 TMA, warps 1 and 2 MMA, warps 4-7 and 8-11 one query row per thread, for keys 0-63 /
 // 64-127 of block j, warps 12-15 write dQ.  TMEM: S 0-127, dP 128-255, dQ 256-383, dS (bf16)
@@ -72,6 +72,34 @@ __device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* 
 // Bits below n (all of them for n >= 32, none for n <= 0).
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// 16 TMEM lanes x 64 columns, lane 4 r + q of the warp holding columns 8 j + 2 q, + 1 of rows r
+// (x[4 j], x[4 j + 1]) and r + 8 (x[4 j + 2], x[4 j + 3]).
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&x)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+          "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
+          "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+          "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Lane q of every four holds word q of four 16-byte pieces; afterwards lane q holds piece q.
+__device__ __forceinline__ void transpose4(uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3, int q) {
+    const bool odd = q & 1, high = q & 2;
+    uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+    (odd ? a0 : a1) = r;
+    r = __shfl_xor_sync(0xffffffffu, odd ? a2 : a3, 1);
+    (odd ? a2 : a3) = r;
+    r = __shfl_xor_sync(0xffffffffu, high ? a0 : a2, 2);
+    (high ? a0 : a2) = r;
+    r = __shfl_xor_sync(0xffffffffu, high ? a1 : a3, 2);
+    (high ? a1 : a3) = r;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -379,35 +407,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<120>();
         // ================================================================ dQ out
         const int wq = warp % 4;
-        const int row = wq * 32 + lane;
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float sc = args.scale;
         bool ok = true;
         int item = 0;
         for (int k = 0, x = item_x(0); x < args.n_items; x = item_x(++k), ++item) {
             const Item I = item_at(x);
-            const int qrow = I.qb * kBlk + row;
             ok = mbar_wait(smem_u32(&bars.all_done), item & 1, lim, &abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            uint32_t w[kD / 2];  // dQ = scale * accumulator, as bf16 pairs
+            // dQ = scale * accumulator as bf16 pairs: rows 16 m + r and 16 m + 8 + r, columns 64 c +
+            // 8 j + 2 q.  (One row per lane, 32 lines a store instruction, kept the dS warps' next
+            // TMEM loads waiting for 2300 cycles behind the stores; here it is 8 lines.)
+            const int r8 = lane / 4, q = lane % 4;
+            uint32_t w[2][2][2][8];
 #pragma unroll
-            for (int h = 0; h < kD / 32; ++h) {
-                uint32_t r[32];
-                tmem_ld32(lb + kColDQ + 32 * h, r);
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[16 * h + i] = pack_bf16x2(__uint_as_float(r[2 * i]) * sc, __uint_as_float(r[2 * i + 1]) * sc);
-            }
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+                    tmem_ld_rows16(lb + (static_cast<uint32_t>(16 * m) << 16) + kColDQ + 64 * c, x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            w[m][c][h][j] = pack_bf16x2(__uint_as_float(x[4 * j + 2 * h]) * sc,
+                                                        __uint_as_float(x[4 * j + 2 * h + 1]) * sc);
+                }
             tc_fence_before();
             mbar_arrive(smem_u32(&bars.dq_read));
-            if (qrow < N) {
-                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.dq) +
-                                                      (static_cast<size_t>(I.bh) * N + qrow) * kD);
 #pragma unroll
-                for (int i = 0; i < kD / 8; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            }
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int qrow = I.qb * kBlk + wq * 32 + 16 * m + 8 * h + r8;
+                    uint16_t* out = static_cast<uint16_t*>(args.dq) + (static_cast<size_t>(I.bh) * N + qrow) * kD;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) {
+                            uint32_t(&p)[8] = w[m][c][h];
+                            transpose4(p[j], p[j + 1], p[j + 2], p[j + 3], q);  // columns 64 c + 8 (j + q) ..
+                            if (qrow < N)
+                                *reinterpret_cast<uint4*>(out + 64 * c + 8 * (j + q)) =
+                                    make_uint4(p[j], p[j + 1], p[j + 2], p[j + 3]);
+                        }
+                }
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
     }

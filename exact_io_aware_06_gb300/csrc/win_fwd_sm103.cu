@@ -17,8 +17,8 @@
 //   * Blocks that are visible whole need no mask; the others take a row's visible keys as four
 //     32-bit words, made by shifts from the row's two bounds, and one bit test per score.
 // Warp roles, TMEM columns, the K/V bundle ring and the order of MMAs are the plain
-// forward's; every wait is bounded, and a wait that runs out is recorded and ends the CTA
-// with its copies and MMAs drained.
+// forward's; O leaves through shared memory and TMA stores.  Every wait is bounded, and a wait
+// that runs out is recorded and ends the CTA with its copies and MMAs drained.
 #include <cmath>
 #include <type_traits>
 
@@ -37,7 +37,6 @@ constexpr int kThreads = 384;  // 12 warps
 constexpr float kTau = 8.0f;   // lazy-rescale threshold, log2 units
 
 struct WinArgs {
-    void* o;       // bf16 [BH][N][D]
     float* lse;
     int N, n_pairs, BH, n_items;
     int window, sinks;
@@ -54,7 +53,8 @@ struct Cfg {
     static constexpr int kOffQ = 0;                    // Q0, Q1
     static constexpr int kOffK = 2 * kTileBytes;       // K[kStages]
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kSmemBytes = kOffV + kStages * kTileBytes;
+    static constexpr int kOffO = kOffV + kStages * kTileBytes;  // 4 KB per softmax warp: 32 rows x 128 bytes
+    static constexpr int kSmemBytes = kOffO + 8 * 4096;
     static constexpr int kSmemAlloc = kSmemBytes + 1024;
     static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
     static constexpr uint32_t kTmemCols = 512;
@@ -74,6 +74,18 @@ __device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* 
     *abort_flag = 1;
     atomicCAS(ctl.status, kDevOk, kDevTimeout);
 }
+
+// Store a box from shared to global memory through the tensor map, in the thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All of this thread's committed bulk operations have read shared memory / have completed.
+__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 32 consecutive TMEM columns of this thread's lane into r[OFF..], no wait.
 template <int OFF, int NC>
@@ -242,7 +254,8 @@ __device__ __forceinline__ void softmax_block(uint32_t lane_base, uint32_t colS,
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     win_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const WinArgs args) {
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                   const WinArgs args) {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) Bars bars;
@@ -278,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_o);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
@@ -517,25 +531,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O_t is read before this warp publishes the next item's first P, so the next item's
             // first P V (which overwrites O_t) comes after these loads
             const float inv = 1.f / l;
-            const size_t orow = (static_cast<size_t>(bh) * N + qrow) * D;
+            // The warp's 32 rows go out 64 columns at a time: each lane writes its row's 128 bytes
+            // into the warp's own 4 KB (16-byte granule g of row r at g ^ (r % 8)), one lane stores
+            // the box, and the next box waits until that has been read.  Rows past N are not
+            // written by the store.  (Each lane storing its row itself: 32 lines an instruction,
+            // in the way of the warps' next TMEM loads.)
+            const uint32_t box = smem_base + C::kOffO + (warp - 4) * 4096;
 #pragma unroll
-            for (int q4 = 0; q4 < D / 32; ++q4) {
-                uint32_t ov[32];
-                tmem_ld32(lane_base + colO + 32 * q4, ov);
-                if (qrow < N) {
-                    uint32_t w[16];
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t ov[2][32];
+                tmem_ld32_async(lane_base + colO + 64 * c, ov[0]);
+                tmem_ld32_async(lane_base + colO + 64 * c + 32, ov[1]);
+                tmem_wait_ld();
+                reg_fence(ov[0]);
+                reg_fence(ov[1]);
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + orow + 32 * q4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                for (int g = 0; g < 8; ++g) {
+                    const uint32_t* f = ov[g / 4] + 8 * (g % 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((g ^ (lane & 7)) << 4)),
+                                 "r"(pack_bf16x2(__uint_as_float(f[0]) * inv, __uint_as_float(f[1]) * inv)),
+                                 "r"(pack_bf16x2(__uint_as_float(f[2]) * inv, __uint_as_float(f[3]) * inv)),
+                                 "r"(pack_bf16x2(__uint_as_float(f[4]) * inv, __uint_as_float(f[5]) * inv)),
+                                 "r"(pack_bf16x2(__uint_as_float(f[6]) * inv, __uint_as_float(f[7]) * inv))
+                                 : "memory");
+                }
+                fence_proxy_async_smem();  // the lanes' writes -> visible to the TMA unit
+                __syncwarp();
+                const int row0 = r0 + t * kBM + wq * 32;
+                if (lane == 0 && row0 < N) {
+                    tma_store_3d(&tm_o, box, 64 * c, row0, bh);
+                    bulk_commit_group();
                 }
             }
             if (qrow < N && args.lse != nullptr)
                 args.lse[static_cast<size_t>(bh) * N + qrow] = (m_ref + log2f(l)) * 0.69314718055994530942f;
         }
+        // the stores complete before the CTA's shared memory goes away
+        if (lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
@@ -552,10 +586,11 @@ int launch_impl(const void* q, const void* k, const void* v, void* o, float* lse
     using C = Cfg<D>;
     const int BH = B * H, BH_kv = B * H_kv;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     int rc = make_map_3d(&tq, q, dt, 2, D, N, BH, 64, kBM);
     if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, N, BH_kv, 64, kBN);
     if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, N, BH_kv, 64, kBN);
+    if (rc == 0) rc = make_map_3d(&to, o, dt, 2, D, N, BH, 64, 32);
     if (rc != 0) return rc;
     int dev = 0, sms = 152;
     cudaError_t e = cudaGetDevice(&dev);
@@ -564,7 +599,6 @@ int launch_impl(const void* q, const void* k, const void* v, void* o, float* lse
     if (e == cudaSuccess) e = allow_smem(win_fwd_kernel<D>, C::kSmemAlloc, smem_done);
     if (e != cudaSuccess) return static_cast<int>(e);
     WinArgs a;
-    a.o = o;
     a.lse = lse;
     a.N = N;
     a.n_pairs = (N + 2 * kBM - 1) / (2 * kBM);
@@ -579,7 +613,7 @@ int launch_impl(const void* q, const void* k, const void* v, void* o, float* lse
     a.ctl = ctl;
     const int grid = a.n_items < sms ? a.n_items : sms;
     return static_cast<int>(
-        launch_pdl(win_fwd_kernel<D>, dim3(grid), dim3(kThreads), C::kSmemAlloc, s, tq, tk, tv, a));
+        launch_pdl(win_fwd_kernel<D>, dim3(grid), dim3(kThreads), C::kSmemAlloc, s, tq, tk, tv, to, a));
 }
 
 }  // namespace
