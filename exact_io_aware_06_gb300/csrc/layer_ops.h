@@ -103,6 +103,9 @@ cudaError_t launch_decode_kv4(const DecodeArgs& a, int d, cudaStream_t s);
 int launch_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv, int N,
                       int d, float c_log2, int window, int sinks, DevCtl ctl, cudaStream_t s);
 
+int launch_fwd_window64(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv, int N,
+                        float c_log2, int window, int sinks, DevCtl ctl, cudaStream_t s);
+
 // The windowed backward's deal: key block j meets query blocks j .. j + reach; the first
 // n_part blocks (those with sinks and more query blocks after that) leave the rest to
 // `pieces` pieces of `per` query blocks.

@@ -16,36 +16,21 @@
 //     32 keys and P V of two K steps instead of 128 and eight, a quarter of the softmax work.
 //   * Blocks that are visible whole need no mask; the others take a row's visible keys as four
 //     32-bit words, made by shifts from the row's two bounds, and one bit test per score.
-// Warp roles, TMEM columns, the K/V bundle ring and the order of MMAs are the plain
-// forward's; O leaves through shared memory and TMA stores.  Every wait is bounded, and a wait
+// This kernel is for d = 128, whose S (P in its place) and O fill TMEM; d = 64 has room for P of its
+// own and another schedule (win_fwd64_sm103.cu).  Warp roles, TMEM columns, the K/V bundle ring and
+// the order of MMAs are the plain forward's; O leaves through shared memory and TMA stores.  Every wait is bounded, and a wait
 // that runs out is recorded and ends the CTA with its copies and MMAs drained.
-#include <cmath>
 #include <type_traits>
 
-#include "layer_ops.h"
-#include "ptx.cuh"
-#include "tma_host.h"
+#include "win_fwd.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kBM = 128;       // query rows per tile
-constexpr int kBN = 128;       // keys per block
-constexpr int kShort = 32;     // keys of a short sink block
 constexpr int kStages = 2;     // K/V ring depth
-constexpr int kThreads = 384;  // 12 warps
-constexpr float kTau = 8.0f;   // lazy-rescale threshold, log2 units
 
-struct WinArgs {
-    float* lse;
-    int N, n_pairs, BH, n_items;
-    int window, sinks;
-    float c_log2;  // scale * log2(e), not 0
-    int H, H_kv;
-    DevCtl ctl;
-};
+constexpr int D = 128;
 
-template <int D>
 struct Cfg {
     static constexpr int kChunks = D / 64;             // 128-byte swizzle columns per row
     static constexpr int kChunkBytes = 128 * 128;
@@ -70,193 +55,16 @@ struct Bars {
     uint64_t drain;
 };
 
-__device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* abort_flag) {
-    *abort_flag = 1;
-    atomicCAS(ctl.status, kDevOk, kDevTimeout);
-}
-
-// Store a box from shared to global memory through the tensor map, in the thread's bulk group.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All of this thread's committed bulk operations have read shared memory / have completed.
-__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// 32 consecutive TMEM columns of this thread's lane into r[OFF..], no wait.
-template <int OFF, int NC>
-__device__ __forceinline__ void ld32_at(uint32_t taddr, uint32_t (&r)[NC]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[OFF + 0]), "=r"(r[OFF + 1]), "=r"(r[OFF + 2]), "=r"(r[OFF + 3]),
-          "=r"(r[OFF + 4]), "=r"(r[OFF + 5]), "=r"(r[OFF + 6]), "=r"(r[OFF + 7]),
-          "=r"(r[OFF + 8]), "=r"(r[OFF + 9]), "=r"(r[OFF + 10]), "=r"(r[OFF + 11]),
-          "=r"(r[OFF + 12]), "=r"(r[OFF + 13]), "=r"(r[OFF + 14]), "=r"(r[OFF + 15]),
-          "=r"(r[OFF + 16]), "=r"(r[OFF + 17]), "=r"(r[OFF + 18]), "=r"(r[OFF + 19]),
-          "=r"(r[OFF + 20]), "=r"(r[OFF + 21]), "=r"(r[OFF + 22]), "=r"(r[OFF + 23]),
-          "=r"(r[OFF + 24]), "=r"(r[OFF + 25]), "=r"(r[OFF + 26]), "=r"(r[OFF + 27]),
-          "=r"(r[OFF + 28]), "=r"(r[OFF + 29]), "=r"(r[OFF + 30]), "=r"(r[OFF + 31])
-        : "r"(taddr)
-        : "memory");
-}
-
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float min3f(float a, float b, float c) {
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-// Max (or, for a negative score scale, min) of NC raw scores: four 3-input chains.
-template <int NC>
-__device__ __forceinline__ float extreme(const uint32_t (&r)[NC], bool want_max) {
-    float a[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) a[k] = __uint_as_float(r[k]);
-    if (want_max) {
-#pragma unroll
-        for (int i = 4; i + 8 <= NC; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                a[k] = max3f(a[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
-        a[0] = max3f(a[0], __uint_as_float(r[NC - 4]), __uint_as_float(r[NC - 3]));
-        a[1] = max3f(a[1], __uint_as_float(r[NC - 2]), __uint_as_float(r[NC - 1]));
-        return max3f(a[0], a[1], fmaxf(a[2], a[3]));
-    }
-#pragma unroll
-    for (int i = 4; i + 8 <= NC; i += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            a[k] = min3f(a[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
-    a[0] = min3f(a[0], __uint_as_float(r[NC - 4]), __uint_as_float(r[NC - 3]));
-    a[1] = min3f(a[1], __uint_as_float(r[NC - 2]), __uint_as_float(r[NC - 1]));
-    return min3f(a[0], a[1], fminf(a[2], a[3]));
-}
-
-// Bits below n (all of them for n >= 32, none for n <= 0).
-__device__ __forceinline__ uint32_t bits_below(int n) {
-    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-// Which key blocks a pair of query tiles visits.  List index n: blocks 0 .. n_sink - 1, then
-// lo .. ; the first is a short one if `shorty`.  Tile 0 leaves out the last entry when tile 1
-// has a diagonal block of its own, tile 1 leaves out entry skip1 (-1: none).
-struct Plan {
-    int n;          // entries
-    int n_sink, lo;
-    int skip1;
-    bool shorty, two;
-    __device__ __forceinline__ int block(int i) const { return i < n_sink ? i : lo + i - n_sink; }
-    __device__ __forceinline__ bool active(int t, int i) const {
-        return t ? (two && i != skip1) : (!two || i != n - 1);
-    }
-};
-__device__ __forceinline__ Plan plan_of(const WinArgs& a, int r0) {
-    Plan p;
-    p.two = r0 + kBM < a.N;
-    p.lo = max(0, static_cast<int>(static_cast<long long>(r0) - a.window + 1)) / kBN;
-    const int lo1 = max(0, static_cast<int>(static_cast<long long>(r0) + kBM - a.window + 1)) / kBN;
-    const int last = r0 / kBN + (p.two ? 1 : 0);
-    p.shorty = a.sinks > 0 && a.sinks <= kShort && p.lo > 0;
-    p.n_sink = min(p.lo, a.sinks / kBN + (a.sinks % kBN ? 1 : 0));
-    p.n = p.n_sink + last - p.lo + 1;
-    // tile 1 sees nothing of block lo if its window starts behind it and no sink lies in it
-    p.skip1 = (p.two && lo1 > p.lo && static_cast<long long>(p.lo) * kBN >= a.sinks) ? p.n_sink : -1;
-    return p;
-}
-
-// One key block for one row: NC raw scores (columns colS ..) to P in the same columns, the
-// reference maximum, the sum and, where the reference moves, O.
-template <int D, int NC>
-__device__ __forceinline__ void softmax_block(uint32_t lane_base, uint32_t colS, uint32_t colO, float c, bool c_pos,
-                                              uint32_t mask_bits, int hi, int lo, int sink, bool first, float& m_ref,
-                                              float& l) {
-    uint32_t r[NC];
-    ld32_at<0>(lane_base + colS, r);
-    if constexpr (NC == 128) {
-        ld32_at<32>(lane_base + colS + 32, r);
-        ld32_at<64>(lane_base + colS + 64, r);
-        ld32_at<96>(lane_base + colS + 96, r);
-    }
-    tmem_wait_ld();
-    reg_fence(r);
-    // keys hi and below, of those the ones from lo on or below `sink`, counted in the block
-    if (hi < NC - 1 || (lo > 0 && sink < NC)) {
-#pragma unroll
-        for (int w = 0; w < NC / 32; ++w) {
-            const uint32_t seen = bits_below(hi + 1 - 32 * w) & (~bits_below(lo - 32 * w) | bits_below(sink - 32 * w));
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (!(seen & (1u << i))) r[32 * w + i] = mask_bits;
-        }
-    }
-    const float mt = c * extreme(r, c_pos);
-    float alpha = 1.f;
-    const bool bump = mt > m_ref + kTau;
-    if (bump) {
-        alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - mt);
-        m_ref = mt;
-        l *= alpha;
-    }
-    const float ref = (m_ref == -INFINITY) ? 0.f : m_ref;
-    const float2 c2 = make_float2(c, c), nref2 = make_float2(-ref, -ref);
-    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-    for (int h = 0; h < (NC + 63) / 64; ++h) {
-        constexpr int kW = NC < 64 ? NC / 2 : 32;
-        uint32_t pk[kW];
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            const int e = 64 * h + 2 * i;
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, nref2);
-            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            if (i & 1)
-                acc1 = __fadd2_rn(acc1, p);
-            else
-                acc0 = __fadd2_rn(acc0, p);
-            pk[i] = pack_bf16x2(p.x, p.y);
-        }
-        if constexpr (NC < 64)
-            tmem_st16(lane_base + colS, pk);
-        else
-            tmem_st32(lane_base + colS + 32 * h, pk);
-    }
-    if (!first && __any_sync(0xffffffffu, bump)) {
-        // O_t += P V of this tile's previous block has completed: it precedes these scores in
-        // issue order
-#pragma unroll
-        for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t ov[32];
-            tmem_ld32(lane_base + colO + 32 * q4, ov);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st32(lane_base + colO + 32 * q4, ov);
-        }
-    }
-    l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
-    tmem_st_wait();
-}
-
 // Persistent: a CTA works through items, its k-th being x = k * gridDim.x + (blockIdx.x, or
 // gridDim.x - 1 - blockIdx.x in odd rounds); items run from the last pair of every head to
 // the first, the heaviest first (the first W / 256 pairs of a head see fewer keys).  Every
 // barrier counts its phases across items: q_full, q_free per item, kv_full, kv_empty per
 // bundle, s_full, p_full per block that the tile visits, o_done per item of the tile.
-template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     win_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                    const WinArgs args) {
-    using C = Cfg<D>;
+    using C = Cfg;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) Bars bars;
     __shared__ uint32_t tmem_slot;
@@ -509,10 +317,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int hi = qrow - kv0;
                 const int lo = static_cast<int>(max(-1ll, static_cast<long long>(hi) - args.window + 1));
                 const int sink = args.sinks - kv0;
+                // P overwrites S, and O_t += P V of the tile's last block precedes these scores in
+                // issue order: nothing to say and nothing to wait for
+                auto taken = [] {};
+                auto free = [] { return true; };
                 if (n == 0 && P.shorty)
-                    softmax_block<D, kShort>(lane_base, colS, colO, c, c_pos, mask_bits, hi, lo, sink, first, m_ref, l);
+                    softmax_block<D, kShort>(lane_base, colS, colS, colO, c, c_pos, mask_bits, hi, lo, sink, first, m_ref, l,
+                                             taken, free);
                 else
-                    softmax_block<D, kBN>(lane_base, colS, colO, c, c_pos, mask_bits, hi, lo, sink, first, m_ref, l);
+                    softmax_block<D, kBN>(lane_base, colS, colS, colO, c, c_pos, mask_bits, hi, lo, sink, first, m_ref, l,
+                                          taken, free);
                 first = false;
                 ++gj;
                 tc_fence_before();
@@ -531,40 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O_t is read before this warp publishes the next item's first P, so the next item's
             // first P V (which overwrites O_t) comes after these loads
             const float inv = 1.f / l;
-            // The warp's 32 rows go out 64 columns at a time: each lane writes its row's 128 bytes
-            // into the warp's own 4 KB (16-byte granule g of row r at g ^ (r % 8)), one lane stores
-            // the box, and the next box waits until that has been read.  Rows past N are not
-            // written by the store.  (Each lane storing its row itself: 32 lines an instruction,
-            // in the way of the warps' next TMEM loads.)
-            const uint32_t box = smem_base + C::kOffO + (warp - 4) * 4096;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t ov[2][32];
-                tmem_ld32_async(lane_base + colO + 64 * c, ov[0]);
-                tmem_ld32_async(lane_base + colO + 64 * c + 32, ov[1]);
-                tmem_wait_ld();
-                reg_fence(ov[0]);
-                reg_fence(ov[1]);
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint32_t* f = ov[g / 4] + 8 * (g % 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((g ^ (lane & 7)) << 4)),
-                                 "r"(pack_bf16x2(__uint_as_float(f[0]) * inv, __uint_as_float(f[1]) * inv)),
-                                 "r"(pack_bf16x2(__uint_as_float(f[2]) * inv, __uint_as_float(f[3]) * inv)),
-                                 "r"(pack_bf16x2(__uint_as_float(f[4]) * inv, __uint_as_float(f[5]) * inv)),
-                                 "r"(pack_bf16x2(__uint_as_float(f[6]) * inv, __uint_as_float(f[7]) * inv))
-                                 : "memory");
-                }
-                fence_proxy_async_smem();  // the lanes' writes -> visible to the TMA unit
-                __syncwarp();
-                const int row0 = r0 + t * kBM + wq * 32;
-                if (lane == 0 && row0 < N) {
-                    tma_store_3d(&tm_o, box, 64 * c, row0, bh);
-                    bulk_commit_group();
-                }
-            }
+            store_rows<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, lane_base + colO, inv, r0 + t * kBM + wq * 32, bh, N);
             if (qrow < N && args.lse != nullptr)
                 args.lse[static_cast<size_t>(bh) * N + qrow] = (m_ref + log2f(l)) * 0.69314718055994530942f;
         }
@@ -580,48 +361,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
-int launch_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv, int N,
-                float c_log2, int window, int sinks, DevCtl ctl, cudaStream_t s) {
-    using C = Cfg<D>;
-    const int BH = B * H, BH_kv = B * H_kv;
-    const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap tq, tk, tv, to;
-    int rc = make_map_3d(&tq, q, dt, 2, D, N, BH, 64, kBM);
-    if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, N, BH_kv, 64, kBN);
-    if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, N, BH_kv, 64, kBN);
-    if (rc == 0) rc = make_map_3d(&to, o, dt, 2, D, N, BH, 64, 32);
-    if (rc != 0) return rc;
-    int dev = 0, sms = 152;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    static std::atomic<uint64_t> smem_done;
-    if (e == cudaSuccess) e = allow_smem(win_fwd_kernel<D>, C::kSmemAlloc, smem_done);
-    if (e != cudaSuccess) return static_cast<int>(e);
-    WinArgs a;
-    a.lse = lse;
-    a.N = N;
-    a.n_pairs = (N + 2 * kBM - 1) / (2 * kBM);
-    a.BH = BH;
-    a.n_items = a.n_pairs * BH;
-    a.window = window;
-    a.sinks = sinks < N ? sinks : N;
-    // a scale of 0 makes all scores 0; the mask multiplies -inf by c, which has to stay -inf
-    a.c_log2 = c_log2 == 0.f ? 1e-30f : c_log2;
-    a.H = H;
-    a.H_kv = H_kv;
-    a.ctl = ctl;
-    const int grid = a.n_items < sms ? a.n_items : sms;
-    return static_cast<int>(
-        launch_pdl(win_fwd_kernel<D>, dim3(grid), dim3(kThreads), C::kSmemAlloc, s, tq, tk, tv, to, a));
-}
-
 }  // namespace
 
 int launch_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv, int N,
                       int d, float c_log2, int window, int sinks, DevCtl ctl, cudaStream_t s) {
-    if (d == 64) return launch_impl<64>(q, k, v, o, lse, B, H, H_kv, N, c_log2, window, sinks, ctl, s);
-    return launch_impl<128>(q, k, v, o, lse, B, H, H_kv, N, c_log2, window, sinks, ctl, s);
+    if (d == 64) return launch_fwd_window64(q, k, v, o, lse, B, H, H_kv, N, c_log2, window, sinks, ctl, s);
+    CUtensorMap m[4];
+    const int rc = win_maps(m, q, k, v, o, B, H, H_kv, N, 128);
+    if (rc != 0) return rc;
+    const WinArgs a = win_args(lse, B, H, H_kv, N, c_log2, window, sinks, ctl);
+    static std::atomic<uint64_t> smem_done;
+    int dev = 0, sms = 152;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = allow_smem(win_fwd_kernel, Cfg::kSmemAlloc, smem_done);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    return static_cast<int>(launch_pdl(win_fwd_kernel, dim3(a.n_items < sms ? a.n_items : sms), dim3(kThreads),
+                                       Cfg::kSmemAlloc, s, m[0], m[1], m[2], m[3], a));
 }
 
 }  // namespace fa
