@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = wq * 32 + lane;
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float2 c2 = make_float2(args.c_log2, args.c_log2);
+        const uint32_t hide = args.c_log2 >= 0.f ? 0xff800000u : 0x7f800000u;  // -inf after the multiply by c
         bool ok = true;
         int g = 0;
         // an item's row values, loaded one item ahead; padded rows exist up to Np
@@ -369,22 +370,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = I.block(j) * kBlk + 64 * half;
                 const int last = qrow - key0, sink = args.sinks - key0;
                 const int first = static_cast<int>(max(-1ll, static_cast<long long>(last) - args.window + 1));
-                const bool cut = last < 63 || (first > 0 && sink < 64);
-                uint32_t seen[2];
+                const bool edge = __any_sync(0xffffffffu, last < 63 || (first > 0 && sink < 64));
+                // a warp's rows are neighbours: of its two runs of 32 keys mostly one holds a bound of
+                // some row and needs the test of every score
+                if (edge) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
-                    seen[w] = bits_below(last + 1 - 32 * w) & (~bits_below(first - 32 * w) | bits_below(sink - 32 * w));
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t seen =
+                            bits_below(last + 1 - 32 * w) & (~bits_below(first - 32 * w) | bits_below(sink - 32 * w));
+                        if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen & (1u << i))) rs[w][i] = hide;
+                        }
+                    }
+                }
                 uint32_t pk[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int e = 2 * (i % 16);
                     const uint32_t* S = rs[i / 16];
                     const uint32_t* P = rp[i / 16];
-                    float2 a = __ffma2_rn(make_float2(__uint_as_float(S[e]), __uint_as_float(S[e + 1])), c2, nl2);
-                    if (cut) {
-                        if (!(seen[i / 16] & (1u << e))) a.x = -INFINITY;
-                        if (!(seen[i / 16] & (2u << e))) a.y = -INFINITY;
-                    }
+                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(S[e]), __uint_as_float(S[e + 1])), c2, nl2);
                     const float2 p = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                     const float2 d = __fadd2_rn(make_float2(__uint_as_float(P[e]), __uint_as_float(P[e + 1])), nd2);
                     const float2 ds = __fmul2_rn(p, d);
@@ -498,7 +505,7 @@ int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void
     a.H_kv = H_kv;
     a.window = sp.window;
     a.sinks = sp.sinks;
-    a.c_log2 = scale * 1.4426950408889634f;
+    a.c_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;  // not 0: the mask multiplies -inf by it
     a.scale = scale;
     a.ctl = ctl;
     // an ordinary launch: with programmatic serialization its CTAs would only sit waiting

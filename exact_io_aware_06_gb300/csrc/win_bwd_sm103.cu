@@ -555,6 +555,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
         const int key_in_blk = wq * 32 + lane;
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float2 c2 = make_float2(args.c_log2, args.c_log2);
+        const uint32_t hide = args.c_log2 >= 0.f ? 0xff800000u : 0x7f800000u;  // -inf after the multiply by c
         int epi_stage = -1;  // warp 4 lane 0: the ring stage whose dV/dK stores are in flight
         bool ok = true;
         int g = 0, kc = 0;
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
                 const int q_first = key - q_blk(I, i) * kBlk - 64 * half;
                 const int q_end = key < args.split.sinks
                     ? 64 : static_cast<int>(min(64ll, static_cast<long long>(q_first) + args.split.window));
-                const bool cut = q_first > 0 || q_end < 64;
+                const bool edge = __any_sync(0xffffffffu, q_first > 0 || q_end < 64);
                 ok = mbar_wait(smem_u32(&bars.q_full[s]), (gi / kQStages) & 1, lim, &abort_flag);
                 if (ok) ok = mbar_wait(smem_u32(&bars.s_full), gi & 1, lim, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -587,18 +588,25 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
                     tmem_wait_ld();
                     reg_fence(r[0]);
                     reg_fence(r[1]);
-                    const uint32_t seen[2] = {bits_below(q_end) & ~bits_below(q_first),
-                                              bits_below(q_end - 32) & ~bits_below(q_first - 32)};
+                    // a warp's keys are neighbours: of its two runs of 32 queries mostly one holds a
+                    // bound of some key and needs the test of every score
+                    if (edge) {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const uint32_t seen = bits_below(q_end - 32 * w) & ~bits_below(q_first - 32 * w);
+                            if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(seen & (1u << i))) r[w][i] = hide;
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int x2 = 0; x2 < 32; ++x2) {
                         const uint32_t* rr = r[x2 / 16];
                         const int e = 2 * (x2 % 16);
-                        float2 a = __ffma2_rn(make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])),
-                                              c2, L2[x2]);
-                        if (cut) {
-                            if (!(seen[x2 / 16] & (1u << e))) a.x = -INFINITY;
-                            if (!(seen[x2 / 16] & (2u << e))) a.y = -INFINITY;
-                        }
+                        const float2 a = __ffma2_rn(make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])),
+                                                    c2, L2[x2]);
                         const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
                         pk[x2] = pack_bf16x2(p0, p1);
                         ph[x2] = pack_f16x2(p0, p1);
@@ -1034,7 +1042,7 @@ int launch_bwd_impl(const void* q, const void* k, const void* v, const void* o, 
     a.H_kv = H_kv;
     a.split = sp;
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes(BH, N, D));
-    a.c_log2 = scale * kLog2e;
+    a.c_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;  // not 0: the mask multiplies -inf by it
     a.scale = scale;
     a.ctl = ctl;
     // persistent: one CTA per SM (fewer if there are fewer items), each looping over items.  An
