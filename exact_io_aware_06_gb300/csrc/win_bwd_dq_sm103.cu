@@ -1,10 +1,10 @@
-// win_bwd_dq_sm103.cu -- dQ of the windowed backward for d = 128, query-parallel, over the
+// win_bwd_dq_sm103.cu -- dQ of the windowed backward, query-parallel, over the
 // key blocks that a 128-query block sees, those of the sinks and those of the window:
 //     S_ij = Q_i K_j^T,  P_ij = exp(S_ij - lse_i),  dP_ij = dO_i V_j^T,
 //     dS_ij = P_ij o (dP_ij - delta_i),  dQ_i = scale * sum_j dS_ij K_j.
 // dQ_i accumulates in TMEM over the sweep and is written once as bf16: no atomics.
 //
-// Three products of 128 x 128 x 128 per pair of blocks, 24 MMAs: 1614 cycles of the tensor pipe.
+// Three products of 128 x 128 x d per pair of blocks, 24 MMAs at d = 128: 1614 cycles of the tensor pipe.
 // The plain backward's dQ kernel writes dS over S, so that the next scores wait for this block's
 // dS and dQ: 3850 cycles a pair.  Here:
 //   * dS has two TMEM buffers of its own, and the tensor core goes on with the next block's S
@@ -20,28 +20,24 @@
 // Warp 0 TMA, warps 1 and 2 MMA, warps 4-7 and 8-11 one query row per thread, for keys 0-63 /
 // 64-127 of block j, warps 12-15 write dQ.  TMEM: S 0-127, dP 128-255, dQ 256-383, dS (bf16)
 // 384-447 and 448-511.
-#include <cmath>
-
-#include "layer_ops.h"
-#include "ptx.cuh"
-#include "tma_host.h"
+#include "win_bwd.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kBlk = 128;
-constexpr int kD = 128;
 constexpr int kThreads = 512;
 constexpr int kKStages = 3, kVStages = 2;
-constexpr int kTile = kBlk * kD * 2;
-constexpr int kOffQ = 0, kOffDO = kTile, kOffK = 2 * kTile, kOffV = kOffK + kKStages * kTile;
-constexpr int kSmemBytes = kOffV + kVStages * kTile;
-constexpr int kSmemAlloc = kSmemBytes + 1024;
-static_assert(kSmemAlloc + 1024 <= 232448, "smem");
+template <int D>
+struct Cfg {
+    static constexpr int kTile = kBlk * D * 2;
+    static constexpr int kOffQ = 0, kOffDO = kTile, kOffK = 2 * kTile, kOffV = kOffK + kKStages * kTile;
+    static constexpr int kSmemAlloc = kOffV + kVStages * kTile + 1024;
+    static constexpr uint32_t kIdescDQ = idesc_bf16(128, D, false, true);  // dQ += dS K
+};
+static_assert(Cfg<128>::kSmemAlloc + 1024 <= 232448, "smem");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescSS = idesc_bf16(128, 128, false, false);  // S, dP
-constexpr uint32_t kIdescDQ = idesc_bf16(128, kD, false, true);    // dQ += dS K
 
 struct DqArgs {
     const float* ws_nlse2;   // [BH][Np]: -lse * log2(e) (-inf on pad rows)
@@ -64,48 +60,13 @@ struct DqBars {
     uint64_t drain, drain2;
 };
 
-__device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* abort_flag) {
-    *abort_flag = 1;
-    atomicCAS(ctl.status, kDevOk, kDevTimeout);
-}
-
-// Bits below n (all of them for n >= 32, none for n <= 0).
-__device__ __forceinline__ uint32_t bits_below(int n) {
-    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-// 16 TMEM lanes x 64 columns, lane 4 r + q of the warp holding columns 8 j + 2 q, + 1 of rows r
-// (x[4 j], x[4 j + 1]) and r + 8 (x[4 j + 2], x[4 j + 3]).
-__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&x)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
-          "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
-          "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
-          "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
-        : "r"(taddr)
-        : "memory");
-}
-// Lane q of every four holds word q of four 16-byte pieces; afterwards lane q holds piece q.
-__device__ __forceinline__ void transpose4(uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3, int q) {
-    const bool odd = q & 1, high = q & 2;
-    uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
-    (odd ? a0 : a1) = r;
-    r = __shfl_xor_sync(0xffffffffu, odd ? a2 : a3, 1);
-    (odd ? a2 : a3) = r;
-    r = __shfl_xor_sync(0xffffffffu, high ? a0 : a2, 2);
-    (high ? a0 : a2) = r;
-    r = __shfl_xor_sync(0xffffffffu, high ? a1 : a3, 2);
-    (high ? a1 : a3) = r;
-}
-
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     win_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                       const DqArgs args) {
+    using C = Cfg<D>;
+    constexpr int kTile = C::kTile, kOffQ = C::kOffQ, kOffDO = C::kOffDO, kOffK = C::kOffK, kOffV = C::kOffV;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) DqBars bars;
     __shared__ uint32_t tmem_slot;
@@ -115,16 +76,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int N = args.N, Np = args.Np;
     const uint64_t lim = args.ctl.wait_ns;
-    auto item_x = [&](int k) {
-        const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-        return k * G + ((k & 1) ? G - 1 - c : c);
-    };
-    struct Item {
+    struct QItem {
         int bh, bh_kv, qb, lo, n_sink, n_kv;
         __device__ __forceinline__ int block(int j) const { return j < n_sink ? j : lo + j - n_sink; }
     };
     auto item_at = [&](int x) {
-        Item I;
+        QItem I;
         I.bh = x % args.BH;
         I.qb = args.n_q - 1 - x / args.BH;
         // grouped-query attention: query head bh reads K/V head bh_kv of its group
@@ -186,13 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int gk = 0, gv = 0;
                 bool ok = true;
                 for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k)) {
-                    const Item I = item_at(x);
+                    const QItem I = item_at(x);
                     if (n > 0 && !mbar_wait(smem_u32(&bars.q_free), (n - 1) & 1, lim, &abort_flag)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(qf, 2 * kTile);
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < D / 64; ++c) {
                         tma_load_3d(sb + kOffQ + c * 16384, &tm_q, qf, 64 * c, I.qb * kBlk, I.bh);
                         tma_load_3d(sb + kOffDO + c * 16384, &tm_do, qf, 64 * c, I.qb * kBlk, I.bh);
                     }
@@ -207,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const uint32_t vf = smem_u32(&bars.v_full[sv]);
                         mbar_arrive_expect_tx(vf, kTile);
-                        for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < D / 64; ++c)
                             tma_load_3d(sb + kOffV + sv * kTile + c * 16384, &tm_v, vf, 64 * c, row, I.bh_kv);
                         gv = g + 1;
                         if (g >= kKStages &&
@@ -217,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const uint32_t kf = smem_u32(&bars.k_full[sk]);
                         mbar_arrive_expect_tx(kf, kTile);
-                        for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < D / 64; ++c)
                             tma_load_3d(sb + kOffK + sk * kTile + c * 16384, &tm_k, kf, 64 * c, row, I.bh_kv);
                         gk = g + 1;
                     }
@@ -248,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint32_t kl = k_lo + sk * kStage16, vl = v_lo + sv * kStage16;
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk) {
+                    for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off16 = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                         if (kk == 0)
                             mma_ss_w<false, -1>(tmem + kColS, q_lo, kl, kDescHi, kIdescSS, 0u);
@@ -256,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_ss_w<false, 1>(tmem + kColS, q_lo + off16, kl + off16, kDescHi, kIdescSS);
                     }
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk) {
+                    for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off16 = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                         if (kk == 0)
                             mma_ss_w<false, -1>(tmem + kColDP, do_lo, vl, kDescHi, kIdescSS, 0u);
@@ -303,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kBlk / 16; ++kk) {
                             if (kk == 0)
-                                mma_ts_w<false, -1>(tmem + kColDQ, ds, km, kDescHi, kIdescDQ, j > 0 ? 1u : 0u);
+                                mma_ts_w<false, -1>(tmem + kColDQ, ds, km, kDescHi, C::kIdescDQ, j > 0 ? 1u : 0u);
                             else
-                                mma_ts_w<false, 1>(tmem + kColDQ, ds + 8 * kk, km + 128 * kk, kDescHi, kIdescDQ);
+                                mma_ts_w<false, 1>(tmem + kColDQ, ds + 8 * kk, km + 128 * kk, kDescHi, C::kIdescDQ);
                         }
                         mma_commit(smem_u32(&bars.ds_empty[g & 1]));
                         mma_commit(smem_u32(&bars.k_empty[sk]));  // S of this pair read K before dS was made
@@ -332,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int g = 0;
         // an item's row values, loaded one item ahead; padded rows exist up to Np
         auto row_at = [&](int x) {
-            const Item I = item_at(x);
+            const QItem I = item_at(x);
             return static_cast<size_t>(I.bh) * Np + I.qb * kBlk + row;
         };
         float next_nl = 0.f, next_nd = 0.f;
@@ -341,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             next_nd = args.ws_ndelta[row_at(item_x(0))];
         }
         for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k)) {
-            const Item I = item_at(x);
+            const QItem I = item_at(x);
             const int qrow = I.qb * kBlk + row;
             const float nl = next_nl, nd = next_nd;
             if (item_x(k + 1) < args.n_items) {
@@ -415,52 +372,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================================================================ dQ out
         const int wq = warp % 4;
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-        const float sc = args.scale;
         bool ok = true;
         int item = 0;
         for (int k = 0, x = item_x(0); x < args.n_items; x = item_x(++k), ++item) {
-            const Item I = item_at(x);
+            const QItem I = item_at(x);
             ok = mbar_wait(smem_u32(&bars.all_done), item & 1, lim, &abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            // dQ = scale * accumulator as bf16 pairs: rows 16 m + r and 16 m + 8 + r, columns 64 c +
-            // 8 j + 2 q.  (One row per lane, 32 lines a store instruction, kept the dS warps' next
-            // TMEM loads waiting for 2300 cycles behind the stores; here it is 8 lines.)
-            const int r8 = lane / 4, q = lane % 4;
-            uint32_t w[2][2][2][8];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t x[32];
-                    tmem_ld_rows16(lb + (static_cast<uint32_t>(16 * m) << 16) + kColDQ + 64 * c, x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            w[m][c][h][j] = pack_bf16x2(__uint_as_float(x[4 * j + 2 * h]) * sc,
-                                                        __uint_as_float(x[4 * j + 2 * h + 1]) * sc);
-                }
+            RowsOut<D> rows;
+            rows.load(lb + kColDQ, args.scale);
             tc_fence_before();
             mbar_arrive(smem_u32(&bars.dq_read));
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int qrow = I.qb * kBlk + wq * 32 + 16 * m + 8 * h + r8;
-                    uint16_t* out = static_cast<uint16_t*>(args.dq) + (static_cast<size_t>(I.bh) * N + qrow) * kD;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int j = 0; j < 8; j += 4) {
-                            uint32_t(&p)[8] = w[m][c][h];
-                            transpose4(p[j], p[j + 1], p[j + 2], p[j + 3], q);  // columns 64 c + 8 (j + q) ..
-                            if (qrow < N)
-                                *reinterpret_cast<uint4*>(out + 64 * c + 8 * (j + q)) =
-                                    make_uint4(p[j], p[j + 1], p[j + 2], p[j + 3]);
-                        }
-                }
+            rows.store(args.dq, static_cast<size_t>(I.bh) * N, I.qb * kBlk + wq * 32, N);
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
     }
@@ -473,21 +397,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-}  // namespace
-
-int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2,
-                         const float* ws_ndelta, void* dq, int B, int H, int H_kv, int N, float scale,
-                         const WinSplit& sp, DevCtl ctl, cudaStream_t s) {
+template <int D>
+int launch_impl(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2, const float* ws_ndelta,
+                void* dq, int B, int H, int H_kv, int N, float scale, const WinSplit& sp, DevCtl ctl, cudaStream_t s) {
     const int BH = B * H, BH_kv = B * H_kv;
     CUtensorMap tq, tk, tv, tdo;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    int rc = make_map_3d(&tq, q, dt, 2, kD, N, BH, 64, kBlk);
-    if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, kD, N, BH_kv, 64, kBlk);
-    if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, kD, N, BH_kv, 64, kBlk);
-    if (rc == 0) rc = make_map_3d(&tdo, dO, dt, 2, kD, N, BH, 64, kBlk);
+    int rc = make_map_3d(&tq, q, dt, 2, D, N, BH, 64, kBlk);
+    if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, N, BH_kv, 64, kBlk);
+    if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, N, BH_kv, 64, kBlk);
+    if (rc == 0) rc = make_map_3d(&tdo, dO, dt, 2, D, N, BH, 64, kBlk);
     if (rc != 0) return rc;
     static std::atomic<uint64_t> smem_done;
-    cudaError_t e = allow_smem(win_bwd_dq_kernel, kSmemAlloc, smem_done);
+    cudaError_t e = allow_smem(win_bwd_dq_kernel<D>, Cfg<D>::kSmemAlloc, smem_done);
     int dev = 0, sms = 152;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -510,8 +432,18 @@ int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void
     a.ctl = ctl;
     // an ordinary launch: with programmatic serialization its CTAs would only sit waiting
     // through the tail of the dK/dV kernel
-    win_bwd_dq_kernel<<<a.n_items < sms ? a.n_items : sms, kThreads, kSmemAlloc, s>>>(tq, tk, tv, tdo, a);
+    win_bwd_dq_kernel<D><<<a.n_items < sms ? a.n_items : sms, kThreads, Cfg<D>::kSmemAlloc, s>>>(tq, tk, tv, tdo, a);
     return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2,
+                         const float* ws_ndelta, void* dq, int B, int H, int H_kv, int N, int d, float scale,
+                         const WinSplit& sp, DevCtl ctl, cudaStream_t s) {
+    return d == 64
+               ? launch_impl<64>(q, k, v, dO, ws_nlse2, ws_ndelta, dq, B, H, H_kv, N, scale, sp, ctl, s)
+               : launch_impl<128>(q, k, v, dO, ws_nlse2, ws_ndelta, dq, B, H, H_kv, N, scale, sp, ctl, s);
 }
 
 }  // namespace fa

@@ -148,20 +148,17 @@ __device__ __forceinline__ bool softmax_block(uint32_t lane_base, uint32_t colS,
     tmem_wait_ld();
     reg_fence(r);
     taken();
-    // Keys hi and below, of those the ones from lo on or below `sink`, counted in the block.  A
-    // warp's rows are neighbours, so of its four runs of 32 keys one or two hold a bound of some
-    // row and need the test of every score.  (Tested all over, a block with a bound took 800
-    // cycles more than one without.  Leaving out the exponentials of runs that no row sees was
-    // slower: the branches around them kept the compiler from interleaving the runs.)
-    if (__any_sync(0xffffffffu, hi < NC - 1 || (lo > 0 && sink < NC))) {
+    // Keys hi and below, of those the ones from lo on or below `sink`, counted in the block.  (Tests
+    // for the runs of 32 keys that hold a bound only, and no exponentials where no row of the warp
+    // sees a key, were both slower, by 1.5% and 25%: branches among the runs keep the compiler from
+    // interleaving them.)
+    if (hi < NC - 1 || (lo > 0 && sink < NC)) {
 #pragma unroll
         for (int w = 0; w < NC / 32; ++w) {
             const uint32_t seen = bits_below(hi + 1 - 32 * w) & (~bits_below(lo - 32 * w) | bits_below(sink - 32 * w));
-            if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (!(seen & (1u << i))) r[32 * w + i] = mask_bits;
-            }
+            for (int i = 0; i < 32; ++i)
+                if (!(seen & (1u << i))) r[32 * w + i] = mask_bits;
         }
     }
     const float mt = c * extreme(r, c_pos);

@@ -362,8 +362,7 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
  *   dq          : [B][H][N][d];  dk, dv : [B][H_kv][N][d] bfloat16, written.
  *   workspace   : at least fa_bwd_window_workspace_size() bytes; its contents on entry do not
  *                 matter.  Calls that overlap in time must not share one.
- * dk and dv (and at d = 128 dq) have the same bits every time; at d = 64 dq is summed with
- * float32 atomics in the workspace, in the order in which key blocks finish, as in fa_bwd.
+ * Nothing is summed by atomics: the same bits every time.
  * Errors: as fa_fwd_window; FA_ERR_INVALID_ARG also for a null lse and a workspace that is
  * too small.
  */

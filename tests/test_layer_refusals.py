@@ -90,9 +90,9 @@ def test_window_backward_refusals(L, change, status):
 
 
 def test_window_workspace(L):
-    # delta, lse and the dQ accumulator as the plain backward's; nothing more without sinks, or
-    # where the window covers the sequence; a sink block's parts otherwise
-    rows = fa.fa_bwd_workspace_size(2, 4, 4096, 64)
+    # delta and lse; nothing more without sinks, or where the window covers the sequence; a sink
+    # block's parts otherwise
+    rows = 2 * 2 * 4 * 4096 * 4
     size = fa.fa_bwd_window_workspace_size
     assert size(2, 4, 2, 4096, 64, 512, 0) == rows
     assert size(2, 4, 2, 4096, 64, 4096, 100) == rows
