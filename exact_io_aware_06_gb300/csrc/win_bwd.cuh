@@ -90,15 +90,16 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// P^T of this thread's key and 64 queries from their raw scores: as bf16 pairs for dV, and as fp16
-// pairs for dS.  The key's queries are q_first .. q_end - 1, counted from the first of the 64.
-__device__ __forceinline__ void probabilities(uint32_t (&r)[2][32], int q_first, int q_end, uint32_t hide, float2 c2,
-                                              const float2* L2, uint32_t (&pk)[32], uint32_t (&ph)[32]) {
-    // a warp's keys are neighbours: of its two runs of 32 queries mostly one holds a bound of some
-    // key and needs the test of every score
-    if (__any_sync(0xffffffffu, q_first > 0 || q_end < 64)) {
+// P^T of this thread's key and a run of 32 NW queries from their raw scores: as bf16 pairs for dV, and
+// as fp16 pairs for dS.  The key's queries are q_first .. q_end - 1, counted from the first of the run.
+template <int NW>
+__device__ __forceinline__ void probabilities(uint32_t (&r)[NW][32], int q_first, int q_end, uint32_t hide, float2 c2,
+                                              const float2* L2, uint32_t (&pk)[16 * NW], uint32_t (&ph)[16 * NW]) {
+    // a warp's keys are neighbours: of two runs of 32 queries mostly one holds a bound of some key
+    // and needs the test of every score
+    if (__any_sync(0xffffffffu, q_first > 0 || q_end < 32 * NW)) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const uint32_t seen = bits_below(q_end - 32 * w) & ~bits_below(q_first - 32 * w);
             if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
@@ -108,7 +109,7 @@ __device__ __forceinline__ void probabilities(uint32_t (&r)[2][32], int q_first,
         }
     }
 #pragma unroll
-    for (int x = 0; x < 32; ++x) {
+    for (int x = 0; x < 16 * NW; ++x) {
         const uint32_t* rr = r[x / 16];
         const int e = 2 * (x % 16);
         const float2 a = __ffma2_rn(make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), c2, L2[x]);
@@ -117,11 +118,10 @@ __device__ __forceinline__ void probabilities(uint32_t (&r)[2][32], int q_first,
         ph[x] = pack_f16x2(p0, p1);
     }
 }
-// A key's queries of a 64-query half that starts at query q0: from the key on, a window's worth, or
-// all for a sink.
+// A key's queries counted from query q0: from the key on, a window's worth, or all for a sink.
 __device__ __forceinline__ void query_range(const WinSplit& sp, int key, int q0, int& q_first, int& q_end) {
     q_first = key - q0;
-    q_end = key < sp.sinks ? 64 : static_cast<int>(min(64ll, static_cast<long long>(q_first) + sp.window));
+    q_end = key < sp.sinks ? kBlk : static_cast<int>(min(static_cast<long long>(kBlk), static_cast<long long>(q_first) + sp.window));
 }
 
 // 16 TMEM lanes x 64 columns, lane 4 r + q of the warp holding columns 8 j + 2 q, + 1 of rows r

@@ -15,15 +15,19 @@
 //     as float32 parts to the workspace; the next item's MMAs wait for its TMEM loads only.
 //   * K and V have two buffers, for the next item's loads.
 //
-// Warp 0 TMA for Q, dO, lse, delta (three stages), warp 3 TMA for K, V, warps 1 and 2 MMA, warps 4-7
-// and 8-11 P and dS (thread = key, for queries 0-63 / 64-127), warps 12-15 dV and dK out.
+//   * Four warpgroups on P and dS, 32 queries each: two of 64 took 2450 cycles a pair at half of the
+//     issue slots and exponentials that they could have had.
+//
+// Warp 0 TMA for Q, dO, lse, delta (three stages), warp 3 TMA for K, V, warps 1 and 2 MMA, warps 4-19 P
+// and dS (thread = key), warps 20-23 dV and dK out.
 #include "win_bwd.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kD = 64;
-constexpr int kThreads = 512;
+constexpr int kPdsThreads = 512;
+constexpr int kThreads = 256 + kPdsThreads;
 constexpr int kQStages = 3;
 constexpr int kTile = kBlk * kD * 2;
 constexpr int kOffK = 0, kOffV = 2 * kTile, kOffQ = 4 * kTile, kOffDO = kOffQ + kQStages * kTile;
@@ -86,12 +90,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars.q_empty[s]), 1);
         }
         mbar_init(smem_u32(&bars.s_full), 1);
-        mbar_init(smem_u32(&bars.s_free), 256);
+        mbar_init(smem_u32(&bars.s_free), kPdsThreads);
         mbar_init(smem_u32(&bars.dp_full), 1);
-        mbar_init(smem_u32(&bars.dp_free), 256);
-        mbar_init(smem_u32(&bars.p_full), 256);
+        mbar_init(smem_u32(&bars.dp_free), kPdsThreads);
+        mbar_init(smem_u32(&bars.p_full), kPdsThreads);
         mbar_init(smem_u32(&bars.p_empty), 1);
-        mbar_init(smem_u32(&bars.ds_full), 256);
+        mbar_init(smem_u32(&bars.ds_full), kPdsThreads);
         mbar_init(smem_u32(&bars.ds_empty), 1);
         mbar_init(smem_u32(&bars.all_done), 1);
         mbar_init(smem_u32(&bars.acc_read), 128);
@@ -116,9 +120,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    // 512 threads x 128 registers at launch: 72 + 2 * 160 + 120 = 4 * 128
+    // 768 threads x 80 registers at launch: 40 + 4 * 88 + 88 = 6 * 80
     if (warp < 4) {
-        regs_dec<72>();
+        regs_dec<40>();
         if (warp == 0) {
             // ============================================================ Q / dO producer
             if (lane == 0) {
@@ -278,10 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(smem_u32(&bars.drain2), 0, kDrainWaitNs, &never);
             }
         }
-    } else if (warp < 12) {
-        regs_inc<160>();
+    } else if (warp < 20) {
+        regs_inc<88>();
         // ================================================================ P / dS warpgroups
-        const int half = (warp - 4) / 4;          // queries 64*half .. 64*half+63
+        // (runs of 32 queries)
+        const int part = (warp - 4) / 4;          // queries 32*part .. 32*part+31
         const int wq = warp % 4;
         const int key_in_blk = wq * 32 + lane;
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -295,23 +300,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < I.n_it; ++i, ++g) {
                 const int s = g % kQStages;
                 int q_first, q_end;
-                query_range(args.split, key, q_blk(I, i) * kBlk + 64 * half, q_first, q_end);
+                query_range(args.split, key, q_blk(I, i) * kBlk + 32 * part, q_first, q_end);
                 ok = mbar_wait(smem_u32(&bars.q_full[s]), (g / kQStages) & 1, lim, &abort_flag);
                 if (ok) ok = mbar_wait(smem_u32(&bars.s_full), g & 1, lim, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                // -lse_i * log2(e) and -delta_i of this block's 64 queries
-                const float2* L2 = reinterpret_cast<const float2*>(sb_ptr + kOffL + s * kBlk * 4) + 32 * half;
-                const float2* D2 = reinterpret_cast<const float2*>(sb_ptr + kOffDelta + s * kBlk * 4) + 32 * half;
-                uint32_t ph[32];
+                // -lse_i * log2(e) and -delta_i of these queries
+                const float2* L2 = reinterpret_cast<const float2*>(sb_ptr + kOffL + s * kBlk * 4) + 16 * part;
+                const float2* D2 = reinterpret_cast<const float2*>(sb_ptr + kOffDelta + s * kBlk * 4) + 16 * part;
+                uint32_t ph[16];
                 {
-                    uint32_t r[2][32], pk[32];
-                    tmem_ld32_async(lb + kColS + 64 * half, r[0]);
-                    tmem_ld32_async(lb + kColS + 64 * half + 32, r[1]);
+                    uint32_t r[1][32], pk[16];
+                    tmem_ld32_async(lb + kColS + 32 * part, r[0]);
                     tmem_wait_ld();
                     reg_fence(r[0]);
-                    reg_fence(r[1]);
                     tc_fence_before();
                     mbar_arrive(smem_u32(&bars.s_free));
                     probabilities(r, q_first, q_end, hide, c2, L2, pk, ph);
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    tmem_st32(lb + kColP + 32 * half, pk);
+                    tmem_st16(lb + kColP + 16 * part, pk);
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(smem_u32(&bars.p_full));
@@ -331,20 +334,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t r[2][32];
-                tmem_ld32_async(lb + kColDP + 64 * half, r[0]);
-                tmem_ld32_async(lb + kColDP + 64 * half + 32, r[1]);
+                uint32_t r[32];
+                tmem_ld32_async(lb + kColDP + 32 * part, r);
                 tmem_wait_ld();
-                reg_fence(r[0]);
-                reg_fence(r[1]);
+                reg_fence(r);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.dp_free));
-                uint32_t w[32];
+                uint32_t w[16];
 #pragma unroll
-                for (int x2 = 0; x2 < 32; ++x2) {
-                    const uint32_t* rr = r[x2 / 16];
-                    const int e = 2 * (x2 % 16);
-                    const float2 gg = __fadd2_rn(make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), D2[x2]);
+                for (int x2 = 0; x2 < 16; ++x2) {
+                    const float2 gg =
+                        __fadd2_rn(make_float2(__uint_as_float(r[2 * x2]), __uint_as_float(r[2 * x2 + 1])), D2[x2]);
                     const float2 ds = __fmul2_rn(unpack_f16x2(ph[x2]), gg);
                     w[x2] = pack_bf16x2(ds.x, ds.y);
                 }
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                 }
-                tmem_st32(lb + kColDS + 32 * half, w);
+                tmem_st16(lb + kColDS + 16 * part, w);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.ds_full));
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
     } else {
-        regs_dec<120>();
+        regs_inc<88>();
         // ================================================================ dV, dK out
         const int wq = warp % 4;
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -384,32 +384,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&bars.acc_read));
                 continue;
             }
-            uint32_t w[2][32];  // this lane's row of dV and of dK times scale, as bf16 pairs
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float f = m ? args.scale : 1.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t r[32];
-                    tmem_ld32(lb + (m ? kColDK : kColDV) + 32 * h, r);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        w[m][16 * h + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
-                }
-            }
-            tc_fence_before();
-            mbar_arrive(smem_u32(&bars.acc_read));
             // 128-byte rows, 16-byte granule g of row r at g ^ (r % 8); the last item's stores have
             // read them
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m) {  // dV; dK times scale
+                const float f = m ? args.scale : 1.f;
 #pragma unroll
-                for (int gr = 0; gr < 8; ++gr)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + m * 4096 + lane * 128 + ((gr ^ (lane & 7)) << 4)),
-                                 "r"(w[m][4 * gr]), "r"(w[m][4 * gr + 1]), "r"(w[m][4 * gr + 2]), "r"(w[m][4 * gr + 3])
-                                 : "memory");
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+                    tmem_ld32(lb + (m ? kColDK : kColDV) + 32 * h, r);
+                    if (m == 1 && h == 1) {
+                        tc_fence_before();
+                        mbar_arrive(smem_u32(&bars.acc_read));
+                    }
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        const float* x = reinterpret_cast<const float*>(r) + 8 * c4;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + m * 4096 + lane * 128 +
+                                                                                      (((4 * h + c4) ^ (lane & 7)) << 4)),
+                                     "r"(pack_bf16x2(x[0] * f, x[1] * f)), "r"(pack_bf16x2(x[2] * f, x[3] * f)),
+                                     "r"(pack_bf16x2(x[4] * f, x[5] * f)), "r"(pack_bf16x2(x[6] * f, x[7] * f))
+                                     : "memory");
+                    }
+                }
+            }
             fence_proxy_async_smem();
             __syncwarp();
             const int row0 = I.kvb * kBlk + wq * 32;
