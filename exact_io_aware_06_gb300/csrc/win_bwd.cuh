@@ -3,8 +3,6 @@
 
 #include <cmath>
 
-#include <cuda_fp16.h>
-
 #include "layer_ops.h"
 #include "ptx.cuh"
 #include "tma_host.h"
@@ -62,10 +60,17 @@ __device__ __forceinline__ Item item_at(const BwdArgs& a, int x) {
     I.n_it = a.H / a.H_kv * I.n_loc;
     return I;
 }
-__device__ __forceinline__ int q_head(const BwdArgs& a, const Item& I, int it) {
-    return (I.bh / a.H_kv) * a.H + (I.bh % a.H_kv) * (a.H / a.H_kv) + it / I.n_loc;
-}
-__device__ __forceinline__ int q_blk(const Item& I, int it) { return I.i0 + it % I.n_loc; }
+// The query blocks of an item one after the other, without a division a step.
+struct Walk {
+    int head, blk, end, i0;
+    __device__ __forceinline__ Walk(const BwdArgs& a, const Item& I) : head((I.bh / a.H_kv) * a.H + (I.bh % a.H_kv) * (a.H / a.H_kv)), blk(I.i0), end(I.i0 + I.n_loc), i0(I.i0) {}
+    __device__ __forceinline__ void next() {
+        if (++blk == end) {
+            blk = i0;
+            ++head;
+        }
+    }
+};
 // This CTA's k-th item, dealt in alternating order.
 __device__ __forceinline__ int item_x(int k) {
     const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
@@ -81,20 +86,12 @@ __device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* 
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-// P^T of this thread's key and a run of 32 NW queries from their raw scores: as bf16 pairs for dV, and
-// as fp16 pairs for dS.  The key's queries are q_first .. q_end - 1, counted from the first of the run.
+// P^T of this thread's key and a run of 32 NW queries from their raw scores, in their place, and as
+// bf16 pairs for dV.  The key's queries are q_first .. q_end - 1, counted from the first of the run;
+// nl: -lse log2(e) of the queries.
 template <int NW>
 __device__ __forceinline__ void probabilities(uint32_t (&r)[NW][32], int q_first, int q_end, uint32_t hide, float2 c2,
-                                              const float2* L2, uint32_t (&pk)[16 * NW], uint32_t (&ph)[16 * NW]) {
+                                              const float4* nl, uint32_t (&pk)[16 * NW]) {
     // a warp's keys are neighbours: of two runs of 32 queries mostly one holds a bound of some key
     // and needs the test of every score
     if (__any_sync(0xffffffffu, q_first > 0 || q_end < 32 * NW)) {
@@ -109,13 +106,34 @@ __device__ __forceinline__ void probabilities(uint32_t (&r)[NW][32], int q_first
         }
     }
 #pragma unroll
-    for (int x = 0; x < 16 * NW; ++x) {
-        const uint32_t* rr = r[x / 16];
-        const int e = 2 * (x % 16);
-        const float2 a = __ffma2_rn(make_float2(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])), c2, L2[x]);
-        const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y);
-        pk[x] = pack_bf16x2(p0, p1);
-        ph[x] = pack_f16x2(p0, p1);
+    for (int x = 0; x < 8 * NW; ++x) {
+        uint32_t* rr = &r[x / 8][4 * (x % 8)];
+        const float4 l = nl[x];
+        const float2 a = __ffma2_rn(make_float2(__uint_as_float(rr[0]), __uint_as_float(rr[1])), c2, make_float2(l.x, l.y));
+        const float2 b = __ffma2_rn(make_float2(__uint_as_float(rr[2]), __uint_as_float(rr[3])), c2, make_float2(l.z, l.w));
+        const float p0 = ex2_approx(a.x), p1 = ex2_approx(a.y), p2 = ex2_approx(b.x), p3 = ex2_approx(b.y);
+        pk[2 * x] = pack_bf16x2(p0, p1);
+        pk[2 * x + 1] = pack_bf16x2(p2, p3);
+        rr[0] = __float_as_uint(p0);
+        rr[1] = __float_as_uint(p1);
+        rr[2] = __float_as_uint(p2);
+        rr[3] = __float_as_uint(p3);
+    }
+}
+// dS^T = P^T o (dP^T - delta) of 32 queries as bf16 pairs; nd: -delta.
+__device__ __forceinline__ void score_gradients(const uint32_t (&p)[32], const uint32_t (&dp)[32], const float4* nd,
+                                                uint32_t (&w)[16]) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const float4 d = nd[x];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int e = 4 * x + 2 * y;
+            const float2 g = __fadd2_rn(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
+                                        y ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
+            const float2 ds = __fmul2_rn(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), g);
+            w[2 * x + y] = pack_bf16x2(ds.x, ds.y);
+        }
     }
 }
 // A key's queries counted from query q0: from the key on, a window's worth, or all for a sink.

@@ -130,9 +130,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                     const Item I = item_at(args, x);
-                    for (int i = 0; i < I.n_it; ++i, ++g) {
+                    Walk at(args, I);
+                    for (int i = 0; i < I.n_it; ++i, ++g, at.next()) {
                         const int s = g % kQStages;
-                        const int qb = q_blk(I, i), qh = q_head(args, I, i);
+                        const int qb = at.blk, qh = at.head;
                         if (g >= kQStages &&
                             !mbar_wait(smem_u32(&bars.q_empty[s]), ((g / kQStages) & 1) ^ 1, lim, &abort_flag)) {
                             ok = false;
@@ -297,27 +298,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
             const Item I = item_at(args, x);
             const int key = I.kvb * kBlk + key_in_blk;
-            for (int i = 0; i < I.n_it; ++i, ++g) {
+            Walk at(args, I);
+            for (int i = 0; i < I.n_it; ++i, ++g, at.next()) {
                 const int s = g % kQStages;
                 int q_first, q_end;
-                query_range(args.split, key, q_blk(I, i) * kBlk + 32 * part, q_first, q_end);
+                query_range(args.split, key, at.blk * kBlk + 32 * part, q_first, q_end);
                 ok = mbar_wait(smem_u32(&bars.q_full[s]), (g / kQStages) & 1, lim, &abort_flag);
                 if (ok) ok = mbar_wait(smem_u32(&bars.s_full), g & 1, lim, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 // -lse_i * log2(e) and -delta_i of these queries
-                const float2* L2 = reinterpret_cast<const float2*>(sb_ptr + kOffL + s * kBlk * 4) + 16 * part;
-                const float2* D2 = reinterpret_cast<const float2*>(sb_ptr + kOffDelta + s * kBlk * 4) + 16 * part;
-                uint32_t ph[16];
+                const float4* nl = reinterpret_cast<const float4*>(sb_ptr + kOffL + s * kBlk * 4) + 8 * part;
+                const float4* nd = reinterpret_cast<const float4*>(sb_ptr + kOffDelta + s * kBlk * 4) + 8 * part;
+                uint32_t p[1][32];  // scores, then P^T
                 {
-                    uint32_t r[1][32], pk[16];
-                    tmem_ld32_async(lb + kColS + 32 * part, r[0]);
+                    uint32_t pk[16];
+                    tmem_ld32_async(lb + kColS + 32 * part, p[0]);
                     tmem_wait_ld();
-                    reg_fence(r[0]);
+                    reg_fence(p[0]);
                     tc_fence_before();
                     mbar_arrive(smem_u32(&bars.s_free));
-                    probabilities(r, q_first, q_end, hide, c2, L2, pk, ph);
+                    probabilities(p, q_first, q_end, hide, c2, nl, pk);
                     if (g > 0) {  // dV of the last pair has read P^T
                         ok = mbar_wait(smem_u32(&bars.p_empty), (g - 1) & 1, lim, &abort_flag);
                         ok = __all_sync(0xffffffffu, ok);
@@ -341,13 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.dp_free));
                 uint32_t w[16];
-#pragma unroll
-                for (int x2 = 0; x2 < 16; ++x2) {
-                    const float2 gg =
-                        __fadd2_rn(make_float2(__uint_as_float(r[2 * x2]), __uint_as_float(r[2 * x2 + 1])), D2[x2]);
-                    const float2 ds = __fmul2_rn(unpack_f16x2(ph[x2]), gg);
-                    w[x2] = pack_bf16x2(ds.x, ds.y);
-                }
+                score_gradients(p[0], r, nd, w);
                 if (g > 0) {  // dK of the last pair has read dS^T
                     ok = mbar_wait(smem_u32(&bars.ds_empty), (g - 1) & 1, lim, &abort_flag);
                     ok = __all_sync(0xffffffffu, ok);

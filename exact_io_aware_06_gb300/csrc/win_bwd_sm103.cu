@@ -22,9 +22,8 @@
 //     in order and rounds once.
 //   * The visible queries of a key row are a range; blocks that hold its ends take them as
 //     bit words made by shifts.
-//   * dS is taken from P before its rounding to bf16 (kept in fp16, whose 2^-12 of a value
-//     below 1 is small against the bf16 rounding of dS itself): with P rounded first, dQ and
-//     dK carried two bf16 roundings before their own.
+//   * dS is taken from P before its rounding to bf16: with P rounded first, dQ and dK carried two
+//     bf16 roundings before their own.
 //
 // The d = 128 main kernel: S^T, dP^T, dV and dK fill TMEM, P^T and dS^T are written over S^T and
 // dP^T, and roles, ring and the order of MMAs are the plain backward's.
@@ -122,9 +121,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                 const Item I = item_at(args, x);
-                for (int i = 0; i < I.n_it; ++i, ++g) {
+                Walk at(args, I);
+                for (int i = 0; i < I.n_it; ++i, ++g, at.next()) {
                     const int s = g % kQStages;
-                    const int qb = q_blk(I, i), qh = q_head(args, I, i);
+                    const int qb = at.blk, qh = at.head;
                     if (g >= kQStages &&
                         !mbar_wait(smem_u32(&bars.q_empty[s]), ((g / kQStages) & 1) ^ 1, lim, &abort_flag)) {
                         ok = false;
@@ -294,28 +294,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item I = item_at(args, x);
             if (I.n_it == 0) continue;
             const int key = I.kvb * kBlk + key_in_blk;
-            for (int i = 0; i < I.n_it; ++i) {
+            Walk at(args, I);
+            for (int i = 0; i < I.n_it; ++i, at.next()) {
                 const int gi = g + i, s = gi % kQStages;
                 int q_first, q_end;
-                query_range(args.split, key, q_blk(I, i) * kBlk + 64 * half, q_first, q_end);
+                query_range(args.split, key, at.blk * kBlk + 64 * half, q_first, q_end);
                 ok = mbar_wait(smem_u32(&bars.q_full[s]), (gi / kQStages) & 1, lim, &abort_flag);
                 if (ok) ok = mbar_wait(smem_u32(&bars.s_full), gi & 1, lim, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 // -lse_i * log2(e) and -delta_i of this block's 64 queries
-                const float2* L2 = reinterpret_cast<const float2*>(sb_ptr + kOffL + s * kBlk * 4) + 32 * half;
-                const float2* D2 = reinterpret_cast<const float2*>(sb_ptr + kOffDelta + s * kBlk * 4) + 32 * half;
-                uint32_t pk[32], ph[32];
-                {
-                    uint32_t r[2][32];
-                    tmem_ld32_async(lb + kColS + 64 * half, r[0]);
-                    tmem_ld32_async(lb + kColS + 64 * half + 32, r[1]);
-                    tmem_wait_ld();
-                    reg_fence(r[0]);
-                    reg_fence(r[1]);
-                    probabilities(r, q_first, q_end, hide, c2, L2, pk, ph);
-                }
+                const float4* nl = reinterpret_cast<const float4*>(sb_ptr + kOffL + s * kBlk * 4) + 16 * half;
+                const float4* nd = reinterpret_cast<const float4*>(sb_ptr + kOffDelta + s * kBlk * 4) + 16 * half;
+                uint32_t p[2][32], pk[32];  // scores, then P^T
+                tmem_ld32_async(lb + kColS + 64 * half, p[0]);
+                tmem_ld32_async(lb + kColS + 64 * half + 32, p[1]);
+                tmem_wait_ld();
+                reg_fence(p[0]);
+                reg_fence(p[1]);
+                probabilities(p, q_first, q_end, hide, c2, nl, pk);
                 // P^T of this half goes inside the columns this half read (the other half's
                 // scores may still be unread): queries 64h..64h+63 -> columns 64h..64h+31
                 tmem_st32(lb + kColS + 64 * half, pk);
@@ -336,14 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t w[16];
-#pragma unroll
-                    for (int x2 = 0; x2 < 16; ++x2) {
-                        const float2 p = unpack_f16x2(ph[16 * h + x2]);
-                        const float2 gg = __fadd2_rn(make_float2(__uint_as_float(r[2 * x2]), __uint_as_float(r[2 * x2 + 1])),
-                                                     D2[16 * h + x2]);
-                        const float2 ds = __fmul2_rn(p, gg);
-                        w[x2] = pack_bf16x2(ds.x, ds.y);
-                    }
+                    score_gradients(p[h], r, nd + 8 * h, w);
                     if (h == 0) tmem_ld32_async(lb + kColDP + 64 * half + 32, r);
                     tmem_st16(lb + kColDP + 64 * half + 16 * h, w);
                     if (h == 0) {
