@@ -45,6 +45,45 @@ def check(got, ref, amplitude, t, what):
     assert (err <= tol).all(), (what, float((err / np.maximum(tol, 1e-300)).max()))
 
 
+def reference_inputs(qkv, H_kv, qw, kw, pos, f):
+    B, N, heads, d = qkv.shape
+    p = np.broadcast_to(np.arange(N), (B, N)) if pos is None else pos.cpu().numpy()
+    return f64(qkv), heads - 2 * H_kv, f64w(qw, d), f64w(kw, d), p, [] if f is None else f.numpy()
+
+
+def compare_forward(qkv, out, qw, kw, pos, f, eps, interleaved):
+    H_kv = out[1].shape[1]
+    x, H, a, b, p, fr = reference_inputs(qkv, H_kv, qw, kw, pos, f)
+    ref = plain64.norm_rope(x, H, H_kv, a, b, p, fr, eps, interleaved)
+    for name, got, r in zip("qkv", out, ref):
+        if name == "v":
+            assert torch.equal(got, qkv[:, :, H + H_kv:].transpose(1, 2))
+        else:  # the pair's amplitude is at most sqrt(2) times the row's largest |w n|
+            check(got, r, 1.5 * np.abs(r).max(-1, keepdims=True) + 1e-30, qkv.dtype, name)
+
+
+def compare_grad(qkv, up, dqkv, dw, qw, kw, pos, f, eps, interleaved):
+    # gradient: |dx| terms are r w g and r n mean(w g n), n = x r; the mean's own error is
+    # under 2e-6 of mean |w g n|
+    H_kv, d = up[1].shape[1], qkv.shape[-1]
+    x, H, a, b, p, fr = reference_inputs(qkv, H_kv, qw, kw, pos, f)
+    rx, rqw, rkw = plain64.norm_rope_grad(x, H, H_kv, a, b, p, fr, eps, interleaved, *map(f64, up))
+    w = np.concatenate([np.tile(a, (H, 1)), np.tile(b, (H_kv, 1)), np.zeros((H_kv, d))])
+    g = np.concatenate([plain64.turn(f64(u).swapaxes(1, 2), p, fr, interleaved, -1.0) for u in up[:2]]
+                       + [f64(up[2]).swapaxes(1, 2)], 2)
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    n = x * r
+    amp = r * (1.5 * np.abs(w * g).max(-1, keepdims=True)
+               + 2 * np.abs(n) * np.abs(w * g * n).mean(-1, keepdims=True))
+    check(dqkv[:, :, :H + H_kv], rx[:, :, :H + H_kv], amp[:, :, :H + H_kv] + 1e-30, qkv.dtype, "dqkv")
+    assert torch.equal(dqkv[:, :, H + H_kv:], up[2].transpose(1, 2))
+    # a weight's gradient is a float32 sum of B N heads products, each off by 2e-6 of the pair's
+    # amplitude, added in runs of at most 64 and then in trees: under 1e-5 of the sum of magnitudes
+    for got, rr, sl in ((dw[0], rqw, slice(0, H)), (dw[1], rkw, slice(H, H + H_kv))):
+        mag = (np.abs(n[:, :, sl]) * 1.5 * np.abs(g[:, :, sl]).max(-1, keepdims=True)).sum((0, 1, 2))
+        assert (np.abs(f64(got) - rr) <= 1e-5 * mag).all()
+
+
 def run_both(B, N, H, H_kv, d, dtype, rot, interleaved, pos, weights=True, eps=1e-6, scale=1.0):
     qkv, qw, kw, up = make(B, N, H, H_kv, d, dtype, scale=scale)
     t = qkv.dtype
@@ -59,32 +98,8 @@ def run_both(B, N, H, H_kv, d, dtype, rot, interleaved, pos, weights=True, eps=1
     fa.fa_qk_norm_rope_bwd(qkv, qw, kw, pos, f, *up, dqkv, *dw, ws, eps, interleaved)
     check_status()
 
-    p = np.broadcast_to(np.arange(N), (B, N)) if pos is None else pos.cpu().numpy()
-    fr = [] if f is None else f.numpy()
-    x, a, b = f64(qkv), f64w(qw, d), f64w(kw, d)
-    ref = plain64.norm_rope(x, H, H_kv, a, b, p, fr, eps, interleaved)
-    for name, got, r in zip("qkv", out, ref):
-        if name == "v":
-            assert torch.equal(got, qkv[:, :, H + H_kv:].transpose(1, 2))
-        else:  # the pair's amplitude is at most sqrt(2) times the row's largest |w n|
-            check(got, r, 1.5 * np.abs(r).max(-1, keepdims=True) + 1e-30, t, name)
-    # gradient: |dx| terms are r w g and r n mean(w g n), n = x r; the mean's own error is
-    # under 2e-6 of mean |w g n|
-    rx, rqw, rkw = plain64.norm_rope_grad(x, H, H_kv, a, b, p, fr, eps, interleaved, *map(f64, up))
-    w = np.concatenate([np.tile(a, (H, 1)), np.tile(b, (H_kv, 1)), np.zeros((H_kv, d))])
-    g = np.concatenate([plain64.turn(f64(u).swapaxes(1, 2), p, fr, interleaved, -1.0) for u in up[:2]]
-                       + [f64(up[2]).swapaxes(1, 2)], 2)
-    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
-    n = x * r
-    amp = r * (1.5 * np.abs(w * g).max(-1, keepdims=True)
-               + 2 * np.abs(n) * np.abs(w * g * n).mean(-1, keepdims=True))
-    check(dqkv[:, :, :H + H_kv], rx[:, :, :H + H_kv], amp[:, :, :H + H_kv] + 1e-30, t, "dqkv")
-    assert torch.equal(dqkv[:, :, H + H_kv:], up[2].transpose(1, 2))
-    # a weight's gradient is a float32 sum of B N heads products, each off by 2e-6 of the pair's
-    # amplitude, added in runs of at most 64 and then in trees: under 1e-5 of the sum of magnitudes
-    for got, rr, sl in ((dw[0], rqw, slice(0, H)), (dw[1], rkw, slice(H, H + H_kv))):
-        mag = (np.abs(n[:, :, sl]) * 1.5 * np.abs(g[:, :, sl]).max(-1, keepdims=True)).sum((0, 1, 2))
-        assert (np.abs(f64(got) - rr) <= 1e-5 * mag).all()
+    compare_forward(qkv, out, qw, kw, pos, f, eps, interleaved)
+    compare_grad(qkv, up, dqkv, dw, qw, kw, pos, f, eps, interleaved)
     return qkv, out, dqkv, dw
 
 
