@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    griddep_wait();  // delta and lse come from the kernel before this one
 
     // 768 threads x 80 registers at launch: 40 + 4 * 88 + 88 = 6 * 80
     if (warp < 4) {
@@ -436,8 +437,8 @@ cudaError_t launch_bwd_window_main64(const CUtensorMap& q, const CUtensorMap& k,
     static std::atomic<uint64_t> smem_done;
     const cudaError_t e = allow_smem(win_bwd64_kernel, kSmemAlloc, smem_done);
     if (e != cudaSuccess) return e;
-    win_bwd64_kernel<<<grid, kThreads, kSmemAlloc, s>>>(q, k, v, dO, dk, dv, a);
-    return cudaGetLastError();
+    // set up while win_bwd_prep runs: 0.8% of a step (the d = 128 kernel lost as much that way)
+    return launch_pdl(win_bwd64_kernel, dim3(grid), dim3(kThreads), kSmemAlloc, s, q, k, v, dO, dk, dv, a);
 }
 
 }  // namespace fa
