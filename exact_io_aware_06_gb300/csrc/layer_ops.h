@@ -117,10 +117,6 @@ size_t bwd_window_workspace_bytes(int B, int H, int H_kv, int N, int d, int wind
 int launch_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
                       void* dq, void* dk, void* dv, void* workspace, int B, int H, int H_kv, int N, int d, float scale,
                       int window, int sinks, DevCtl ctl, cudaStream_t s);
-// dQ, from the workspace's negated rows.
-int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2,
-                         const float* ws_ndelta, void* dq, int B, int H, int H_kv, int N, int d, float scale,
-                         const WinSplit& sp, DevCtl ctl, cudaStream_t s);
 
 constexpr int kDevIndex = 5;  // == FA_ERR_DEVICE_INDEX: a page or length outside the cache
 

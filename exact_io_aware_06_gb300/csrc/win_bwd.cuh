@@ -228,11 +228,47 @@ __device__ __forceinline__ void write_part_row(const BwdArgs& a, const Item& I, 
     }
 }
 
+// dV and dK of the blocks that were dealt in parts: the parts added in order, dK times scale,
+// rounded once.  Thread t of n, eight neighbouring values at a time.
+template <int D>
+__device__ __forceinline__ void join_parts(const BwdArgs& a, int t, int n) {
+    constexpr int kVec = D / 8;
+    const WinSplit& sp = a.split;
+    const size_t work = static_cast<size_t>(a.BH) * sp.n_part * 2 * kBlk * kVec;
+    for (size_t x = t; x < work; x += n) {
+        const int vec = static_cast<int>(x % kVec), row = static_cast<int>(x / kVec % kBlk);
+        const int which = static_cast<int>(x / (kVec * kBlk) % 2);
+        const size_t blk = x / (2 * kVec * kBlk);  // bh * n_part + kvb
+        const int kvb = static_cast<int>(blk % sp.n_part);
+        const size_t bh = blk / sp.n_part;
+        const int key = kvb * kBlk + row;
+        if (key >= a.N) continue;
+        const int slots = 1 + (a.n_kv - 1 - sp.reach - kvb + sp.per - 1) / sp.per;
+        const float4* src = reinterpret_cast<const float4*>(a.part) +
+                            ((blk * (sp.pieces + 1) * 2 + which) * kBlk + row) * (D / 4) + 2 * vec;
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
+#pragma unroll 4
+        for (int i = 0; i < slots; ++i) {
+            const float4 y = src[0], z = src[1];
+            u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
+            w.x += z.x, w.y += z.y, w.z += z.z, w.w += z.w;
+            src += 2 * kBlk * (D / 4);
+        }
+        const float f = which ? a.scale : 1.f;
+        static_cast<uint4*>(which ? a.dk : a.dv)[(bh * a.N + key) * kVec + vec] =
+            make_uint4(pack_bf16x2(u.x * f, u.y * f), pack_bf16x2(u.z * f, u.w * f), pack_bf16x2(w.x * f, w.y * f),
+                       pack_bf16x2(w.z * f, w.w * f));
+    }
+}
+
 }  // namespace
 
 // dK and dV of the windowed backward for d = 64; grid: CTAs.
 cudaError_t launch_bwd_window_main64(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
                                      const CUtensorMap& dk, const CUtensorMap& dv, const WinBwdArgs& a, int grid,
                                      cudaStream_t s);
+// dQ, and the join of the parts that the dK/dV kernel has left.
+int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, void* dq, const WinBwdArgs& a, int d,
+                         cudaStream_t s);
 
 }  // namespace fa

@@ -38,17 +38,12 @@ static_assert(Cfg<128>::kSmemAlloc + 1024 <= 232448, "smem");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescSS = idesc_bf16(128, 128, false, false);  // S, dP
+constexpr uint32_t kIdescShort = idesc_bf16(128, 32, false, false);  // of up to 32 sinks
 
 struct DqArgs {
-    const float* ws_nlse2;   // [BH][Np]: -lse * log2(e) (-inf on pad rows)
-    const float* ws_ndelta;  // [BH][Np]: -delta
+    WinBwdArgs w;
     void* dq;
-    int N, Np, n_q, BH, n_items;  // BH: query heads (B * H)
-    int H, H_kv;
-    int window, sinks;
-    float c_log2;            // scale * log2(e)
-    float scale;
-    DevCtl ctl;
+    int n_items;  // 128-query blocks of all query heads
 };
 
 struct DqBars {
@@ -64,7 +59,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     win_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                      const DqArgs args) {
+                      const DqArgs dq_args) {
     using C = Cfg<D>;
     constexpr int kTile = C::kTile, kOffQ = C::kOffQ, kOffDO = C::kOffDO, kOffK = C::kOffK, kOffV = C::kOffV;
     extern __shared__ uint8_t smem_raw[];
@@ -74,22 +69,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int N = args.N, Np = args.Np;
+    const WinBwdArgs& args = dq_args.w;
+    const int N = args.N, Np = args.Np, n_items = dq_args.n_items;
+    const int q_heads = args.BH / args.H_kv * args.H;
     const uint64_t lim = args.ctl.wait_ns;
     struct QItem {
         int bh, bh_kv, qb, lo, n_sink, n_kv;
+        bool shorty;  // the first block is that of up to 32 sinks, in front of the window
         __device__ __forceinline__ int block(int j) const { return j < n_sink ? j : lo + j - n_sink; }
     };
     auto item_at = [&](int x) {
         QItem I;
-        I.bh = x % args.BH;
-        I.qb = args.n_q - 1 - x / args.BH;
+        I.bh = x % q_heads;
+        I.qb = args.n_kv - 1 - x / q_heads;
         // grouped-query attention: query head bh reads K/V head bh_kv of its group
         I.bh_kv = (I.bh / args.H) * args.H_kv + (I.bh % args.H) / (args.H / args.H_kv);
         // key blocks: the sinks' in front of the window, then lo .. qb
-        I.lo = max(0, static_cast<int>(static_cast<long long>(I.qb) * kBlk - args.window + 1)) / kBlk;
-        I.n_sink = min(I.lo, (args.sinks + kBlk - 1) / kBlk);
+        I.lo = max(0, static_cast<int>(static_cast<long long>(I.qb) * kBlk - args.split.window + 1)) / kBlk;
+        I.n_sink = min(I.lo, (args.split.sinks + kBlk - 1) / kBlk);
         I.n_kv = I.n_sink + I.qb - I.lo + 1;
+        I.shorty = I.n_sink > 0 && args.split.sinks <= 32;
         return I;
     };
 
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int g = 0, n = 0;  // pairs and items whose loads were issued
                 int gk = 0, gv = 0;
                 bool ok = true;
-                for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k)) {
+                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                     const QItem I = item_at(x);
                     if (n > 0 && !mbar_wait(smem_u32(&bars.q_free), (n - 1) & 1, lim, &abort_flag)) {
                         ok = false;
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t q_lo = sdesc_sw128_lo(sb + kOffQ, 16), do_lo = sdesc_sw128_lo(sb + kOffDO, 16);
                 const uint32_t k_lo = sdesc_sw128_lo(sb + kOffK, 16), v_lo = sdesc_sw128_lo(sb + kOffV, 16);
                 // S = Q K_j^T and dP = dO V_j^T of pair g (both operands K-major along d)
-                auto issue_sp = [&](int g, int item, bool first, bool last) -> bool {
+                auto issue_sp = [&](int g, int item, bool first, bool last, uint32_t idesc) -> bool {
                     const int sk = g % kKStages, sv = g % kVStages;
                     if (first && !mbar_wait(smem_u32(&bars.q_full), item & 1, lim, &abort_flag)) return false;
                     if (!mbar_wait(smem_u32(&bars.k_full[sk]), (g / kKStages) & 1, lim, &abort_flag)) return false;
@@ -208,17 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off16 = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                         if (kk == 0)
-                            mma_ss_w<false, -1>(tmem + kColS, q_lo, kl, kDescHi, kIdescSS, 0u);
+                            mma_ss_w<false, -1>(tmem + kColS, q_lo, kl, kDescHi, idesc, 0u);
                         else
-                            mma_ss_w<false, 1>(tmem + kColS, q_lo + off16, kl + off16, kDescHi, kIdescSS);
+                            mma_ss_w<false, 1>(tmem + kColS, q_lo + off16, kl + off16, kDescHi, idesc);
                     }
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off16 = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                         if (kk == 0)
-                            mma_ss_w<false, -1>(tmem + kColDP, do_lo, vl, kDescHi, kIdescSS, 0u);
+                            mma_ss_w<false, -1>(tmem + kColDP, do_lo, vl, kDescHi, idesc, 0u);
                         else
-                            mma_ss_w<false, 1>(tmem + kColDP, do_lo + off16, vl + off16, kDescHi, kIdescSS);
+                            mma_ss_w<false, 1>(tmem + kColDP, do_lo + off16, vl + off16, kDescHi, idesc);
                     }
                     mma_commit(smem_u32(&bars.sp_full));
                     mma_commit(smem_u32(&bars.v_empty[sv]));
@@ -227,9 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 int g = 0, item = 0;
                 bool ok = true;
-                for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k), ++item) {
-                    const int n_kv = item_at(x).n_kv;
-                    for (int j = 0; j < n_kv && ok; ++j, ++g) ok = issue_sp(g, item, j == 0, j + 1 == n_kv);
+                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k), ++item) {
+                    const QItem I = item_at(x);
+                    for (int j = 0; j < I.n_kv && ok; ++j, ++g)
+                        ok = issue_sp(g, item, j == 0, j + 1 == I.n_kv, I.shorty && j == 0 ? kIdescShort : kIdescSS);
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
                 mma_commit(smem_u32(&bars.drain));
@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t k_mn = sdesc_sw128_lo(sb + kOffK, 16384);
                 int g = 0, item = 0;
                 bool ok = true;
-                for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k), ++item) {
-                    const int n_kv = item_at(x).n_kv;
-                    for (int j = 0; j < n_kv; ++j, ++g) {
+                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k), ++item) {
+                    const QItem I = item_at(x);
+                    for (int j = 0; j < I.n_kv; ++j, ++g) {
                         const int sk = g % kKStages;
                         ok = mbar_wait(smem_u32(&bars.k_full[sk]), (g / kKStages) & 1, lim, &abort_flag);
                         // the last item's dQ has been read out
@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t km = k_mn + sk * (kTile >> 4), ds = tmem + kColDS + 64 * (g & 1);
 #pragma unroll
                         for (int kk = 0; kk < kBlk / 16; ++kk) {
+                            if (kk == 2 && I.shorty && j == 0) break;
                             if (kk == 0)
                                 mma_ts_w<false, -1>(tmem + kColDQ, ds, km, kDescHi, C::kIdescDQ, j > 0 ? 1u : 0u);
                             else
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         mma_commit(smem_u32(&bars.ds_empty[g & 1]));
                         mma_commit(smem_u32(&bars.k_empty[sk]));  // S of this pair read K before dS was made
-                        if (j + 1 == n_kv) mma_commit(smem_u32(&bars.all_done));
+                        if (j + 1 == I.n_kv) mma_commit(smem_u32(&bars.all_done));
                     }
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
@@ -274,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const volatile int never = 0;
                 mbar_wait(smem_u32(&bars.drain2), 0, kDrainWaitNs, &never);
             }
+        } else if (args.split.n_part > 0) {
+            // ============================================================ the sinks' parts
+            join_parts<D>(args, static_cast<int>(blockIdx.x) * 32 + lane, static_cast<int>(gridDim.x) * 32);
         }
-        // warp 3 has no role
     } else if (warp < 12) {
         regs_inc<160>();
         // ================================================================ dS warpgroups
@@ -293,17 +296,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             return static_cast<size_t>(I.bh) * Np + I.qb * kBlk + row;
         };
         float next_nl = 0.f, next_nd = 0.f;
-        if (item_x(0) < args.n_items) {
-            next_nl = args.ws_nlse2[row_at(item_x(0))];
-            next_nd = args.ws_ndelta[row_at(item_x(0))];
+        if (item_x(0) < n_items) {
+            next_nl = args.ws_lse2[row_at(item_x(0))];
+            next_nd = args.ws_delta[row_at(item_x(0))];
         }
-        for (int k = 0, x = item_x(0); x < args.n_items && ok; x = item_x(++k)) {
+        for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
             const QItem I = item_at(x);
             const int qrow = I.qb * kBlk + row;
             const float nl = next_nl, nd = next_nd;
-            if (item_x(k + 1) < args.n_items) {
-                next_nl = args.ws_nlse2[row_at(item_x(k + 1))];
-                next_nd = args.ws_ndelta[row_at(item_x(k + 1))];
+            if (item_x(k + 1) < n_items) {
+                next_nl = args.ws_lse2[row_at(item_x(k + 1))];
+                next_nd = args.ws_delta[row_at(item_x(k + 1))];
             }
             const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
             for (int j = 0; j < I.n_kv; ++j, ++g) {
@@ -311,57 +314,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t rs[2][32], rp[2][32];
-                tmem_ld32_async(lb + kColS + 64 * half, rs[0]);
-                tmem_ld32_async(lb + kColS + 64 * half + 32, rs[1]);
-                tmem_ld32_async(lb + kColDP + 64 * half, rp[0]);
-                tmem_ld32_async(lb + kColDP + 64 * half + 32, rp[1]);
-                tmem_wait_ld();
-                reg_fence(rs[0]);
-                reg_fence(rs[1]);
-                reg_fence(rp[0]);
-                reg_fence(rp[1]);
-                tc_fence_before();
-                mbar_arrive(smem_u32(&bars.sp_free));
-                // the row's keys, counted from this half's first: from `first` or below `sink`, to `last`
-                const int key0 = I.block(j) * kBlk + 64 * half;
-                const int last = qrow - key0, sink = args.sinks - key0;
-                const int first = static_cast<int>(max(-1ll, static_cast<long long>(last) - args.window + 1));
-                const bool edge = __any_sync(0xffffffffu, last < 63 || (first > 0 && sink < 64));
-                // a warp's rows are neighbours: of its two runs of 32 keys mostly one holds a bound of
-                // some row and needs the test of every score
-                if (edge) {
+                // dQ of pair g - 2 has read this pair's dS buffer
+                auto buffer_free = [&]() -> bool {
+                    if (g < 2) return true;
+                    const bool done = mbar_wait(smem_u32(&bars.ds_empty[g & 1]), ((g >> 1) & 1) ^ 1, lim, &abort_flag);
+                    if (!__all_sync(0xffffffffu, done)) return false;
+                    tc_fence_after();
+                    return true;
+                };
+                // NW runs of 32 keys from this half's first on
+                auto pair = [&](auto nw) -> bool {
+                    constexpr int NW = decltype(nw)::value;
+                    uint32_t rs[NW][32], rp[NW][32];
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t seen =
-                            bits_below(last + 1 - 32 * w) & (~bits_below(first - 32 * w) | bits_below(sink - 32 * w));
-                        if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+                    for (int w = 0; w < NW; ++w) {
+                        tmem_ld32_async(lb + kColS + 64 * half + 32 * w, rs[w]);
+                        tmem_ld32_async(lb + kColDP + 64 * half + 32 * w, rp[w]);
+                    }
+                    tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(seen & (1u << i))) rs[w][i] = hide;
+                    for (int w = 0; w < NW; ++w) {
+                        reg_fence(rs[w]);
+                        reg_fence(rp[w]);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&bars.sp_free));
+                    // the row's keys, counted from this half's first: from `first` or below `sink`, to `last`
+                    const int key0 = I.block(j) * kBlk + 64 * half;
+                    const int last = qrow - key0, sink = args.split.sinks - key0;
+                    const int first = static_cast<int>(max(-1ll, static_cast<long long>(last) - args.split.window + 1));
+                    const bool edge = __any_sync(0xffffffffu, last < 32 * NW - 1 || (first > 0 && sink < 32 * NW));
+                    // a warp's rows are neighbours: of its two runs of 32 keys mostly one holds a bound of
+                    // some row and needs the test of every score
+                    if (edge) {
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            const uint32_t seen =
+                                bits_below(last + 1 - 32 * w) & (~bits_below(first - 32 * w) | bits_below(sink - 32 * w));
+                            if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(seen & (1u << i))) rs[w][i] = hide;
+                            }
                         }
                     }
-                }
-                uint32_t pk[32];
+                    uint32_t pk[16 * NW];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = 2 * (i % 16);
-                    const uint32_t* S = rs[i / 16];
-                    const uint32_t* P = rp[i / 16];
-                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(S[e]), __uint_as_float(S[e + 1])), c2, nl2);
-                    const float2 p = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-                    const float2 d = __fadd2_rn(make_float2(__uint_as_float(P[e]), __uint_as_float(P[e + 1])), nd2);
-                    const float2 ds = __fmul2_rn(p, d);
-                    pk[i] = pack_bf16x2(ds.x, ds.y);
+                    for (int i = 0; i < 16 * NW; ++i) {
+                        const int e = 2 * (i % 16);
+                        const uint32_t* S = rs[i / 16];
+                        const uint32_t* P = rp[i / 16];
+                        const float2 a = __ffma2_rn(make_float2(__uint_as_float(S[e]), __uint_as_float(S[e + 1])), c2, nl2);
+                        const float2 p = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                        const float2 d = __fadd2_rn(make_float2(__uint_as_float(P[e]), __uint_as_float(P[e + 1])), nd2);
+                        const float2 ds = __fmul2_rn(p, d);
+                        pk[i] = pack_bf16x2(ds.x, ds.y);
+                    }
+                    if (!buffer_free()) return false;
+                    const uint32_t dst = lb + kColDS + 64 * (g & 1) + 32 * half;
+                    if constexpr (NW == 2)
+                        tmem_st32(dst, pk);
+                    else
+                        tmem_st16(dst, pk);
+                    tmem_st_wait();
+                    return true;
+                };
+                if (!(I.shorty && j == 0)) {
+                    ok = pair(std::integral_constant<int, 2>{});
+                } else if (half == 0) {
+                    ok = pair(std::integral_constant<int, 1>{});
+                } else {  // no keys
+                    mbar_arrive(smem_u32(&bars.sp_free));
+                    ok = buffer_free();
                 }
-                if (g >= 2) {  // dQ of pair g - 2 has read this buffer
-                    ok = mbar_wait(smem_u32(&bars.ds_empty[g & 1]), ((g >> 1) & 1) ^ 1, lim, &abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                tmem_st32(lb + kColDS + 64 * (g & 1) + 32 * half, pk);
-                tmem_st_wait();
+                if (!ok) break;
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.ds_full[g & 1]));
             }
@@ -374,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         bool ok = true;
         int item = 0;
-        for (int k = 0, x = item_x(0); x < args.n_items; x = item_x(++k), ++item) {
+        for (int k = 0, x = item_x(0); x < n_items; x = item_x(++k), ++item) {
             const QItem I = item_at(x);
             ok = mbar_wait(smem_u32(&bars.all_done), item & 1, lim, &abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -384,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rows.load(lb + kColDQ, args.scale);
             tc_fence_before();
             mbar_arrive(smem_u32(&bars.dq_read));
-            rows.store(args.dq, static_cast<size_t>(I.bh) * N, I.qb * kBlk + wq * 32, N);
+            rows.store(dq_args.dq, static_cast<size_t>(I.bh) * N, I.qb * kBlk + wq * 32, N);
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
     }
@@ -398,9 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-int launch_impl(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2, const float* ws_ndelta,
-                void* dq, int B, int H, int H_kv, int N, float scale, const WinSplit& sp, DevCtl ctl, cudaStream_t s) {
-    const int BH = B * H, BH_kv = B * H_kv;
+int launch_impl(const void* q, const void* k, const void* v, const void* dO, const DqArgs& a, cudaStream_t s) {
+    const int BH_kv = a.w.BH, BH = BH_kv / a.w.H_kv * a.w.H, N = a.w.N;
     CUtensorMap tq, tk, tv, tdo;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     int rc = make_map_3d(&tq, q, dt, 2, D, N, BH, 64, kBlk);
@@ -414,36 +439,21 @@ int launch_impl(const void* q, const void* k, const void* v, const void* dO, con
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return static_cast<int>(e);
-    DqArgs a;
-    a.ws_nlse2 = ws_nlse2;
-    a.ws_ndelta = ws_ndelta;
-    a.dq = dq;
-    a.N = N;
-    a.Np = round_up(N, kBlk);
-    a.n_q = a.Np / kBlk;
-    a.BH = BH;
-    a.n_items = a.n_q * BH;
-    a.H = H;
-    a.H_kv = H_kv;
-    a.window = sp.window;
-    a.sinks = sp.sinks;
-    a.c_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;  // not 0: the mask multiplies -inf by it
-    a.scale = scale;
-    a.ctl = ctl;
     // An ordinary launch.  Launched with programmatic serialization, its CTAs taking over the SMs as
-    // those of the dK/dV kernel finish (of which it needs nothing), a step took 2-3% longer.
+    // those of the dK/dV kernel finish (of which dQ needs nothing), a step took 2-3% longer.
     win_bwd_dq_kernel<D><<<a.n_items < sms ? a.n_items : sms, kThreads, Cfg<D>::kSmemAlloc, s>>>(tq, tk, tv, tdo, a);
     return static_cast<int>(cudaGetLastError());
 }
 
 }  // namespace
 
-int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, const float* ws_nlse2,
-                         const float* ws_ndelta, void* dq, int B, int H, int H_kv, int N, int d, float scale,
-                         const WinSplit& sp, DevCtl ctl, cudaStream_t s) {
-    return d == 64
-               ? launch_impl<64>(q, k, v, dO, ws_nlse2, ws_ndelta, dq, B, H, H_kv, N, scale, sp, ctl, s)
-               : launch_impl<128>(q, k, v, dO, ws_nlse2, ws_ndelta, dq, B, H, H_kv, N, scale, sp, ctl, s);
+int launch_bwd_window_dq(const void* q, const void* k, const void* v, const void* dO, void* dq, const WinBwdArgs& a, int d,
+                         cudaStream_t s) {
+    DqArgs x;
+    x.w = a;
+    x.dq = dq;
+    x.n_items = a.n_kv * (a.BH / a.H_kv * a.H);
+    return d == 64 ? launch_impl<64>(q, k, v, dO, x, s) : launch_impl<128>(q, k, v, dO, x, s);
 }
 
 }  // namespace fa

@@ -7,9 +7,9 @@
 //     dS = P o (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q.
 //
 // Kernels on one stream: win_bwd_prep (delta and padded -lse log2 e), the main kernel (dK and dV in
-// TMEM per 128-key block: here for d = 128, win_bwd64_sm103.cu for d = 64), win_bwd_join for the
-// sinks, and a query-parallel kernel for dQ (win_bwd_dq_sm103.cu).  Nothing is summed by atomics:
-// the same bits every time.  (For d = 64 the plain backward's scheme, dQ partials added to a
+// TMEM per 128-key block: here for d = 128, win_bwd64_sm103.cu for d = 64), and a query-parallel
+// kernel for dQ (win_bwd_dq_sm103.cu), which also joins the sinks' parts.  Nothing is summed by
+// atomics: the same bits every time.  (For d = 64 the plain backward's scheme, dQ partials added to a
 // float32 accumulator by TMA reductions, was also measured: the main kernel took 79 us of a B4 H16
 // N2048 W512 step, zeroing and converting the accumulator 13 more; dK/dV and dQ take 54 and 39.)
 //
@@ -18,8 +18,8 @@
 //   * A block that holds sinks meets all later query blocks too: N / 128 of them where the
 //     others meet W / 128, so that one CTA would still be at it long after the rest are done.
 //     Its later query blocks are dealt in pieces, as items of their own, first of all; the
-//     pieces of a block leave float32 dK and dV in the workspace and win_bwd_join adds them
-//     in order and rounds once.
+//     pieces of a block leave float32 dK and dV in the workspace, and an idle warp of the dQ
+//     kernel adds them in order and rounds once.
 //   * The visible queries of a key row are a range; blocks that hold its ends take them as
 //     bit words made by shifts.
 //   * dS is taken from P before its rounding to bf16: with P rounded first, dQ and dK carried two
@@ -416,40 +416,6 @@ __global__ void win_bwd_prep_kernel(const uint4* __restrict__ o, const uint4* __
     }
 }
 
-// dV and dK of the blocks that were dealt in parts: the parts added in order, dK times
-// scale, rounded once.  Eight neighbouring values per thread.
-template <int D>
-__global__ void __launch_bounds__(256)
-    win_bwd_join_kernel(const float* __restrict__ part, uint4* __restrict__ dk, uint4* __restrict__ dv, const WinSplit sp,
-                        int N, int n_q, size_t work, float scale) {
-    griddep_wait();
-    constexpr int kVec = D / 8;
-    const size_t step = static_cast<size_t>(gridDim.x) * blockDim.x;
-    for (size_t x = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; x < work; x += step) {
-        const int vec = static_cast<int>(x % kVec), row = static_cast<int>(x / kVec % kBlk);
-        const int which = static_cast<int>(x / (kVec * kBlk) % 2);
-        const size_t blk = x / (2 * kVec * kBlk);  // bh * n_part + kvb
-        const int kvb = static_cast<int>(blk % sp.n_part);
-        const size_t bh = blk / sp.n_part;
-        const int key = kvb * kBlk + row;
-        if (key >= N) continue;
-        const int slots = 1 + (n_q - 1 - sp.reach - kvb + sp.per - 1) / sp.per;
-        const float4* src = reinterpret_cast<const float4*>(part) +
-                            ((blk * (sp.pieces + 1) * 2 + which) * kBlk + row) * (D / 4) + 2 * vec;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        for (int s = 0; s < slots; ++s) {
-            const float4 u = src[0], w = src[1];
-            a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
-            b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
-            src += 2 * kBlk * (D / 4);
-        }
-        const float f = which ? scale : 1.f;
-        (which ? dk : dv)[(bh * N + key) * kVec + vec] =
-            make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f), pack_bf16x2(b.x * f, b.y * f),
-                       pack_bf16x2(b.z * f, b.w * f));
-    }
-}
-
 int grid_for(size_t work, int threads, int max_blocks) {
     size_t b = (work + threads - 1) / threads;
     if (b > static_cast<size_t>(max_blocks)) b = max_blocks;
@@ -559,14 +525,7 @@ int launch_bwd_window(const void* q, const void* k, const void* v, const void* o
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return static_cast<int>(e);
-    if (sp.n_part > 0) {
-        const size_t work = static_cast<size_t>(BH_kv) * sp.n_part * 2 * kBlk * (d / 8);
-        e = launch_pdl(d == 64 ? win_bwd_join_kernel<64> : win_bwd_join_kernel<128>,
-                       dim3(grid_for(work, 256, sms * 8)), dim3(256), 0, s, a.part, static_cast<uint4*>(dk),
-                       static_cast<uint4*>(dv), sp, N, a.n_kv, work, scale);
-        if (e != cudaSuccess) return static_cast<int>(e);
-    }
-    return launch_bwd_window_dq(q, k, v, dO, ws_lse2, ws_delta, dq, B, H, H_kv, N, d, scale, sp, ctl, s);
+    return launch_bwd_window_dq(q, k, v, dO, dq, a, d, s);
 }
 
 }  // namespace fa
