@@ -26,7 +26,9 @@
 //     bf16 roundings before their own.
 //
 // The d = 128 main kernel: S^T, dP^T, dV and dK fill TMEM, P^T and dS^T are written over S^T and
-// dP^T, and roles, ring and the order of MMAs are the plain backward's.
+// dP^T, and roles and the order of MMAs are the plain backward's.  Q and dO have rings of their own,
+// and the issuing thread waits for the next Q behind dV and for the next dO behind dK: with both under
+// one barrier, in front of dV, it waited 530 of a pair's 2800 cycles for them.
 #include <type_traits>
 
 #include "win_bwd.cuh"
@@ -53,7 +55,7 @@ constexpr uint32_t kIdescTS = idesc_bf16(128, kD, false, true);    // dV, dK
 
 struct Bars {
     uint64_t k_full, k_empty, v_full, v_empty;
-    uint64_t q_full[kQStages], q_empty[kQStages];
+    uint64_t q_full[kQStages], q_empty[kQStages], do_full[kQStages], do_empty[kQStages];
     uint64_t s_full, dp_full, p_full;
     uint64_t ds_full[2];  // one per parity, as a waiter may fall one phase behind
     uint64_t all_done, drain;
@@ -88,6 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kQStages; ++s) {
             mbar_init(smem_u32(&bars.q_full[s]), 1);
             mbar_init(smem_u32(&bars.q_empty[s]), 1);
+            mbar_init(smem_u32(&bars.do_full[s]), 1);
+            mbar_init(smem_u32(&bars.do_empty[s]), 1);
         }
         mbar_init(smem_u32(&bars.s_full), 1);
         mbar_init(smem_u32(&bars.dp_full), 1);
@@ -115,9 +119,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ================================================================ Q / dO producer
-        // The ring runs across item boundaries: it waits only for its own stages.
+        // The rings run across item boundaries: they wait only for their own stages.  A stage of dO is
+        // free after dV, one of Q (with lse and delta) after dK.
         if (lane == 0) {
-            int g = 0;
+            int g = 0, nq = 0, ndo = 0;  // pairs; Q, dO loads issued
             bool ok = true;
             for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                 const Item I = item_at(args, x);
@@ -125,27 +130,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < I.n_it; ++i, ++g, at.next()) {
                     const int s = g % kQStages;
                     const int qb = at.blk, qh = at.head;
-                    if (g >= kQStages &&
-                        !mbar_wait(smem_u32(&bars.q_empty[s]), ((g / kQStages) & 1) ^ 1, lim, &abort_flag)) {
+                    const uint32_t par = ((g / kQStages) & 1) ^ 1;
+                    if (g >= kQStages && !mbar_wait(smem_u32(&bars.do_empty[s]), par, lim, &abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t df = smem_u32(&bars.do_full[s]);
+                    mbar_arrive_expect_tx(df, kTile);
+                    for (int c = 0; c < kChunks; ++c)
+                        tma_load_3d(sb + kOffDO + s * kTile + c * 16384, &tm_do, df, 64 * c, qb * kBlk, qh);
+                    ndo = g + 1;
+                    if (g >= kQStages && !mbar_wait(smem_u32(&bars.q_empty[s]), par, lim, &abort_flag)) {
                         ok = false;
                         break;
                     }
                     const uint32_t qf = smem_u32(&bars.q_full[s]);
-                    mbar_arrive_expect_tx(qf, 2 * kTile + 2 * kBlk * 4);
-                    for (int c = 0; c < kChunks; ++c) {
+                    mbar_arrive_expect_tx(qf, kTile + 2 * kBlk * 4);
+                    for (int c = 0; c < kChunks; ++c)
                         tma_load_3d(sb + kOffQ + s * kTile + c * 16384, &tm_q, qf, 64 * c, qb * kBlk, qh);
-                        tma_load_3d(sb + kOffDO + s * kTile + c * 16384, &tm_do, qf, 64 * c, qb * kBlk, qh);
-                    }
                     const size_t row = static_cast<size_t>(qh) * Np + static_cast<size_t>(qb) * kBlk;
                     bulk_load(sb + kOffL + s * kBlk * 4, args.ws_lse2 + row, kBlk * 4, qf);
                     bulk_load(sb + kOffDelta + s * kBlk * 4, args.ws_delta + row, kBlk * 4, qf);
+                    nq = g + 1;
                 }
             }
             if (!ok) record_timeout(args.ctl, &abort_flag);
             // drain: the newest load of every stage has landed
             const volatile int never = 0;
-            for (int q = max(0, g - kQStages); q < g; ++q)
+            for (int q = max(0, nq - kQStages); q < nq; ++q)
                 mbar_wait(smem_u32(&bars.q_full[q % kQStages]), (q / kQStages) & 1, kDrainWaitNs, &never);
+            for (int q = max(0, ndo - kQStages); q < ndo; ++q)
+                mbar_wait(smem_u32(&bars.do_full[q % kQStages]), (q / kQStages) & 1, kDrainWaitNs, &never);
         }
     } else if (warp == 3) {
         // ================================================================ K / V producer
@@ -230,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_ss(kColS, k_lo, q_lo, g % kQStages, bars.s_full);
                 if (I.n_it == 1) mma_commit(smem_u32(&bars.k_empty));
                 ok = mbar_wait(smem_u32(&bars.v_full), kc & 1, lim, &abort_flag);
+                if (ok) ok = mbar_wait(smem_u32(&bars.do_full[g % kQStages]), (g / kQStages) & 1, lim, &abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 issue_ss(kColDP, v_lo, do_lo, g % kQStages, bars.dp_full);
@@ -244,20 +260,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int gi = g + i, s = gi % kQStages, s1 = (gi + 1) % kQStages;
                     // P of an item's first block is computed after the P/dS warps have read the
                     // previous item's dV and dK, so dV, dK may then be overwritten
-                    bool okb = mbar_wait(smem_u32(&bars.p_full), gi & 1, lim, &abort_flag);
-                    if (okb && more)
-                        okb = mbar_wait(smem_u32(&bars.q_full[s1]), ((gi + 1) / kQStages) & 1, lim, &abort_flag);
-                    if (!okb) return false;
+                    const uint32_t par1 = ((gi + 1) / kQStages) & 1;
+                    if (!mbar_wait(smem_u32(&bars.p_full), gi & 1, lim, &abort_flag)) return false;
                     tc_fence_after();
                     issue_ts(kColDV, kColS, do_mn + s * kStage16, i > 0);
+                    mma_commit(smem_u32(&bars.do_empty[s]));
                     if constexpr (more) {  // the P/dS warps keep P_i in registers
+                        if (!mbar_wait(smem_u32(&bars.q_full[s1]), par1, lim, &abort_flag)) return false;
+                        tc_fence_after();
                         issue_ss(kColS, k_lo, q_lo, s1, bars.s_full);
                         if constexpr (last2) mma_commit(smem_u32(&bars.k_empty));
                     }
                     if (!mbar_wait(smem_u32(&bars.ds_full[gi & 1]), (gi >> 1) & 1, lim, &abort_flag)) return false;
+                    if (more && !mbar_wait(smem_u32(&bars.do_full[s1]), par1, lim, &abort_flag)) return false;
                     tc_fence_after();
                     issue_ts(kColDK, kColDP, q_mn + s * kStage16, i > 0);
-                    mma_commit(smem_u32(&bars.q_empty[s]));  // Q_i, dO_i, lse_i, delta_i consumed
+                    mma_commit(smem_u32(&bars.q_empty[s]));  // Q_i, lse_i, delta_i consumed
                     if constexpr (more) {
                         issue_ss(kColDP, v_lo, do_lo, s1, bars.dp_full);
                         if constexpr (last2) mma_commit(smem_u32(&bars.v_empty));
