@@ -27,6 +27,7 @@
 namespace fa {
 
 constexpr int kTileTokens = 16;
+constexpr int kMaxTokens = 0x7fffff00;  // of a request: token numbers, and a tile's more, stay within int
 
 // Byte offset of word (t, c) in a K token row.
 __host__ __device__ constexpr int kv4_k_word(int d, int t, int c) { return 4 * (t * (d / 32) + c); }

@@ -5,6 +5,7 @@
 
 #include "../../include/fa.h"
 #include "internal.h"
+#include "kv4.cuh"
 #include "layer_ops.h"
 
 namespace fa {
@@ -71,7 +72,7 @@ int cache_args(Kv4Cache* c, const void* kc, const void* ks, const void* vc, cons
     while (log2 < 8 && (1 << log2) != page) ++log2;
     if ((1 << log2) != page) return FA_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(max_blocks) * page > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_blocks) * page > kMaxTokens) return FA_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(B) * H_kv > (1ll << 24)) return FA_ERR_UNSUPPORTED;
     c->codes[0] = static_cast<uint8_t*>(const_cast<void*>(kc));
     c->codes[1] = static_cast<uint8_t*>(const_cast<void*>(vc));

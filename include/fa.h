@@ -321,7 +321,7 @@ int fa_qk_norm_rope(const void* qkv, const float* q_weight, const float* k_weigh
  *     dx = r (w g - r^2 x mean(w g x)),    dw = sum over all rows of g r x.
  *
  *   dq, dk, dv : gradients of q, k, v, in their layouts, read only.
- *   dqkv       : gradient of qkv, in its layout, written.
+ *   dqkv       : gradient of qkv, in its layout, written; it must not overlap the inputs.
  *   dq_weight, dk_weight : [d] float32, written (the sum over all rows), or NULL if not
  *                wanted.  The sums have a fixed order: the same bits every time.
  *   workspace  : at least fa_qk_norm_rope_bwd_workspace_size() bytes of device memory; NULL
@@ -362,7 +362,8 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
  *   dq          : [B][H][N][d];  dk, dv : [B][H_kv][N][d] bfloat16, written.
  *   workspace   : at least fa_bwd_window_workspace_size() bytes; its contents on entry do not
  *                 matter.  Calls that overlap in time must not share one.
- * Nothing is summed by atomics: the same bits every time.
+ * Nothing is summed by atomics: the same bits every time.  A NaN or an infinity in q, k, v, o or dO
+ * reaches the gradients of the rows whose 128-row blocks meet its own, hidden pairs or not (0 * NaN).
  * Errors: as fa_fwd_window; FA_ERR_INVALID_ARG also for a null lse and a workspace that is
  * too small.
  */
@@ -398,8 +399,8 @@ size_t fa_bwd_window_workspace_size(int B, int H, int H_kv, int N, int d, int wi
  *   k, v  : [B][H_kv][N][d] bfloat16, read only.
  *   first : [B] int32, device: tokens that the requests had before.   count : [B] int32 or NULL.
  * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, sizes < 1, bad page),
- * FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, max_blocks * page or B*H_kv*N
- * beyond 2^31 - 1), FA_ERR_CUDA.
+ * FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, max_blocks * page beyond
+ * 2^31 - 256, B*H_kv*N beyond 2^31 - 1), FA_ERR_CUDA.
  */
 int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes,
                   void* v_scales, const int* block_table, const int* first, const int* count, int B,

@@ -332,3 +332,25 @@ def test_decode_nan_in_a_visible_group_shows_and_elsewhere_does_not():
     assert not o.isnan().any()
     o, _, _ = decode(q, c, [10])                # token 10 behind the end, in the same tile
     assert not o.isnan().any()
+
+
+def test_pages_beyond_32_bits():
+    # codes of K and V take 5 GB each; the request's pages are the last ones, in falling order
+    n, d, page, H_kv, n_pages = 700, 128, 256, 8, 40000
+    k, v, q = rand((1, H_kv, n, d), 41), rand((1, H_kv, n, d), 42), rand((1, 16, 1, d), 43)
+    results = []
+    for pages, table in ((n_pages, [39999, 39998, 39997]), (3, [0, 1, 2])):
+        arrays, table = fa.kv4_cache(pages, H_kv, page, d), ints([table])
+        assert pages == 3 or arrays[0].numel() > 2 ** 32
+        fa.fa_kv4_append(k, v, *arrays, table, ints([0]))
+        back = [torch.empty_like(k), torch.empty_like(v)]
+        fa.fa_kv4_read(*arrays, table, ints([n]), *back)
+        o, lse = torch.empty_like(q), torch.empty((1, 16, 1), device="cuda")
+        ws = torch.empty(fa.fa_decode_kv4_workspace_size(1, 16, H_kv, 1, d), dtype=torch.uint8, device="cuda")
+        fa.fa_decode_kv4(q, *arrays, table, ints([n]), o, lse, ws, d ** -0.5)
+        check_status()
+        results.append((*back, o, lse))
+        del arrays
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert np.array_equal(f64(results[0][0]), plain64.bf16_round(plain64.kv4_values(f64(k))))
+    compare(q, results[0][2], results[0][3], plain64.kv4_values(f64(k)), plain64.kv4_values(f64(v)), [n])

@@ -167,3 +167,33 @@ def test_prompt_in_two_pieces(d):
         top = 2e-5 * (1 + scale * np.abs(Q @ keys[h // 2].T).max(-1))
         assert (np.abs(f64(o)[0, h] - ref) <= 2.0 ** -8 * (2 * A + np.abs(ref)) + top[:, None] * A).all()
         assert (np.abs(f64(lse)[0, h] - ref_lse) <= 2.0 ** -8 + top).all()
+
+
+def test_binding_refuses_tensors_that_kernels_would_misread():
+    q, o = win.rand((1, 2, 8, 64), 1), empty(1, 2, 8, 64)
+    lse = empty(1, 2, 8, dtype=torch.float32)
+    bad = [(q.float(), q, q, o, lse), (q.transpose(2, 3).contiguous().transpose(2, 3), q, q, o, lse),
+           (q, q[:, :, :4], q, o, lse), (q, q, q, o[:, :1], lse), (q, q, q, o, lse.double()), (q.cpu(), q, q, o, lse),
+           (q[0], q, q, o, lse)]
+    for args in bad:
+        with pytest.raises(ValueError):
+            fa.fa_fwd_window(*args, 0.125, 4, 0)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    ws = space(fa.fa_bwd_window_workspace_size(1, 2, 2, 8, 64, 4, 0))
+    for dq, w in ((grads[0][:, :, :7], ws), (grads[0], ws.cpu()), (grads[0], ws[::2])):
+        with pytest.raises(ValueError):
+            fa.fa_bwd_window(q, q, q, o, lse, q, dq, *grads[1:], w, 0.125, 4, 0)
+    c = kv4.Cache([8], 2, 64, 16)
+    n = kv4.ints([8])
+    ws = space(fa.fa_decode_kv4_workspace_size(1, 4, 2, 1, 64))
+    q1 = win.rand((1, 4, 1, 64), 2)
+    for args in ((q1, *c.arrays, c.table.long(), n, q1, None, ws), (q1, *c.arrays, c.table, n.cpu(), q1, None, ws),
+                 (q1, *c.arrays[:3], c.arrays[3].float(), c.table, n, q1, None, ws),
+                 (q1, c.arrays[0][:, :, :8], *c.arrays[1:], c.table, n, q1, None, ws),
+                 (q1, *c.arrays, c.table, kv4.ints([8, 8]), q1, None, ws)):
+        with pytest.raises(ValueError):
+            fa.fa_decode_kv4(*args, 0.125)
+    for first in (n.float(), n[None], n.cpu()):
+        with pytest.raises(ValueError):
+            fa.fa_kv4_append(q[:, :, :1].contiguous(), q[:, :, :1].contiguous(), *c.args, first)
+    assert fa.fa_last_device_error() == 0

@@ -294,3 +294,19 @@ def test_backward_short_wait_limit_reports_and_recovers():
             fa.fa_set_wait_timeout_ns(0)
         grads = backward(q, k, v, o, lse, do, scale_for(d), 500, 4, ws)
         check_backward(q[:1], k[:1], v[:1], do[:1], [g[:1] for g in grads], scale_for(d), 500, 4, kv_heads=[0, 15])
+
+
+def test_backward_large_offsets():
+    # operands and gradients beyond 2^31 bytes from the base; without sinks no block is dealt in
+    # parts, so that a head's bits do not depend on its neighbours
+    B, H, N, d = 70, 8, 16384, 128
+    small = inputs(1, 1, 1, N, d, seed=17)
+    big = [torch.zeros((B, H, N, d), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for t, x in zip(big, small):
+        t[-1, -1] = x[0, 0]
+    outs = []
+    for q, k, v, do in (big, small):
+        o, lse = forward(q, k, v, scale_for(d), 200, 0)
+        outs.append(backward(q, k, v, o, lse, do, scale_for(d), 200, 0))
+    for b, s in zip(*outs):
+        assert torch.equal(b[-1, -1], s[0, 0]) and (b[0] == 0).all()

@@ -107,7 +107,7 @@ CACHE_BAD = [
     (dict(kc=None), 1), (dict(ks=MIS), 1), (dict(vc=None), 1), (dict(vs=MIS), 1), (dict(table=None), 1),
     (dict(B=0), 1), (dict(H_kv=0), 1), (dict(N=0), 1), (dict(n_pages=0), 1), (dict(max_blocks=0), 1),
     (dict(page=8), 1), (dict(page=24), 1), (dict(page=512), 1), (dict(page=0), 1), (dict(d=96), 2),
-    (dict(max_blocks=1 << 28), 2)]
+    (dict(max_blocks=1 << 28), 2), (dict(max_blocks=(1 << 27) - 1), 2)]  # the last: 2^31 - 16 tokens
 
 
 @pytest.mark.parametrize("change,status", CACHE_BAD + [
