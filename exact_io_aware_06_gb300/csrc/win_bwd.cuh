@@ -17,7 +17,7 @@ struct WinBwdArgs {
     int N, Np, n_kv, BH;    // BH: K/V heads (B * H_kv), the grid's head count
     int H, H_kv;            // query heads and K/V heads per batch; H_kv divides H
     WinSplit split;         // sink blocks' pieces
-    float* part;            // their dV, dK: [BH][n_part][pieces + 1][2][128][d] float32
+    float* part;            // their dV, dK: [BH][n_part][pieces + 1][2][d / 4][128][4] float32
     float c_log2;           // scale * log2(e), not 0
     float scale;
     DevCtl ctl;
@@ -213,49 +213,52 @@ struct RowsOut {
 };
 
 // This thread's key row of dV (which = 0) or dK, unscaled, from TMEM to its place in the
-// workspace.  Rows past N are zeros and fill their places too.
+// workspace, where four columns of all rows lie side by side: a warp's store is 512 bytes in a run.
+// Rows past N are zeros and fill their places too.
 template <int D>
 __device__ __forceinline__ void write_part_row(const BwdArgs& a, const Item& I, int which, int row, uint32_t taddr) {
-    float* dst = a.part + ((((static_cast<size_t>(I.bh) * a.split.n_part + I.kvb) * (a.split.pieces + 1) + I.slot) * 2 + which) *
-                               kBlk + row) * D;
+    uint4* dst = reinterpret_cast<uint4*>(a.part) +
+                 (((static_cast<size_t>(I.bh) * a.split.n_part + I.kvb) * (a.split.pieces + 1) + I.slot) * 2 + which) * (kBlk * D / 4) + row;
 #pragma unroll
     for (int h = 0; h < D / 32; ++h) {
         uint32_t r[32];
         tmem_ld32(taddr + 32 * h, r);
-        uint4* o4 = reinterpret_cast<uint4*>(dst + 32 * h);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) o4[x] = make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
+        for (int x = 0; x < 8; ++x) dst[(8 * h + x) * kBlk] = make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
     }
 }
 
 // dV and dK of the blocks that were dealt in parts: the parts added in order, dK times scale,
-// rounded once.  Thread t of n, eight neighbouring values at a time.
+// rounded once.  Thread t of n (both multiples of 32 apart from the lane), eight neighbouring values
+// of a row at a time: a warp takes 8 rows x 32 columns, whole lines of the parts and 64-byte runs of
+// the result.
 template <int D>
 __device__ __forceinline__ void join_parts(const BwdArgs& a, int t, int n) {
-    constexpr int kVec = D / 8;
+    constexpr int kCols = D / 32, kTiles = kCols * (kBlk / 8);  // such tiles of a block's dV or dK
     const WinSplit& sp = a.split;
-    const size_t work = static_cast<size_t>(a.BH) * sp.n_part * 2 * kBlk * kVec;
+    const size_t work = static_cast<size_t>(a.BH) * sp.n_part * 2 * kTiles * 32;
     for (size_t x = t; x < work; x += n) {
-        const int vec = static_cast<int>(x % kVec), row = static_cast<int>(x / kVec % kBlk);
-        const int which = static_cast<int>(x / (kVec * kBlk) % 2);
-        const size_t blk = x / (2 * kVec * kBlk);  // bh * n_part + kvb
+        const int lane = static_cast<int>(x % 32), tile = static_cast<int>(x / 32 % kTiles);
+        const int row = tile / kCols * 8 + lane % 8, vec = tile % kCols * 4 + lane / 8;
+        const int which = static_cast<int>(x / (32 * kTiles) % 2);
+        const size_t blk = x / (2 * 32 * kTiles);  // bh * n_part + kvb
         const int kvb = static_cast<int>(blk % sp.n_part);
         const size_t bh = blk / sp.n_part;
         const int key = kvb * kBlk + row;
         if (key >= a.N) continue;
         const int slots = 1 + (a.n_kv - 1 - sp.reach - kvb + sp.per - 1) / sp.per;
-        const float4* src = reinterpret_cast<const float4*>(a.part) +
-                            ((blk * (sp.pieces + 1) * 2 + which) * kBlk + row) * (D / 4) + 2 * vec;
+        const float4* src =
+            reinterpret_cast<const float4*>(a.part) + (blk * (sp.pieces + 1) * 2 + which) * (kBlk * D / 4) + 2 * vec * kBlk + row;
         float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
 #pragma unroll 4
         for (int i = 0; i < slots; ++i) {
-            const float4 y = src[0], z = src[1];
+            const float4 y = src[0], z = src[kBlk];
             u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
             w.x += z.x, w.y += z.y, w.z += z.z, w.w += z.w;
-            src += 2 * kBlk * (D / 4);
+            src += 2 * (kBlk * D / 4);
         }
         const float f = which ? a.scale : 1.f;
-        static_cast<uint4*>(which ? a.dk : a.dv)[(bh * a.N + key) * kVec + vec] =
+        static_cast<uint4*>(which ? a.dk : a.dv)[(bh * a.N + key) * (D / 8) + vec] =
             make_uint4(pack_bf16x2(u.x * f, u.y * f), pack_bf16x2(u.z * f, u.w * f), pack_bf16x2(w.x * f, w.y * f),
                        pack_bf16x2(w.z * f, w.w * f));
     }
