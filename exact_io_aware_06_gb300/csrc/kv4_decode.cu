@@ -31,6 +31,9 @@
 //     requests or a part of one.  Whole requests are written at once; parts go to the
 //     workspace, and decode_join_kernel adds them.  The cut depends on the lengths alone, so
 //     results do not change from call to call.
+// Measured (H32 H_kv8 d128): 64 requests of 1000 to 32768 tokens 318 us (3.9 TB/s; about 400
+// instructions per 16 tokens and head, 63% of the integer pipe; three CTAs of 168 registers an SM: two
+// 347 us, four with spills 349); one request of 16000 tokens 15.4 us.
 #include <atomic>
 #include <cmath>
 

@@ -229,9 +229,8 @@ __device__ __forceinline__ void write_part_row(const BwdArgs& a, const Item& I, 
 }
 
 // dV and dK of the blocks that were dealt in parts: the parts added in order, dK times scale,
-// rounded once.  Thread t of n (both multiples of 32 apart from the lane), eight neighbouring values
-// of a row at a time: a warp takes 8 rows x 32 columns, whole lines of the parts and 64-byte runs of
-// the result.
+// rounded once.  Thread t of n (whole warps), eight neighbouring values of a row at a time: a warp
+// takes 8 rows x 32 columns, whole lines of the parts and 64-byte runs of the result.
 template <int D>
 __device__ __forceinline__ void join_parts(const BwdArgs& a, int t, int n) {
     constexpr int kCols = D / 32, kTiles = kCols * (kBlk / 8);  // such tiles of a block's dV or dK

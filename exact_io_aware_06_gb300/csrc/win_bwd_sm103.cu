@@ -28,7 +28,9 @@
 // The d = 128 main kernel: S^T, dP^T, dV and dK fill TMEM, P^T and dS^T are written over S^T and
 // dP^T, and roles and the order of MMAs are the plain backward's.  Q and dO have rings of their own,
 // and the issuing thread waits for the next Q behind dV and for the next dO behind dK: with both under
-// one barrier, in front of dV, it waited 530 of a pair's 2800 cycles for them.
+// one barrier, in front of dV, it waited 530 of a pair's 2800 cycles for them.  Measured (N8191 W1024,
+// 16 sinks, H16 H_kv4): 110 us, 2640 cycles a pair of blocks inside an item, of which the tensor pipe
+// works 2152.
 #include <type_traits>
 
 #include "win_bwd.cuh"
