@@ -77,6 +77,58 @@ def test_training_step(B, H, H_kv, N, d, window, n_sink):
     check()
 
 
+def test_two_captured_steps_at_once_on_two_streams():
+    # each with its own tensors and workspaces; the same bits as one after the other
+    d, H, H_kv, N, window = 64, 8, 2, 1500, 200
+    f, eps = fa.rope_frequencies(d), EPS
+
+    class Layer:
+        def __init__(self, seed):
+            self.qkv, self.qw, self.kw, _ = nr.make(1, N, H, H_kv, d, "bf16", seed=seed)
+            self.do = win.rand((1, H, N, d), seed + 1)
+            self.q, self.k, self.v = empty(1, H, N, d), empty(1, H_kv, N, d), empty(1, H_kv, N, d)
+            self.o, self.lse = empty(1, H, N, d), empty(1, H, N, dtype=torch.float32)
+            self.grads = [torch.full_like(t, float("nan")) for t in (self.q, self.k, self.v)]
+            self.dqkv, self.dw = torch.full_like(self.qkv, float("nan")), [empty(d, dtype=torch.float32) for _ in "qk"]
+            self.ws = space(max(fa.fa_bwd_window_workspace_size(1, H, H_kv, N, d, window, 4),
+                                fa.fa_qk_norm_rope_bwd_workspace_size(1, H, H_kv, N, d)))
+            self.c = kv4.Cache([N], H_kv, d, 32, seed=seed)
+            self.first, self.n = kv4.ints([0]), kv4.ints([N])
+            self.q1, self.o1 = win.rand((1, H, 1, d), seed + 2), empty(1, H, 1, d)
+            self.ws1 = space(fa.fa_decode_kv4_workspace_size(1, H, H_kv, 1, d))
+
+        def run(self):
+            fa.fa_qk_norm_rope(self.qkv, self.qw, self.kw, None, f, self.q, self.k, self.v, eps)
+            fa.fa_fwd_window(self.q, self.k, self.v, self.o, self.lse, 0.125, window, 4)
+            fa.fa_kv4_append(self.k, self.v, *self.c.args, self.first)
+            fa.fa_bwd_window(self.q, self.k, self.v, self.o, self.lse, self.do, *self.grads, self.ws, 0.125, window, 4)
+            fa.fa_decode_kv4(self.q1, *self.c.args, self.n, self.o1, None, self.ws1, 0.125, window, 4)
+            fa.fa_qk_norm_rope_bwd(self.qkv, self.qw, self.kw, None, f, *self.grads, self.dqkv, *self.dw, self.ws, eps)
+
+        def results(self):
+            return [self.o, self.lse, self.dqkv, *self.dw, self.o1]
+
+    layers = [Layer(3), Layer(30)]
+    for layer in layers:
+        layer.run()
+    check_status()
+    ref = [[t.clone() for t in layer.results()] for layer in layers]
+    graphs = [captured(layer.run) for layer in layers]
+    for layer in layers:
+        for t in layer.results():
+            t.fill_(float("nan"))
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    check_status()
+    for layer, r in zip(layers, ref):
+        assert all(torch.equal(a, b) for a, b in zip(layer.results(), r))
+
+
 @pytest.mark.parametrize("d,H,H_kv,page,window,n_sink", [(64, 4, 2, 16, 60, 4), (128, 6, 1, 32, 5000, 0),
                                                          (64, 3, 3, 64, 33, 40)])
 def test_prompt_then_tokens(d, H, H_kv, page, window, n_sink):
