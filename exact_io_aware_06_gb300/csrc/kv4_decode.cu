@@ -36,6 +36,7 @@
 // 347 us, four with spills 349); one request of 16000 tokens 15.4 us.
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "layer_ops.h"
@@ -269,29 +270,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                 atomicCAS(a.ctl.status, kDevOk, kDevIndex);
             }
         };
-        // the lanes' copies of a tile; one that is not there is not copied
-        auto copy = [&](uint32_t dst, int tok, int page) {
-            if (tok == kNowhere) return;
-            const size_t row = page * page_rows + (tok & page_mask);
-            const uint8_t* ks = k_src + row * (D / 2);
-            const uint8_t* vs = v_src + row * (D / 2);
+        // the lanes' copies of a tile from its row of the cache on, and of both tiles of a step: the
+        // second is mostly the next one in the same page.  One that is not there is not copied.
+        auto copy_row = [&](uint32_t dst, const uint8_t* ks, const uint8_t* vs, const uint8_t* ss) {
 #pragma unroll
             for (int x = 0; x < T::kCodes; x += 512) {
                 cp_async16(dst + x + lane * 16, ks + x);
                 cp_async16(dst + T::kOffV + x + lane * 16, vs + x);
             }
-            if (lane < 2 * kPieces) cp_async16(dst + T::kOffKs + lane * 16, s_src + row * (D / 16));
+            if (lane < 2 * kPieces) cp_async16(dst + T::kOffKs + lane * 16, ss);
+        };
+        auto copy = [&](uint32_t dst, const int (&tok)[kTiles], const int (&page)[kTiles]) {
+            bool next = false;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                if (next || tok[j] == kNowhere) {
+                    next = false;
+                    continue;
+                }
+                const size_t row = page[j] * page_rows + (tok[j] & page_mask);
+                const uint8_t* ks = k_src + row * (D / 2);
+                const uint8_t* vs = v_src + row * (D / 2);
+                const uint8_t* ss = s_src + row * (D / 16);
+                copy_row(dst + j * T::kBytes, ks, vs, ss);
+                if (j + 1 < kTiles && tok[j + 1] == tok[j] + kTileTokens && page[j + 1] == page[j]) {
+                    copy_row(dst + (j + 1) * T::kBytes, ks + T::kCodes, vs + T::kCodes, ss + T::kScales);
+                    next = true;
+                }
+            }
         };
         const uint32_t ring0 = smem_u32(ring);
         int toks[kStages][kTiles], next_tok[kTiles], next_page[kTiles];  // toks[s]: the s-th step from here on
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
-                int page;
-                place(i, j, toks[i][j], page);
-                copy(ring0 + (i * kTiles + j) * T::kBytes, toks[i][j], page);
-            }
+            for (int j = 0; j < kTiles; ++j) place(i, j, toks[i][j], next_page[j]);
+            copy(ring0 + i * kTiles * T::kBytes, toks[i], next_page);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
 #pragma unroll
@@ -374,11 +388,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         for (int i = 0; i < n_mine; ++i) {
             // the ring position that step i - 1 has left, which every lane has read, takes step
             // i + kStages - 1
+            copy(ring0 + fill * kTiles * T::kBytes, next_tok, next_page);
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
-                copy(ring0 + (fill * kTiles + j) * T::kBytes, next_tok[j], next_page[j]);
-                toks[kStages - 1][j] = next_tok[j];
-            }
+            for (int j = 0; j < kTiles; ++j) toks[kStages - 1][j] = next_tok[j];
             asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) place(i + kStages, j, next_tok[j], next_page[j]);
@@ -488,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                     load_words(sj + T::kOffV + (r * 32 + lane) * (D / 8), vw[r]);
                     load_words(sj + T::kOffVs + (r * 4 + g / 2) * (D / 8), vs[r]);
                 }
+                auto pv = [&](auto edge_c) {
 #pragma unroll
                 for (int c = 0; c < G; ++c) {
                     uint32_t f[2][4];
@@ -506,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                         for (int r = 0; r < 2; ++r) {
                             const float s = __uint_as_float(__byte_perm(vs[r][c], 0u, half_sel));
                             float y0 = p[n][2 * r] * s, y1 = p[n][2 * r + 1] * s;
-                            if (edge[j]) {  // a hidden token's scale may be anything
+                            if constexpr (decltype(edge_c)::value) {  // a hidden token's scale may be anything
                                 if (x[j][n][2 * r] == -INFINITY) y0 = 0.f;
                                 if (x[j][n][2 * r + 1] == -INFINITY) y1 = 0.f;
                             }
@@ -516,6 +529,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
                         mma_bf16(o[n][c][1], f[1], ps[0], ps[1], o[n][c][1]);
                     }
                 }
+                };
+                if (edge[j])
+                    pv(std::true_type{});
+                else
+                    pv(std::false_type{});
             }
             __syncwarp();  // every lane has read the step
             fill = stage;
