@@ -49,7 +49,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTiles = 2;                      // tiles of 16 tokens that a warp works on together
 constexpr int kUnitTiles = kWarps * kTiles;    // tiles of a unit
-constexpr int kStages = 3;                     // ring of such steps per warp
+constexpr int kStages = 2;                     // ring of such steps per warp
 constexpr int kNowhere = kMaxTokens;           // the "token" of a tile that is not there: hidden to every row
 constexpr float kTau = 8.0f;        // lazy rescale: the reference moves by more than this (log2)
 constexpr int kMaxCtas = 1024;
