@@ -26,14 +26,14 @@
 //     one movmatrix per 8 x 8 block.
 //   * Copies.  Each warp runs its own ring of 16-token tiles, filled by 16-byte asynchronous
 //     copies of its lanes (a tile never crosses a page); no barrier between warps.
-//   * Splitting.  The units of 128 tokens of all requests and heads form one list that is cut
+//   * Splitting.  The units of 64 or 128 tokens (32 a warp) of all requests and heads form one list that is cut
 //     evenly over the resident CTAs, whatever the lengths are: a CTA's share may cover several
 //     requests or a part of one.  Whole requests are written at once; parts go to the
 //     workspace, and decode_join_kernel adds them.  The cut depends on the lengths alone, so
 //     results do not change from call to call.
-// Measured (H32 H_kv8 d128): 64 requests of 1000 to 32768 tokens 318 us (3.9 TB/s; about 400
-// instructions per 16 tokens and head, 63% of the integer pipe; three CTAs of 168 registers an SM: two
-// 347 us, four with spills 349); one request of 16000 tokens 15.4 us.
+// Measured (H32 H_kv8 d128): 64 requests of 1000 to 32768 tokens 294 us (4.2 TB/s, 63% of
+// the copy rate, bound by the instructions that expand codes; twelve warps of 168 registers an SM:
+// eight took 8% longer, sixteen with spills 10%; rings of three steps 1%); one of 16000 tokens 15.1 us.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -45,10 +45,7 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kTiles = 2;                      // tiles of 16 tokens that a warp works on together
-constexpr int kUnitTiles = kWarps * kTiles;    // tiles of a unit
 constexpr int kStages = 2;                     // ring of such steps per warp
 constexpr int kNowhere = kMaxTokens;           // the "token" of a tile that is not there: hidden to every row
 constexpr float kTau = 8.0f;        // lazy rescale: the reference moves by more than this (log2)
@@ -70,6 +67,7 @@ struct Reach {
     int len, sink, start, n_tiles, n_units;
 };
 
+template <int UNIT>  // tiles of a unit
 __device__ __forceinline__ Reach reach_of(const DecodeArgs& a, long long b) {
     Reach r;
     r.len = a.lengths[b];
@@ -85,7 +83,7 @@ __device__ __forceinline__ Reach reach_of(const DecodeArgs& a, long long b) {
     const int end = (r.len + kTileTokens - 1) / kTileTokens;
     r.n_tiles = r.sink + max(0, end - r.start);
     if (r.len == 0) r.n_tiles = 0;
-    r.n_units = (r.n_tiles + kUnitTiles - 1) / kUnitTiles;
+    r.n_units = (r.n_tiles + UNIT - 1) / UNIT;
     return r;
 }
 
@@ -164,13 +162,15 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
     }
 }
 
-// NT: tiles of 8 query rows that share the expanded codes (1 or 2).
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+// NT: tiles of 8 query rows that share the expanded codes (1 or 2); kWarps: warps of a CTA, whose
+// resident ones are twelve an SM (eight for NT = 2).
+template <int D, int NT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 12 : 8) / kWarps)
     decode_kv4_kernel(const __grid_constant__ DecodeArgs a, const Work work, const int row_tiles) {
     using T = TileCfg<D>;
     constexpr int G = D / 32;      // groups of 32 values
     constexpr int ROWS = 8 * NT;
+    constexpr int kThreads = 32 * kWarps, kUnitTiles = kWarps * kTiles;
     extern __shared__ __align__(128) uint8_t smem[];  // the warps' rings; at an entry's end their results
     __shared__ long long s_sum[kWarps];
     __shared__ long long s_found[2];  // request of the first unit, units before it
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += reach_of(a, b).n_units;
+    for (int b = b0; b < b1; ++b) mine += reach_of<kUnitTiles>(a, b).n_units;
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
         long long at = before;
         for (int b = b0; b < b1; ++b) {
             work.prefix[b] = at;
-            at += reach_of(a, b).n_units;
+            at += reach_of<kUnitTiles>(a, b).n_units;
         }
         if (b1 == a.B && b0 < b1) work.prefix[a.B] = at;
     }
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     if (u_begin >= before * entries && u_begin < (before + mine) * entries) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
-            const int n = reach_of(a, b).n_units;
+            const int n = reach_of<kUnitTiles>(a, b).n_units;
             if (u_begin < (at + n) * entries) {
                 s_found[0] = b;
                 s_found[1] = at;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     const uint32_t half_sel = (g & 1) ? 0x3244u : 0x1044u;  // this token's half of a pair's word, as a float
     const int rows_all = a.H / a.cache.H_kv * a.N_q;  // query rows of a K/V head
     for (long long u = u_begin; u < u_end;) {
-        const Reach R = reach_of(a, b);
+        const Reach R = reach_of<kUnitTiles>(a, b);
         if (R.n_units == 0) {
             ++b;
             continue;
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, int kWarps>
 cudaError_t launch_impl(const DecodeArgs& a, cudaStream_t s) {
     constexpr int kRings = kWarps * kStages * kTiles * TileCfg<D>::kBytes;
     constexpr int kResults = kWarps * 8 * NT * (D + 2) * static_cast<int>(sizeof(float));
@@ -719,10 +719,10 @@ cudaError_t launch_impl(const DecodeArgs& a, cudaStream_t s) {
     int ctas = dev < 64 ? resident[dev].load() : 0;
     if (ctas == 0) {
         int sms = 0, per_sm = 0;
-        e = cudaFuncSetAttribute(decode_kv4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(decode_kv4_kernel<D, NT, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kv4_kernel<D, NT>, kThreads, kSmem);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kv4_kernel<D, NT, kWarps>, 32 * kWarps, kSmem);
         if (e != cudaSuccess) return e;
         ctas = sms * (per_sm < 1 ? 1 : per_sm);
         if (ctas > kMaxCtas) ctas = kMaxCtas;
@@ -731,13 +731,13 @@ cudaError_t launch_impl(const DecodeArgs& a, cudaStream_t s) {
     const int rows = a.H / a.cache.H_kv * a.N_q;
     const int row_tiles = (rows + 8 * NT - 1) / (8 * NT);
     // no more CTAs than units that the tables could hold
-    const long long most_units = ((static_cast<long long>(a.cache.max_blocks) << a.cache.page_log2) / (16 * kUnitTiles) + 1) *
+    const long long most_units = ((static_cast<long long>(a.cache.max_blocks) << a.cache.page_log2) / (16 * kWarps * kTiles) + 1) *
                                  a.B * a.cache.H_kv * row_tiles;
     const long long grid = ctas < most_units ? ctas : most_units;
     Work w;
     w.prefix = static_cast<long long*>(a.workspace);
     w.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + prefix_bytes(a.B));
-    e = launch_pdl(decode_kv4_kernel<D, NT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a, w,
+    e = launch_pdl(decode_kv4_kernel<D, NT, kWarps>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), kSmem, s, a, w,
                    row_tiles);
     if (e != cudaSuccess) return e;
     return launch_pdl(decode_join_kernel<D>, dim3(static_cast<unsigned>(a.B * a.H * a.N_q)), dim3(256), 0, s, a, w,
@@ -751,10 +751,23 @@ size_t decode_kv4_workspace_bytes(int B, int H, int H_kv, int N_q, int d) {
     return prefix_bytes(B) + static_cast<size_t>(2 * kMaxCtas) * (rows <= 8 ? 8 : 16) * (d + 2) * sizeof(float);
 }
 
+namespace {
+// With about as many heads to attend to as SMs or more, CTAs of two warps (their entries end apart
+// from one another); with fewer, of four, which leave half the parts to join.  Two against four, 8 K/V heads of
+// d = 128: 64 requests of 1000 to 32768 tokens 294 us against 301, 64 of 100 to 1000 32 against 37, 16
+// of 2000 to 8000 34.1 against 34.8; 8 of 4000 to 8000 26.8 against 25.8, 4 of 8000 22.1 against 21.8, one of
+// 16000 16.6 against 15.1.
+template <int D, int NT>
+cudaError_t launch_warps(const DecodeArgs& a, cudaStream_t s) {
+    const bool many = static_cast<long long>(a.B) * a.cache.H_kv >= 128;
+    return many ? launch_impl<D, NT, 2>(a, s) : launch_impl<D, NT, 4>(a, s);
+}
+}  // namespace
+
 cudaError_t launch_decode_kv4(const DecodeArgs& a, int d, cudaStream_t s) {
     const int rows = a.H / a.cache.H_kv * a.N_q;
-    if (d == 64) return rows <= 8 ? launch_impl<64, 1>(a, s) : launch_impl<64, 2>(a, s);
-    return rows <= 8 ? launch_impl<128, 1>(a, s) : launch_impl<128, 2>(a, s);
+    if (d == 64) return rows <= 8 ? launch_warps<64, 1>(a, s) : launch_warps<64, 2>(a, s);
+    return rows <= 8 ? launch_warps<128, 1>(a, s) : launch_warps<128, 2>(a, s);
 }
 
 }  // namespace fa

@@ -267,6 +267,13 @@ def test_decode_many_requests_and_one_long_one():
     run_and_compare([7] * 300 + [4000], 4, 2, 1, 64, 16)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,H_kv,N_q,window", [(8, 2, 1, 0), (4, 2, 5, 0), (4, 2, 5, 40), (2, 2, 1, 60)])
+def test_decode_more_heads_than_sms(H, H_kv, N_q, window, d):
+    # more K/V heads of requests than SMs: CTAs of two warps
+    run_and_compare([(37 * i) % 300 for i in range(80)], H, H_kv, N_q, d, 32, window, 4)
+
+
 def test_decode_long_single_head():
     run_and_compare([30011], 2, 1, 1, 128, 256)
 
