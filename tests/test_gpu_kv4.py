@@ -98,6 +98,20 @@ def test_append_and_read_ragged(d, page):
         assert torch.equal(got.cpu(), bf16_of(ref))
 
 
+@pytest.mark.parametrize("d,lengths", [(64, [9001, 3, 0, 8192]), (128, [5001, 5000, 1, 16])])
+def test_read_many_rows(d, lengths):
+    # enough rows for two a thread; odd and even lengths, and an odd number of rows
+    c = Cache(lengths, 8, d, 64)
+    k, v = c.fill(51)
+    N = max(lengths)
+    back = [torch.full((4, 8, N, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    fa.fa_kv4_read(*c.args, ints(lengths), *back)
+    check_status()
+    for t, values in zip(back, (k, v)):
+        for b, n in enumerate(lengths):
+            assert np.array_equal(f64(t[b, :, :n]), plain64.bf16_round(values[b][:, :n])) and (t[b, :, n:] == 0).all()
+
+
 def test_values_at_the_format_s_edges():
     # ties, zeros, one value alone, the smallest and largest bfloat16, infinities and NaN
     d, n = 64, 12
