@@ -6,7 +6,7 @@
 // maximum is two shuffles.  A thread takes a row of K and the same row of V: the way to their
 // bytes (request, its first token, its page: three dependent loads) is gone once for both.
 // Instructions bound these kernels next to memory, hence the arithmetic below.  Measured for two
-// prompts of 8192 tokens, 8 heads of d = 128 (67 MB of bf16): append and read 32.2 us together, 5.4 TB/s.
+// prompts of 8192 tokens, 8 heads of d = 128 (67 MB of bf16): append and read 31.3 us together, 5.5 TB/s.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -40,11 +40,13 @@ __device__ __forceinline__ float bf16_at(uint32_t w, int i) {
 //
 // x / s has to round as the quotient itself does, halves to even.  x and s have 8 bits each, so a
 // quotient below 8 that is no half of an odd integer is at least 2^-10 from one: x times the
-// reciprocal of s (off by 2^-21), rounded to a multiple of 2^-12 by adding and taking away
-// 1.5 2^11, is on a half exactly where the quotient is, and on the quotient's side of it
-// elsewhere.  Division took 260 operations a row and 32 us for 131072 rows of K and V, where
-// memory needs 13.  A subnormal s, which has fewer bits and whose reciprocal may overflow, divides.
+// reciprocal of s (off by 2^-20), rounded to a multiple of 2^-12 by adding 1.5 2^11, is on a half
+// exactly where the quotient is, and on the quotient's side of it elsewhere.  Adding the rest of
+// 1.5 2^23 + 8 rounds to the integer, and leaves the nibble in the low bits.  Division took 260
+// operations a row and 32 us for 131072 rows of K and V, where memory needs 13.  A subnormal s, which
+// has fewer bits and whose reciprocal may overflow, divides.
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float s) {
+    constexpr float kInt = 12582920.f;  // 1.5 2^23 + 8
     float q[8];
     if (s >= 0x1p-120f) {
         float inv;
@@ -52,26 +54,21 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float s) {
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float2 t = __fmul2_rn(make_float2(bf16_at(w[i], 0), bf16_at(w[i], 1)), inv2);
-            t = __fadd2_rn(__fadd2_rn(t, make_float2(3072.f, 3072.f)), make_float2(-3072.f, -3072.f));
-            // the nearest integer, halves to even
-            t = __fadd2_rn(__fadd2_rn(t, make_float2(12582912.f, 12582912.f)), make_float2(-12582912.f, -12582912.f));
+            float2 t = __ffma2_rn(make_float2(bf16_at(w[i], 0), bf16_at(w[i], 1)), inv2, make_float2(3072.f, 3072.f));
+            t = __fadd2_rn(t, make_float2(kInt - 3072.f, kInt - 3072.f));
             q[2 * i] = t.x;
             q[2 * i + 1] = t.y;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            q[i] = fminf(fmaxf(rintf(__fdiv_rn(bf16_at(w[i / 2], i & 1), s)), -7.f), 7.f);
+            q[i] = fminf(fmaxf(rintf(__fdiv_rn(bf16_at(w[i / 2], i & 1), s)), -7.f), 7.f) + kInt;
     }
-    // sum of (q + 8) 16^i over four values: below 2^16, an integer that 2^23 puts in the low bits
-    uint32_t half[2];
+    // sum of bits 16^i; what kInt's own bits, 0x4B400008 without the 8, add to it comes off again
+    uint32_t word = __float_as_uint(q[7]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float lo = fmaf(q[4 * h + 1], 16.f, q[4 * h]), hi = fmaf(q[4 * h + 3], 16.f, q[4 * h + 2]);
-        half[h] = __float_as_uint(fmaf(hi, 256.f, lo) + (8388608.f + 0x8888));
-    }
-    return __byte_perm(half[0], half[1], 0x5410);
+    for (int i = 6; i >= 0; --i) word = word * 16 + __float_as_uint(q[i]);
+    return word - 0x3F400000u;
 }
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
