@@ -46,7 +46,7 @@ __device__ __forceinline__ float bf16_at(uint32_t w, int i) {
 // operations a row and 32 us for 131072 rows of K and V, where memory needs 13.  A subnormal s, which
 // has fewer bits and whose reciprocal may overflow, divides.
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float s) {
-    constexpr float kInt = 12582920.f;  // 1.5 2^23 + 8
+    constexpr float kSnap = 0x1.8p11f, kInt = 0x1.8p23f + 8.f;
     float q[8];
     if (s >= 0x1p-120f) {
         float inv;
@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float s) {
         const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float2 t = __ffma2_rn(make_float2(bf16_at(w[i], 0), bf16_at(w[i], 1)), inv2, make_float2(3072.f, 3072.f));
-            t = __fadd2_rn(t, make_float2(kInt - 3072.f, kInt - 3072.f));
+            float2 t = __ffma2_rn(make_float2(bf16_at(w[i], 0), bf16_at(w[i], 1)), inv2, make_float2(kSnap, kSnap));
+            t = __fadd2_rn(t, make_float2(kInt - kSnap, kInt - kSnap));
             q[2 * i] = t.x;
             q[2 * i + 1] = t.y;
         }
