@@ -227,7 +227,8 @@ cudaError_t launch_kv4_append(const Kv4Cache& c, const void* k, const void* v, c
 namespace {
 template <int D, int ROWS>
 cudaError_t launch_read(const Kv4Cache& c, const int* lengths, void* k, void* v, int B, int N, DevCtl ctl, cudaStream_t s) {
-    const uint32_t per_head = (static_cast<uint32_t>(N) + ROWS - 1) / ROWS, runs = static_cast<uint32_t>(B) * c.H_kv * per_head;
+    const uint32_t per_head = (static_cast<uint32_t>(N) + ROWS - 1) / ROWS;
+    const uint32_t runs = static_cast<uint32_t>(B) * c.H_kv * per_head;
     return launch_pdl(kv4_read_kernel<D, ROWS>, grid_of(runs, D / 8), dim3(kThreads), 0, s, c, lengths,
                       static_cast<uint4*>(k), static_cast<uint4*>(v), make_div(per_head), make_div(c.H_kv),
                       static_cast<uint32_t>(N), runs, ctl);

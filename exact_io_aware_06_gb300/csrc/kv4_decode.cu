@@ -17,11 +17,11 @@
 //     as they stand, five operations for eight values; Q is scaled to fit (exactly), and the
 //     codes' offset 8 costs nothing: the accumulators start at -8 sum_d q_d of each group of 32.
 //     V meets P s, whose range only bf16 holds: (word >> 4 i) & 0x000F000F | 0x43004300 is a
-//     pair of 128 + u, and one packed subtraction (exact) makes it u - 8.  (Adding up P in a further product, with A = -136 in
-//     one group's rows and 0 elsewhere, is cheaper, but 0 * NaN would carry a NaN scale from
-//     its own group's outputs into the others'.)  Scales: K's multiply the group's accumulators
-//     in float; V's multiply P in float, and the product is rounded to bf16 once, by at most
-//     2^-8 of its value.  The row sum, and with it lse, adds the unrounded P.
+//     pair of 128 + u, and one packed subtraction (exact) makes it u - 8.  (Taking 136 out by a
+//     further product with P is slower, and 0 * NaN would carry a NaN scale from its own group's
+//     outputs into the others'.)  Scales: K's multiply the group's accumulators in float; V's
+//     multiply P in float, and the product is rounded to bf16 once, by at most 2^-8 of its value.
+//     The row sum, and with it lse, adds the unrounded P.
 //   * S^T to P^T.  The accumulator layout of S^T transposed is the operand layout of P^T:
 //     one movmatrix per 8 x 8 block.
 //   * Copies.  Each warp runs its own ring of 16-token tiles, filled by 16-byte asynchronous
@@ -500,35 +500,36 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 12 : 8) / kWarps)
                     load_words(sj + T::kOffV + (r * 32 + lane) * (D / 8), vw[r]);
                     load_words(sj + T::kOffVs + (r * 4 + g / 2) * (D / 8), vs[r]);
                 }
+                // (a branch for each scale, within the loops, took 2% longer)
                 auto pv = [&](auto edge_c) {
 #pragma unroll
-                for (int c = 0; c < G; ++c) {
-                    uint32_t f[2][4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        // 16-bit words of this lane's two tokens side by side
-                        const uint32_t w = __byte_perm(vw[r][c / 2], vw[r][G / 2 + c / 2], (c & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e / 2][2 * r + (e & 1)] = sub_bf16x2(expand(w, e), 0x43084308u);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        // P times the group's scale, transposed into the operand of the second product
-                        uint32_t ps[2];
+                    for (int c = 0; c < G; ++c) {
+                        uint32_t f[2][4];
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float s = __uint_as_float(__byte_perm(vs[r][c], 0u, half_sel));
-                            float y0 = p[n][2 * r] * s, y1 = p[n][2 * r + 1] * s;
-                            if constexpr (decltype(edge_c)::value) {  // a hidden token's scale may be anything
-                                if (x[j][n][2 * r] == -INFINITY) y0 = 0.f;
-                                if (x[j][n][2 * r + 1] == -INFINITY) y1 = 0.f;
-                            }
-                            ps[r] = transpose8x8(pack_bf16x2(y0, y1));
+                            // 16-bit words of this lane's two tokens side by side
+                            const uint32_t w = __byte_perm(vw[r][c / 2], vw[r][G / 2 + c / 2], (c & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[e / 2][2 * r + (e & 1)] = sub_bf16x2(expand(w, e), 0x43084308u);
                         }
-                        mma_bf16(o[n][c][0], f[0], ps[0], ps[1], o[n][c][0]);
-                        mma_bf16(o[n][c][1], f[1], ps[0], ps[1], o[n][c][1]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            // P times the group's scale, transposed into the operand of the second product
+                            uint32_t ps[2];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float s = __uint_as_float(__byte_perm(vs[r][c], 0u, half_sel));
+                                float y0 = p[n][2 * r] * s, y1 = p[n][2 * r + 1] * s;
+                                if constexpr (decltype(edge_c)::value) {  // a hidden token's scale may be anything
+                                    if (x[j][n][2 * r] == -INFINITY) y0 = 0.f;
+                                    if (x[j][n][2 * r + 1] == -INFINITY) y1 = 0.f;
+                                }
+                                ps[r] = transpose8x8(pack_bf16x2(y0, y1));
+                            }
+                            mma_bf16(o[n][c][0], f[0], ps[0], ps[1], o[n][c][0]);
+                            mma_bf16(o[n][c][1], f[1], ps[0], ps[1], o[n][c][1]);
+                        }
                     }
-                }
                 };
                 if (edge[j])
                     pv(std::true_type{});
@@ -753,10 +754,10 @@ size_t decode_kv4_workspace_bytes(int B, int H, int H_kv, int N_q, int d) {
 
 namespace {
 // With about as many heads to attend to as SMs or more, CTAs of two warps (their entries end apart
-// from one another); with fewer, of four, which leave half the parts to join.  Two against four, 8 K/V heads of
-// d = 128: 64 requests of 1000 to 32768 tokens 294 us against 301, 64 of 100 to 1000 32 against 37, 16
-// of 2000 to 8000 34.1 against 34.8; 8 of 4000 to 8000 26.8 against 25.8, 4 of 8000 22.1 against 21.8, one of
-// 16000 16.6 against 15.1.
+// from one another); with fewer, of four, which leave half the parts to join.  Two against four, 8
+// K/V heads of d = 128: 64 requests of 1000 to 32768 tokens 294 us against 301, 64 of 100 to 1000 32
+// against 37, 16 of 2000 to 8000 34.1 against 34.8; 8 of 4000 to 8000 26.8 against 25.8, 4 of 8000
+// 22.1 against 21.8, one of 16000 16.6 against 15.1.
 template <int D, int NT>
 cudaError_t launch_warps(const DecodeArgs& a, cudaStream_t s) {
     const bool many = static_cast<long long>(a.B) * a.cache.H_kv >= 128;

@@ -233,8 +233,8 @@ __device__ __forceinline__ void heads_of(const NormRopeArgs& a, const Split& sp,
 // The loads of the next batch (of this token or the warp's next one) are in flight while one
 // is worked on: 4 KB a warp, 64 KB an SM.  Measured at B1 N16384 H32 H_kv8 d128 (403 MB):
 // batches of 8 passes and 4 blocks an SM 68.7 us (5.9 TB/s, 87% of the copy rate), 4 and 5
-// 69.8, 4 and 4 71.3, 2 and 5 83; waiting for each batch 113.  And weights are multiplied into a token's cosines and sines once for Q's
-// heads and once for K's.
+// 69.8, 4 and 4 71.3, 2 and 5 83; waiting for each batch 113.  And weights are multiplied into a
+// token's cosines and sines once for Q's heads and once for K's.
 template <int D, bool F32, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Split sp) {

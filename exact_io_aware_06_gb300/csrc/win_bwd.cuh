@@ -63,7 +63,8 @@ __device__ __forceinline__ Item item_at(const BwdArgs& a, int x) {
 // The query blocks of an item one after the other, without a division a step.
 struct Walk {
     int head, blk, end, i0;
-    __device__ __forceinline__ Walk(const BwdArgs& a, const Item& I) : head((I.bh / a.H_kv) * a.H + (I.bh % a.H_kv) * (a.H / a.H_kv)), blk(I.i0), end(I.i0 + I.n_loc), i0(I.i0) {}
+    __device__ __forceinline__ Walk(const BwdArgs& a, const Item& I)
+        : head((I.bh / a.H_kv) * a.H + (I.bh % a.H_kv) * (a.H / a.H_kv)), blk(I.i0), end(I.i0 + I.n_loc), i0(I.i0) {}
     __device__ __forceinline__ void next() {
         if (++blk == end) {
             blk = i0;
@@ -139,7 +140,8 @@ __device__ __forceinline__ void score_gradients(const uint32_t (&p)[32], const u
 // A key's queries counted from query q0: from the key on, a window's worth, or all for a sink.
 __device__ __forceinline__ void query_range(const WinSplit& sp, int key, int q0, int& q_first, int& q_end) {
     q_first = key - q0;
-    q_end = key < sp.sinks ? kBlk : static_cast<int>(min(static_cast<long long>(kBlk), static_cast<long long>(q_first) + sp.window));
+    const long long end = static_cast<long long>(q_first) + sp.window;
+    q_end = key < sp.sinks ? kBlk : static_cast<int>(min(static_cast<long long>(kBlk), end));
 }
 
 // 16 TMEM lanes x 64 columns, lane 4 r + q of the warp holding columns 8 j + 2 q, + 1 of rows r
@@ -217,8 +219,8 @@ struct RowsOut {
 // Rows past N are zeros and fill their places too.
 template <int D>
 __device__ __forceinline__ void write_part_row(const BwdArgs& a, const Item& I, int which, int row, uint32_t taddr) {
-    uint4* dst = reinterpret_cast<uint4*>(a.part) +
-                 (((static_cast<size_t>(I.bh) * a.split.n_part + I.kvb) * (a.split.pieces + 1) + I.slot) * 2 + which) * (kBlk * D / 4) + row;
+    const size_t part = (static_cast<size_t>(I.bh) * a.split.n_part + I.kvb) * (a.split.pieces + 1) + I.slot;
+    uint4* dst = reinterpret_cast<uint4*>(a.part) + (2 * part + which) * (kBlk * D / 4) + row;
 #pragma unroll
     for (int h = 0; h < D / 32; ++h) {
         uint32_t r[32];

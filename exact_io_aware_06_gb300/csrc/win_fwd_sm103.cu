@@ -18,8 +18,9 @@
 //     32-bit words, made by shifts from the row's two bounds, and one bit test per score.
 // This kernel is for d = 128, whose S (P in its place) and O fill TMEM; d = 64 has room for P of its
 // own and another schedule (win_fwd64_sm103.cu).  Warp roles, TMEM columns, the K/V bundle ring and
-// the order of MMAs are the plain forward's; O leaves through shared memory and TMA stores.  Every wait is bounded, and a wait
-// that runs out is recorded and ends the CTA with its copies and MMAs drained.
+// the order of MMAs are the plain forward's; O leaves through shared memory and TMA stores.  Every
+// wait is bounded, and a wait that runs out is recorded and ends the CTA with its copies and MMAs
+// drained.
 // Measured: N16384 W4096, 4 sinks, H32 H_kv8 620 us, 1553 TFLOP/s of visible pairs (81% of the bf16
 // peak); N8191 W1024, 16 sinks, H16 71 us.
 #include <type_traits>
