@@ -455,22 +455,35 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
 }
 
-// Sum of `rows` partial rows of 2 D values: a block owns 8 columns, 32 threads each.
+// Sum of `rows` partial rows of 2 D values: a block owns 8 columns, 32 threads each, which have 16
+// rows' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(256)
     dweight_sum_kernel(const float* __restrict__ part, int rows, float* dq, float* dk) {
-    __shared__ float sums[32][9];
+    constexpr int kTogether = 16;
+    __shared__ float sums[8][8];
     griddep_wait();
-    const int col = threadIdx.x % 8, k = threadIdx.x / 8;
+    const int col = threadIdx.x % 8, k = threadIdx.x / 8, warp = threadIdx.x / 32;
     const int x = blockIdx.x * 8 + col;
     float v = 0.f;
-    for (int r = k; r < rows; r += 32) v += part[static_cast<size_t>(r) * 2 * D + x];
-    sums[k][col] = v;
+    for (int r0 = k; r0 < rows; r0 += 32 * kTogether) {
+        float t[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+            const int r = r0 + 32 * i;
+            t[i] = r < rows ? part[static_cast<size_t>(r) * 2 * D + x] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) v += t[i];
+    }
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (threadIdx.x % 32 < 8) sums[warp][col] = v;
     __syncthreads();
-    if (k == 0) {
+    if (threadIdx.x < 8) {
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v += sums[i][col];
+        for (int i = 0; i < 8; ++i) v += sums[i][col];
         float* dst = x < D ? dq : dk;
         if (dst != nullptr) dst[x % D] = v;
     }
