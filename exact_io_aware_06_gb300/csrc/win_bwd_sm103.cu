@@ -397,41 +397,109 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- pre / post passes
-// -delta_i = -(dO_i . O_i) and -lse_i * log2(e) (rows past N: 0 and -inf, so that recomputed P is
-// exactly 0 there).  Both are stored negated so the main kernels add them with packed FMA/FADD.
-// D/8 threads per row, each reading 16 bytes of O and dO.
+// -delta_i and -lse_i * log2(e) (rows past N: 0 and -inf, so that recomputed P is exactly 0 there).
+// Both are stored negated so the main kernels add them with packed FMA/FADD.  D / 8 threads per row.
+//
+// delta_i = dO_i . O_i takes the O that the forward rounded to bf16, which is off by up to 2^-9 |O| |dO|
+// beside dP's spread: little against dS's own rounding where many keys average out in O, as much as
+// it at four keys.  A head's first kFirst rows, which see no more keys than that and have the largest
+// gradients, take delta_i = sum_j P_ij dP_ij instead, in `extra` CTAs beside the others, a warp a row
+// (dQ's error relative to 64 bits, N1024 W512 d64: 2.54e-3 -> 2.46e-3 for 1% of a step).  The same for
+// all rows of narrow windows would give 2.35e-3 for the 2.7e-3 of W8 and the 3.8e-3 of W2, at up to
+// half of a step: loads of single rows wait behind the stream of the others.
+constexpr int kFirst = 16;
+
+struct PrepArgs {
+    const uint4 *o, *dO, *q, *k, *v;
+    const float* lse;
+    float *ws_delta, *ws_lse2;
+    int BH, H, H_kv, N, Np;
+    int window, sinks;
+    float c_log2;
+    int extra;
+};
+
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sum = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), sum);
+        sum = fmaf(__uint_as_float(a[e] & 0xFFFF0000u), __uint_as_float(b[e] & 0xFFFF0000u), sum);
+    }
+    return sum;
+}
+template <int FROM, int TO>
+__device__ __forceinline__ float lanes_sum(float x) {  // over the lanes that differ in bits FROM .. TO / 2
+#pragma unroll
+    for (int off = FROM; off < TO; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// sum_j P_ij dP_ij of row i < min(N, kFirst) of query head bh, by one warp: D / 8 lanes a key, two
+// such rounds of keys at a time.
 template <int D>
-__global__ void win_bwd_prep_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dO,
-                                const float* __restrict__ lse, float* __restrict__ ws_delta,
-                                float* __restrict__ ws_lse2, int BH, int N, int Np) {
+__device__ __forceinline__ float delta_of_first(const PrepArgs& a, int bh, int i) {
+    constexpr int kT = D / 8, kSlots = 32 / kT;
+    const int lane = threadIdx.x % 32, part = lane % kT;
+    const int lo = max(0, static_cast<int>(max(-1ll, static_cast<long long>(i) - a.window + 1)));
+    const int front = min(a.sinks, lo), n = front + i - lo + 1;  // sinks in front of the window; keys
+    const size_t row = static_cast<size_t>(bh) * a.N + i;
+    const size_t kv = static_cast<size_t>((bh / a.H) * a.H_kv + (bh % a.H) / (a.H / a.H_kv)) * a.N;
+    const uint4 q = a.q[row * kT + part], d = a.dO[row * kT + part], zero = make_uint4(0, 0, 0, 0);
+    const float nl = -a.lse[row] * kLog2e;
+    float delta = 0.f;
+    for (int t = lane / kT; t - lane / kT < n; t += 2 * kSlots) {
+        uint4 k[2], v[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int x = t + u * kSlots;
+            const size_t at = (kv + (x < front ? x : lo + x - front)) * kT + part;
+            k[u] = x < n ? a.k[at] : zero;
+            v[u] = x < n ? a.v[at] : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float p = ex2_approx(fmaf(lanes_sum<1, kT>(dot8(q, k[u])), a.c_log2, nl));
+            const float dp = lanes_sum<1, kT>(dot8(d, v[u]));
+            if (t + u * kSlots < n) delta = fmaf(p, dp, delta);
+        }
+    }
+    return lanes_sum<kT, 32>(delta);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 8) win_bwd_prep_kernel(const PrepArgs a) {
     griddep_wait();               // O, dO may come from the kernel before this one
     griddep_launch_dependents();  // the main kernel may launch and set up meanwhile
-    const size_t tid = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const size_t nthreads = static_cast<size_t>(gridDim.x) * blockDim.x;
-    const size_t rows = static_cast<size_t>(BH) * Np;
-    constexpr int kT = D / 8;  // threads per row (8 or 16): the shuffles stay inside a warp
+    constexpr int kT = D / 8;     // threads per row (8 or 16): the shuffles stay inside a warp
+    const int N = a.N, Np = a.Np, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (static_cast<int>(blockIdx.x) < a.extra) {
+        const long long rows = static_cast<long long>(a.BH) * kFirst, step = a.extra * 8;
+        for (long long r = blockIdx.x * 8 + warp; r < rows; r += step) {
+            const int bh = static_cast<int>(r / kFirst), i = static_cast<int>(r % kFirst);
+            if (i >= N) continue;
+            const float delta = delta_of_first<D>(a, bh, i);
+            if (lane == 0) a.ws_delta[static_cast<size_t>(bh) * Np + i] = -delta;
+        }
+        return;
+    }
+    const int part = lane % kT;
+    const size_t tid = static_cast<size_t>(blockIdx.x - a.extra) * blockDim.x + threadIdx.x;
+    const size_t nthreads = static_cast<size_t>(gridDim.x - a.extra) * blockDim.x;
+    const size_t rows = static_cast<size_t>(a.BH) * Np;
     for (size_t base = tid; base < rows * kT; base += nthreads) {
         const size_t r = base / kT;
-        const int part = static_cast<int>(base % kT);
         const int bh = static_cast<int>(r / Np), i = static_cast<int>(r % Np);
         float sum = 0.f;
         if (i < N) {
             const size_t src = (static_cast<size_t>(bh) * N + i) * kT + part;
-            const uint4 a = o[src], b = dO[src];
-            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                sum = fmaf(__uint_as_float(av[x] << 16), __uint_as_float(bv[x] << 16), sum);
-                sum = fmaf(__uint_as_float(av[x] & 0xFFFF0000u), __uint_as_float(bv[x] & 0xFFFF0000u), sum);
-            }
+            sum = dot8(a.o[src], a.dO[src]);
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        if (kT == 16) sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum = lanes_sum<1, kT>(sum);
         if (part == 0) {
-            ws_delta[r] = -sum;
-            ws_lse2[r] = (i < N) ? -lse[static_cast<size_t>(bh) * N + i] * kLog2e : -INFINITY;
+            if (i >= N || i >= kFirst) a.ws_delta[r] = -sum;
+            a.ws_lse2[r] = (i < N) ? -a.lse[static_cast<size_t>(bh) * N + i] * kLog2e : -INFINITY;
         }
     }
 }
@@ -499,9 +567,26 @@ int launch_bwd_window(const void* q, const void* k, const void* v, const void* o
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return static_cast<int>(e);
-    e = launch_pdl(d == 64 ? win_bwd_prep_kernel<64> : win_bwd_prep_kernel<128>,
-                   dim3(grid_for(static_cast<size_t>(BH) * Np * (d / 8), 256, sms * 8)), dim3(256), 0, s,
-                   static_cast<const uint4*>(o), static_cast<const uint4*>(dO), lse, ws_delta, ws_lse2, BH, N, Np);
+    PrepArgs pa;
+    pa.o = static_cast<const uint4*>(o);
+    pa.dO = static_cast<const uint4*>(dO);
+    pa.q = static_cast<const uint4*>(q);
+    pa.k = static_cast<const uint4*>(k);
+    pa.v = static_cast<const uint4*>(v);
+    pa.lse = lse;
+    pa.ws_delta = ws_delta;
+    pa.ws_lse2 = ws_lse2;
+    pa.BH = BH;
+    pa.H = H;
+    pa.H_kv = H_kv;
+    pa.N = N;
+    pa.Np = Np;
+    pa.window = window;
+    pa.sinks = sp.sinks;
+    pa.c_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;
+    pa.extra = grid_for(static_cast<size_t>(BH) * kFirst, 8, 2 * sms);
+    const int others = grid_for(static_cast<size_t>(BH) * Np * (d / 8), 256, sms * 8 - pa.extra);
+    e = launch_pdl(d == 64 ? win_bwd_prep_kernel<64> : win_bwd_prep_kernel<128>, dim3(others + pa.extra), dim3(256), 0, s, pa);
     if (e != cudaSuccess) return static_cast<int>(e);
 
     CUtensorMap tq, tk, tv, tdo, tdk, tdv;
