@@ -404,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // beside dP's spread: little against dS's own rounding where many keys average out in O, as much as
 // it at four keys.  A head's first kFirst rows, which see no more keys than that and have the largest
 // gradients, take delta_i = sum_j P_ij dP_ij instead, in `extra` CTAs beside the others, a warp a row
-// (dQ's error relative to 64 bits, N1024 W512 d64: 2.54e-3 -> 2.46e-3 for 1% of a step).  The same for
-// all rows of narrow windows would give 2.35e-3 for the 2.7e-3 of W8 and the 3.8e-3 of W2, at up to
-// half of a step: loads of single rows wait behind the stream of the others.
-constexpr int kFirst = 16;
+// (dQ's error relative to 64 bits, N1024 W512 d64: 2.54e-3 -> 2.46e-3 for 1% of a step).  So do all rows
+// of sequences of up to kShort, and under a window and sinks of up to kNarrow keys in all, in a kernel
+// of their own.
+constexpr int kFirst = 16, kNarrow = 24, kShort = 128;
 
 struct PrepArgs {
     const uint4 *o, *dO, *q, *k, *v;
@@ -504,6 +504,84 @@ __global__ void __launch_bounds__(256, 8) win_bwd_prep_kernel(const PrepArgs a) 
     }
 }
 
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same rows of the workspace for few keys: delta_i = sum_j P_ij dP_ij.  A warp takes 16
+// query rows with the keys that any of them sees, eight at a time: S and dP as m16n8k16 products of
+// the same layout, multiplied element by element.  Against dO . o, a step of B4 H16 N2048 d64: W2 83 ->
+// 92 us and dQ's error 3.8e-3 -> 2.35e-3, W16 84 -> 95 and 2.5e-3 -> 2.34e-3 (W32 84 -> 100 and 2.48e-3 ->
+// 2.36e-3, hence kNarrow).  The order of d in a product is free, so that a lane
+// (row or key g, t) loads its operands as 16 neighbouring bytes: values 32 c + 8 t .. + 7, of which the
+// first four serve one product and the rest the next.  Bound by memory: q, k, v and dO are read here
+// (and by the kernels after this one, from L2) where the other kernel reads o and dO.
+template <int D>
+__global__ void __launch_bounds__(256) win_bwd_narrow_prep_kernel(const PrepArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int kC = D / 32, kT = D / 8;  // 16-byte loads of a lane and of a row
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int N = a.N, Np = a.Np, tiles_head = Np / 16;
+    const long long tiles = static_cast<long long>(a.BH) * tiles_head;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (long long x = static_cast<long long>(blockIdx.x) * 8 + warp; x < tiles; x += static_cast<long long>(gridDim.x) * 8) {
+        const int bh = static_cast<int>(x / tiles_head), i0 = static_cast<int>(x % tiles_head) * 16;
+        const size_t q_row = static_cast<size_t>(bh) * N;
+        const size_t k_row = static_cast<size_t>((bh / a.H) * a.H_kv + (bh % a.H) / (a.H / a.H_kv)) * N;
+        uint4 q[2][kC], d[2][kC];  // rows i0 + g, i0 + g + 8
+        float nl[2], delta[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = i0 + g + 8 * r;
+            const size_t at = (q_row + i) * kT + t;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                q[r][c] = i < N ? a.q[at + 4 * c] : zero;
+                d[r][c] = i < N ? a.dO[at + 4 * c] : zero;
+            }
+            nl[r] = i < N ? -a.lse[q_row + i] * kLog2e : -INFINITY;
+        }
+        const int start = max(0, i0 - a.window + 1) & ~7, end = min(i0 + 16, N);  // the window's keys
+        const int front = min(a.sinks, start);                                    // sinks before them
+        for (int kt = front > 0 ? 0 : start; kt < end; kt = kt < front && kt + 8 >= front ? start : kt + 8) {
+            const bool of_front = kt < front;
+            const int key = kt + g;  // this lane's
+            const bool there = key < N;
+            const size_t at = (k_row + key) * kT + t;
+            float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const uint4 k = there ? a.k[at + 4 * c] : zero, v = there ? a.v[at + 4 * c] : zero;
+                mma_bf16(s, q[0][c].x, q[1][c].x, q[0][c].y, q[1][c].y, k.x, k.y);
+                mma_bf16(s, q[0][c].z, q[1][c].z, q[0][c].w, q[1][c].w, k.z, k.w);
+                mma_bf16(dp, d[0][c].x, d[1][c].x, d[0][c].y, d[1][c].y, v.x, v.y);
+                mma_bf16(dp, d[0][c].z, d[1][c].z, d[0][c].w, d[1][c].w, v.z, v.w);
+            }
+            // rows g, g + 8 and keys 2 t, 2 t + 1
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + g + 8 * (e / 2), j = kt + 2 * t + e % 2;
+                const bool seen = of_front ? j < front : j <= i && (j > i - a.window || j < a.sinks);
+                if (seen) delta[e / 2] = fmaf(ex2_approx(fmaf(s[e], a.c_log2, nl[e / 2])), dp[e], delta[e / 2]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float sum = lanes_sum<1, 4>(delta[r]);
+            if (t == 0) {
+                const size_t at = static_cast<size_t>(bh) * Np + i0 + g + 8 * r;
+                a.ws_delta[at] = -sum;
+                a.ws_lse2[at] = nl[r];
+            }
+        }
+    }
+}
+
 int grid_for(size_t work, int threads, int max_blocks) {
     size_t b = (work + threads - 1) / threads;
     if (b > static_cast<size_t>(max_blocks)) b = max_blocks;
@@ -584,9 +662,16 @@ int launch_bwd_window(const void* q, const void* k, const void* v, const void* o
     pa.window = window;
     pa.sinks = sp.sinks;
     pa.c_log2 = scale == 0.f ? 1e-30f : scale * kLog2e;
-    pa.extra = grid_for(static_cast<size_t>(BH) * kFirst, 8, 2 * sms);
-    const int others = grid_for(static_cast<size_t>(BH) * Np * (d / 8), 256, sms * 8 - pa.extra);
-    e = launch_pdl(d == 64 ? win_bwd_prep_kernel<64> : win_bwd_prep_kernel<128>, dim3(others + pa.extra), dim3(256), 0, s, pa);
+    if (N <= kShort || static_cast<long long>(window) + sp.sinks <= kNarrow) {
+        pa.extra = 0;
+        e = launch_pdl(d == 64 ? win_bwd_narrow_prep_kernel<64> : win_bwd_narrow_prep_kernel<128>,
+                       dim3(grid_for(static_cast<size_t>(BH) * Np / 16, 8, sms * 4)), dim3(256), 0, s, pa);
+    } else {
+        pa.extra = grid_for(static_cast<size_t>(BH) * kFirst, 8, 2 * sms);
+        const int others = grid_for(static_cast<size_t>(BH) * Np * (d / 8), 256, sms * 8 - pa.extra);
+        e = launch_pdl(d == 64 ? win_bwd_prep_kernel<64> : win_bwd_prep_kernel<128>, dim3(others + pa.extra), dim3(256), 0,
+                       s, pa);
+    }
     if (e != cudaSuccess) return static_cast<int>(e);
 
     CUtensorMap tq, tk, tv, tdo, tdk, tdv;
