@@ -11,7 +11,7 @@
 // kernel for dQ (win_bwd_dq_sm103.cu), which also joins the sinks' parts.  Nothing is summed by
 // atomics: the same bits every time.  (For d = 64 the plain backward's scheme, dQ partials added to a
 // float32 accumulator by TMA reductions, was also measured: the main kernel took 79 us of a B4 H16
-// N2048 W512 step, zeroing and converting the accumulator 13 more; dK/dV and dQ take 54 and 39.)
+// N2048 W512 step, zeroing and converting the accumulator 13 more; dK/dV and dQ take 52 and 42.)
 //
 // What the window changes:
 //   * A key block j meets the query blocks j .. j + (W + 126) / 128 only.
