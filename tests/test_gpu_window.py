@@ -6,8 +6,9 @@ float32 scores and sums add under 1e-5 (1 + max |score|) of A.  lse: 1e-5 (1 + m
 
 Backward tolerance, with t = 1e-5 (1 + max |score|) for the recomputed P: dV takes P in bfloat16
 (2^-8 P^T |dO|); dS = P (dP - delta) is rounded to bfloat16 (2^-8), and delta = dO . o takes the o that
-the forward rounded: its error is |dO| . (o's tolerance).  Each gradient adds its own rounding, 2^-8 of
-the value.  Group sums add up."""
+the forward rounded: its error is |dO| . (o's tolerance).  (Where few keys are seen it is the sum of
+P dP in float32 instead: t + 1e-6 of |dO| . A.)  Each gradient adds its own rounding, 2^-8 of the value.
+Group sums add up."""
 import numpy as np
 import pytest
 import torch
@@ -160,7 +161,7 @@ def backward(q, k, v, o, lse, do, scale, window, n_sink, ws=None):
     return out
 
 
-def check_backward(q, k, v, do, grads, scale, window, n_sink, kv_heads=None):
+def check_backward(q, k, v, do, grads, scale, window, n_sink, kv_heads=None, few_keys=False):
     B, H, N, d = q.shape
     H_kv = k.shape[1]
     G = H // H_kv
@@ -182,7 +183,8 @@ def check_backward(q, k, v, do, grads, scale, window, n_sink, kv_heads=None):
                 dP = dO @ V.T
                 diff = dP - (dO * o).sum(-1, keepdims=True)
                 A = P @ aV
-                d_delta = (adO * (2.0 ** -8 * (A + np.abs(o)) + t * A)).sum(-1, keepdims=True)
+                o_tol = (t + 1e-6) * A if few_keys else 2.0 ** -8 * (A + np.abs(o)) + t * A
+                d_delta = (adO * o_tol).sum(-1, keepdims=True)
                 e_dS = (2.0 ** -8 + t) * np.abs(P * diff) + P * d_delta + 1e-6 * P * (adO @ aV.T)
                 dS = P * diff
                 rq, tq = scale * dS @ K, a * e_dS @ aK
@@ -310,3 +312,14 @@ def test_backward_large_offsets():
         outs.append(backward(q, k, v, o, lse, do, scale_for(d), 200, 0))
     for b, s in zip(*outs):
         assert torch.equal(b[-1, -1], s[0, 0]) and (b[0] == 0).all()
+
+
+@pytest.mark.parametrize("H,H_kv,N,window,n_sink", [(4, 2, 300, 1, 0), (4, 2, 300, 2, 0), (3, 1, 389, 20, 4), (2, 2, 257, 24, 0),
+                                                    (4, 4, 200, 3, 17), (2, 1, 100, 5000, 0), (2, 2, 128, 60, 4), (1, 1, 1, 1, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_delta_of_few_keys(H, H_kv, N, window, n_sink, d):
+    # without the share of o's rounding
+    q, k, v, do = inputs(2, H, H_kv, N, d, seed=23)
+    o, lse = forward(q, k, v, scale_for(d), window, n_sink)
+    grads = backward(q, k, v, o, lse, do, scale_for(d), window, n_sink)
+    check_backward(q, k, v, do, grads, scale_for(d), window, n_sink, few_keys=True)
