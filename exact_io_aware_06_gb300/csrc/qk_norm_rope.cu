@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (u >= at.count) break;
+            const bool there = h + u * kHeads < heads;
             if (at.seg < 2) {
                 const Quad x = unpack<F32, INTER>(rx[u]), dy = unpack<F32, INTER>(rg[u]);
                 Quad g, wg;
@@ -404,9 +405,10 @@ __global__ void __launch_bounds__(kThreads, 3)
                     wg.first[k] = mul2(g.first[k], wf[k]);
                     wg.second[k] = mul2(g.second[k], ws[k]);
                 }
-                const float r = rsqrtf(fmaf(row_sum<kLanes>(dot(x, x)), 1.f / D, a.eps));
+                const float sq = fmaf(row_sum<kLanes>(dot(x, x)), 1.f / D, a.eps);
+                // rows of heads past the end are zeros: with a finite r (for eps = 0 too) they add nothing
+                const float r = there ? rsqrtf(sq) : 0.f;
                 const float m = row_sum<kLanes>(dot(wg, x)) * (1.f / D) * r * r;
-                // rows of heads past the end are zeros: they add nothing
                 const float2 r2 = both(r), m2 = both(-m);
                 Quad dx;
 #pragma unroll
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                 }
                 rg[u] = pack<F32, INTER>(dx);
             }
-            if (h + u * kHeads < heads) store8<F32>(dst + u * kPass, dst + gap + u * kPass, rg[u]);
+            if (there) store8<F32>(dst + u * kPass, dst + gap + u * kPass, rg[u]);
         }
         at = next;
 #pragma unroll

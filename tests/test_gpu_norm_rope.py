@@ -169,3 +169,11 @@ def test_binding_refuses_wrong_tensors():
                  (qkv, qw, kw, None, f, out[0].float(), out[1], out[2])):
         with pytest.raises(ValueError):
             fa.fa_qk_norm_rope(*args, 1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (3, 1), (6, 3), (5, 6)])
+def test_without_eps(H, H_kv, d, dtype):
+    # heads that do not fill a warp's pass: what has no head adds nothing to the weight gradients
+    run_both(2, 19, H, H_kv, d, dtype, d, False, None, eps=0.0)
