@@ -7,6 +7,7 @@
 #include "internal.h"
 #include "kv4.cuh"
 #include "layer_ops.h"
+#include "rope_turns.h"
 
 namespace fa {
 namespace {
@@ -45,11 +46,8 @@ int norm_rope_args(NormRopeArgs* a, const void* qkv, const float* qw, const floa
     if (dtype != FA_F32 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
     *a = NormRopeArgs{};
     for (int p = 0; p < rot / 2; ++p) {
-        if (!std::isfinite(inv_freq[p])) return FA_ERR_INVALID_ARG;
-        // turns per position, whole ones dropped, as a 64-bit fraction
-        const double turns = inv_freq[p] * 0.15915494309189533577;
-        const double frac = turns - std::floor(turns);  // in [0, 1]; 1 after rounding is 0
-        a->freq.f[p] = frac >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(frac, 64));
+        if (!(std::fabs(inv_freq[p]) <= kMaxRopeFreq)) return FA_ERR_INVALID_ARG;  // nor NaN
+        a->freq.f[p] = rope_turns(inv_freq[p]);
     }
     a->qkv = qkv;
     a->weight[0] = qw;

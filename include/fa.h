@@ -299,9 +299,9 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *   q_weight, k_weight : [d] float32, or NULL (ones).
  *   positions : [B][N] int32 (negative ones turn backwards), or NULL: the index in the
  *               sequence.
- *   inv_freq  : HOST array of rot / 2 finite doubles, radians per position; read before the
- *               call returns.  May be NULL if rot is 0.  Angles are exact to 2^-24 of a turn
- *               at every int32 position.
+ *   inv_freq  : HOST array of rot / 2 doubles, radians per position, of up to 2^64 in magnitude;
+ *               read before the call returns.  May be NULL if rot is 0.  Angles are exact to
+ *               2^-24 of a turn at every int32 position.
  *   q, k, v   : [B][H][N][d] and twice [B][H_kv][N][d] of `dtype`, written; they must not
  *               overlap qkv.
  *   d : 64 or 128.  rot : a multiple of 16, 0 to d.  eps : finite, >= 0.

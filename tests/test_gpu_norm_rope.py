@@ -4,6 +4,8 @@ Tolerances.  A value is a sum of at most two products w_a n_a cos, w_b n_b sin w
 its float32 error is at most (12 additions of the mean, halved by the root, + 2 units for
 rsqrt + 3 products + cos and sin, whose angle is off by 2^-25 half turns: 2 pi 2^-25 + 2^-23)
 under 2e-6 of the pair's amplitude.  bfloat16 results add half a step, 2^-8 of the value."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -177,3 +179,51 @@ def test_binding_refuses_wrong_tensors():
 def test_without_eps(H, H_kv, d, dtype):
     # heads that do not fill a warp's pass: what has no head adds nothing to the weight gradients
     run_both(2, 19, H, H_kv, d, dtype, d, False, None, eps=0.0)
+
+
+def exact_angles(positions, inv_freq):
+    """positions [n] times frequencies [p], less whole turns, from integers: float64 in [-pi, pi]."""
+    bits = 1400
+    atan = lambda x: sum((-1) ** k * ((1 << bits) // ((2 * k + 1) * x ** (2 * k + 1))) for k in range(bits // 4))  # noqa: E731
+    two_pi = 8 * (4 * atan(5) - atan(239))  # Machin; off by under 2^-1380
+    out = np.empty((len(positions), len(inv_freq)))
+    for i, t in enumerate(positions):
+        for j, f in enumerate(inv_freq):
+            m, e = Fraction(float(f)).as_integer_ratio()
+            rest = (int(t) * m << bits) // e % two_pi
+            out[i, j] = float(Fraction(rest - (two_pi if 2 * rest > two_pi else 0), 1 << bits))
+    return out
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_frequencies_of_any_size_at_far_positions(interleaved):
+    # the angle's error does not grow with the frequency
+    B, H, H_kv, d, eps = 1, 2, 1, 64, 1e-6
+    positions = [0, 1, -1, 7, 4099, -123456789, 2 ** 31 - 1, -2 ** 31]
+    N = len(positions)
+    f = torch.tensor([2.0 ** 64, -2.0 ** 64, 1.7e19, 1e12 + 0.1, 2.0 ** 53 + 2, 1e6, -54321.098, 4096.0, 1234.5, 100.0, 10.0,
+                      2 * np.pi, 3.7, 1.0, 0.99, -0.5, 1 / 3, 0.1, 1e-3, 1e-6, 1e-9, -1e-12, 1e-20, 1e-30, 5e-324, -5e-324,
+                      0.0, 2.2250738585072014e-308, 50.0, 20.0, 5.0, 2.0], dtype=torch.float64)
+    qkv, qw, kw, up = make(B, N, H, H_kv, d, "f32")
+    pos = torch.tensor([positions], dtype=torch.int32, device="cuda")
+    out = outputs(B, N, H, H_kv, d, torch.float32)
+    fa.fa_qk_norm_rope(qkv, qw, kw, pos, f, *out, eps, interleaved)
+    dqkv = torch.full_like(qkv, float("nan"))
+    fa.fa_qk_norm_rope_bwd(qkv, qw, kw, pos, f, *up, dqkv, None, None, None, eps, interleaved)
+    check_status()
+    angles = exact_angles(positions, f.numpy())
+    for n in range(N):
+        one = lambda x: x[:, :, n:n + 1].contiguous()  # noqa: E731
+        x, first = qkv[:, n:n + 1].contiguous(), torch.ones((1, 1), dtype=torch.int32)
+        angle = torch.from_numpy(angles[n].copy())
+        compare_forward(x, [one(t) for t in out], qw, kw, first, angle, eps, interleaved)
+        ref = plain64.norm_rope_grad(f64(x), H, H_kv, f64(qw), f64(kw), first.numpy(), angle.numpy(), eps, interleaved,
+                                     *(f64(one(u)) for u in up))[0]
+        g = np.concatenate([f64(one(u)).swapaxes(1, 2) for u in up[:2]], 2)
+        w = np.concatenate([np.tile(f64(qw), (H, 1)), np.tile(f64(kw), (H_kv, 1))])
+        r = 1 / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True) + eps)[:, :, :H + H_kv]
+        xn = f64(x)[:, :, :H + H_kv] * r
+        # as in compare_grad, with |g| before its turn: a turn makes it sqrt(2) larger at most
+        top = 2.2 * np.abs(w).max() * np.abs(g).max(-1, keepdims=True)
+        check(dqkv[:, n:n + 1, :H + H_kv], ref[:, :, :H + H_kv], r * (top + 2 * np.abs(xn) * top * np.abs(xn).mean(-1, keepdims=True)),
+              torch.float32, "dqkv")

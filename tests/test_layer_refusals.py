@@ -152,6 +152,14 @@ def test_workspace_sizes_of_refused_sizes_are_zero(L):
     assert fa.fa_qk_norm_rope_bwd_workspace_size(1, 4, 0, 1, 64) == 0
 
 
+def test_frequencies_beyond_2_64_are_refused(L):
+    for f in (2.0 ** 64 * (1 + 2.0 ** -52), -1e20, 1e300):
+        a = dict(NORM, f=freq(32))
+        a["f"][7] = f
+        assert L.fa_qk_norm_rope(a["qkv"], a["qw"], a["kw"], a["pos"], a["f"], a["q"], a["k"], a["v"], a["B"],
+                                 a["H"], a["H_kv"], a["N"], a["d"], a["rot"], 0, a["eps"], a["dtype"], None) == 1
+
+
 def test_status_name(L):
     assert fa.fa_status_string(fa.FA_ERR_DEVICE_INDEX) == "FA_ERR_DEVICE_INDEX"
 
