@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(kThreads)
             const long long p = static_cast<long long>(first[r.b]) + r.n;
             pos = p < 0 || p > 0x7fffffff ? -1 : static_cast<int>(p);
             page = page_of(c, ctl, r.b, pos);
+        } else if (count[r.b] < 0) {
+            record_index(ctl);
         }
     }
     uint32_t word[2], sbits[2];
@@ -163,19 +165,32 @@ __device__ __forceinline__ uint4 values_of(uint32_t word, uint32_t scale) {
                       __byte_perm(e[0], e[1], 0x7632), __byte_perm(e[2], e[3], 0x7632));
 }
 
+// Bad lengths are recorded by CTAs of their own behind those of the rows, which do not meet them all.
+// (A test in the rows' threads took 1 to 4% longer.)
+__device__ __forceinline__ void check_lengths(const Kv4Cache& c, const int* __restrict__ lengths, int B, uint32_t row_ctas,
+                                              const DevCtl& ctl) {
+    const uint32_t step = (gridDim.x - row_ctas) * kThreads;
+    for (uint32_t b = (blockIdx.x - row_ctas) * kThreads + threadIdx.x; b < static_cast<uint32_t>(B); b += step)
+        if (lengths[b] < 0 || lengths[b] > c.max_blocks << c.page_log2) record_index(ctl);
+}
+
 // A thread reads ROWS (1 or 2) rows of K and of V from row n = ROWS i on: an even token and the next
 // one are in the same tile of the same page.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
     kv4_read_kernel(const Kv4Cache c, const int* __restrict__ lengths, uint4* __restrict__ k,
-                    uint4* __restrict__ v, const Div by_runs, const Div by_heads, uint32_t N, uint32_t runs, DevCtl ctl) {
+                    uint4* __restrict__ v, const Div by_runs, const Div by_heads, uint32_t N, uint32_t runs, int B,
+                    uint32_t row_ctas, DevCtl ctl) {
     constexpr int kLanes = D / 8;
     const int j = threadIdx.x % kLanes;
     const int grp = j / 4, t = j % 4;
     const uint32_t run = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
     griddep_wait();
     griddep_launch_dependents();
-    if (run >= runs) return;
+    if (run >= runs) {
+        if (blockIdx.x >= row_ctas) check_lengths(c, lengths, B, row_ctas, ctl);
+        return;
+    }
     const Row r = row_at(run, by_runs, by_heads);
     const uint32_t n = ROWS * r.n;
     const int len = lengths[r.b];
@@ -209,9 +224,9 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-dim3 grid_of(uint32_t rows, int lanes) {
+uint32_t ctas_of(uint32_t rows, int lanes) {
     const uint32_t per = kThreads / lanes;
-    return dim3((rows + per - 1) / per);
+    return (rows + per - 1) / per;
 }
 
 }  // namespace
@@ -219,8 +234,8 @@ dim3 grid_of(uint32_t rows, int lanes) {
 cudaError_t launch_kv4_append(const Kv4Cache& c, const void* k, const void* v, const int* first,
                               const int* count, int B, int N, int d, DevCtl ctl, cudaStream_t s) {
     const uint32_t rows = static_cast<uint32_t>(B) * c.H_kv * N;
-    return launch_pdl(d == 64 ? kv4_append_kernel<64> : kv4_append_kernel<128>, grid_of(rows, d / 8), dim3(kThreads), 0,
-                      s, c, static_cast<const uint4*>(k), static_cast<const uint4*>(v), first, count, make_div(N),
+    return launch_pdl(d == 64 ? kv4_append_kernel<64> : kv4_append_kernel<128>, dim3(ctas_of(rows, d / 8)), dim3(kThreads),
+                      0, s, c, static_cast<const uint4*>(k), static_cast<const uint4*>(v), first, count, make_div(N),
                       make_div(c.H_kv), rows, ctl);
 }
 
@@ -229,9 +244,11 @@ template <int D, int ROWS>
 cudaError_t launch_read(const Kv4Cache& c, const int* lengths, void* k, void* v, int B, int N, DevCtl ctl, cudaStream_t s) {
     const uint32_t per_head = (static_cast<uint32_t>(N) + ROWS - 1) / ROWS;
     const uint32_t runs = static_cast<uint32_t>(B) * c.H_kv * per_head;
-    return launch_pdl(kv4_read_kernel<D, ROWS>, grid_of(runs, D / 8), dim3(kThreads), 0, s, c, lengths,
+    const uint32_t row_ctas = ctas_of(runs, D / 8);
+    const uint32_t checks = B < 64 * kThreads ? (B + kThreads - 1) / kThreads : 64;  // CTAs of check_lengths
+    return launch_pdl(kv4_read_kernel<D, ROWS>, dim3(row_ctas + checks), dim3(kThreads), 0, s, c, lengths,
                       static_cast<uint4*>(k), static_cast<uint4*>(v), make_div(per_head), make_div(c.H_kv),
-                      static_cast<uint32_t>(N), runs, ctl);
+                      static_cast<uint32_t>(N), runs, B, row_ctas, ctl);
 }
 }  // namespace
 

@@ -390,12 +390,14 @@ size_t fa_bwd_window_workspace_size(int B, int H, int H_kv, int N, int d, int wi
  *                        not read.
  *   page : 16, 32, 64, 128 or 256 tokens.   d : 64 or 128.
  * A page, position or length outside the cache that a kernel meets is left out (not written;
- * read as zeros; hidden from attention) and recorded as FA_ERR_DEVICE_INDEX.
+ * read as zeros; hidden from attention) and recorded as FA_ERR_DEVICE_INDEX.  A negative length
+ * or count is taken as 0, a length beyond max_blocks * page as that, in all three calls.
  */
 
 /*
  * Store rows of K and V: row i of request b becomes its token first[b] + i, for
- * i < count[b] (count NULL: all N).  Two rows of one call must not name the same token.
+ * i < count[b] (count NULL, or N and more: all N).  Two rows of one call must not name the same
+ * token.
  *   k, v  : [B][H_kv][N][d] bfloat16, read only.
  *   first : [B] int32, device: tokens that the requests had before.   count : [B] int32 or NULL.
  * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, sizes < 1, bad page),

@@ -375,3 +375,54 @@ def test_pages_beyond_32_bits():
     assert all(torch.equal(a, b) for a, b in zip(*results))
     assert np.array_equal(f64(results[0][0]), plain64.bf16_round(plain64.kv4_values(f64(k))))
     compare(q, results[0][2], results[0][3], plain64.kv4_values(f64(k)), plain64.kv4_values(f64(v)), [n])
+
+
+@pytest.mark.parametrize("N", [1, 40, 300])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 10 ** 6])
+def test_read_reports_lengths_outside_the_cache(N, bad):
+    # a negative length holds nothing; one beyond the table is cut to it
+    d, page, H_kv = 64, 16, 2
+    c = Cache([64, 64], H_kv, d, page)
+    k, v = c.fill(61)
+    for lengths in ([bad, 64], [64, bad]):
+        out = [torch.full((2, H_kv, N, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        fa.fa_kv4_read(*c.args, ints(lengths), *out)
+        assert fa.fa_last_device_error() == fa.FA_ERR_DEVICE_INDEX
+        for t, values in zip(out, (k, v)):
+            for b, n in enumerate(lengths):
+                n = min(N, 64, max(n, 0))
+                assert np.array_equal(f64(t[b, :, :n]), plain64.bf16_round(values[b][:, :n])) and (t[b, :, n:] == 0).all()
+    fa.fa_kv4_read(*c.args, ints([64, 0]), *out)
+    check_status()
+
+
+def test_read_of_many_rows_reports_lengths_outside_the_cache():
+    # two rows a thread
+    c = Cache([8192, 16], 8, 64, 64)
+    c.fill(63)
+    back = [torch.empty((2, 8, 20000, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    fa.fa_kv4_read(*c.args, ints([8192, 16]), *back)
+    check_status()
+    for lengths in ([8193, 16], [8192, -16]):
+        fa.fa_kv4_read(*c.args, ints(lengths), *back)
+        assert fa.fa_last_device_error() == fa.FA_ERR_DEVICE_INDEX
+
+
+def test_append_reports_a_negative_count():
+    c = Cache([40, 40], 2, 64, 16)
+    c.fill(65)
+    before = [a.clone() for a in c.arrays]
+    new = rand((2, 2, 5, 64), 66)
+    for count in ([-1, 0], [0, -2 ** 31]):
+        fa.fa_kv4_append(new, new, *c.args, ints([3, 3]), ints(count))
+        assert fa.fa_last_device_error() == fa.FA_ERR_DEVICE_INDEX
+    fa.fa_kv4_append(new, new, *c.args, ints([3, 3]), ints([0, 0]))
+    check_status()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(c.arrays, before))
+    # more than there are rows: all rows
+    fa.fa_kv4_append(new, new, *c.args, ints([3, 3]), ints([5, 6]))
+    check_status()
+    back = [torch.empty((2, 2, 8, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    fa.fa_kv4_read(*c.args, ints([8, 8]), *back)
+    ref = plain64.bf16_round(plain64.kv4_values(f64(new)))
+    assert all(np.array_equal(f64(t[:, :, 3:]), ref) for t in back)
