@@ -30,6 +30,12 @@ def _sizes(what, t):
     return t.shape
 
 
+def _int(x):
+    """x as a C int, those beyond one as the nearest: a window or a number of sinks that covers
+    everything still does, and sizes are refused (ctypes would drop the upper bits without a word)."""
+    return x if -0x80000000 <= x <= 0x7FFFFFFF else 0x7FFFFFFF if x > 0 else -0x80000000
+
+
 def _handle(stream, device):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(device)
@@ -83,7 +89,7 @@ def fa_qk_norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, eps, 
 
 
 def fa_qk_norm_rope_bwd_workspace_size(B, H, H_kv, N, d):
-    return int(lib().fa_qk_norm_rope_bwd_workspace_size(B, H, H_kv, N, d))
+    return int(lib().fa_qk_norm_rope_bwd_workspace_size(*map(_int, (B, H, H_kv, N, d))))
 
 
 def fa_qk_norm_rope_bwd(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv, dqkv, dq_weight,
@@ -112,11 +118,12 @@ def fa_fwd_window(q, k, v, o, lse, scale, window, n_sink, dtype=FA_BF16, stream=
     _check(lib().fa_fwd_window(_dense("q", q, _BF16, rows, device), _dense("k", k, _BF16, kv_rows, device),
                                _dense("v", v, _BF16, kv_rows, device), _dense("o", o, _BF16, rows, device),
                                None if lse is None else _dense("lse", lse, _F32, (B, H, N), device), B, H,
-                               H_kv, N, d, scale, window, n_sink, dtype, _handle(stream, device)), "fa_fwd_window")
+                               H_kv, N, d, scale, _int(window), _int(n_sink), dtype, _handle(stream, device)),
+           "fa_fwd_window")
 
 
 def fa_bwd_window_workspace_size(B, H, H_kv, N, d, window, n_sink):
-    return int(lib().fa_bwd_window_workspace_size(B, H, H_kv, N, d, window, n_sink))
+    return int(lib().fa_bwd_window_workspace_size(*map(_int, (B, H, H_kv, N, d, window, n_sink))))
 
 
 def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_sink, dtype=FA_BF16,
@@ -132,7 +139,7 @@ def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_s
         _dense("lse", lse, _F32, (B, H, N), device), _dense("do", do, _BF16, rows, device),
         _dense("dq", dq, _BF16, rows, device), _dense("dk", dk, _BF16, kv_rows, device),
         _dense("dv", dv, _BF16, kv_rows, device), *_space(workspace, device), B, H, H_kv, N, d, scale,
-        window, n_sink, dtype, _handle(stream, device)), "fa_bwd_window")
+        _int(window), _int(n_sink), dtype, _handle(stream, device)), "fa_bwd_window")
 
 
 # ---------------------------------------------------------------- the 4-bit cache
@@ -154,7 +161,7 @@ def _cache(k_codes, k_scales, v_codes, v_scales, block_table, B, H_kv, d, device
     return ((_dense("k_codes", k_codes, _U8, codes, device), _dense("k_scales", k_scales, _BF16, scales, device),
              _dense("v_codes", v_codes, _U8, codes, device), _dense("v_scales", v_scales, _BF16, scales, device),
              _dense("block_table", block_table, _I32, (B, max_blocks), device)),
-            (page, n_pages, max_blocks))
+            (page, n_pages, _int(max_blocks)))
 
 
 def fa_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, block_table, first, count=None,
@@ -182,7 +189,7 @@ def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, block_table, lengths, k, v
 
 
 def fa_decode_kv4_workspace_size(B, H, H_kv, N_q, d):
-    return int(lib().fa_decode_kv4_workspace_size(B, H, H_kv, N_q, d))
+    return int(lib().fa_decode_kv4_workspace_size(*map(_int, (B, H, H_kv, N_q, d))))
 
 
 def fa_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, lengths, o, lse, workspace,
@@ -197,4 +204,4 @@ def fa_decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, lengths,
                                _dense("o", o, _BF16, rows, device),
                                None if lse is None else _dense("lse", lse, _F32, (B, H, N_q), device),
                                *_space(workspace, device), B, H, k_codes.shape[1], N_q, d, *pages, scale,
-                               window, n_sink, _handle(stream, device)), "fa_decode_kv4")
+                               _int(window), _int(n_sink), _handle(stream, device)), "fa_decode_kv4")

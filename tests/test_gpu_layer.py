@@ -249,3 +249,23 @@ def test_binding_refuses_tensors_that_kernels_would_misread():
         with pytest.raises(ValueError):
             fa.fa_kv4_append(q[:, :, :1].contiguous(), q[:, :, :1].contiguous(), *c.args, first)
     assert fa.fa_last_device_error() == 0
+
+
+@pytest.mark.parametrize("window,n_sink", [(2 ** 31, 0), (2 ** 32 + 1, 2), (2 ** 63, 3), (3, 2 ** 32), (5, 2 ** 40 + 1)])
+def test_windows_and_sinks_beyond_32_bits(window, n_sink):
+    # as any others that cover the sequence
+    B, H, H_kv, N, d, scale = 1, 2, 1, 200, 64, 0.125
+    q, k, v, do = win.inputs(B, H, H_kv, N, d)
+    results = []
+    for w, s in ((window, n_sink), (min(window, N), min(n_sink, N))):
+        o, lse = win.forward(q, k, v, scale, w, s)
+        grads = win.backward(q, k, v, o, lse, do, scale, w, s)
+        c = kv4.Cache([N, 77], H_kv, d, 16)
+        c.fill(3)
+        one = kv4.decode(win.rand((2, H, 1, d), 4), c, [N, 77], w, s, scale)[:2]
+        results.append((o, lse, *grads, *one))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    with pytest.raises(RuntimeError):
+        fa.fa_fwd_window(q, k, v, o, lse, scale, 5 - 2 ** 32, 0)
+    with pytest.raises(RuntimeError):
+        fa.fa_fwd_window(q, k, v, o, lse, scale, 5, 5 - 2 ** 32)

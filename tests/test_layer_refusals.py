@@ -152,6 +152,20 @@ def test_workspace_sizes_of_refused_sizes_are_zero(L):
     assert fa.fa_qk_norm_rope_bwd_workspace_size(1, 4, 0, 1, 64) == 0
 
 
+def test_workspace_sizes_of_sizes_beyond_32_bits_are_zero(L):
+    big = 2 ** 32
+    for i in range(5):
+        sizes = [1, 4, 2, 16, 64]
+        sizes[i] += big
+        assert fa.fa_decode_kv4_workspace_size(*sizes) == 0
+        assert fa.fa_qk_norm_rope_bwd_workspace_size(*sizes) == 0
+        assert fa.fa_bwd_window_workspace_size(*sizes, 4, 0) == 0
+    size = fa.fa_bwd_window_workspace_size
+    assert size(1, 4, 2, 4096, 64, big + 1, 4) == size(1, 4, 2, 4096, 64, 4096, 4) > 0
+    assert size(1, 4, 2, 4096, 64, 130, big) == size(1, 4, 2, 4096, 64, 130, 4096) > 0
+    assert size(1, 4, 2, 4096, 64, 5 - big, 4) == size(1, 4, 2, 4096, 64, 5, 5 - big) == 0
+
+
 def test_frequencies_beyond_2_64_are_refused(L):
     for f in (2.0 ** 64 * (1 + 2.0 ** -52), -1e20, 1e300):
         a = dict(NORM, f=freq(32))
