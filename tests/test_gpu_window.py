@@ -323,3 +323,12 @@ def test_backward_delta_of_few_keys(H, H_kv, N, window, n_sink, d):
     o, lse = forward(q, k, v, scale_for(d), window, n_sink)
     grads = backward(q, k, v, o, lse, do, scale_for(d), window, n_sink)
     check_backward(q, k, v, do, grads, scale_for(d), window, n_sink, few_keys=True)
+
+
+@pytest.mark.parametrize("H,H_kv,N,d", [(4, 2, 1100, 128), (3, 3, 517, 64)])
+def test_forward_and_the_causal_forward_where_the_window_covers_everything(H, H_kv, N, d):
+    # o and lse of both calls against the same float64 form, on both sides
+    q, k, v, _ = inputs(2, H, H_kv, N, d, seed=5)
+    check_forward(q, k, v, *fa.attention_forward(q, k, v, causal=True), scale_for(d), N, 0)
+    for window, n_sink in ((N, 0), (N + 5000, 3), (2 ** 31 - 1, 0), (1, N)):
+        check_forward(q, k, v, *forward(q, k, v, scale_for(d), window, n_sink), scale_for(d), N, 0)
