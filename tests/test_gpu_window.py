@@ -332,3 +332,44 @@ def test_forward_and_the_causal_forward_where_the_window_covers_everything(H, H_
     check_forward(q, k, v, *fa.attention_forward(q, k, v, causal=True), scale_for(d), N, 0)
     for window, n_sink in ((N, 0), (N + 5000, 3), (2 ** 31 - 1, 0), (1, N)):
         check_forward(q, k, v, *forward(q, k, v, scale_for(d), window, n_sink), scale_for(d), N, 0)
+
+
+def until_a_wait_runs_out(call, results, ref):
+    """Calls under wait limits far below a load's latency, until one reports that a wait ran out; those
+    that report nothing have to be right, and so has the first one under the default limit."""
+    elsewhere = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    reported = False
+    try:
+        for limit_ns in (300, 1, 1, 1, 1, 1, 1, 1):
+            fa.fa_set_wait_timeout_ns(limit_ns)
+            for t in results:
+                t.fill_(float("nan"))
+            elsewhere.zero_()  # the inputs leave L2: the first loads take longest
+            call()
+            status = fa.fa_last_device_error()
+            reported = status == fa.FA_ERR_DEVICE_TIMEOUT
+            if reported:
+                break
+            assert status == fa.FA_OK and all(torch.equal(a, b) for a, b in zip(results, ref))
+    finally:
+        fa.fa_set_wait_timeout_ns(0)
+    assert reported
+    call()
+    check_status()
+    assert all(torch.equal(a, b) for a, b in zip(results, ref))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_that_runs_out_is_reported(d):
+    B, H, N, window, n_sink = 2, 16, 2048, 500, 4
+    q, k, v, do = inputs(B, H, H, N, d, seed=13)
+    o, lse = forward(q, k, v, scale_for(d), window, n_sink)
+    check_forward(q[:1], k[:1], v[:1], o[:1], lse[:1], scale_for(d), window, n_sink, heads=[0, 15])
+    out = [torch.empty_like(q), torch.empty_like(lse)]
+    until_a_wait_runs_out(lambda: fa.fa_fwd_window(q, k, v, *out, scale_for(d), window, n_sink), out, (o, lse))
+
+    ws = torch.empty(fa.fa_bwd_window_workspace_size(B, H, H, N, d, window, n_sink), dtype=torch.uint8, device="cuda")
+    ref = backward(q, k, v, o, lse, do, scale_for(d), window, n_sink, ws)
+    check_backward(q[:1], k[:1], v[:1], do[:1], [g[:1] for g in ref], scale_for(d), window, n_sink, kv_heads=[0, 15])
+    out = [torch.empty_like(t) for t in ref]
+    until_a_wait_runs_out(lambda: fa.fa_bwd_window(q, k, v, o, lse, do, *out, ws, scale_for(d), window, n_sink), out, ref)
