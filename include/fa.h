@@ -305,7 +305,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *   q, k, v   : [B][H][N][d] and twice [B][H_kv][N][d] of `dtype`, written; they must not
  *               overlap qkv.
  *   d : 64 or 128.  rot : a multiple of 16, 0 to d.  eps : finite, >= 0.
- *   dtype : FA_BF16 or FA_F32 (arithmetic in float32 either way).
+ *   dtype : FA_BF16 or FA_F32 (arithmetic in float32 either way: x^2 is summed in it, so that a
+ *   row's largest magnitude has to be below 2^60, and with eps below 2^-100 above 2^-60).
  * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, B, H, H_kv, N < 1, bad rot, eps,
  * frequencies or dtype), FA_ERR_UNSUPPORTED (other d, sizes beyond the limits above, B*N
  * beyond 2^31 - 1), FA_ERR_CUDA (launch failure).
@@ -428,6 +429,8 @@ int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes,
  *   q, o  : [B][H][N_q][d] bfloat16.   lse : [B][H][N_q] float32, or NULL.  The scores take
  *           q to 2^-28 of its row's largest magnitude, which has to lie between 2^-85 and
  *           2^115 (or be 0).
+ *   V       : P times V's scales is rounded to bfloat16 in that type's range: values above 2^100 in
+ *           magnitude may overflow, groups of 32 below 2^-100 lose bits.
  *   lengths : [B] int32, device.
  *   workspace : at least fa_decode_kv4_workspace_size() bytes; its contents on entry do not
  *           matter.  Calls that overlap in time must not share one.

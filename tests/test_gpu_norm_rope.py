@@ -181,6 +181,14 @@ def test_without_eps(H, H_kv, d, dtype):
     run_both(2, 19, H, H_kv, d, dtype, d, False, None, eps=0.0)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("exponent", [-57, 57])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+def test_magnitudes_at_the_ends_of_the_range(exponent, eps, dtype, d):
+    # rows whose largest value is near 2^-56 or 2^59: squares and their sums stay within float32
+    run_both(1, 9, 3, 1, d, dtype, d, False, None, eps=eps, scale=2.0 ** exponent)
+
+
 def exact_angles(positions, inv_freq):
     """positions [n] times frequencies [p], less whole turns, from integers: float64 in [-pi, pi]."""
     bits = 1400
