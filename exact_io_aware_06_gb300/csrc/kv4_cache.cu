@@ -6,7 +6,8 @@
 // maximum is two shuffles.  A thread takes a row of K and the same row of V: the way to their
 // bytes (request, its first token, its page: three dependent loads) is gone once for both.
 // Instructions bound these kernels next to memory, hence the arithmetic below.  Measured for two
-// prompts of 8192 tokens, 8 heads of d = 128 (67 MB of bf16): append and read 31.3 us together, 5.5 TB/s.
+// prompts of 8192 tokens, 8 heads of d = 128 (67 MB of bf16): append and read 31.2 us together for 153 MB,
+// 4.9 TB/s (the codes counted once: what the read finds in L2 is not traffic).
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"

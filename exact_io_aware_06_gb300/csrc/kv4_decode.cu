@@ -31,9 +31,14 @@
 //     requests or a part of one.  Whole requests are written at once; parts go to the
 //     workspace, and decode_join_kernel adds them.  The cut depends on the lengths alone, so
 //     results do not change from call to call.
-// Measured (H32 H_kv8 d128): 64 requests of 1000 to 32768 tokens 294 us (4.2 TB/s, 63% of
-// the copy rate, bound by the instructions that expand codes; twelve warps of 168 registers an SM:
-// eight took 8% longer, sixteen with spills 10%; rings of three steps 1%); one of 16000 tokens 15.1 us.
+// Measured (H32 H_kv8 d128): 64 requests of 1000 to 32768 tokens 294 us (4.2 TB/s, 63% of the copy
+// rate).  0.61 instructions a cycle and scheduler, the integer pipe 60% busy: neither is full, and what
+// limits is the latency of a step's chain (codes, product, maximum, exponentials, product) with three
+// warps a scheduler (twelve of 168 registers an SM: eight took 8% longer, sixteen with spills 10%; rings of
+// three steps 1%).  One request of 16000 tokens 15.1 us.
+// More than 16 rows of a K/V head read and expand its codes once for every 16 of them: the same batch
+// with 1, 2, 4 and 8 new tokens (4, 8, 16 and 32 rows) 294, 304, 429 and 842 us.  A window of 4096 and 4
+// sinks 85 us, d = 64 193 us.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -313,8 +318,9 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 12 : 8) / kWarps)
         int stage = 0, fill = kStages - 1;  // ring positions of this step and of the one to be fetched
 
         // Q^T fragments in fp16, in the order of d that a lane's K words have.  A row is scaled by
-        // a power of two to below 2^14 (back in c_row), so that its bf16 values are exact down to
-        // 2^-28 of the largest, and where K's nibble comes as 16 u, q is divided by 16.
+        // a power of two to below 2^14 (back in c_row), and where K's nibble comes as 16 u, q is
+        // divided by 16: its bf16 values are exact down to 2^-26 of the largest and off by 2^-34 of
+        // it at most below.
         uint32_t qf[NT][D / 16][2];
         float q0[NT][G][2];  // -8 sum of q by group, times 2^-24: what takes the codes' 8 out
         float c_row[NT][2];  // scale * log2(e) * 2^24 over the rows' factors

@@ -234,7 +234,7 @@ __device__ __forceinline__ void heads_of(const NormRopeArgs& a, const Split& sp,
 // The loads of the next batch (of this token or the warp's next one) are in flight while one
 // is worked on: 4 KB a warp, 64 KB an SM.  Measured at B1 N16384 H32 H_kv8 d128 (403 MB):
 // batches of 8 passes and 4 blocks an SM 68.7 us (5.9 TB/s, 87% of the copy rate), 4 and 5
-// 69.8, 4 and 4 71.3, 2 and 5 83; waiting for each batch 113.  And weights are multiplied into a
+// 69.8, 4 and 4 71.3, 2 and 5 83; waiting for each batch 113.  In float32 132 us (805 MB, 6.1 TB/s).  And weights are multiplied into a
 // token's cosines and sines once for Q's heads and once for K's.
 template <int D, bool F32, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4)
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 // Gradient.  Each lane keeps its eight elements' sums of dw over all of the warp's rows; the
 // block's warps are then added in order and written as one partial row per block, and
 // dweight_sum_kernel adds the blocks in order: no atomics, the same bits every time.
-// Measured at B4 N4096 H32 H_kv8 d128 (570 MB): batches of 4 passes and 3 blocks an SM 102 us
+// Measured at B4 N4096 H32 H_kv8 d128 (570 MB): batches of 4 passes and 3 blocks an SM 101 us
 // (5.6 TB/s), 2 and 4 112, 1 and 4 157.
 template <int D, bool F32, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3)

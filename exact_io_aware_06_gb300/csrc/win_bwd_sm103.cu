@@ -400,9 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -delta_i and -lse_i * log2(e) (rows past N: 0 and -inf, so that recomputed P is exactly 0 there).
 // Both are stored negated so the main kernels add them with packed FMA/FADD.  D / 8 threads per row.
 //
-// delta_i = dO_i . O_i takes the O that the forward rounded to bf16, which is off by up to 2^-9 |O| |dO|
+// delta_i = dO_i . O_i takes the O that the forward rounded to bf16, which is off by up to 2^-8 |O| |dO|
 // beside dP's spread: little against dS's own rounding where many keys average out in O, as much as
-// it at four keys.  A head's first kFirst rows, which see no more keys than that and have the largest
+// it at four keys.  A head's first kFirst rows, which see kFirst keys at most and have the largest
 // gradients, take delta_i = sum_j P_ij dP_ij instead, in `extra` CTAs beside the others, a warp a row
 // (dQ's error relative to 64 bits, N1024 W512 d64: 2.54e-3 -> 2.46e-3 for 1% of a step).  So do all rows
 // of sequences of up to kShort, and under a window and sinks of up to kNarrow keys in all, in a kernel
@@ -602,7 +602,8 @@ size_t rows_bytes(int BH, int N) {
 // How a sink block's later query blocks are dealt: pieces no shorter than a window's run of
 // blocks, at most 64 a block, and together about two per SM, which keeps any one of them
 // below the mean load of a CTA (B1 H_kv1 N131072 W1024: 1024 later blocks in 64 pieces of 16
-// against 60 blocks a CTA).
+// against 60 blocks a CTA).  Two per SM of 152, whatever the current device: the workspace's size and
+// the order of the sums follow from the sizes alone.
 WinSplit win_split(int B, int H_kv, int N, int window, int sinks) {
     const int n_q = (N + kBlk - 1) / kBlk;
     WinSplit sp;

@@ -21,8 +21,9 @@
 // the order of MMAs are the plain forward's; O leaves through shared memory and TMA stores.  Every
 // wait is bounded, and a wait that runs out is recorded and ends the CTA with its copies and MMAs
 // drained.
-// Measured: N16384 W4096, 4 sinks, H32 H_kv8 620 us, 1553 TFLOP/s of visible pairs (81% of the bf16
-// peak); N8191 W1024, 16 sinks, H16 71 us.
+// Measured: N16384 W4096, 4 sinks, H32 H_kv8 623 us on a cool GPU, 1546 TFLOP/s of visible pairs (80% of
+// the bf16 peak), 660-683 us (1412-1460) called for a second or more, when the power cap lowers the clock;
+// N8191 W1024, 16 sinks, H16 71 us.
 #include <type_traits>
 
 #include "win_fwd.cuh"
