@@ -24,7 +24,9 @@ __all__ = [
 _LAYER = (
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_fwd_window",
     "fa_bwd_window", "fa_bwd_window_workspace_size", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
-    "fa_decode_kv4_workspace_size", "rope_frequencies", "kv4_cache",
+    "fa_decode_kv4_workspace_size", "rope_frequencies", "kv4_cache", "fa_qk_norm_rope_axes",
+    "fa_qk_norm_rope_axes_bwd", "rope_axes", "fa_fwd_cross", "fa_fwd_cross_workspace_size", "fa_fwd_prefix",
+    "fa_fwd_prefix_workspace_size",
 )
 __all__ += _LAYER
 
@@ -92,12 +94,24 @@ def lib():
         L.fa_qk_norm_rope_bwd.restype = i
         L.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i] * 5
         L.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+        L.fa_qk_norm_rope_axes.argtypes = [vp] * 9 + [i] * 8 + [f, i, vp]
+        L.fa_qk_norm_rope_axes.restype = i
+        L.fa_qk_norm_rope_axes_bwd.argtypes = [vp] * 13 + [sz] + [i] * 8 + [f, i, vp]
+        L.fa_qk_norm_rope_axes_bwd.restype = i
         L.fa_fwd_window.argtypes = [vp] * 5 + [i] * 5 + [f, i, i, i, vp]
         L.fa_fwd_window.restype = i
         L.fa_bwd_window.argtypes = [vp] * 10 + [sz] + [i] * 5 + [f, i, i, i, vp]
         L.fa_bwd_window.restype = i
         L.fa_bwd_window_workspace_size.argtypes = [i] * 7
         L.fa_bwd_window_workspace_size.restype = sz
+        L.fa_fwd_cross.argtypes = [vp] * 7 + [sz] + [i] * 7 + [f, i, vp]
+        L.fa_fwd_cross.restype = i
+        L.fa_fwd_cross_workspace_size.argtypes = [i] * 7
+        L.fa_fwd_cross_workspace_size.restype = sz
+        L.fa_fwd_prefix.argtypes = [vp] * 9 + [sz] + [i] * 7 + [f, i, vp]
+        L.fa_fwd_prefix.restype = i
+        L.fa_fwd_prefix_workspace_size.argtypes = [i] * 7
+        L.fa_fwd_prefix_workspace_size.restype = sz
         L.fa_kv4_append.argtypes = [vp] * 9 + [i] * 7 + [vp]
         L.fa_kv4_append.restype = i
         L.fa_kv4_read.argtypes = [vp] * 8 + [i] * 7 + [vp]

@@ -55,8 +55,21 @@ def rope_frequencies(rot, base=10000.0):
     return float(base) ** (-torch.arange(rot // 2, dtype=torch.float64) * 2 / rot)
 
 
-def _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, device):
-    """Pointers of qkv, weights, positions, frequencies, q, k, v; B, H, H_kv, N, d, rot; dtype code."""
+def rope_axes(sections, base=10000.0, shared=False):
+    """inv_freq (float64) and axis (int32) of rot / 2 pairs, host tensors, for sections[a] rotated
+    elements of axis a, in order: each axis with a run of frequencies of its own, from 1 down to
+    about 1 / base, or with `shared` one run over all of them."""
+    if any(n % 2 or n < 0 for n in sections):
+        raise ValueError(f"sections: even numbers of elements expected, got {sections}")
+    axis = torch.repeat_interleave(torch.arange(len(sections), dtype=_I32), torch.tensor(sections) // 2)
+    if shared:
+        return rope_frequencies(sum(sections), base), axis
+    return torch.cat([rope_frequencies(n, base) for n in sections]), axis
+
+
+def _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, device, axes=None):
+    """Pointers of qkv, weights, positions, frequencies, q, k, v; B, H, H_kv, N, d, rot; dtype code.
+    axes: the number of positions' axes, a dimension in front, where it has one."""
     t = qkv.dtype
     if t is not _BF16 and t is not _F32:
         raise ValueError(f"qkv: float32 or bfloat16 expected, got {t}")
@@ -71,7 +84,8 @@ def _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, device):
     return ((_dense("qkv", qkv, t, (B, N, H + 2 * H_kv, d), device),
              None if q_weight is None else _dense("q_weight", q_weight, _F32, (d,), device),
              None if k_weight is None else _dense("k_weight", k_weight, _F32, (d,), device),
-             None if positions is None else _dense("positions", positions, _I32, (B, N), device),
+             None if positions is None else _dense("positions", positions, _I32,
+                                                   (B, N) if axes is None else (axes, B, N), device),
              inv_freq.data_ptr() if rot else None, _dense("q", q, t, (B, H, N, d), device),
              _dense("k", k, t, kv, device), _dense("v", v, t, kv, device)),
             (B, H, H_kv, N, d, rot), FA_BF16 if t is _BF16 else FA_F32)
@@ -107,6 +121,45 @@ def fa_qk_norm_rope_bwd(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv
         *sizes, bool(interleaved), eps, code, _handle(stream, device)), "fa_qk_norm_rope_bwd")
 
 
+def _axes(positions, inv_freq, axis):
+    """Number of axes of positions [axes, B, N], and the host pointer of axis, one entry a pair."""
+    if positions is None and inv_freq is None:  # nothing is turned
+        return 1, None
+    if positions is None or positions.dim() != 3:
+        raise ValueError("positions: [axes, B, N] expected")
+    n = 0 if inv_freq is None else inv_freq.numel()
+    if n and (axis is None or axis.dtype is not _I32 or axis.is_cuda or not axis.is_contiguous() or axis.numel() != n):
+        raise ValueError(f"axis: a contiguous int32 tensor of {n} entries on the host (rope_axes)")
+    return positions.shape[0], axis.data_ptr() if n else None
+
+
+def fa_qk_norm_rope_axes(qkv, q_weight, k_weight, positions, inv_freq, axis, q, k, v, eps, interleaved=False,
+                         stream=None):
+    """fa_qk_norm_rope with positions of several axes (int32 [axes, B, N]); axis: the axis of each of
+    inv_freq's pairs (int32 host tensor, as from rope_axes).  All three may be None: no rotation."""
+    device = _current_device()
+    n_axes, which = _axes(positions, inv_freq, axis)
+    pointers, sizes, code = _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, q, k, v, device, n_axes)
+    _check(lib().fa_qk_norm_rope_axes(*pointers[:5], which, *pointers[5:], *sizes, n_axes, bool(interleaved), eps,
+                                      code, _handle(stream, device)), "fa_qk_norm_rope_axes")
+
+
+def fa_qk_norm_rope_axes_bwd(qkv, q_weight, k_weight, positions, inv_freq, axis, dq, dk, dv, dqkv, dq_weight,
+                             dk_weight, workspace, eps, interleaved=False, stream=None):
+    """dqkv and (float32 [d], or None) dq_weight, dk_weight <- gradient of fa_qk_norm_rope_axes; its
+    workspace (fa_qk_norm_rope_bwd_workspace_size) may be None if neither weight gradient is wanted."""
+    device = _current_device()
+    n_axes, which = _axes(positions, inv_freq, axis)
+    pointers, sizes, code = _norm_rope(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv, device, n_axes)
+    d = sizes[4]
+    space, nbytes = (None, 0) if workspace is None else _space(workspace, device)
+    _check(lib().fa_qk_norm_rope_axes_bwd(
+        *pointers[:5], which, *pointers[5:], _dense("dqkv", dqkv, qkv.dtype, qkv.shape, device),
+        None if dq_weight is None else _dense("dq_weight", dq_weight, _F32, (d,), device),
+        None if dk_weight is None else _dense("dk_weight", dk_weight, _F32, (d,), device), space, nbytes,
+        *sizes, n_axes, bool(interleaved), eps, code, _handle(stream, device)), "fa_qk_norm_rope_axes_bwd")
+
+
 # ---------------------------------------------------------------- windowed attention
 def fa_fwd_window(q, k, v, o, lse, scale, window, n_sink, dtype=FA_BF16, stream=None):
     """Forward under a causal window of `window` keys and the first n_sink keys: q, o
@@ -140,6 +193,47 @@ def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_s
         _dense("dq", dq, _BF16, rows, device), _dense("dk", dk, _BF16, kv_rows, device),
         _dense("dv", dv, _BF16, kv_rows, device), *_space(workspace, device), B, H, H_kv, N, d, scale,
         _int(window), _int(n_sink), dtype, _handle(stream, device)), "fa_bwd_window")
+
+
+# ---------------------------------------------------------------- another sequence's keys
+def _cross(q, k, v, kv_lengths, o, lse, workspace, device):
+    """Pointers of q, k, v, lengths, o, lse; of the workspace, and its bytes; B, B_kv, H, H_kv, N_q, N_kv, d."""
+    B, H, N_q, d = rows = _sizes("q", q)
+    B_kv, H_kv, N_kv, _ = _sizes("k", k)
+    kv_rows = (B_kv, H_kv, N_kv, d)
+    return ((_dense("q", q, _BF16, rows, device), _dense("k", k, _BF16, kv_rows, device),
+             _dense("v", v, _BF16, kv_rows, device),
+             None if kv_lengths is None else _dense("kv_lengths", kv_lengths, _I32, (B_kv,), device),
+             _dense("o", o, _BF16, rows, device),
+             None if lse is None else _dense("lse", lse, _F32, (B, H, N_q), device)),
+            (None, 0) if workspace is None else _space(workspace, device), (B, B_kv, H, H_kv, N_q, N_kv, d))
+
+
+def fa_fwd_cross_workspace_size(B, B_kv, H, H_kv, N_q, N_kv, d):
+    return int(lib().fa_fwd_cross_workspace_size(*map(_int, (B, B_kv, H, H_kv, N_q, N_kv, d))))
+
+
+def fa_fwd_cross(q, k, v, kv_lengths, o, lse, workspace, scale, dtype=FA_BF16, stream=None):
+    """o (and lse, may be None) <- attention of q [B, H, N_q, d] to k, v [B_kv, H_kv, N_kv, d] (bfloat16),
+    batch b to K/V batch b // (B // B_kv), of whose keys the first kv_lengths (int32 [B_kv], None: all) are
+    seen.  workspace may be None if none is needed."""
+    device = _current_device()
+    pointers, space, sizes = _cross(q, k, v, kv_lengths, o, lse, workspace, device)
+    _check(lib().fa_fwd_cross(*pointers, *space, *sizes, scale, dtype, _handle(stream, device)), "fa_fwd_cross")
+
+
+def fa_fwd_prefix_workspace_size(B, B_kv, H, H_kv, N_q, N_kv, d):
+    return int(lib().fa_fwd_prefix_workspace_size(*map(_int, (B, B_kv, H, H_kv, N_q, N_kv, d))))
+
+
+def fa_fwd_prefix(q, k, v, kv_lengths, o_own, lse_own, o, lse, workspace, scale, dtype=FA_BF16, stream=None):
+    """fa_fwd_cross to a prefix that the batches share (k, v [B_kv, H_kv, N_kv, d]), merged with o_own and lse_own,
+    the queries' attention to their own tokens.  o may be o_own, lse may be lse_own or None."""
+    device = _current_device()
+    (*qkv, out, out_lse), space, sizes = _cross(q, k, v, kv_lengths, o, lse, workspace, device)
+    _check(lib().fa_fwd_prefix(*qkv, _dense("o_own", o_own, _BF16, q.shape, device),
+                               _dense("lse_own", lse_own, _F32, q.shape[:3], device), out, out_lse, *space, *sizes,
+                               scale, dtype, _handle(stream, device)), "fa_fwd_prefix")
 
 
 # ---------------------------------------------------------------- the 4-bit cache

@@ -53,6 +53,7 @@ int norm_rope_args(NormRopeArgs* a, const void* qkv, const float* qw, const floa
     a->weight[0] = qw;
     a->weight[1] = kw;
     a->pos = pos;
+    a->axes = 1;
     a->heads[0] = H;
     a->heads[1] = a->heads[2] = H_kv;
     a->N = N;
@@ -100,12 +101,68 @@ int window_args(int B, int H, int H_kv, int N, int d, float scale, int window, i
     return FA_OK;
 }
 
+// Sizes of attention to another sequence's keys.
+int cross_sizes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
+    if (B < 1 || B_kv < 1 || H < 1 || H_kv < 1 || N_q < 1 || N_kv < 1 || B % B_kv != 0 || H % H_kv != 0)
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (!sizes_supported(B, H, N_q) || !sizes_supported(B_kv, H_kv, N_kv)) return FA_ERR_UNSUPPORTED;
+    // the rows that share a K/V head in one batch are counted in an int, a tile's past the end included
+    if (static_cast<int64_t>(H / H_kv) * N_q > 0x7fffffffll - 256) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+int cross_args(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d, float scale, int dtype) {
+    if (!std::isfinite(scale) || (dtype != FA_F32 && dtype != FA_BF16)) return FA_ERR_INVALID_ARG;
+    const int rc = cross_sizes(B, B_kv, H, H_kv, N_q, N_kv, d);
+    if (rc != FA_OK) return rc;
+    return dtype == FA_BF16 ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 }  // namespace fa
 
 using namespace fa;
 
 #define FA_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+// Positions' axes and each pair's own.
+int norm_rope_axes(NormRopeArgs* a, const int* axis, int n_axes) {
+    if (n_axes < 1 || n_axes > kMaxRopeAxes) return FA_ERR_INVALID_ARG;
+    if (a->rot > 0 && (axis == nullptr || a->pos == nullptr)) return FA_ERR_INVALID_ARG;
+    a->axes = n_axes;
+    for (int p = 0; p < a->rot / 2; ++p) {
+        if (axis[p] < 0 || axis[p] >= n_axes) return FA_ERR_INVALID_ARG;
+        a->axis[p] = static_cast<uint8_t>(axis[p]);
+    }
+    return FA_OK;
+}
+
+int norm_rope_forward(NormRopeArgs& a, void* q, void* k, void* v, int d, int interleaved, int dtype, void* stream) {
+    a.out[0] = q;
+    a.out[1] = k;
+    a.out[2] = v;
+    return from_cuda(launch_qk_norm_rope(a, d, dtype == FA_F32, interleaved ? 1 : 0, static_cast<cudaStream_t>(stream)));
+}
+
+int norm_rope_backward(NormRopeArgs& a, const void* dq, const void* dk, const void* dv, void* dqkv, float* dq_weight,
+                       float* dk_weight, void* workspace, size_t workspace_bytes, int d, int interleaved, int dtype,
+                       void* stream) {
+    if ((dq_weight != nullptr || dk_weight != nullptr) &&
+        (workspace == nullptr || workspace_bytes < qk_norm_rope_bwd_workspace_bytes(d)))
+        return FA_ERR_INVALID_ARG;
+    a.grad[0] = dq;
+    a.grad[1] = dk;
+    a.grad[2] = dv;
+    a.dqkv = dqkv;
+    a.part = static_cast<float*>(workspace);
+    float* const dw[2] = {dq_weight, dk_weight};
+    return from_cuda(
+        launch_qk_norm_rope_bwd(a, dw, d, dtype == FA_F32, interleaved ? 1 : 0, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
 
 FA_API int fa_qk_norm_rope(const void* qkv, const float* q_weight, const float* k_weight, const int* positions,
                            const double* inv_freq, void* q, void* k, void* v, int B, int H, int H_kv, int N, int d,
@@ -114,10 +171,19 @@ FA_API int fa_qk_norm_rope(const void* qkv, const float* q_weight, const float* 
     NormRopeArgs a;
     const int rc = norm_rope_args(&a, qkv, q_weight, k_weight, positions, inv_freq, B, H, H_kv, N, d, rot, eps, dtype);
     if (rc != FA_OK) return rc;
-    a.out[0] = q;
-    a.out[1] = k;
-    a.out[2] = v;
-    return from_cuda(launch_qk_norm_rope(a, d, dtype == FA_F32, interleaved ? 1 : 0, static_cast<cudaStream_t>(stream)));
+    return norm_rope_forward(a, q, k, v, d, interleaved, dtype, stream);
+}
+
+FA_API int fa_qk_norm_rope_axes(const void* qkv, const float* q_weight, const float* k_weight, const int* positions,
+                                const double* inv_freq, const int* axis, void* q, void* k, void* v, int B, int H,
+                                int H_kv, int N, int d, int rot, int n_axes, int interleaved, float eps, int dtype,
+                                void* stream) {
+    if (!pointers_ok(q, k, v)) return FA_ERR_INVALID_ARG;
+    NormRopeArgs a;
+    int rc = norm_rope_args(&a, qkv, q_weight, k_weight, positions, inv_freq, B, H, H_kv, N, d, rot, eps, dtype);
+    if (rc == FA_OK) rc = norm_rope_axes(&a, axis, n_axes);
+    if (rc != FA_OK) return rc;
+    return norm_rope_forward(a, q, k, v, d, interleaved, dtype, stream);
 }
 
 FA_API size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int H_kv, int N, int d) {
@@ -133,17 +199,22 @@ FA_API int fa_qk_norm_rope_bwd(const void* qkv, const float* q_weight, const flo
     NormRopeArgs a;
     const int rc = norm_rope_args(&a, qkv, q_weight, k_weight, positions, inv_freq, B, H, H_kv, N, d, rot, eps, dtype);
     if (rc != FA_OK) return rc;
-    if ((dq_weight != nullptr || dk_weight != nullptr) &&
-        (workspace == nullptr || workspace_bytes < qk_norm_rope_bwd_workspace_bytes(d)))
-        return FA_ERR_INVALID_ARG;
-    a.grad[0] = dq;
-    a.grad[1] = dk;
-    a.grad[2] = dv;
-    a.dqkv = dqkv;
-    a.part = static_cast<float*>(workspace);
-    float* const dw[2] = {dq_weight, dk_weight};
-    return from_cuda(
-        launch_qk_norm_rope_bwd(a, dw, d, dtype == FA_F32, interleaved ? 1 : 0, static_cast<cudaStream_t>(stream)));
+    return norm_rope_backward(a, dq, dk, dv, dqkv, dq_weight, dk_weight, workspace, workspace_bytes, d, interleaved,
+                              dtype, stream);
+}
+
+FA_API int fa_qk_norm_rope_axes_bwd(const void* qkv, const float* q_weight, const float* k_weight,
+                                    const int* positions, const double* inv_freq, const int* axis, const void* dq,
+                                    const void* dk, const void* dv, void* dqkv, float* dq_weight, float* dk_weight,
+                                    void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int N, int d,
+                                    int rot, int n_axes, int interleaved, float eps, int dtype, void* stream) {
+    if (!pointers_ok(dq, dk, dv, dqkv) || !optional_ok(dq_weight, dk_weight, workspace)) return FA_ERR_INVALID_ARG;
+    NormRopeArgs a;
+    int rc = norm_rope_args(&a, qkv, q_weight, k_weight, positions, inv_freq, B, H, H_kv, N, d, rot, eps, dtype);
+    if (rc == FA_OK) rc = norm_rope_axes(&a, axis, n_axes);
+    if (rc != FA_OK) return rc;
+    return norm_rope_backward(a, dq, dk, dv, dqkv, dq_weight, dk_weight, workspace, workspace_bytes, d, interleaved,
+                              dtype, stream);
 }
 
 FA_API int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int H_kv,
@@ -237,4 +308,48 @@ FA_API int fa_decode_kv4(const void* q, const void* k_codes, const void* k_scale
     int err = FA_OK;
     if (!device_ctl(&a.ctl, &err)) return err;
     return from_cuda(launch_decode_kv4(a, d, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+int cross_forward(const void* q, const void* k, const void* v, const int* lengths, const void* o_own,
+                  const float* lse_own, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int B_kv,
+                  int H, int H_kv, int N_q, int N_kv, int d, float scale, int dtype, void* stream) {
+    if (!pointers_ok(q, k, v, o) || !optional_ok(lengths, lse, workspace)) return FA_ERR_INVALID_ARG;
+    int rc = cross_args(B, B_kv, H, H_kv, N_q, N_kv, d, scale, dtype);
+    if (rc != FA_OK) return rc;
+    const size_t need = fwd_cross_workspace_bytes(B, B_kv, H, H_kv, N_q, N_kv, d);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+    DevCtl ctl;
+    if (!device_ctl(&ctl, &rc)) return rc;
+    const int e = launch_fwd_cross(q, k, v, lengths, o_own, lse_own, o, lse, workspace, B, B_kv, H, H_kv, N_q, N_kv, d,
+                                   scale * 1.4426950408889634f, ctl, static_cast<cudaStream_t>(stream));
+    return e == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+FA_API int fa_fwd_cross(const void* q, const void* k, const void* v, const int* kv_lengths, void* o, float* lse,
+                        void* workspace, size_t workspace_bytes, int B, int B_kv, int H, int H_kv, int N_q, int N_kv,
+                        int d, float scale, int dtype, void* stream) {
+    return cross_forward(q, k, v, kv_lengths, nullptr, nullptr, o, lse, workspace, workspace_bytes, B, B_kv, H, H_kv,
+                         N_q, N_kv, d, scale, dtype, stream);
+}
+
+FA_API size_t fa_fwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
+    return cross_sizes(B, B_kv, H, H_kv, N_q, N_kv, d) == FA_OK
+               ? fwd_cross_workspace_bytes(B, B_kv, H, H_kv, N_q, N_kv, d)
+               : 0;
+}
+
+FA_API int fa_fwd_prefix(const void* q, const void* k, const void* v, const int* kv_lengths, const void* o_own,
+                         const float* lse_own, void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
+                         int B_kv, int H, int H_kv, int N_q, int N_kv, int d, float scale, int dtype, void* stream) {
+    if (!pointers_ok(o_own, lse_own)) return FA_ERR_INVALID_ARG;
+    return cross_forward(q, k, v, kv_lengths, o_own, lse_own, o, lse, workspace, workspace_bytes, B, B_kv, H, H_kv,
+                         N_q, N_kv, d, scale, dtype, stream);
+}
+
+FA_API size_t fa_fwd_prefix_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
+    return fa_fwd_cross_workspace_size(B, B_kv, H, H_kv, N_q, N_kv, d);
 }

@@ -39,6 +39,8 @@ inline Div make_div(uint32_t d) {
     return {d, static_cast<uint32_t>((((1ull << l) - d) << 32) / d + 1), l};
 }
 
+constexpr int kMaxRopeAxes = 8;  // of positions: time, height, width, ...
+
 // Angle of position t in rotation pair p, in turns: frac(t * f[p] / 2^64).
 struct RopeFreq {
     uint64_t f[64];
@@ -47,7 +49,7 @@ struct RopeFreq {
 struct NormRopeArgs {
     const void* qkv;        // [B][N][H + 2 H_kv][d]
     const float* weight[2]; // q, k; null: ones
-    const int* pos;         // [B][N]; null: the index in the sequence
+    const int* pos;         // [B][N], or with several axes [axes][B][N]; null: the index in the sequence
     void* out[3];           // forward: q, k, v
     const void* grad[3];    // backward: dq, dk, dv
     void* dqkv;             // backward
@@ -57,6 +59,8 @@ struct NormRopeArgs {
     uint32_t tokens;        // B * N, below 2^31
     float eps;
     RopeFreq freq;
+    int axes;               // of positions
+    uint8_t axis[64];       // of each pair, where axes > 1
 };
 
 // d in {64, 128}; rot a multiple of 16, at most d.
@@ -117,6 +121,13 @@ size_t bwd_window_workspace_bytes(int B, int H, int H_kv, int N, int d, int wind
 int launch_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
                       void* dq, void* dk, void* dv, void* workspace, int B, int H, int H_kv, int N, int d, float scale,
                       int window, int sinks, DevCtl ctl, cudaStream_t s);
+
+// Attention of q [B][H][N_q][d] to k, v [B_kv][H_kv][N_kv][d], batch b to K/V batch b / (B / B_kv), of whose
+// keys the first lengths[b / ..] are real (null: all); with lse_own merged with (o_own, lse_own).
+size_t fwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d);
+int launch_fwd_cross(const void* q, const void* k, const void* v, const int* lengths, const void* o_own,
+                     const float* lse_own, void* o, float* lse, void* workspace, int B, int B_kv, int H, int H_kv, int N_q,
+                     int N_kv, int d, float c_log2, DevCtl ctl, cudaStream_t s);
 
 constexpr int kDevIndex = 5;  // == FA_ERR_DEVICE_INDEX: a page or length outside the cache
 

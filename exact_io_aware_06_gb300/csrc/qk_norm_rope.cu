@@ -17,12 +17,16 @@
 // and serve all of its heads.  At 43 cycles of an SM per pass (read and write at the copy
 // rate) the instructions count too: pairs within a lane, packed float32 arithmetic.
 //
+// Positions may have several axes (time, height and width of a video's tokens): pair p then turns by
+// t[axis_p] f_p, and a lane keeps the axes of its pairs and fetches its own positions a batch ahead.
+//
 // Angles: t f_p / (2 pi) turns.  A float product would lose the fraction at far positions
 // (t = 10^6: errors of 0.06 rad); a table would be read again by every token.  f_p / (2 pi)
 // is held as a 64-bit fraction instead, off by under 2^-62 (rope_turns.h), and t times it modulo
 // 2^64 is an integer product that drops whole turns exactly.  Of the product the upper 32 bits are
 // taken and rounded to a float: at |t| = 2^31 the angle is off by 2^-31 + 2^-32 + 2^-26 turns.
 #include <atomic>
+#include <type_traits>
 
 #include "layer_ops.h"
 #include "ptx.cuh"
@@ -145,14 +149,15 @@ __device__ __forceinline__ void lane_groups(int rot, int j, int& ea, int& eb) {
     }
 }
 
-// cos and sin of the lane's pairs at position t (1 and 0 past rot); `tab` is the warp's own.
-template <int D, bool INTER>
-__device__ __forceinline__ void token_angles(const NormRopeArgs& a, int t, float2* tab, int lane, float2 (&c)[2],
-                                             float2 (&s)[2]) {
+// cos and sin of the lane's pairs at the token's position (1 and 0 past rot); `tab` is the warp's own.
+template <int D, bool INTER, int AXES>
+__device__ __forceinline__ void token_angles(const NormRopeArgs& a, const int (&pos)[AXES], float2* tab, int lane,
+                                             float2 (&c)[2], float2 (&s)[2]) {
     constexpr int kLanes = D / 8;
     const int half = a.rot / 2, j = lane % kLanes;
     __syncwarp();  // the last token's factors have been read
     for (int p = lane; p < half; p += 32) {
+        const int t = AXES == 2 && p >= 32 ? pos[AXES - 1] : pos[0];
         // signed fraction of a turn, in half turns: [-1, 1)
         const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(t)) * a.freq.f[p];
         const float h = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
@@ -180,23 +185,35 @@ struct Split {
     Div by_tokens, by_n;
 };
 
-// A warp's place in its work: a batch of up to AHEAD passes of one of Q, K, V of a token.
+// The axes of the lane's pairs, lane and lane + 32; -1 past rot.
+struct LaneAxes {
+    int of[2];
+    __device__ __forceinline__ LaneAxes(const NormRopeArgs& a, int lane) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) of[i] = lane + 32 * i < a.rot / 2 ? a.axis[lane + 32 * i] : -1;
+    }
+};
+
+// A warp's place in its work: a batch of up to AHEAD passes of one of Q, K, V of a token.  With several
+// axes (AXES = 2) the positions are those of the lane's two pairs.
+template <int AXES>
 struct Place {
     uint32_t it, tk, b;
-    int n, pos;
+    int n, pos[AXES];
     int seg, p, p1;     // this batch's first pass, and the item's end
     int count;          // passes of the batch
     bool fresh;         // the item's first batch
 };
-template <int AHEAD>
-__device__ __forceinline__ void batch_at(const Split& sp, Place& p) {
+template <int AHEAD, int AXES>
+__device__ __forceinline__ void batch_at(const Split& sp, Place<AXES>& p) {
     p.seg = (p.p >= sp.first[1]) + (p.p >= sp.first[2]);
     const int end = p.seg == 0 ? sp.first[1] : p.seg == 1 ? sp.first[2] : sp.first[3];
     p.count = min(AHEAD, min(end, p.p1) - p.p);
 }
-template <int AHEAD>
-__device__ __forceinline__ Place place_at(const NormRopeArgs& a, const Split& sp, uint32_t it, uint32_t items) {
-    Place p;
+template <int AHEAD, int AXES>
+__device__ __forceinline__ Place<AXES> place_at(const NormRopeArgs& a, const Split& sp, const LaneAxes& axis,
+                                                uint32_t it, uint32_t items) {
+    Place<AXES> p;
     p.it = it;
     p.fresh = true;
     if (it < items) {
@@ -206,24 +223,30 @@ __device__ __forceinline__ Place place_at(const NormRopeArgs& a, const Split& sp
         p.p1 = min(p.p + sp.per, sp.first[3]);
         p.b = sp.by_n.of(p.tk);
         p.n = static_cast<int>(p.tk - p.b * sp.by_n.d);
-        p.pos = a.pos ? __ldg(a.pos + p.tk) : p.n;
+        if constexpr (AXES == 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                p.pos[i] = axis.of[i] < 0 ? 0 : __ldg(a.pos + (static_cast<size_t>(axis.of[i]) * a.tokens + p.tk));
+        } else {
+            p.pos[0] = a.pos ? __ldg(a.pos + p.tk) : p.n;
+        }
         batch_at<AHEAD>(sp, p);
     }
     return p;
 }
-template <int AHEAD>
-__device__ __forceinline__ Place place_after(const NormRopeArgs& a, const Split& sp, const Place& at, uint32_t step,
-                                             uint32_t items) {
-    if (at.p + at.count >= at.p1) return place_at<AHEAD>(a, sp, at.it + step, items);
-    Place p = at;
+template <int AHEAD, int AXES>
+__device__ __forceinline__ Place<AXES> place_after(const NormRopeArgs& a, const Split& sp, const LaneAxes& axis,
+                                                   const Place<AXES>& at, uint32_t step, uint32_t items) {
+    if (at.p + at.count >= at.p1) return place_at<AHEAD, AXES>(a, sp, axis, at.it + step, items);
+    Place<AXES> p = at;
     p.p += at.count;
     p.fresh = false;
     batch_at<AHEAD>(sp, p);
     return p;
 }
 // The batch's first head of this lane among Q's, K's or V's; their number; heads before them.
-template <int HEADS>
-__device__ __forceinline__ void heads_of(const NormRopeArgs& a, const Split& sp, const Place& p, int grp, int& h,
+template <int HEADS, int AXES>
+__device__ __forceinline__ void heads_of(const NormRopeArgs& a, const Split& sp, const Place<AXES>& p, int grp, int& h,
                                          int& heads, int& before) {
     const int first = p.seg == 0 ? 0 : p.seg == 1 ? sp.first[1] : sp.first[2];
     h = (p.p - first) * HEADS + grp;
@@ -236,7 +259,7 @@ __device__ __forceinline__ void heads_of(const NormRopeArgs& a, const Split& sp,
 // batches of 8 passes and 4 blocks an SM 68.7 us (5.9 TB/s, 87% of the copy rate), 4 and 5
 // 69.8, 4 and 4 71.3, 2 and 5 83; waiting for each batch 113.  In float32 132 us (805 MB, 6.1 TB/s).  And weights are multiplied into a
 // token's cosines and sines once for Q's heads and once for K's.
-template <int D, bool F32, bool INTER>
+template <int D, bool F32, bool INTER, int AXES>
 __global__ void __launch_bounds__(kThreads, 4)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Split sp) {
     constexpr int kLanes = D / 8, kHeads = 32 / kLanes, kElem = F32 ? 4 : 2;
@@ -253,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     griddep_wait();
     griddep_launch_dependents();
     const uint32_t items = a.tokens * sp.chunks, step = gridDim.x * kWarps;
-    auto load = [&](const Place& at, Raw<F32>(&raw)[kAhead]) {
+    auto load = [&](const Place<AXES>& at, Raw<F32>(&raw)[kAhead]) {
         int h, heads, before;
         heads_of<kHeads>(a, sp, at, grp, h, heads, before);
         const char* src = static_cast<const char*>(a.qkv) +
@@ -262,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int u = 0; u < kAhead; ++u)
             raw[u] = load8<F32>(src + u * kPass, src + gap + u * kPass, u < at.count && h + u * kHeads < heads);
     };
-    Place at = place_at<kAhead>(a, sp, blockIdx.x * kWarps + warp, items);
+    const LaneAxes axis(a, lane);
+    Place<AXES> at = place_at<kAhead, AXES>(a, sp, axis, blockIdx.x * kWarps + warp, items);
     Raw<F32> raw[kAhead];
     if (at.it < items) load(at, raw);
     for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
@@ -274,13 +298,13 @@ __global__ void __launch_bounds__(kThreads, 4)
     float2 c[2], s[2];                          // the token's, of this lane's pairs
     float2 cf[2], cs[2], sf[2], ss[2];          // times the weights of first and second elements
     while (at.it < items) {
-        const Place next = place_after<kAhead>(a, sp, at, step, items);
+        const Place<AXES> next = place_after<kAhead>(a, sp, axis, at, step, items);
         Raw<F32> ahead[kAhead];
         if (next.it < items) load(next, ahead);
         int h, heads, before;
         heads_of<kHeads>(a, sp, at, grp, h, heads, before);
         if (at.seg < 2 && (at.fresh || at.p == sp.first[1])) {
-            if (at.fresh) token_angles<D, INTER>(a, at.pos, tab[warp], lane, c, s);
+            if (at.fresh) token_angles<D, INTER, AXES>(a, at.pos, tab[warp], lane, c, s);
             const float4 wa = *reinterpret_cast<const float4*>(&w[at.seg][ea]);
             const float4 wb = *reinterpret_cast<const float4*>(&w[at.seg][eb]);
             const float2 wf[2] = {INTER ? make_float2(wa.x, wa.z) : make_float2(wa.x, wa.y),
@@ -326,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 // dweight_sum_kernel adds the blocks in order: no atomics, the same bits every time.
 // Measured at B4 N4096 H32 H_kv8 d128 (570 MB): batches of 4 passes and 3 blocks an SM 101 us
 // (5.6 TB/s), 2 and 4 112, 1 and 4 157.
-template <int D, bool F32, bool INTER>
+template <int D, bool F32, bool INTER, int AXES>
 __global__ void __launch_bounds__(kThreads, 3)
     qk_norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Split sp) {
     constexpr int kLanes = D / 8, kHeads = 32 / kLanes, kElem = F32 ? 4 : 2;
@@ -345,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     griddep_launch_dependents();
     const uint32_t items = a.tokens * sp.chunks, step = gridDim.x * kWarps;
     const size_t grad_pass = static_cast<size_t>(a.N) * kPass;
-    auto load = [&](const Place& at, Raw<F32>(&rx)[kAhead], Raw<F32>(&rg)[kAhead]) {
+    auto load = [&](const Place<AXES>& at, Raw<F32>(&rx)[kAhead], Raw<F32>(&rg)[kAhead]) {
         int h, heads, before;
         heads_of<kHeads>(a, sp, at, grp, h, heads, before);
         const char* src = static_cast<const char*>(a.qkv) +
@@ -360,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 3)
             grad += grad_pass;
         }
     };
-    Place at = place_at<kAhead>(a, sp, blockIdx.x * kWarps + warp, items);
+    const LaneAxes axis(a, lane);
+    Place<AXES> at = place_at<kAhead, AXES>(a, sp, axis, blockIdx.x * kWarps + warp, items);
     Raw<F32> rx[kAhead], rg[kAhead];
     if (at.it < items) load(at, rx, rg);
     for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
@@ -376,13 +401,13 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
         for (int k = 0; k < 2; ++k) dw[i].first[k] = dw[i].second[k] = make_float2(0.f, 0.f);
     while (at.it < items) {
-        const Place next = place_after<kAhead>(a, sp, at, step, items);
+        const Place<AXES> next = place_after<kAhead>(a, sp, axis, at, step, items);
         Raw<F32> nx[kAhead], ng[kAhead];
         if (next.it < items) load(next, nx, ng);
         int h, heads, before;
         heads_of<kHeads>(a, sp, at, grp, h, heads, before);
         if (at.seg < 2 && (at.fresh || at.p == sp.first[1])) {
-            if (at.fresh) token_angles<D, INTER>(a, at.pos, tab[warp], lane, c, s);
+            if (at.fresh) token_angles<D, INTER, AXES>(a, at.pos, tab[warp], lane, c, s);
             const float4 wa = *reinterpret_cast<const float4*>(&w[at.seg][ea]);
             const float4 wb = *reinterpret_cast<const float4*>(&w[at.seg][eb]);
             wf[0] = INTER ? make_float2(wa.x, wa.z) : make_float2(wa.x, wa.y);
@@ -541,23 +566,23 @@ cudaError_t resident_ctas(K kernel, std::atomic<int> (&known)[64], int* sms, int
     return cudaSuccess;
 }
 
-template <int D, bool F32, bool INTER>
+template <int D, bool F32, bool INTER, int AXES>
 cudaError_t launch_fwd(const NormRopeArgs& a, cudaStream_t s) {
     static std::atomic<int> known[64];
     int sms = 0, cap = 0;
-    const cudaError_t e = resident_ctas(qk_norm_rope_kernel<D, F32, INTER>, known, &sms, &cap);
+    const cudaError_t e = resident_ctas(qk_norm_rope_kernel<D, F32, INTER, AXES>, known, &sms, &cap);
     if (e != cudaSuccess) return e;
     const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps);
     const long long blocks = (static_cast<long long>(a.tokens) * sp.chunks + kWarps - 1) / kWarps;
-    return launch_pdl(qk_norm_rope_kernel<D, F32, INTER>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
+    return launch_pdl(qk_norm_rope_kernel<D, F32, INTER, AXES>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
                       dim3(kThreads), 0, s, a, sp);
 }
 
-template <int D, bool F32, bool INTER>
+template <int D, bool F32, bool INTER, int AXES>
 cudaError_t launch_bwd(NormRopeArgs a, float* const (&dweight)[2], cudaStream_t s) {
     static std::atomic<int> known[64];
     int sms = 0, cap = 0;
-    const cudaError_t e = resident_ctas(qk_norm_rope_bwd_kernel<D, F32, INTER>, known, &sms, &cap);
+    const cudaError_t e = resident_ctas(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, known, &sms, &cap);
     if (e != cudaSuccess) return e;
     const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps);
     const bool want = dweight[0] != nullptr || dweight[1] != nullptr;
@@ -565,10 +590,24 @@ cudaError_t launch_bwd(NormRopeArgs a, float* const (&dweight)[2], cudaStream_t 
     const long long blocks = (static_cast<long long>(a.tokens) * sp.chunks + kWarps - 1) / kWarps;
     if (cap > kBwdMaxBlocks) cap = kBwdMaxBlocks;
     const int grid = static_cast<int>(blocks < cap ? blocks : cap);
-    const cudaError_t e2 = launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER>, dim3(grid), dim3(kThreads), 0, s, a, sp);
+    const cudaError_t e2 = launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, dim3(grid), dim3(kThreads), 0, s, a, sp);
     if (e2 != cudaSuccess || !want) return e2;
     return launch_pdl(dweight_sum_kernel<D>, dim3(2 * D / 8), dim3(256), 0, s, a.part, grid, dweight[0],
                       dweight[1]);
+}
+
+// f with the kernel variant's parameters: d, float32, neighbouring pairs, several axes (2) or one.
+template <typename F>
+cudaError_t pick(const NormRopeArgs& a, int d, int f32, int interleaved, F f) {
+    auto axes = [&](auto D, auto F32, auto INTER) {
+        return a.axes > 1 ? f(D, F32, INTER, std::integral_constant<int, 2>{})
+                          : f(D, F32, INTER, std::integral_constant<int, 1>{});
+    };
+    auto pairs = [&](auto D, auto F32) {
+        return interleaved ? axes(D, F32, std::true_type{}) : axes(D, F32, std::false_type{});
+    };
+    auto type = [&](auto D) { return f32 ? pairs(D, std::true_type{}) : pairs(D, std::false_type{}); };
+    return d == 64 ? type(std::integral_constant<int, 64>{}) : type(std::integral_constant<int, 128>{});
 }
 
 }  // namespace
@@ -578,28 +617,17 @@ size_t qk_norm_rope_bwd_workspace_bytes(int d) {
 }
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int d, int f32, int interleaved, cudaStream_t s) {
-    if (d == 64) {
-        if (f32) return interleaved ? launch_fwd<64, true, true>(a, s) : launch_fwd<64, true, false>(a, s);
-        return interleaved ? launch_fwd<64, false, true>(a, s) : launch_fwd<64, false, false>(a, s);
-    }
-    if (f32) return interleaved ? launch_fwd<128, true, true>(a, s) : launch_fwd<128, true, false>(a, s);
-    return interleaved ? launch_fwd<128, false, true>(a, s) : launch_fwd<128, false, false>(a, s);
+    return pick(a, d, f32, interleaved, [&](auto D, auto F32, auto INTER, auto AXES) {
+        return launch_fwd<decltype(D)::value, decltype(F32)::value, decltype(INTER)::value, decltype(AXES)::value>(a, s);
+    });
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const NormRopeArgs& a, float* const (&dweight)[2], int d, int f32,
                                     int interleaved, cudaStream_t s) {
-    if (d == 64) {
-        if (f32)
-            return interleaved ? launch_bwd<64, true, true>(a, dweight, s)
-                               : launch_bwd<64, true, false>(a, dweight, s);
-        return interleaved ? launch_bwd<64, false, true>(a, dweight, s)
-                           : launch_bwd<64, false, false>(a, dweight, s);
-    }
-    if (f32)
-        return interleaved ? launch_bwd<128, true, true>(a, dweight, s)
-                           : launch_bwd<128, true, false>(a, dweight, s);
-    return interleaved ? launch_bwd<128, false, true>(a, dweight, s)
-                       : launch_bwd<128, false, false>(a, dweight, s);
+    return pick(a, d, f32, interleaved, [&](auto D, auto F32, auto INTER, auto AXES) {
+        return launch_bwd<decltype(D)::value, decltype(F32)::value, decltype(INTER)::value, decltype(AXES)::value>(
+            a, dweight, s);
+    });
 }
 
 }  // namespace fa

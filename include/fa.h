@@ -341,6 +341,33 @@ int fa_qk_norm_rope_bwd(const void* qkv, const float* q_weight, const float* k_w
 size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int H_kv, int N, int d);
 
 /*
+ * Norm and rotation as fa_qk_norm_rope with positions of several axes, such as the frame, row and
+ * column of a video's tokens: pair p turns by A = t[axis[p]] inv_freq[p].
+ *
+ *   positions : [n_axes][B][N] int32 (may be NULL if rot is 0).
+ *   axis      : HOST array of rot / 2 ints, the axis 0 .. n_axes - 1 of each pair; read before the
+ *               call returns.  May be NULL if rot is 0.
+ *   n_axes    : 1 to 8.
+ *   Other arguments as fa_qk_norm_rope, with whose results these agree to the bit where all axes hold
+ *   the same positions.
+ * Errors: as fa_qk_norm_rope; FA_ERR_INVALID_ARG also for a bad axis or n_axes.
+ */
+int fa_qk_norm_rope_axes(const void* qkv, const float* q_weight, const float* k_weight,
+                         const int* positions, const double* inv_freq, const int* axis, void* q,
+                         void* k, void* v, int B, int H, int H_kv, int N, int d, int rot, int n_axes,
+                         int interleaved, float eps, int dtype, void* stream);
+
+/*
+ * Gradient of fa_qk_norm_rope_axes, as fa_qk_norm_rope_bwd, whose workspace size holds here too.
+ */
+int fa_qk_norm_rope_axes_bwd(const void* qkv, const float* q_weight, const float* k_weight,
+                             const int* positions, const double* inv_freq, const int* axis,
+                             const void* dq, const void* dk, const void* dv, void* dqkv,
+                             float* dq_weight, float* dk_weight, void* workspace,
+                             size_t workspace_bytes, int B, int H, int H_kv, int N, int d, int rot,
+                             int n_axes, int interleaved, float eps, int dtype, void* stream);
+
+/*
  * Forward under a causal sliding window with sinks: query i sees key j iff j <= i and
  * (j > i - window or j < n_sink), the `window` newest keys (its own among them) and the
  * first n_sink ones.  O, lse and the grouping of heads as fa_fwd_gqa; only key blocks that
@@ -374,6 +401,52 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
                   int window, int n_sink, int dtype, void* stream);
 /* 0 for sizes that the call refuses. */
 size_t fa_bwd_window_workspace_size(int B, int H, int H_kv, int N, int d, int window, int n_sink);
+
+/*
+ * Cross attention: N_q queries a batch to the N_kv keys of another sequence, such as an encoder's
+ * states or a prompt that several samples continue.  Query batch b reads K/V batch
+ * b / (B / B_kv) (B_kv = B: each its own) and query head h K/V head h / (H / H_kv); of a K/V
+ * batch's keys the first kv_lengths[b] are seen by every query.  O and lse as fa_fwd; a sequence
+ * of length 0 gives O = 0, lse = -inf.
+ *
+ *   q, o       : [B][H][N_q][d] bfloat16;  k, v : [B_kv][H_kv][N_kv][d] bfloat16;
+ *                lse : [B][H][N_q] float32, or NULL.
+ *   kv_lengths : [B_kv] int32, device, or NULL (all of N_kv).  Negative ones are taken as 0, those
+ *                beyond N_kv as N_kv.  K and V from there on may hold anything, NaN too.
+ *   workspace  : at least fa_fwd_cross_workspace_size() bytes (NULL if that is 0); its contents
+ *                on entry do not matter.  Calls that overlap in time must not share one.
+ *   dtype      : FA_BF16.   d : 64 or 128.
+ * The work is divided by the lengths that the kernel reads, so that a captured call follows them;
+ * the result depends on the inputs and the device alone.
+ * Errors: FA_ERR_INVALID_ARG (null or misaligned pointers, sizes < 1, B % B_kv or H % H_kv not 0,
+ * a scale that is not finite, bad dtype, a workspace that is too small), FA_ERR_UNSUPPORTED (other
+ * dtype or d, sizes beyond the limits above for queries or keys, H / H_kv * N_q beyond 2^31 - 257),
+ * FA_ERR_CUDA.
+ */
+int fa_fwd_cross(const void* q, const void* k, const void* v, const int* kv_lengths, void* o,
+                 float* lse, void* workspace, size_t workspace_bytes, int B, int B_kv, int H,
+                 int H_kv, int N_q, int N_kv, int d, float scale, int dtype, void* stream);
+/* 0 for sizes that the call refuses, and where none is needed. */
+size_t fa_fwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d);
+
+/*
+ * Attention to a shared prefix and to each request's own tokens: fa_fwd_cross merged with
+ * (o_own, lse_own), the same queries' attention to keys outside of k (from fa_decode_kv4, fa_fwd_window,
+ * fa_fwd_gqa, ...):  lse = ln(e^lse_prefix + e^lse_own),
+ * O = e^(lse_prefix - lse) O_prefix + e^(lse_own - lse) o_own.  The prefix is read once for all
+ * batches that share it, whose rows fill tiles together.
+ *
+ *   o_own, lse_own : as o and lse, read; a row with lse_own = -inf has no keys of its own, and its o_own is
+ *                    not used.  o may be o_own and lse may be lse_own (in place); they must not
+ *                    overlap otherwise.
+ *   lse            : may be NULL.   Other arguments and errors as fa_fwd_cross.
+ */
+int fa_fwd_prefix(const void* q, const void* k, const void* v, const int* kv_lengths,
+                  const void* o_own, const float* lse_own, void* o, float* lse, void* workspace,
+                  size_t workspace_bytes, int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d,
+                  float scale, int dtype, void* stream);
+/* 0 for sizes that the call refuses, and where none is needed. */
+size_t fa_fwd_prefix_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d);
 
 /*
  * A paged K/V cache in 4 bits.  32 neighbouring values of a head share one scale
