@@ -26,7 +26,7 @@ _LAYER = (
     "fa_bwd_window", "fa_bwd_window_workspace_size", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
     "fa_decode_kv4_workspace_size", "rope_frequencies", "kv4_cache", "fa_qk_norm_rope_axes",
     "fa_qk_norm_rope_axes_bwd", "rope_axes", "fa_fwd_cross", "fa_fwd_cross_workspace_size", "fa_fwd_prefix",
-    "fa_fwd_prefix_workspace_size",
+    "fa_fwd_prefix_workspace_size", "fa_bwd_cross", "fa_bwd_cross_workspace_size",
 )
 __all__ += _LAYER
 
@@ -108,6 +108,10 @@ def lib():
         L.fa_fwd_cross.restype = i
         L.fa_fwd_cross_workspace_size.argtypes = [i] * 7
         L.fa_fwd_cross_workspace_size.restype = sz
+        L.fa_bwd_cross.argtypes = [vp] * 11 + [sz] + [i] * 7 + [f, i, vp]
+        L.fa_bwd_cross.restype = i
+        L.fa_bwd_cross_workspace_size.argtypes = [i] * 7
+        L.fa_bwd_cross_workspace_size.restype = sz
         L.fa_fwd_prefix.argtypes = [vp] * 9 + [sz] + [i] * 7 + [f, i, vp]
         L.fa_fwd_prefix.restype = i
         L.fa_fwd_prefix_workspace_size.argtypes = [i] * 7

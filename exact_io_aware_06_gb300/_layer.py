@@ -222,6 +222,20 @@ def fa_fwd_cross(q, k, v, kv_lengths, o, lse, workspace, scale, dtype=FA_BF16, s
     _check(lib().fa_fwd_cross(*pointers, *space, *sizes, scale, dtype, _handle(stream, device)), "fa_fwd_cross")
 
 
+def fa_bwd_cross_workspace_size(B, B_kv, H, H_kv, N_q, N_kv, d):
+    return int(lib().fa_bwd_cross_workspace_size(*map(_int, (B, B_kv, H, H_kv, N_q, N_kv, d))))
+
+
+def fa_bwd_cross(q, k, v, kv_lengths, o, lse, do, dq, dk, dv, workspace, scale, dtype=FA_BF16, stream=None):
+    """dq, dk, dv <- backward of fa_fwd_cross, from its o and lse."""
+    device = _current_device()
+    (*qkv, out, row_lse), space, sizes = _cross(q, k, v, kv_lengths, o, lse, workspace, device)
+    _check(lib().fa_bwd_cross(*qkv, out, row_lse, _dense("do", do, _BF16, q.shape, device),
+                              _dense("dq", dq, _BF16, q.shape, device), _dense("dk", dk, _BF16, k.shape, device),
+                              _dense("dv", dv, _BF16, k.shape, device), *space, *sizes, scale, dtype,
+                              _handle(stream, device)), "fa_bwd_cross")
+
+
 def fa_fwd_prefix_workspace_size(B, B_kv, H, H_kv, N_q, N_kv, d):
     return int(lib().fa_fwd_prefix_workspace_size(*map(_int, (B, B_kv, H, H_kv, N_q, N_kv, d))))
 

@@ -1,0 +1,69 @@
+// cross_bwd_dq_sm103.cu -- dQ of the backward of attention to another sequence's keys.
+#include "bwd_dq.cuh"
+#include "cross_bwd.cuh"
+
+namespace fa {
+
+// A head's query blocks one after the other, so that neighbouring CTAs read the same K and V.  A sequence
+// without keys has one block, all of it hidden: its queries' gradients are zeros from it.
+struct CrossQItem {
+    int bh, bh_kv, qb, n_kv, len;
+    static constexpr bool shorty = false;
+    __device__ __forceinline__ int block(int j) const { return j; }
+};
+static __device__ __forceinline__ CrossQItem q_item_at(const CrossBwdArgs& a, int x) {
+    CrossQItem I;
+    I.bh = x / a.n_q;
+    I.qb = x - I.bh * a.n_q;
+    const int b = I.bh / a.H_kv, kv_batch = b / a.share;
+    I.bh_kv = kv_batch * a.H_kv + I.bh - b * a.H_kv;
+    I.len = key_count(a, kv_batch);
+    I.n_kv = max(1, (I.len + kBlk - 1) / kBlk);
+    return I;
+}
+static __device__ __forceinline__ void key_range(const CrossBwdArgs&, const CrossQItem& I, int, int key0, int& first,
+                                                 int& last, int& sink) {
+    first = -1;
+    last = I.len - 1 - key0;
+    sink = 0;
+}
+static __device__ __forceinline__ bool hidden_rows(const CrossBwdArgs& a, const CrossQItem& I, int block, int& r0, int& r1) {
+    r0 = max(0, I.len - block * kBlk);
+    r1 = min(kBlk, a.N_kv - block * kBlk);
+    return r0 < r1;
+}
+template <int D>
+static __device__ __forceinline__ void idle_warp(const CrossBwdArgs&, std::integral_constant<int, D>, int, int) {}
+
+namespace {
+
+template <int D>
+int launch_impl(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a,
+                cudaStream_t s) {
+    const int heads = a.BH_kv * a.share, n_items = heads * a.n_q;
+    CUtensorMap tq, tk, tv, tdo;
+    const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    int rc = make_map_3d(&tq, q, dt, 2, D, a.N, heads, 64, kBlk);
+    if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, a.N_kv, a.BH_kv, 64, kBlk);
+    if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, a.N_kv, a.BH_kv, 64, kBlk);
+    if (rc == 0) rc = make_map_3d(&tdo, dO, dt, 2, D, a.N, heads, 64, kBlk);
+    if (rc != 0) return rc;
+    static std::atomic<uint64_t> smem_done;
+    cudaError_t e = allow_smem(bwd_dq_kernel<D, CrossBwdArgs>, Cfg<D>::kSmemAlloc, smem_done);
+    int dev = 0, sms = 152;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    bwd_dq_kernel<D, CrossBwdArgs>
+        <<<n_items < sms ? n_items : sms, kThreads, Cfg<D>::kSmemAlloc, s>>>(tq, tk, tv, tdo, a, dq, n_items);
+    return static_cast<int>(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_bwd_cross_dq(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a, int d,
+                        cudaStream_t s) {
+    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, s) : launch_impl<128>(q, k, v, dO, dq, a, s);
+}
+
+}  // namespace fa

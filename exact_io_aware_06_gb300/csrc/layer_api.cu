@@ -342,6 +342,27 @@ FA_API size_t fa_fwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int 
                : 0;
 }
 
+FA_API int fa_bwd_cross(const void* q, const void* k, const void* v, const int* kv_lengths, const void* o,
+                        const float* lse, const void* dO, void* dq, void* dk, void* dv, void* workspace,
+                        size_t workspace_bytes, int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d, float scale,
+                        int dtype, void* stream) {
+    if (!pointers_ok(q, k, v, o, lse, dO, dq, dk, dv, workspace) || !optional_ok(kv_lengths)) return FA_ERR_INVALID_ARG;
+    int rc = cross_args(B, B_kv, H, H_kv, N_q, N_kv, d, scale, dtype);
+    if (rc != FA_OK) return rc;
+    if (workspace_bytes < bwd_cross_workspace_bytes(B, B_kv, H, H_kv, N_q, N_kv, d)) return FA_ERR_INVALID_ARG;
+    DevCtl ctl;
+    if (!device_ctl(&ctl, &rc)) return rc;
+    const int e = launch_bwd_cross(q, k, v, kv_lengths, o, lse, dO, dq, dk, dv, workspace, B, B_kv, H, H_kv, N_q, N_kv, d,
+                                   scale, ctl, static_cast<cudaStream_t>(stream));
+    return e == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+FA_API size_t fa_bwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
+    return cross_sizes(B, B_kv, H, H_kv, N_q, N_kv, d) == FA_OK
+               ? bwd_cross_workspace_bytes(B, B_kv, H, H_kv, N_q, N_kv, d)
+               : 0;
+}
+
 FA_API int fa_fwd_prefix(const void* q, const void* k, const void* v, const int* kv_lengths, const void* o_own,
                          const float* lse_own, void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
                          int B_kv, int H, int H_kv, int N_q, int N_kv, int d, float scale, int dtype, void* stream) {

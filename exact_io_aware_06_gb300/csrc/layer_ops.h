@@ -128,6 +128,10 @@ size_t fwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int 
 int launch_fwd_cross(const void* q, const void* k, const void* v, const int* lengths, const void* o_own,
                      const float* lse_own, void* o, float* lse, void* workspace, int B, int B_kv, int H, int H_kv, int N_q,
                      int N_kv, int d, float c_log2, DevCtl ctl, cudaStream_t s);
+size_t bwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d);
+int launch_bwd_cross(const void* q, const void* k, const void* v, const int* lengths, const void* o, const float* lse,
+                     const void* dO, void* dq, void* dk, void* dv, void* workspace, int B, int B_kv, int H, int H_kv,
+                     int N_q, int N_kv, int d, float scale, DevCtl ctl, cudaStream_t s);
 
 constexpr int kDevIndex = 5;  // == FA_ERR_DEVICE_INDEX: a page or length outside the cache
 

@@ -430,6 +430,26 @@ int fa_fwd_cross(const void* q, const void* k, const void* v, const int* kv_leng
 size_t fa_fwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d);
 
 /*
+ * Backward of fa_fwd_cross, by recomputation from its lse.  dK and dV are summed over the query heads
+ * and the batches that share a K/V head, in float32 and rounded once; those of keys that no query
+ * sees (from kv_lengths[b] on) are zeros, and so is dQ of queries without keys.
+ *
+ *   o, lse     : from fa_fwd_cross with the same kv_lengths.
+ *   dO, dq     : [B][H][N_q][d] bfloat16;  dk, dv : [B_kv][H_kv][N_kv][d] bfloat16, written.
+ *   workspace  : at least fa_bwd_cross_workspace_size() bytes; its contents on entry do not matter.
+ *                Calls that overlap in time must not share one.
+ * Nothing is summed by atomics: the same bits every time.  A NaN or an infinity in q, o or dO reaches the
+ * gradients of the keys of its head that are seen, and may reach those of hidden keys.
+ * Errors: as fa_fwd_cross; FA_ERR_INVALID_ARG also for a null lse.
+ */
+int fa_bwd_cross(const void* q, const void* k, const void* v, const int* kv_lengths, const void* o,
+                 const float* lse, const void* dO, void* dq, void* dk, void* dv, void* workspace,
+                 size_t workspace_bytes, int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d,
+                 float scale, int dtype, void* stream);
+/* 0 for sizes that the call refuses. */
+size_t fa_bwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d);
+
+/*
  * Attention to a shared prefix and to each request's own tokens: fa_fwd_cross merged with
  * (o_own, lse_own), the same queries' attention to keys outside of k (from fa_decode_kv4, fa_fwd_window,
  * fa_fwd_gqa, ...):  lse = ln(e^lse_prefix + e^lse_own),

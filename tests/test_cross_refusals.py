@@ -86,6 +86,17 @@ def test_prefix_refusals(L, change, status):
                            max(0, n - a["short"]), *(a[x] for x in CROSS_SIZES), a["scale"], a["dtype"], None) == status
 
 
+@pytest.mark.parametrize("change,status", CROSS_BAD + [
+    (dict(lse=None), 1), (dict(do=None), 1), (dict(dq=MIS), 1), (dict(dk=None), 1), (dict(dv=MIS), 1), (dict(ws=None), 1),
+    (dict(short=4), 1)])
+def test_cross_backward_refusals(L, change, status):
+    a = dict(CROSS, lse=P, do=P, dq=P, dk=P, dv=P, ws=P, short=0)
+    a.update(change)
+    n = fa.fa_bwd_cross_workspace_size(*(a[x] for x in CROSS_SIZES))
+    assert L.fa_bwd_cross(a["q"], a["k"], a["v"], a["n"], a["o"], a["lse"], a["do"], a["dq"], a["dk"], a["dv"], a["ws"],
+                          max(0, n - a["short"]), *(a[x] for x in CROSS_SIZES), a["scale"], a["dtype"], None) == status
+
+
 def test_cross_workspaces(L):
     size = fa.fa_fwd_cross_workspace_size
     # one row of one head over 12 blocks of keys: twelve CTAs with two parts of 32 rows
@@ -94,3 +105,10 @@ def test_cross_workspaces(L):
     assert size(8, 8, 16, 16, 2400, 100, 64) == 0
     for bad in ((0, 1, 1, 1, 1, 1, 64), (3, 2, 1, 1, 1, 1, 64), (1, 1, 3, 2, 1, 1, 64), (1, 1, 1, 1, 1, 1, 80), (1, 1, 1, 1, 1 << 40, 1, 64)):
         assert size(*bad) == 0
+        assert fa.fa_bwd_cross_workspace_size(*bad) == 0
+    # delta and lse of the rows of a K/V head in whole blocks: 2 heads of 5 rows, in each of 6 batches and 2 heads
+    assert fa.fa_bwd_cross_workspace_size(6, 6, 4, 2, 5, 700, 64) == 2 * 6 * 2 * 128 * 4
+    # and the parts of the 4 key blocks' pieces
+    rows = 2 * 40960 * 4
+    assert (fa.fa_bwd_cross_workspace_size(1, 1, 1, 1, 40960, 512, 64) - rows) % (4 * 2 * 128 * 64 * 4) == 0
+    assert fa.fa_bwd_cross_workspace_size(1, 1, 1, 1, 40960, 512, 64) > rows

@@ -300,6 +300,185 @@ def test_binding_refuses_wrong_tensors():
         fa.fa_fwd_cross(q[:3].contiguous(), k, v, n, o[:3], lse[:3], ws, 0.125)  # 3 batches to 2
 
 
+# ---------------------------------------------------------------- backward
+def backward(q, k, v, lengths, o, lse, do, scale, ws=None):
+    dq, dk, dv = (torch.full_like(t, float("nan")) for t in (q, k, v))
+    ws = space(fa.fa_bwd_cross_workspace_size(*sizes(q, k))) if ws is None else ws
+    fa.fa_bwd_cross(q, k, v, on_device(lengths), o, lse, do, dq, dk, dv, ws, scale)
+    check_status()
+    return dq, dk, dv
+
+
+def check_backward(q, k, v, lengths, do, grads, scale, kv_batches=None):
+    share, few = q.shape[0] // k.shape[0], 24
+    heads = list(each_head(q, k, lengths))
+    q, k, v, do = (f64(t) for t in (q, k, v, do))
+    dq, dk, dv = (f64(t) for t in grads)
+    rk, rv, tk, tv = (np.zeros(k.shape) for _ in range(4))
+    for b, h, kb, kh, n in heads:
+        if kv_batches is not None and kb not in kv_batches:
+            continue
+        seen = np.ones((q.shape[2], n), dtype=bool)
+        Q, K, V, dO = q[b, h], k[kb, kh, :n], v[kb, kh, :n], do[b, h]
+        o, _, P = plain64.attention(Q, K, V, scale, seen)
+        gq, gk, gv = plain64.attention_grad(Q, K, V, dO, scale, seen)
+        rk[kb, kh, :n] += gk
+        rv[kb, kh, :n] += gv
+        t = 1e-5 * (1 + (np.abs(scale) * np.abs(Q @ K.T).max(initial=0)))
+        A = P @ np.abs(V)
+        dP, size = dO @ V.T, np.abs(dO) @ np.abs(V).T
+        if n <= few:
+            d_delta = (t + 1e-6) * (np.abs(dO) * A).sum(-1, keepdims=True)
+        else:
+            d_delta = (np.abs(dO) * (2.0 ** -8 * (A + np.abs(o)) + t * A)).sum(-1, keepdims=True)
+        delta = (dO * o).sum(-1, keepdims=True)
+        d_dS = P * (d_delta + 1e-6 * size + (2.0 ** -8 + t) * (np.abs(dP - delta) + d_delta))
+        tq = np.abs(scale) * d_dS @ np.abs(K) + 2.0 ** -8 * np.abs(gq) + 1e-30
+        err = np.abs(dq[b, h] - gq)
+        assert np.isfinite(dq[b, h]).all() and (err <= tq).all(), (b, h, float((err / tq).max()))
+        tk[kb, kh, :n] += np.abs(scale) * d_dS.T @ np.abs(Q)
+        tv[kb, kh, :n] += (2.0 ** -8 + t) * P.T @ np.abs(dO)
+    for b in range(k.shape[0]) if kv_batches is None else kv_batches:
+        for got, ref, tol in ((dk[b], rk[b], tk[b]), (dv[b], rv[b], tv[b])):
+            tol = tol + 2.0 ** -8 * np.abs(ref) + 1e-30 * (tol > 0)
+            err = np.abs(got - ref)  # of hidden keys: zeros
+            assert np.isfinite(got).all() and (err <= tol).all(), (b, float((err / np.maximum(tol, 1e-30)).max()))
+
+
+def step(B, B_kv, H, H_kv, N_q, N_kv, d, lengths, seed=0, scale=None, poison=True):
+    q, k, v, do = inputs(B, B_kv, H, H_kv, N_q, N_kv, d, seed)
+    if poison and lengths is not None:
+        for b, n in enumerate(lengths):
+            k[b, :, max(n, 0):], v[b, :, max(n, 0):] = float("nan"), float("inf")
+    scale = scale_for(d) if scale is None else scale
+    o, lse = forward(q, k, v, lengths, scale)
+    return q, k, v, do, o, lse, backward(q, k, v, lengths, o, lse, do, scale), scale
+
+
+@pytest.mark.parametrize("N_q", [1, 2, 127, 128, 129, 300])
+@pytest.mark.parametrize("N_kv", [1, 5, 24, 25, 128, 129, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_lengths(N_q, N_kv, d):
+    q, k, v, do, _, _, grads, scale = step(2, 2, 3, 1, N_q, N_kv, d, None, seed=N_q)
+    check_backward(q, k, v, None, do, grads, scale)
+
+
+@pytest.mark.parametrize("lengths", [[0, 0, 0], [1, 128, 127], [300, 0, 129], [-7, 256, 10 ** 9], [24, 25, 2]])
+@pytest.mark.parametrize("N_q,H,H_kv", [(1, 2, 2), (5, 8, 2), (130, 4, 2), (300, 2, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_ragged_keys(lengths, N_q, H, H_kv, d):
+    q, k, v, do, _, _, grads, scale = step(3, 3, H, H_kv, N_q, 300, d, lengths, seed=1)
+    check_backward(q, k, v, lengths, do, grads, scale)
+
+
+@pytest.mark.parametrize("B,B_kv,H,H_kv,N_q", [(4, 1, 2, 2, 1), (6, 2, 8, 2, 1), (6, 3, 2, 1, 33), (4, 2, 2, 1, 200)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_batches_that_share_keys(B, B_kv, H, H_kv, N_q, d):
+    lengths = [333, 200, 0][:B_kv]
+    q, k, v, do, _, _, grads, scale = step(B, B_kv, H, H_kv, N_q, 333, d, lengths, seed=B)
+    check_backward(q, k, v, lengths, do, grads, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_of_pieces_and_of_many_items(d):
+    # many queries on few keys: key blocks are dealt in pieces; many heads: more items than SMs
+    q, k, v, do, _, _, grads, scale = step(2, 2, 2, 1, 3000, 200, d, [200, 60], seed=3)
+    check_backward(q, k, v, [200, 60], do, grads, scale)
+    lengths = [700, 10, 300, 0, 650, 129]
+    q, k, v, do, _, _, grads, scale = step(6, 6, 16, 8, 200, 700, d, lengths, seed=4)
+    check_backward(q, k, v, lengths, do, grads, scale, kv_batches=[1, 3, 5])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+def test_backward_scales(scale):
+    q, k, v, do, _, _, grads, scale = step(1, 1, 2, 2, 200, 300, 64, [270], seed=3, scale=scale)
+    check_backward(q, k, v, [270], do, grads, scale)
+
+
+def test_backward_against_differences():
+    # the loss sum(o * do) moves by the gradient's share along a random direction: bf16 inputs a step of 2^-4
+    # apart, whose o is known to 2^-8 A from float64
+    B, H, H_kv, N_q, N_kv, d = 2, 2, 1, 6, 40, 64
+    q, k, v, do, _, _, grads, scale = step(B, 1, H, H_kv, N_q, N_kv, d, [33], seed=9, poison=False)
+
+    def loss(q, k, v):
+        total = 0.0
+        for b, h, kb, kh, n in each_head(do, k, [33]):
+            o = plain64.attention(q[b, h], k[kb, kh, :n], v[kb, kh, :n], scale, np.ones((N_q, n), dtype=bool))[0]
+            total += (o * f64(do[b, h])).sum()
+        return total
+
+    base = [f64(t) for t in (q, k, v)]
+    for i in range(3):
+        direction = np.random.default_rng(i).standard_normal(base[i].shape)
+        eps = 1e-4
+        sides = []
+        for sign in (1, -1):
+            moved = list(base)
+            moved[i] = base[i] + sign * eps * direction
+            sides.append(loss(*moved))
+        slope = (sides[0] - sides[1]) / (2 * eps)
+        got, size = (f64(grads[i]) * direction).sum(), (np.abs(f64(grads[i])) * np.abs(direction)).sum()
+        # each entry is off by under 3 roundings of 2^-8 (its own, dS or P, delta) of the gradient's terms, whose
+        # magnitudes add up to a few times the gradient's own
+        assert abs(got - slope) <= 3 * 2.0 ** -8 * 4 * size
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_repeats_bit_for_bit(d):
+    q, k, v, do, o, lse, grads, scale = step(3, 1, 4, 2, 500, 260, d, [260], seed=5)
+    for a, b in zip(grads, backward(q, k, v, [260], o, lse, do, scale)):
+        assert torch.equal(a, b)
+
+
+def test_captured_step_follows_the_lengths():
+    q, k, v, do = inputs(4, 2, 4, 2, 150, 300, 64, seed=15)
+    lengths = on_device([5, 5])
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    ws = space(max(fa.fa_fwd_cross_workspace_size(*sizes(q, k)), fa.fa_bwd_cross_workspace_size(*sizes(q, k))))
+
+    def call():
+        fa.fa_fwd_cross(q, k, v, lengths, o, lse, ws, 0.125)
+        fa.fa_bwd_cross(q, k, v, lengths, o, lse, do, dq, dk, dv, ws, 0.125)
+
+    graph = captured(call)
+    for new in ([300, 17], [0, 129], [128, 300]):
+        lengths.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        check_status()
+        check_forward(q, k, v, new, o, lse, 0.125)
+        check_backward(q, k, v, new, do, (dq, dk, dv), 0.125)
+
+
+def test_backward_large_offsets():
+    # K/V gradients and queries beyond 2^31 bytes from the base
+    for B, N_q, N_kv in ((70, 100, 16384), (70, 16384, 100)):
+        q = torch.zeros((B, 8, N_q, 128), dtype=torch.bfloat16, device="cuda")
+        k = torch.zeros((B, 8, N_kv, 128), dtype=torch.bfloat16, device="cuda")
+        v, do = torch.zeros_like(k), torch.zeros_like(q)
+        one = inputs(1, 1, 1, 1, N_q, N_kv, 128, seed=11)
+        q[-1, -1], k[-1, -1], v[-1, -1], do[-1, -1] = (t[0, 0] for t in one)
+        o, lse = forward(q, k, v, None, scale_for(128))
+        grads = backward(q, k, v, None, o, lse, do, scale_for(128))
+        check_backward(*one[:3], None, one[3], [g[-1:, -1:] for g in grads], scale_for(128))
+        assert all((g[0] == 0).all() for g in grads)
+
+
+def test_backward_short_wait_limit_reports_and_recovers():
+    q, k, v, do, o, lse, _, scale = step(2, 2, 8, 8, 1024, 700, 128, None, seed=13)
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    ws = space(fa.fa_bwd_cross_workspace_size(*sizes(q, k)))
+    fa.fa_set_wait_timeout_ns(1)
+    try:
+        fa.fa_bwd_cross(q, k, v, None, o, lse, do, dq, dk, dv, ws, scale)
+        first = fa.fa_last_device_error()
+    finally:
+        fa.fa_set_wait_timeout_ns(0)
+    assert first in (0, fa.FA_ERR_DEVICE_TIMEOUT)
+    check_backward(q, k, v, None, do, backward(q, k, v, None, o, lse, do, scale), scale, kv_batches=[0])
+
+
 # ---------------------------------------------------------------- shared prefixes
 def own_attention(q, seed):
     """What the queries' own tokens gave: rows of every kind, some without any."""
