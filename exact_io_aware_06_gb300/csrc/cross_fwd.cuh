@@ -21,7 +21,8 @@ struct CrossArgs {
     float* lse;            // [B][H_kv][R] or null
     const void* o_own;     // as o, merged into it; null: none
     const float* lse_own;
-    float* part;           // two parts a CTA: [2][d / 4][part_rows][4] O, then [2][part_rows] m, l
+    int4* cut;             // an item that was cut, by the CTA that begins it: last CTA, b, item, 0; or last CTA -1
+    float* part;           // two parts a CTA: [d / 4][part_rows][4] O, then m and l of part_rows each
     int R, share, H_kv, B_kv, N_kv;
     int nb, tiles_b, tiles, n_pairs, part_rows;
     int stream;            // 0: whole items; 1: equal runs of key blocks, items cut where they end
@@ -40,27 +41,43 @@ __device__ __forceinline__ int cross_length(const CrossArgs& a, int b) {
 // A sequence without keys has one block, all of it hidden: its rows get O = 0, lse = -inf from it.
 __device__ __forceinline__ int cross_blocks(int len) { return len > 0 ? (len + kBN - 1) / kBN : 1; }
 
-// The key blocks of all items, item by item, batch by batch: their number, and where unit u lies.  By a
-// whole warp, 32 batches at a time.
+// n / d; 64-bit division takes some hundred cycles, a 32-bit one a quarter.
+__device__ __forceinline__ long long quotient(long long n, long long d) {
+    if ((n | d) >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+
+// The key blocks of all items ("units"), item by item, batch by batch, in equal runs for the CTAs.  By a whole
+// warp, 32 batches at a time.
 struct UnitPlace {
     int b, item, kb;  // K/V batch, item of the batch, key block
 };
-__device__ __forceinline__ long long total_units(const CrossArgs& a) {
-    const long long items = static_cast<long long>(a.H_kv) * a.n_pairs;
-    if (!a.lengths) return items * a.B_kv * cross_blocks(a.N_kv);
-    long long n = 0;
-    for (int b = threadIdx.x % 32; b < a.B_kv; b += 32) n += cross_blocks(cross_length(a, b));
+struct Units {
+    long long total, each;  // every CTA has `each`, the first `more` one more; those behind the last none
+    int more;
+    __device__ __forceinline__ explicit Units(const CrossArgs& a) {
+        const long long items = static_cast<long long>(a.H_kv) * a.n_pairs;
+        if (!a.lengths) {
+            total = items * a.B_kv * cross_blocks(a.N_kv);
+        } else {
+            long long n = 0;
+            for (int b = threadIdx.x % 32; b < a.B_kv; b += 32) n += cross_blocks(cross_length(a, b));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-    return n * items;
-}
+            for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+            total = n * items;
+        }
+        each = quotient(total, a.ctas);
+        more = static_cast<int>(total - each * a.ctas);
+    }
+    __device__ __forceinline__ long long first(int cta) const { return each * cta + min(cta, more); }
+};
 __device__ __forceinline__ UnitPlace unit_place(const CrossArgs& a, long long u) {
     const long long items = static_cast<long long>(a.H_kv) * a.n_pairs;
     UnitPlace p;
     int n;
     if (!a.lengths) {
         n = cross_blocks(a.N_kv);
-        p.b = static_cast<int>(u / (items * n));
+        p.b = static_cast<int>(quotient(u, items * n));
         u -= p.b * items * n;
     } else {
         const int lane = threadIdx.x % 32;
@@ -83,77 +100,10 @@ __device__ __forceinline__ UnitPlace unit_place(const CrossArgs& a, long long u)
             u -= __shfl_sync(0xffffffffu, upto, 31) * items;
         }
     }
-    p.item = static_cast<int>(u / n);
+    p.item = static_cast<int>(quotient(u, n));
     p.kb = static_cast<int>(u - static_cast<long long>(p.item) * n);
     return p;
 }
-// CTA `cta`'s first unit.  No CTA is without one but those behind the last.
-__device__ __forceinline__ long long first_unit(const CrossArgs& a, long long total, int cta) {
-    const long long n = total < a.ctas ? total : a.ctas;
-    return cta >= n ? total : total / n * cta + total % n * cta / n;
-}
-
-// A run of key blocks of an item.
-struct Segment {
-    int b, h, pair;     // K/V batch and head, the tiles 2 pair and 2 pair + 1
-    int len;            // the sequence's keys
-    int k0, n, blocks;  // key blocks k0 .. k0 + n - 1 of `blocks`
-    bool solo;          // one tile
-    __device__ __forceinline__ bool whole() const { return n == blocks; }
-    __device__ __forceinline__ int slot() const { return k0 > 0 ? 0 : 1; }  // of the CTA's two parts
-};
-
-// This CTA's segments, one after the other: every role goes through them on its own.
-struct Walk {
-    int b, item, kb, blocks, len;
-    long long left;
-    __device__ __forceinline__ explicit Walk(const CrossArgs& a) {
-        if (a.stream) {
-            const long long total = total_units(a), u = first_unit(a, total, blockIdx.x);
-            left = first_unit(a, total, blockIdx.x + 1) - u;
-            if (left > 0) {
-                const UnitPlace p = unit_place(a, u);
-                b = p.b, item = p.item, kb = p.kb;
-                len = cross_length(a, b);
-                blocks = cross_blocks(len);
-            }
-        } else {
-            left = 0;  // rounds
-        }
-    }
-    __device__ __forceinline__ bool next(const CrossArgs& a, Segment& s) {
-        const int per = a.H_kv * a.n_pairs;
-        if (a.stream) {
-            if (left <= 0) return false;
-            s.b = b, s.k0 = kb, s.blocks = blocks, s.len = len;
-            s.n = static_cast<int>(left < blocks - kb ? left : blocks - kb);
-            place(a, s, item);
-            left -= s.n;
-            kb = 0;
-            if (++item == per && left > 0) {
-                item = 0;
-                len = cross_length(a, ++b);
-                blocks = cross_blocks(len);
-            }
-            return true;
-        }
-        // whole items in alternating order
-        const long long G = gridDim.x, x = left * G + ((left & 1) ? G - 1 - blockIdx.x : blockIdx.x);
-        if (x >= static_cast<long long>(a.B_kv) * per) return false;
-        ++left;
-        s.b = static_cast<int>(x / per);
-        s.len = cross_length(a, s.b);
-        s.k0 = 0;
-        s.n = s.blocks = cross_blocks(s.len);
-        place(a, s, static_cast<int>(x - static_cast<long long>(s.b) * per));
-        return true;
-    }
-    __device__ __forceinline__ static void place(const CrossArgs& a, Segment& s, int item) {
-        s.h = item / a.n_pairs;
-        s.pair = item - s.h * a.n_pairs;
-        s.solo = 2 * s.pair + 1 >= a.tiles;
-    }
-};
 
 // Where a tile's rows come from: its first batch and, for nb = 1, its first row there; rows in use.
 struct TileRows {
@@ -179,29 +129,82 @@ __device__ __forceinline__ size_t global_row(const CrossArgs& a, const TileRows&
     return (static_cast<size_t>(t.b + over) * a.H_kv + h) * a.R + (t.r0 + row - over * a.R);
 }
 
-// A row's state (reference maximum m in log2 units, sum l) with its own attention's: the factors of the
-// unnormalised O and of the own O, and the lse of both.
-struct RowEnd {
-    float f, f_own, lse;
+// A run of key blocks of an item: what the kernel's roles read of it.  The blocks of tiles of all segments,
+// both tiles' in turn or a lone tile's one after the other, go to the two softmax warpgroups alternately.
+struct __align__(16) Segment {
+    int n;       // its blocks; 0: none follows
+    int k0;      // the first
+    int len;     // the sequence's keys
+    int flags;
+    int bh_kv, h;
+    TileRows rows[2];
+    __device__ __forceinline__ bool solo() const { return flags & 1; }        // one tile
+    // the warpgroup that takes the first tile, or a lone tile's first block
+    __device__ __forceinline__ int first() const { return flags >> 1 & 1; }
+    __device__ __forceinline__ bool whole() const { return flags & 4; }       // all blocks of the item
+    __device__ __forceinline__ int slot() const { return k0 > 0 ? 0 : 1; }    // of the CTA's two parts
 };
-__device__ __forceinline__ RowEnd row_end(const CrossArgs& a, float m, float l, size_t row, bool there) {
-    constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
-    RowEnd e;
-    const bool any = !(l == 0.f);  // a NaN stays one
-    const float own = a.lse_own && there ? a.lse_own[row] * kLog2e : -INFINITY;
-    const float mine = any ? m + log2f(l) : -INFINITY;
-    if (own == -INFINITY) {
-        e.f = any ? 1.f / l : 0.f;
-        e.f_own = 0.f;
-        e.lse = mine * kLn2;
-        return e;
+
+// This CTA's segments, one after the other.
+struct Walk {
+    int b, item, kb, blocks, len;
+    int turn = 0;  // blocks of tiles so far, modulo 2
+    long long left;
+    __device__ __forceinline__ Walk(const CrossArgs& a, const Units& units) {
+        const long long u = units.first(blockIdx.x);
+        left = a.stream ? units.first(blockIdx.x + 1) - u : 0;  // blocks, or rounds
+        if (left > 0) {
+            const UnitPlace p = unit_place(a, u);
+            b = p.b, item = p.item, kb = p.kb;
+            len = cross_length(a, b);
+            blocks = cross_blocks(len);
+        }
     }
-    const float top = fmaxf(mine, own);
-    const float w = any ? exp2f(mine - top) : 0.f, w_own = exp2f(own - top), sum = w + w_own;
-    e.f = any ? w / (sum * l) : 0.f;
-    e.f_own = w_own / sum;
-    e.lse = (top + log2f(sum)) * kLn2;
-    return e;
+    // Whether there is one more; `at` its item of the batch, `behind` the item's blocks after it.
+    __device__ __forceinline__ bool next(const CrossArgs& a, Segment& s, int& batch, int& at, int& behind) {
+        const int per = a.H_kv * a.n_pairs;
+        s.n = 0;
+        if (a.stream) {
+            if (left <= 0) return false;
+            batch = b, at = item, s.k0 = kb, s.len = len;
+            s.n = static_cast<int>(left < blocks - kb ? left : blocks - kb);
+            behind = blocks - kb - s.n;
+            left -= s.n;
+            kb = 0;
+            if (++item == per && left > 0) {
+                item = 0;
+                len = cross_length(a, ++b);
+                blocks = cross_blocks(len);
+            }
+        } else {
+            // whole items in alternating order
+            const long long G = gridDim.x;
+            const long long x = left * G + ((left & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+            if (x >= static_cast<long long>(a.B_kv) * per) return false;
+            ++left;
+            batch = static_cast<int>(quotient(x, per));
+            at = static_cast<int>(x - static_cast<long long>(batch) * per);
+            s.len = cross_length(a, batch);
+            s.k0 = 0;
+            s.n = cross_blocks(s.len);
+            behind = 0;
+        }
+        s.h = at / a.n_pairs;
+        const int pair = at - s.h * a.n_pairs;
+        const bool solo = 2 * pair + 1 >= a.tiles;
+        s.bh_kv = batch * a.H_kv + s.h;
+        s.rows[0] = tile_rows(a, batch, 2 * pair);
+        if (!solo) s.rows[1] = tile_rows(a, batch, 2 * pair + 1);
+        s.flags = (solo ? 1 : 0) | turn << 1 | (s.k0 == 0 && behind == 0 ? 4 : 0);
+        if (solo) turn ^= s.n & 1;
+        return true;
+    }
+};
+
+// A row's end from its state (reference maximum m in log2 units, sum l): the factor of O, and lse.
+__device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 // Floats of one part: O of its rows, then m and l.

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "cross_fwd.cuh"
+#include "rows_out.cuh"
 #include "tma_host.h"
 
 namespace fa {
@@ -15,6 +16,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 152;
+constexpr size_t kCutBytes = kMaxCtas * sizeof(int4);
 
 template <int D>
 struct Cfg {
@@ -22,21 +24,23 @@ struct Cfg {
     static constexpr int kChunks = D / 64;           // 128-byte swizzle columns per row
     static constexpr int kChunkBytes = 128 * 128;
     static constexpr int kTileBytes = kChunks * kChunkBytes;
-    static constexpr int kOffQ = 0;
+    static constexpr int kOffQ = 0;                  // two tiles
     static constexpr int kOffK = 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kOffO = kOffV + kStages * kTileBytes;  // 4 KB per softmax warp
-    static constexpr int kSmemAlloc = kOffO + 8 * 4096 + 1024;
-    static constexpr uint32_t kColS = 0, kColO = 256;  // + 128, + D for the second tile
+    static constexpr int kSmemAlloc = kOffV + kStages * kTileBytes + 1024;
+    static constexpr uint32_t kColS = 0, kColO = 256;  // + 128, + D for the second warpgroup
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdescS = idesc_bf16(kBM, kBN, false, false);
     static constexpr uint32_t kIdescO = idesc_bf16(kBM, D, false, true);
 };
-static_assert(Cfg<128>::kSmemAlloc + 1536 <= 232448, "smem");
+static_assert(Cfg<128>::kSmemAlloc + 3072 <= 232448, "smem");
 
+constexpr int kSegments = 8;   // ring of segments
+constexpr int kReaders = 10;   // the loading thread, the MMA thread, 8 softmax warps
 template <int STAGES>
 struct Bars {
-    uint64_t q_full, q_free;
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
+    uint64_t q_full[2], q_free[2];  // of a tile's Q: landed; read by its last S
     uint64_t kv_full[STAGES], kv_empty[STAGES];
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t merge_ml, merge_done;  // one tile: warpgroup 1's state is in shared memory; its O was read
@@ -51,7 +55,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// 32 columns of this thread's row of the accumulator(s) at `first` (and `second`), weighted.
+// 32 columns of this thread's row of the accumulator at `first`, weighted, and with w1 != 0 for any row (two) of
+// that at `second`.
 __device__ __forceinline__ void weighted32(uint32_t first, float w0, uint32_t second, float w1, bool two, float (&x)[32]) {
     uint32_t r[32];
     tmem_ld32(first, r);
@@ -63,36 +68,69 @@ __device__ __forceinline__ void weighted32(uint32_t first, float w0, uint32_t se
         for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(r[e]), w1, x[e]);
     }
 }
-// x times 1 and the row's own O (when f_own is not 0), as bf16.
-__device__ __forceinline__ void store32(const CrossArgs& a, const float (&x)[32], float f_own, size_t at) {
-    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at);
-    const uint4* own = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o_own) + at);
+
+// A warp's 32 rows of O as bf16 from TMEM to global memory in runs of 64 bytes of 8 rows (one row a lane makes
+// every store touch 32 lines, and the SM's next TMEM loads wait behind them).  Lane r has row r's weights of
+// the accumulator(s) and its place (`at`, rows; -1: not stored).
+template <int D>
+__device__ __forceinline__ void store_weighted(uint32_t first, float w0, uint32_t second, float w1, bool two, void* o,
+                                               long long at) {
+    const int lane = threadIdx.x % 32, q = lane % 4;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float y[8];
+    for (int m = 0; m < 2; ++m) {
+        float f0[2], f1[2];
+        long long to[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[8 * g + e];
-        if (f_own != 0.f) {
-            const uint4 v = own[g];
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int h = 0; h < 2; ++h) {  // rows 16 m + 8 h + lane / 4
+            const int from = 16 * m + 8 * h + lane / 4;
+            f0[h] = __shfl_sync(0xffffffffu, w0, from);
+            f1[h] = two ? __shfl_sync(0xffffffffu, w1, from) : 0.f;
+            to[h] = __shfl_sync(0xffffffffu, at, from);
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[2 * e] = fmaf(__uint_as_float(u[e] << 16), f_own, y[2 * e]);
-                y[2 * e + 1] = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), f_own, y[2 * e + 1]);
+        for (int c = 0; c < D / 64; ++c) {
+            const uint32_t part = (static_cast<uint32_t>(16 * m) << 16) + 64 * c;
+            uint32_t x[32], w[2][8];
+            tmem_ld_rows16(first + part, x);
+            if (two) {
+                uint32_t y[32];
+                tmem_ld_rows16(second + part, y);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f1[e / 2 % 2], __uint_as_float(x[e]) * f0[e / 2 % 2]));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float f = two ? 1.f : f0[h];
+                    w[h][j] = pack_bf16x2(__uint_as_float(x[4 * j + 2 * h]) * f, __uint_as_float(x[4 * j + 2 * h + 1]) * f);
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(o) + to[h] * D) + 8 * c + q;
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    transpose4(w[h][j], w[h][j + 1], w[h][j + 2], w[h][j + 3], q);  // columns 64 c + 8 (j + q) ..
+                    if (to[h] >= 0) dst[j] = make_uint4(w[h][j], w[h][j + 1], w[h][j + 2], w[h][j + 3]);
+                }
             }
         }
-        out[g] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
     }
 }
 
+// Persistent.  A warp of its own works out the CTA's segments (some hundred instructions each, which
+// took the other roles 1400 to 2000 cycles) and hands them to the others through a ring in shared memory.
+// Every barrier counts its phases across segments: q_* per tile, kv_* per bundle, s_full and p_full per block
+// of a warpgroup, o_done per segment in which the warpgroup has any.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                     const CrossArgs args) {
+                     const __grid_constant__ CUtensorMap tm_v, const CrossArgs args) {
     using C = Cfg<D>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ Segment segments[kSegments];
     __shared__ __align__(8) Bars<kStages> bars;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
@@ -103,13 +141,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        mbar_init(smem_u32(&bars.q_full), 1);
-        mbar_init(smem_u32(&bars.q_free), 1);
+        for (int s = 0; s < kSegments; ++s) {
+            mbar_init(smem_u32(&bars.seg_full[s]), 1);
+            mbar_init(smem_u32(&bars.seg_empty[s]), kReaders);
+        }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&bars.kv_full[s]), 1);
             mbar_init(smem_u32(&bars.kv_empty[s]), 1);
         }
         for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bars.q_full[t]), 1);
+            mbar_init(smem_u32(&bars.q_free[t]), 1);
             mbar_init(smem_u32(&bars.s_full[t]), 1);
             mbar_init(smem_u32(&bars.p_full[t]), 128);
             mbar_init(smem_u32(&bars.o_done[t]), 1);
@@ -123,7 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
-        tma_prefetch_desc(&tm_o);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
@@ -136,36 +177,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t lim = args.ctl.wait_ns;
     griddep_wait();
     griddep_launch_dependents();
-    Walk walk(args);
-    Segment seg;
+
+    // Waits for the i-th segment; taken(i) after it was read.
+    auto segment_there = [&](int i) -> bool {
+        return mbar_wait(smem_u32(&bars.seg_full[i % kSegments]), (i / kSegments) & 1, lim, &abort_flag);
+    };
+    auto segment_taken = [&](int i) { mbar_arrive(smem_u32(&bars.seg_empty[i % kSegments])); };
 
     // 384 threads x 168 registers at launch: 128 * 120 + 256 * 184 <= 384 * 168
     if (warp < 4) {
         regs_dec<120>();
-        if (warp == 0) {
+        if (warp == 3) {
+            // ============================================================ segments
+            const Units units(args);
+            Walk walk(args, units);
+            int4 cut = make_int4(-1, 0, 0, 0);
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                Segment s;
+                int batch, item, behind;
+                const bool more = walk.next(args, s, batch, item, behind);
+                const int u = i % kSegments;
+                if (i >= kSegments) {
+                    ok = mbar_wait(smem_u32(&bars.seg_empty[u]), ((i / kSegments) & 1) ^ 1, lim, &abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+                if (lane == 0) {
+                    segments[u] = s;
+                    mbar_arrive(smem_u32(&bars.seg_full[u]));
+                }
+                if (!more) break;
+                if (s.k0 == 0 && behind > 0) cut = make_int4(0, batch, item, behind);
+            }
+            if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
+            // An item that this CTA begins and leaves cut: its last CTA, for the join.
+            if (args.stream && args.ctas > 1) {
+                if (cut.x == 0) {
+                    const long long end = units.first(blockIdx.x + 1) + cut.w;  // behind the item's last unit
+                    cut.x = static_cast<int>(blockIdx.x);
+                    for (;; cut.x += 32) {
+                        const int cta = cut.x + 1 + lane;
+                        const unsigned in = __ballot_sync(0xffffffffu, cta < args.ctas && units.first(cta) < end);
+                        if (in != 0xffffffffu) {
+                            cut.x += __popc(in);
+                            break;
+                        }
+                    }
+                }
+                if (lane == 0) args.cut[blockIdx.x] = cut;
+            }
+        } else if (warp == 0) {
             // ============================================================ TMA producer
             if (lane == 0) {
-                const uint32_t qf = smem_u32(&bars.q_full);
                 const int q_rows = args.nb > 1 ? args.nb * args.R : kBM;  // of a box
-                int gb = 0, kq = 0;  // bundles and segments issued
+                int gb = 0, kq[2] = {0, 0};  // bundles and tiles issued
                 bool ok = true;
                 const volatile int never = 0;
-                while (ok && walk.next(args, seg)) {
-                    if (kq > 0 && !mbar_wait(smem_u32(&bars.q_free), (kq - 1) & 1, lim, &abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const int n_q = seg.solo ? 1 : 2, bh_kv = seg.b * args.H_kv + seg.h;
-                    mbar_arrive_expect_tx(qf, n_q * C::kChunks * q_rows * 128);
-                    for (int t = 0; t < n_q; ++t) {
-                        const TileRows T = tile_rows(args, seg.b, 2 * seg.pair + t);
+                for (int i = 0; ok; ++i) {
+                    ok = segment_there(i);
+                    if (!ok) break;
+                    const Segment s = segments[i % kSegments];
+                    segment_taken(i);
+                    if (s.n == 0) break;
+                    auto load_q = [&](int t) -> bool {
+                        if (kq[t] > 0 && !mbar_wait(smem_u32(&bars.q_free[t]), (kq[t] - 1) & 1, lim, &abort_flag)) return false;
+                        const uint32_t qf = smem_u32(&bars.q_full[t]);
+                        mbar_arrive_expect_tx(qf, C::kChunks * q_rows * 128);
                         for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_4d(smem_base + C::kOffQ + t * C::kTileBytes + c * C::kChunkBytes, &tm_q, qf, c * 64, T.r0,
-                                        seg.h, T.b);
-                    }
-                    ++kq;
-                    // bundle n = {K of block n (n < seg.n), V of block n - 1 (n >= 1)}
-                    for (int n = 0; n <= seg.n; ++n, ++gb) {
+                            tma_load_4d(smem_base + C::kOffQ + t * C::kTileBytes + c * C::kChunkBytes, &tm_q, qf, c * 64,
+                                        s.rows[t].r0, s.h, s.rows[t].b);
+                        ++kq[t];
+                        return true;
+                    };
+                    ok = load_q(0);
+                    // bundle n = {K of block n (n < s.n), V of block n - 1 (n >= 1)}
+                    for (int n = 0; ok && n <= s.n; ++n) {
                         const int u = gb % kStages;
                         if (gb >= kStages &&
                             !mbar_wait(smem_u32(&bars.kv_empty[u]), ((gb / kStages) & 1) ^ 1, lim, &abort_flag)) {
@@ -173,20 +260,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         const uint32_t fb = smem_u32(&bars.kv_full[u]);
-                        mbar_arrive_expect_tx(fb, ((n < seg.n ? 1 : 0) + (n >= 1 ? 1 : 0)) * C::kTileBytes);
-                        if (n < seg.n)
+                        mbar_arrive_expect_tx(fb, ((n < s.n ? 1 : 0) + (n >= 1 ? 1 : 0)) * C::kTileBytes);
+                        ++gb;
+                        if (n < s.n)
                             for (int c = 0; c < C::kChunks; ++c)
                                 tma_load_3d(smem_base + C::kOffK + u * C::kTileBytes + c * C::kChunkBytes, &tm_k, fb, c * 64,
-                                            (seg.k0 + n) * kBN, bh_kv);
+                                            (s.k0 + n) * kBN, s.bh_kv);
                         if (n >= 1)
                             for (int c = 0; c < C::kChunks; ++c)
                                 tma_load_3d(smem_base + C::kOffV + u * C::kTileBytes + c * C::kChunkBytes, &tm_v, fb, c * 64,
-                                            (seg.k0 + n - 1) * kBN, bh_kv);
+                                            (s.k0 + n - 1) * kBN, s.bh_kv);
+                        if (n == 0 && !s.solo()) ok = load_q(1);
                     }
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
-                // the last Q and the newest bundle of every slot have landed before exit
-                if (kq > 0) mbar_wait(qf, (kq - 1) & 1, kDrainWaitNs, &never);
+                // the newest load of every slot has landed before exit
+                for (int t = 0; t < 2; ++t)
+                    if (kq[t] > 0) mbar_wait(smem_u32(&bars.q_full[t]), (kq[t] - 1) & 1, kDrainWaitNs, &never);
                 for (int n = max(0, gb - kStages); n < gb; ++n)
                     mbar_wait(smem_u32(&bars.kv_full[n % kStages]), (n / kStages) & 1, kDrainWaitNs, &never);
             }
@@ -197,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t q_lo = sdesc_sw128_lo(smem_base + C::kOffQ, 16);
                 const uint32_t k_lo = sdesc_sw128_lo(smem_base + C::kOffK, 16);
                 const uint32_t v_lo = sdesc_sw128_lo(smem_base + C::kOffV, C::kChunkBytes);
-                // S in the columns of tile (or warpgroup) t from query tile q and K in slot u
+                // S in the columns of warpgroup t from query tile q and K in slot u
                 auto issue_s = [&](int t, int q, int u) {
                     const uint32_t ql = q_lo + q * (C::kTileBytes >> 4), kl = k_lo + u * (C::kTileBytes >> 4);
                     const uint32_t col = tmem + C::kColS + 128 * t;
@@ -222,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_ts_w<false, 1>(colO, colP + kk * 8, vl + ((kk * 16 * 128) >> 4), kDescHi, C::kIdescO);
                     }
                 };
-                int gb = 0, kq = 0;
-                int c0 = 0, c1 = 0;  // blocks of warpgroup 0 / 1 before the segment
-                bool ok = true;
+                int gb = 0, kq0 = 0, kq1 = 0;
+                int c0 = 0, c1 = 0;    // blocks of warpgroup 0 / 1 before the segment
+                bool ok = true, begun;  // O begins with the own attention's
                 // Block j of two tiles: P_t V_j, then the next block's scores, tile by tile; the last two
                 // blocks run outside the loop, which keeps its body free of branches.
                 auto block = [&](int j, int g1, uint32_t p0, uint32_t p1, auto more_c, auto last2_c) -> bool {
@@ -233,36 +323,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!mbar_wait(smem_u32(&bars.kv_full[u]), (g1 / kStages) & 1, lim, &abort_flag)) return false;
                     if (!mbar_wait(smem_u32(&bars.p_full[0]), p0, lim, &abort_flag)) return false;
                     tc_fence_after();
-                    issue_pv(0, u, j > 0);
+                    issue_pv(0, u, j > 0 || begun);
                     if constexpr (more)
                         issue_s(0, 0, u);
                     else
                         mma_commit(smem_u32(&bars.o_done[0]));
+                    if constexpr (last2) mma_commit(smem_u32(&bars.q_free[0]));
                     if (!mbar_wait(smem_u32(&bars.p_full[1]), p1, lim, &abort_flag)) return false;
                     tc_fence_after();
-                    issue_pv(1, u, j > 0);
+                    issue_pv(1, u, j > 0 || begun);
                     if constexpr (more)
                         issue_s(1, 1, u);
                     else
                         mma_commit(smem_u32(&bars.o_done[1]));
-                    if constexpr (last2) mma_commit(smem_u32(&bars.q_free));
+                    if constexpr (last2) mma_commit(smem_u32(&bars.q_free[1]));
                     mma_commit(smem_u32(&bars.kv_empty[u]));
                     return true;
                 };
                 using T = std::true_type;
                 using F = std::false_type;
-                while (ok && walk.next(args, seg)) {
-                    const int n = seg.n;
-                    ok = mbar_wait(smem_u32(&bars.q_full), kq & 1, lim, &abort_flag);
+                for (int x = 0; ok; ++x) {
+                    ok = segment_there(x);
+                    if (!ok) break;
+                    const int n = segments[x % kSegments].n;
+                    const bool solo = segments[x % kSegments].solo();
+                    begun = args.o_own != nullptr && segments[x % kSegments].k0 == 0;
+                    segment_taken(x);
+                    if (n == 0) break;
+                    ok = mbar_wait(smem_u32(&bars.q_full[0]), kq0++ & 1, lim, &abort_flag);
                     if (ok) ok = mbar_wait(smem_u32(&bars.kv_full[gb % kStages]), (gb / kStages) & 1, lim, &abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const int u0 = gb % kStages;
                     issue_s(0, 0, u0);
-                    if (!seg.solo) issue_s(1, 1, u0);
-                    if (n == 1) mma_commit(smem_u32(&bars.q_free));
+                    if (n == 1) mma_commit(smem_u32(&bars.q_free[0]));
+                    if (!solo) {
+                        ok = mbar_wait(smem_u32(&bars.q_full[1]), kq1++ & 1, lim, &abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(1, 1, u0);
+                        if (n == 1) mma_commit(smem_u32(&bars.q_free[1]));
+                    }
                     mma_commit(smem_u32(&bars.kv_empty[u0]));
-                    if (seg.solo) {
+                    if (solo) {
                         // One tile: block i belongs to warpgroup i % 2, whose S, P and O columns it uses.
                         for (int i = 1; i <= n; ++i) {
                             const int g = gb + i, u = g % kStages;
@@ -271,13 +374,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_fence_after();
                             if (i < n) {
                                 issue_s(i & 1, 0, u);
-                                if (i == n - 1) mma_commit(smem_u32(&bars.q_free));
+                                if (i == n - 1) mma_commit(smem_u32(&bars.q_free[0]));
                             }
                             const int j = i - 1, t = j & 1;
                             ok = mbar_wait(smem_u32(&bars.p_full[t]), ((t ? c1 : c0) + j / 2) & 1, lim, &abort_flag);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_pv(t, u, j >= 2);
+                            issue_pv(t, u, j >= 2 || (j == 0 && begun));
                             if (j + 2 >= n) mma_commit(smem_u32(&bars.o_done[t]));  // the warpgroup's last
                             mma_commit(smem_u32(&bars.kv_empty[u]));
                         }
@@ -292,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         c1 += n;
                     }
                     gb += n + 1;
-                    ++kq;
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
                 mma_commit(smem_u32(&bars.drain));
@@ -300,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(smem_u32(&bars.drain), 0, kDrainWaitNs, &never);
             }
         }
-        // warps 2-3 have no role
+        // warp 2 has no role
     } else {
         regs_inc<184>();
         // ================================================================ softmax warpgroups
@@ -316,19 +418,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         int gj = 0, kd = 0;  // this warpgroup's blocks before the segment, and segments with any
         int ns = 0;          // solo segments
         bool ok = true;
-        while (ok && walk.next(args, seg)) {
-            const int n = seg.n, step = seg.solo ? 2 : 1;
-            const TileRows T = tile_rows(args, seg.b, 2 * seg.pair + (seg.solo ? 0 : t));
+        for (int x = 0;; ++x) {
+            ok = segment_there(x);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const Segment* seg = &segments[x % kSegments];
+            const int n = seg->n, k0 = seg->k0, len = seg->len;
+            const bool solo = seg->solo();
+            const bool whole = seg->whole();
+            const int slot = seg->slot();
+            const TileRows T = seg->rows[solo ? 0 : t];
+            const long long at = row < T.rows ? static_cast<long long>(global_row(args, T, seg->h, row)) : -1;  // among o's rows
+            __syncwarp();
+            if (lane == 0) segment_taken(x);
+            if (n == 0) break;
             const bool busy = wq * 32 < T.rows;  // some of the warp's rows are in use
             float m_ref = -INFINITY, l = 0.f;
+            const bool begun = args.o_own != nullptr && k0 == 0 && (!solo || t == 0);
+            if (begun && busy) {
+                // The queries' own attention is the state to begin with: m = lse_own, l = 1, O = o_own (where
+                // there is any: nothing of a row with lse_own = -inf).
+                m_ref = at >= 0 ? args.lse_own[at] * 1.4426950408889634f : -INFINITY;
+                const bool any = m_ref != -INFINITY;
+                l = any ? 1.f : 0.f;
+                const uint4* own = static_cast<const uint4*>(args.o_own) + (any ? at : 0) * (D / 8);
+                uint4 v[D / 8];
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) v[e] = any ? own[e] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t u[4] = {v[4 * q + e].x, v[4 * q + e].y, v[4 * q + e].z, v[4 * q + e].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) r[8 * e + 2 * k] = u[k] << 16, r[8 * e + 2 * k + 1] = u[k] & 0xFFFF0000u;
+                    }
+                    tmem_st32(lane_base + colO + 32 * q, r);
+                }
+                tmem_st_wait();
+            }
             int i = 0;
-            for (int j = seg.solo ? t : 0; j < n; j += step, ++i) {
+            for (int j = solo ? t : 0; j < n; j += solo ? 2 : 1, ++i) {
                 ok = mbar_wait(smem_u32(&bars.s_full[t]), (gj + i) & 1, lim, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const int kv0 = (seg.k0 + j) * kBN, valid = seg.len - kv0;
-                if (valid < kBN && seg.len < args.N_kv) {
+                const int kv0 = (k0 + j) * kBN, valid = len - kv0;
+                if (valid < kBN && len < args.N_kv) {
                     // What the caller left behind the sequence's end (an infinity, a NaN) would reach O as
                     // 0 * V: the block's rows of V from there on are made zeros before P V.
                     const int g = gb + j + 1, u = g % kStages;
@@ -337,16 +474,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const uint32_t vb = smem_base + C::kOffV + u * C::kTileBytes;
                     const int r1 = min(kBN, args.N_kv - kv0);
-                    for (int x = max(valid, 0) * 8 + (warp % 4) * 32 + lane; x < r1 * 8; x += 128)
+                    for (int y = max(valid, 0) * 8 + row; y < r1 * 8; y += 128)
 #pragma unroll
                         for (int ch = 0; ch < C::kChunks; ++ch)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + ch * C::kChunkBytes + x * 16), "r"(0)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + ch * C::kChunkBytes + y * 16), "r"(0)
                                          : "memory");
                     fence_proxy_async_smem();
                 }
                 if (busy)
-                    softmax_block<D, kBN>(lane_base, colS, colS, colO, c, c_pos, mask_bits, valid - 1, -1, 0, i == 0, m_ref, l,
-                                          [] {}, [] { return true; });
+                    softmax_block<D, kBN>(lane_base, colS, colS, colO, c, c_pos, mask_bits, valid - 1, -1, 0, i == 0 && !begun,
+                                          m_ref, l, [] {}, [] { return true; });
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.p_full[t]));
             }
@@ -361,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             float w0 = 1.f, w1 = 0.f;
             bool two = false;
-            if (seg.solo) {
+            if (solo) {
                 // Two states over disjoint keys: m = max(m_0, m_1), l and O weighted by 2^(m_t - m).
                 if (t == 1) {
                     merge_m[row] = m_ref;
@@ -371,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = mbar_wait(smem_u32(&bars.merge_done), ns & 1, lim, &abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     ++ns;
+                    if (!ok) break;
                     continue;
                 }
                 ok = mbar_wait(smem_u32(&bars.merge_ml), ns & 1, lim, &abort_flag);
@@ -387,50 +525,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // O_t is read before this warp publishes the next segment's first P, so the next segment's
             // first P V (which overwrites O_t) comes after these loads
-            const bool there = row < T.rows;
-            const uint32_t col1 = C::kColO + D;
-            if (!seg.whole()) {
-                const int slot = static_cast<int>(blockIdx.x) * 2 + seg.slot();
-                float* part = args.part + slot * part_floats(D, args.part_rows);
-                const int at = row + (seg.solo ? 0 : t * kPartTile);
-                if (busy) {
+            const uint32_t col = lane_base + colO, col1 = lane_base + C::kColO + D;
+            if (busy && !whole) {
+                float* part = args.part + (static_cast<int>(blockIdx.x) * 2 + slot) * part_floats(D, args.part_rows);
+                const int to = row + (solo ? 0 : t * kPartTile);
 #pragma unroll
-                    for (int q4 = 0; q4 < D / 32; ++q4) {
-                        float x[32];
-                        weighted32(lane_base + colO + 32 * q4, w0, lane_base + col1 + 32 * q4, w1, two, x);
+                for (int q = 0; q < D / 32; ++q) {
+                    float y[32];
+                    weighted32(col + 32 * q, w0, col1 + 32 * q, w1, two, y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<float4*>(part)[static_cast<size_t>(8 * q4 + e) * args.part_rows + at] =
-                                make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-                    }
-                    float* ml = part + static_cast<size_t>(args.part_rows) * D;
-                    ml[at] = m_ref;
-                    ml[args.part_rows + at] = l;
+                    for (int e = 0; e < 8; ++e)
+                        reinterpret_cast<float4*>(part)[static_cast<size_t>(8 * q + e) * args.part_rows + to] =
+                            make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                 }
-            } else {
-                const size_t out = there ? global_row(args, T, seg.h, row) : 0;
-                const RowEnd e = row_end(args, m_ref, l, out, there);
-                if (!seg.solo && args.nb == 1 && args.o_own == nullptr) {
-                    store_rows<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, lane_base + colO, e.f, T.r0 + wq * 32,
-                                  T.b * args.H_kv + seg.h, args.R);
-                } else if (busy) {
-#pragma unroll
-                    for (int q4 = 0; q4 < D / 32; ++q4) {
-                        float x[32];
-                        weighted32(lane_base + colO + 32 * q4, w0 * e.f, lane_base + col1 + 32 * q4, w1 * e.f, two, x);
-                        if (there) store32(args, x, e.f_own, out * D + 32 * q4);
-                    }
-                }
-                if (there && args.lse != nullptr) args.lse[out] = e.lse;
+                float* ml = part + static_cast<size_t>(args.part_rows) * D;
+                ml[to] = m_ref;
+                ml[args.part_rows + to] = l;
+            } else if (busy) {
+                const float f = row_factor(l);
+                store_weighted<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
+                if (at >= 0 && args.lse != nullptr) args.lse[at] = row_lse(m_ref, l);
             }
-            if (seg.solo) {
+            if (solo) {
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.merge_done));
             }
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
-        // the stores complete before the CTA's shared memory goes away
-        if (lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
@@ -441,68 +562,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Items that were cut: CTA boundary c = blockIdx.x + 1, if it is the first inside its item, adds up the
-// item's parts in order, kJoinRows of its rows at a time (blockIdx.y).  A warp takes 8 rows x 32 columns:
-// 128-byte runs of the parts, 64-byte runs of the result.
-constexpr int kJoinRows = 32;
+// Items that were cut: the parts of the one that CTA blockIdx.x begins, kJoinRows of its rows at a time
+// (blockIdx.y), in order.  A warp takes 8 rows x 32 columns: 128-byte runs of the parts, 64-byte runs of the
+// result; kTogether parts' loads are in flight together.
+constexpr int kJoinRows = 16, kTogether = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinRows * D / 8) cross_join_kernel(const CrossArgs args) {
     griddep_wait();
     griddep_launch_dependents();
-    const int c = static_cast<int>(blockIdx.x) + 1;
-    const long long total = total_units(args), u = first_unit(args, total, c);
-    if (u >= total) return;
-    const UnitPlace p = unit_place(args, u);
-    if (p.kb == 0 || u - p.kb < first_unit(args, total, c - 1)) return;
-    const int blocks = cross_blocks(cross_length(args, p.b));
-    const int h = p.item / args.n_pairs, pair = p.item - h * args.n_pairs;
-    int last = c;  // the last CTA with a part of the item
-    while (first_unit(args, total, last + 1) < u - p.kb + blocks) ++last;
-
+    const int c = static_cast<int>(blockIdx.x);
+    const int4 cut = args.cut[c];  // last CTA, batch, item
+    if (cut.x < 0) return;
+    const int h = cut.z / args.n_pairs, pair = cut.z - h * args.n_pairs;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     constexpr int kCols = D / 32;
     const int vec = warp % kCols * 4 + lane / 8;  // 8 columns
     const int at = blockIdx.y * kJoinRows + warp / kCols * 8 + lane % 8;
-    const int tile = 2 * pair + at / kPartTile;
+    const int tile = 2 * pair + at / kPartTile, row = at % kPartTile;
     if (tile >= args.tiles || at >= args.part_rows) return;
-    const TileRows T = tile_rows(args, p.b, tile);
-    const int row = at % kPartTile;
+    const TileRows T = tile_rows(args, cut.y, tile);
     if (row >= T.rows) return;
-    const size_t size = part_floats(D, args.part_rows);
-    auto part = [&](int cta) { return args.part + (cta * 2 + (cta < c ? 1 : 0)) * size; };
-    const size_t ml = static_cast<size_t>(args.part_rows) * D + at;
-    float m = -INFINITY;
-    for (int k = c - 1; k <= last; ++k) m = fmaxf(m, part(k)[ml]);
-    float l = 0.f, x[8];
+    const size_t size = part_floats(D, args.part_rows), ml = static_cast<size_t>(args.part_rows) * D + at;
+    const size_t o_at = static_cast<size_t>(2 * vec) * args.part_rows + at;
+    float m = -INFINITY, l = 0.f, x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = 0.f;
-#pragma unroll 4
-    for (int k = c - 1; k <= last; ++k) {
-        const float* src = part(k);
-        const float mk = src[ml], lk = src[ml + args.part_rows];
-        const float w = mk == -INFINITY ? 0.f : exp2f(mk - m);
-        const float4* o = reinterpret_cast<const float4*>(src) + static_cast<size_t>(2 * vec) * args.part_rows + at;
-        const float4 y = o[0], z = o[args.part_rows];
-        l = fmaf(w, lk, l);
-        x[0] = fmaf(w, y.x, x[0]), x[1] = fmaf(w, y.y, x[1]), x[2] = fmaf(w, y.z, x[2]), x[3] = fmaf(w, y.w, x[3]);
-        x[4] = fmaf(w, z.x, x[4]), x[5] = fmaf(w, z.y, x[5]), x[6] = fmaf(w, z.z, x[6]), x[7] = fmaf(w, z.w, x[7]);
-    }
-    const size_t out = global_row(args, T, h, row);
-    const RowEnd e = row_end(args, m, l, out, true);
+    for (int k0 = c; k0 <= cut.x; k0 += kTogether) {
+        float mk[kTogether], lk[kTogether];
+        float4 y[kTogether], z[kTogether];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= e.f;
-    if (e.f_own != 0.f) {
-        const uint4 v = reinterpret_cast<const uint4*>(args.o_own)[out * (D / 8) + vec];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < kTogether; ++i) {
+            const int k = k0 + i;
+            const bool there = k <= cut.x;
+            // the item's first part is its CTA's second slot, the others are their CTAs' first
+            const float* src = args.part + static_cast<size_t>(there ? 2 * k + (k == c) : 2 * c + 1) * size;
+            mk[i] = there ? src[ml] : -INFINITY;
+            lk[i] = src[ml + args.part_rows];
+            y[i] = reinterpret_cast<const float4*>(src)[o_at];
+            z[i] = reinterpret_cast<const float4*>(src)[o_at + args.part_rows];
+        }
+        float top = m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = fmaf(__uint_as_float(w[i] << 16), e.f_own, x[2 * i]);
-            x[2 * i + 1] = fmaf(__uint_as_float(w[i] & 0xFFFF0000u), e.f_own, x[2 * i + 1]);
+        for (int i = 0; i < kTogether; ++i) top = fmaxf(top, mk[i]);
+        const float keep = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= keep;
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+            if (k0 + i > cut.x) break;
+            // of a part whose keys' scores are all -inf nothing; a NaN in l stays
+            const float w = mk[i] == -INFINITY && lk[i] == 0.f ? 0.f : ex2_approx(mk[i] == m ? 0.f : mk[i] - m);
+            l = fmaf(w, lk[i], l);
+            x[0] = fmaf(w, y[i].x, x[0]), x[1] = fmaf(w, y[i].y, x[1]);
+            x[2] = fmaf(w, y[i].z, x[2]), x[3] = fmaf(w, y[i].w, x[3]);
+            x[4] = fmaf(w, z[i].x, x[4]), x[5] = fmaf(w, z[i].y, x[5]);
+            x[6] = fmaf(w, z[i].z, x[6]), x[7] = fmaf(w, z[i].w, x[7]);
         }
     }
+    const size_t out = global_row(args, T, h, row);
+    const float f = row_factor(l);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= f;
     reinterpret_cast<uint4*>(args.o)[out * (D / 8) + vec] =
         make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    if (vec == 0 && args.lse != nullptr) args.lse[out] = e.lse;
+    if (vec == 0 && args.lse != nullptr) args.lse[out] = row_lse(m, l);
 }
 
 // How a call's rows are tiled and its work dealt, from its sizes alone.
@@ -546,12 +671,11 @@ int row_map(CUtensorMap* map, const void* base, int D, const CrossArgs& a, int r
 template <int D>
 int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a, cudaStream_t s) {
     const int BH_kv = a.B_kv * a.H_kv;
-    CUtensorMap tq, tk, tv, to;
+    CUtensorMap tq, tk, tv;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     int rc = row_map(&tq, q, D, a, a.nb > 1 ? a.R : kBM, a.nb);
     if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, a.N_kv, BH_kv, 64, kBN);
     if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, a.N_kv, BH_kv, 64, kBN);
-    if (rc == 0) rc = make_map_3d(&to, a.o, dt, 2, D, a.R, static_cast<uint64_t>(BH_kv) * a.share, 64, 32);
     if (rc != 0) return rc;
     static std::atomic<uint64_t> smem_done;
     cudaError_t e = allow_smem(cross_fwd_kernel<D>, Cfg<D>::kSmemAlloc, smem_done);
@@ -561,7 +685,7 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
     if (e != cudaSuccess) return static_cast<int>(e);
     CrossArgs x = a;
     if (x.ctas > sms) x.ctas = sms;
-    e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, to, x);
+    e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, x);
     if (e == cudaSuccess && x.stream && x.ctas > 1)
         e = launch_pdl(cross_join_kernel<D>, dim3(x.ctas - 1, (x.part_rows + kJoinRows - 1) / kJoinRows),
                        dim3(kJoinRows * D / 8), 0, s, x);
@@ -572,7 +696,7 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
 
 size_t fwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     const CrossArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv);
-    return a.stream && a.ctas > 1 ? 2 * a.ctas * part_floats(d, a.part_rows) * sizeof(float) : 0;
+    return a.stream && a.ctas > 1 ? kCutBytes + 2 * a.ctas * part_floats(d, a.part_rows) * sizeof(float) : 0;
 }
 
 int launch_fwd_cross(const void* q, const void* k, const void* v, const int* lengths, const void* o_own,
@@ -584,7 +708,8 @@ int launch_fwd_cross(const void* q, const void* k, const void* v, const int* len
     a.lse = lse;
     a.o_own = o_own;
     a.lse_own = lse_own;
-    a.part = static_cast<float*>(workspace);
+    a.cut = static_cast<int4*>(workspace);
+    a.part = static_cast<float*>(workspace) + kCutBytes / sizeof(float);
     // a scale of 0 makes all scores 0; the mask multiplies -inf by c, which has to stay -inf
     a.c_log2 = c_log2 == 0.f ? 1e-30f : c_log2;
     a.ctl = ctl;
