@@ -202,7 +202,7 @@ struct Walk {
 };
 
 // A row's end from its state (reference maximum m in log2 units, sum l): the factor of O, and lse.
-__device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }

@@ -27,13 +27,14 @@ struct Cfg {
     static constexpr int kOffQ = 0;                  // two tiles
     static constexpr int kOffK = 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kSmemAlloc = kOffV + kStages * kTileBytes + 1024;
+    static constexpr int kOffO = kOffV + kStages * kTileBytes;  // two boxes of 32 rows x 64 bytes a softmax warp
+    static constexpr int kSmemAlloc = kOffO + 8 * 4096 + 1024;
     static constexpr uint32_t kColS = 0, kColO = 256;  // + 128, + D for the second warpgroup
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kIdescS = idesc_bf16(kBM, kBN, false, false);
     static constexpr uint32_t kIdescO = idesc_bf16(kBM, D, false, true);
 };
-static_assert(Cfg<128>::kSmemAlloc + 3072 <= 232448, "smem");
+static_assert(Cfg<128>::kSmemAlloc + 2000 <= 232448, "smem");
 
 constexpr int kSegments = 8;   // ring of segments
 constexpr int kReaders = 10;   // the loading thread, the MMA thread, 8 softmax warps
@@ -119,6 +120,43 @@ __device__ __forceinline__ void store_weighted(uint32_t first, float w0, uint32_
     }
 }
 
+// The same for whole tiles of one batch, by TMA: 32 columns a box, two boxes in turn, so that one is filled
+// while the other is stored, and the warp goes on with its next block while the last ones leave.  16-byte
+// granule g of row r lies at g ^ (r / 2 % 4).
+template <int D>
+__device__ __forceinline__ void store_boxes(const CUtensorMap& tm_o, uint32_t boxes, uint32_t taddr, float f, int row0, int bh,
+                                            int N) {
+    const int lane = threadIdx.x % 32;
+    uint32_t r[2][32];
+    tmem_ld32_async(taddr, r[0]);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const uint32_t box = boxes + (c & 1) * 2048;
+        tmem_wait_ld();
+        reg_fence(r[c & 1]);
+        if (c + 1 < D / 32) tmem_ld32_async(taddr + 32 * (c + 1), r[(c + 1) & 1]);
+        // the store before the last has read this box
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t* x = r[c & 1] + 8 * g;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 64 + ((g ^ (lane >> 1 & 3)) << 4)),
+                         "r"(pack_bf16x2(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f)),
+                         "r"(pack_bf16x2(__uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f)),
+                         "r"(pack_bf16x2(__uint_as_float(x[4]) * f, __uint_as_float(x[5]) * f)),
+                         "r"(pack_bf16x2(__uint_as_float(x[6]) * f, __uint_as_float(x[7]) * f))
+                         : "memory");
+        }
+        fence_proxy_async_smem();  // the lanes' writes -> visible to the TMA unit
+        __syncwarp();
+        if (lane == 0) {
+            if (row0 < N) tma_store_3d(&tm_o, box, 32 * c, row0, bh);
+            bulk_commit_group();
+        }
+    }
+}
+
 // Persistent.  A warp of its own works out the CTA's segments (some hundred instructions each, which
 // took the other roles 1400 to 2000 cycles) and hands them to the others through a ring in shared memory.
 // Every barrier counts its phases across segments: q_* per tile, kv_* per bundle, s_full and p_full per block
@@ -126,7 +164,8 @@ __device__ __forceinline__ void store_weighted(uint32_t first, float w0, uint32_
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const CrossArgs args) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                     const CrossArgs args) {
     using C = Cfg<D>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -165,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_o);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
@@ -418,26 +458,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         int gj = 0, kd = 0;  // this warpgroup's blocks before the segment, and segments with any
         int ns = 0;          // solo segments
         bool ok = true;
+        // Of a segment only what the loop over its blocks needs is kept in registers, of which that has none to
+        // spare; the rest is read from the ring again after it.
+        auto place = [&](const Segment& s, int tile) -> long long {  // the thread's row among o's rows, or -1
+            const TileRows T = s.rows[tile];
+            return row < T.rows ? static_cast<long long>(global_row(args, T, s.h, row)) : -1;
+        };
         for (int x = 0;; ++x) {
             ok = segment_there(x);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const Segment* seg = &segments[x % kSegments];
-            const int n = seg->n, k0 = seg->k0, len = seg->len;
-            const bool solo = seg->solo();
-            const bool whole = seg->whole();
-            const int slot = seg->slot();
-            const TileRows T = seg->rows[solo ? 0 : t];
-            const long long at = row < T.rows ? static_cast<long long>(global_row(args, T, seg->h, row)) : -1;  // among o's rows
-            __syncwarp();
-            if (lane == 0) segment_taken(x);
+            const Segment& seg = segments[x % kSegments];
+            const int n = seg.n, k0 = seg.k0, len = seg.len;
             if (n == 0) break;
-            const bool busy = wq * 32 < T.rows;  // some of the warp's rows are in use
+            const bool solo = seg.solo();
+            const int tile = solo ? 0 : t;
+            const bool busy = wq * 32 < seg.rows[tile].rows;  // some of the warp's rows are in use
             float m_ref = -INFINITY, l = 0.f;
             const bool begun = args.o_own != nullptr && k0 == 0 && (!solo || t == 0);
             if (begun && busy) {
                 // The queries' own attention is the state to begin with: m = lse_own, l = 1, O = o_own (where
                 // there is any: nothing of a row with lse_own = -inf).
+                const long long at = place(seg, tile);
                 m_ref = at >= 0 ? args.lse_own[at] * 1.4426950408889634f : -INFINITY;
                 const bool any = m_ref != -INFINITY;
                 l = any ? 1.f : 0.f;
@@ -497,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             float w0 = 1.f, w1 = 0.f;
-            bool two = false;
+            const bool two = solo && n >= 2;
             if (solo) {
                 // Two states over disjoint keys: m = max(m_0, m_1), l and O weighted by 2^(m_t - m).
                 if (t == 1) {
@@ -509,6 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     ++ns;
                     if (!ok) break;
+                    __syncwarp();
+                    if (lane == 0) segment_taken(x);
                     continue;
                 }
                 ok = mbar_wait(smem_u32(&bars.merge_ml), ns & 1, lim, &abort_flag);
@@ -516,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ns;
                 if (!ok) break;
                 tc_fence_after();
-                two = n >= 2;
                 const float m1 = merge_m[row], l1 = merge_l[row], mm = fmaxf(m_ref, m1);
                 w0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mm);
                 w1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
@@ -526,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O_t is read before this warp publishes the next segment's first P, so the next segment's
             // first P V (which overwrites O_t) comes after these loads
             const uint32_t col = lane_base + colO, col1 = lane_base + C::kColO + D;
-            if (busy && !whole) {
-                float* part = args.part + (static_cast<int>(blockIdx.x) * 2 + slot) * part_floats(D, args.part_rows);
+            if (busy && !seg.whole()) {
+                float* part = args.part + (static_cast<int>(blockIdx.x) * 2 + seg.slot()) * part_floats(D, args.part_rows);
                 const int to = row + (solo ? 0 : t * kPartTile);
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
@@ -543,15 +586,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ml[args.part_rows + to] = l;
             } else if (busy) {
                 const float f = row_factor(l);
-                store_weighted<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
+                const long long at = place(seg, tile);
+                if (!solo && args.nb == 1)
+                    store_boxes<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, col, f, seg.rows[tile].r0 + wq * 32,
+                                   seg.rows[tile].b * args.H_kv + seg.h, args.R);
+                else
+                    store_weighted<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
                 if (at >= 0 && args.lse != nullptr) args.lse[at] = row_lse(m_ref, l);
             }
             if (solo) {
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.merge_done));
             }
+            __syncwarp();
+            if (lane == 0) segment_taken(x);
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
+        // the stores complete before the CTA's shared memory goes away
+        if (lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
@@ -652,28 +704,35 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     return a;
 }
 
-// q or o as [B][H_kv][R][d], read in boxes of `rows` rows of `nb` batches.
-int row_map(CUtensorMap* map, const void* base, int D, const CrossArgs& a, int rows, int nb) {
+// q as [B][H_kv][R][d] in boxes of `rows` rows of nb batches, 64 columns, or o in boxes of a warp's 32 rows, 32
+// columns.
+int row_map(CUtensorMap* map, const void* base, int D, const CrossArgs& a, int cols, int rows, int nb) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (fn == nullptr) return -1;
     const cuuint64_t line = static_cast<cuuint64_t>(D) * 2;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.R), static_cast<cuuint64_t>(a.H_kv),
                           static_cast<cuuint64_t>(a.B_kv) * a.share};
     cuuint64_t strides[3] = {line, line * a.R, line * a.R * a.H_kv};
-    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, static_cast<cuuint32_t>(nb)};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(rows), 1, static_cast<cuuint32_t>(nb)};
+    int rank = 4;
+    if (cols == 32) {  // heads and batches as one dimension
+        dims[2] *= dims[3];
+        rank = 3;
+    }
     cuuint32_t one[4] = {1, 1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? 0 : static_cast<int>(r);
 }
 
 template <int D>
 int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a, cudaStream_t s) {
     const int BH_kv = a.B_kv * a.H_kv;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    int rc = row_map(&tq, q, D, a, a.nb > 1 ? a.R : kBM, a.nb);
+    int rc = row_map(&tq, q, D, a, 64, a.nb > 1 ? a.R : kBM, a.nb);
+    if (rc == 0) rc = row_map(&to, a.o, D, a, 32, 32, 1);
     if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, a.N_kv, BH_kv, 64, kBN);
     if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, a.N_kv, BH_kv, 64, kBN);
     if (rc != 0) return rc;
@@ -685,7 +744,7 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
     if (e != cudaSuccess) return static_cast<int>(e);
     CrossArgs x = a;
     if (x.ctas > sms) x.ctas = sms;
-    e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, x);
+    e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, to, x);
     if (e == cudaSuccess && x.stream && x.ctas > 1)
         e = launch_pdl(cross_join_kernel<D>, dim3(x.ctas - 1, (x.part_rows + kJoinRows - 1) / kJoinRows),
                        dim3(kJoinRows * D / 8), 0, s, x);
