@@ -21,11 +21,14 @@ struct CrossArgs {
     float* lse;            // [B][H_kv][R] or null
     const void* o_own;     // as o, merged into it; null: none
     const float* lse_own;
-    int4* cut;             // an item that was cut, by the CTA that begins it: last CTA, b, item, 0; or last CTA -1
+    // Items that were cut, each by the CTA that begins it: last CTA (-1: none), batch, item, first CTA; in the
+    // item's place (by_item) or the CTA's, whichever are fewer.
+    int4* cut;
     float* part;           // two parts a CTA: [d / 4][part_rows][4] O, then m and l of part_rows each
     int R, share, H_kv, B_kv, N_kv;
     int nb, tiles_b, tiles, n_pairs, part_rows;
     int stream;            // 0: whole items; 1: equal runs of key blocks, items cut where they end
+    int by_item, join_rows;
     int ctas;
     float c_log2;          // scale * log2(e), not 0
     DevCtl ctl;

@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ============================================================ segments
             const Units units(args);
             Walk walk(args, units);
-            int4 cut = make_int4(-1, 0, 0, 0);
+            // An item that this CTA begins and leaves cut, and its last CTA, for the join.
+            int4 cut = make_int4(-1, 0, 0, static_cast<int>(blockIdx.x));
+            int cut_at = static_cast<int>(blockIdx.x), behind_it = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 Segment s;
@@ -248,25 +250,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(smem_u32(&bars.seg_full[u]));
                 }
                 if (!more) break;
-                if (s.k0 == 0 && behind > 0) cut = make_int4(0, batch, item, behind);
+                if (s.k0 > 0 || !args.stream || args.ctas == 1) continue;
+                const int place = batch * args.H_kv * args.n_pairs + item;
+                if (behind > 0) {
+                    cut = make_int4(0, batch, item, cut.w);
+                    behind_it = behind;
+                    if (args.by_item) cut_at = place;
+                } else if (args.by_item && lane == 0) {
+                    args.cut[place] = make_int4(-1, 0, 0, 0);
+                }
             }
             if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
-            // An item that this CTA begins and leaves cut: its last CTA, for the join.
-            if (args.stream && args.ctas > 1) {
-                if (cut.x == 0) {
-                    const long long end = units.first(blockIdx.x + 1) + cut.w;  // behind the item's last unit
-                    cut.x = static_cast<int>(blockIdx.x);
-                    for (;; cut.x += 32) {
-                        const int cta = cut.x + 1 + lane;
-                        const unsigned in = __ballot_sync(0xffffffffu, cta < args.ctas && units.first(cta) < end);
-                        if (in != 0xffffffffu) {
-                            cut.x += __popc(in);
-                            break;
-                        }
+            if (cut.x == 0) {
+                const long long end = units.first(blockIdx.x + 1) + behind_it;  // behind the item's last unit
+                cut.x = static_cast<int>(blockIdx.x);
+                for (;; cut.x += 32) {
+                    const int cta = cut.x + 1 + lane;
+                    const unsigned in = __ballot_sync(0xffffffffu, cta < args.ctas && units.first(cta) < end);
+                    if (in != 0xffffffffu) {
+                        cut.x += __popc(in);
+                        break;
                     }
                 }
-                if (lane == 0) args.cut[blockIdx.x] = cut;
             }
+            // (an item's place is written by the CTA that begins it, a CTA's by itself)
+            if (lane == 0 && args.stream && args.ctas > 1 && (cut.x >= 0 || !args.by_item)) args.cut[cut_at] = cut;
         } else if (warp == 0) {
             // ============================================================ TMA producer
             if (lane == 0) {
@@ -614,72 +622,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Items that were cut: the parts of the one that CTA blockIdx.x begins, kJoinRows of its rows at a time
-// (blockIdx.y), in order.  A warp takes 8 rows x 32 columns: 128-byte runs of the parts, 64-byte runs of the
-// result; kTogether parts' loads are in flight together.
-constexpr int kJoinRows = 16, kTogether = 4;
-template <int D>
-__global__ void __launch_bounds__(kJoinRows * D / 8) cross_join_kernel(const CrossArgs args) {
+// Items that were cut: the parts of the one in place blockIdx.x of the table, some of its rows at a time
+// (blockIdx.y), in a fixed order.  A warp takes 8 rows x 32 columns (128-byte runs of the parts, 64-byte runs of
+// the result) of every GROUPS-th part, kTogether parts' loads in flight; the groups' states meet in shared
+// memory.  Items of many parts take four groups (16 items of 9 parts each 7.0 -> 3.5 us, 8 of 19 13.7 -> 8.8);
+// where there are two to four parts four groups are idle and in the way (64 items 8 -> 34 us), and the reads
+// of 128 KB a part at d = 128 count.
+constexpr int kTogether = 4;
+template <int GROUPS>
+constexpr int kJoinRows = GROUPS == 1 ? 16 : 8;
+struct JoinState {
+    float m, l, x[8];
+    // this and another state over other keys
+    __device__ __forceinline__ void add(float mk, float lk, const float (&y)[8]) {
+        const float top = fmaxf(m, mk);
+        // of a part whose keys' scores are all -inf nothing; a NaN in l stays
+        const float keep = m == -INFINITY && l == 0.f ? 0.f : ex2_approx(m == top ? 0.f : m - top);
+        const float w = mk == -INFINITY && lk == 0.f ? 0.f : ex2_approx(mk == top ? 0.f : mk - top);
+        m = top;
+        l = fmaf(w, lk, keep * l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(w, y[e], keep * x[e]);
+    }
+};
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(GROUPS == 1 ? 2 * D : GROUPS * D) cross_join_kernel(const CrossArgs args) {
+    constexpr int kCols = D / 32, kWarpRows = kJoinRows<GROUPS> / 8;
+    __shared__ JoinState states[GROUPS > 1 ? GROUPS - 1 : 1][GROUPS > 1 ? kCols * 32 : 1];
     griddep_wait();
     griddep_launch_dependents();
-    const int c = static_cast<int>(blockIdx.x);
-    const int4 cut = args.cut[c];  // last CTA, batch, item
+    const int4 cut = args.cut[blockIdx.x];  // last CTA (-1: not cut), batch, item, first CTA
     if (cut.x < 0) return;
+    const int c = cut.w;
     const int h = cut.z / args.n_pairs, pair = cut.z - h * args.n_pairs;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    constexpr int kCols = D / 32;
-    const int vec = warp % kCols * 4 + lane / 8;  // 8 columns
-    const int at = blockIdx.y * kJoinRows + warp / kCols * 8 + lane % 8;
+    const int group = warp / (kCols * kWarpRows), vec = warp % kCols * 4 + lane / 8;  // 8 columns
+    const int at = blockIdx.y * kJoinRows<GROUPS> + warp / kCols % kWarpRows * 8 + lane % 8;
     const int tile = 2 * pair + at / kPartTile, row = at % kPartTile;
-    if (tile >= args.tiles || at >= args.part_rows) return;
-    const TileRows T = tile_rows(args, cut.y, tile);
-    if (row >= T.rows) return;
+    TileRows T = {0, 0, 0};
+    if (tile < args.tiles && at < args.part_rows) T = tile_rows(args, cut.y, tile);
+    const bool mine = row < T.rows;
+    if (GROUPS == 1 ? !mine : !__syncthreads_or(mine)) return;
     const size_t size = part_floats(D, args.part_rows), ml = static_cast<size_t>(args.part_rows) * D + at;
     const size_t o_at = static_cast<size_t>(2 * vec) * args.part_rows + at;
-    float m = -INFINITY, l = 0.f, x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    for (int k0 = c; k0 <= cut.x; k0 += kTogether) {
+    JoinState s = {-INFINITY, 0.f, {}};
+    for (int k0 = c + group; mine && k0 <= cut.x; k0 += GROUPS * kTogether) {
         float mk[kTogether], lk[kTogether];
         float4 y[kTogether], z[kTogether];
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
-            const int k = k0 + i;
+            const int k = k0 + GROUPS * i;
             const bool there = k <= cut.x;
             // the item's first part is its CTA's second slot, the others are their CTAs' first
             const float* src = args.part + static_cast<size_t>(there ? 2 * k + (k == c) : 2 * c + 1) * size;
             mk[i] = there ? src[ml] : -INFINITY;
-            lk[i] = src[ml + args.part_rows];
+            lk[i] = there ? src[ml + args.part_rows] : 0.f;
             y[i] = reinterpret_cast<const float4*>(src)[o_at];
             z[i] = reinterpret_cast<const float4*>(src)[o_at + args.part_rows];
         }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < kTogether; ++i) top = fmaxf(top, mk[i]);
-        const float keep = m == -INFINITY ? 0.f : ex2_approx(m - top);
-        m = top;
-        l *= keep;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= keep;
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
-            if (k0 + i > cut.x) break;
-            // of a part whose keys' scores are all -inf nothing; a NaN in l stays
-            const float w = mk[i] == -INFINITY && lk[i] == 0.f ? 0.f : ex2_approx(mk[i] == m ? 0.f : mk[i] - m);
-            l = fmaf(w, lk[i], l);
-            x[0] = fmaf(w, y[i].x, x[0]), x[1] = fmaf(w, y[i].y, x[1]);
-            x[2] = fmaf(w, y[i].z, x[2]), x[3] = fmaf(w, y[i].w, x[3]);
-            x[4] = fmaf(w, z[i].x, x[4]), x[5] = fmaf(w, z[i].y, x[5]);
-            x[6] = fmaf(w, z[i].z, x[6]), x[7] = fmaf(w, z[i].w, x[7]);
+            const float x[8] = {y[i].x, y[i].y, y[i].z, y[i].w, z[i].x, z[i].y, z[i].z, z[i].w};
+            if (k0 + GROUPS * i <= cut.x) s.add(mk[i], lk[i], x);
         }
     }
-    const size_t out = global_row(args, T, h, row);
-    const float f = row_factor(l);
+    if constexpr (GROUPS > 1) {
+        const int place = threadIdx.x % (kCols * 32);
+        if (group > 0) states[group - 1][place] = s;
+        __syncthreads();
+        if (group > 0 || !mine) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= f;
+        for (int g = 0; g < GROUPS - 1; ++g)
+            if (c + g + 1 <= cut.x) s.add(states[g][place].m, states[g][place].l, states[g][place].x);
+    }
+    const size_t out = global_row(args, T, h, row);
+    const float f = row_factor(s.l);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s.x[i] *= f;
     reinterpret_cast<uint4*>(args.o)[out * (D / 8) + vec] =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    if (vec == 0 && args.lse != nullptr) args.lse[out] = row_lse(m, l);
+        make_uint4(pack_bf16x2(s.x[0], s.x[1]), pack_bf16x2(s.x[2], s.x[3]), pack_bf16x2(s.x[4], s.x[5]), pack_bf16x2(s.x[6], s.x[7]));
+    if (vec == 0 && args.lse != nullptr) args.lse[out] = row_lse(s.m, s.l);
 }
 
 // How a call's rows are tiled and its work dealt, from its sizes alone.
@@ -698,7 +720,9 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     const int rows = a.nb > 1 ? a.nb * a.R : a.R;  // of a lone tile
     a.part_rows = a.tiles > 1 ? 2 * kBM : round_up(rows < kBM ? rows : kBM, 32);
     const long long items = static_cast<long long>(B_kv) * H_kv * a.n_pairs;
+    a.join_rows = a.tiles > 1 ? 2 * kBM : rows < kBM ? rows : kBM;
     a.stream = items < 8 * kMaxCtas;
+    a.by_item = items < kMaxCtas;
     const long long units = items * ((N_kv + kBN - 1) / kBN);
     a.ctas = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);
     return a;
@@ -726,6 +750,12 @@ int row_map(CUtensorMap* map, const void* base, int D, const CrossArgs& a, int c
     return r == CUDA_SUCCESS ? 0 : static_cast<int>(r);
 }
 
+template <int D, int GROUPS>
+cudaError_t join(const CrossArgs& x, int places, cudaStream_t s) {
+    return launch_pdl(cross_join_kernel<D, GROUPS>, dim3(places, (x.join_rows + kJoinRows<GROUPS> - 1) / kJoinRows<GROUPS>),
+                      dim3(GROUPS == 1 ? 2 * D : GROUPS * D), 0, s, x);
+}
+
 template <int D>
 int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a, cudaStream_t s) {
     const int BH_kv = a.B_kv * a.H_kv;
@@ -745,9 +775,9 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
     CrossArgs x = a;
     if (x.ctas > sms) x.ctas = sms;
     e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, to, x);
+    const int items = x.by_item ? x.B_kv * x.H_kv * x.n_pairs : x.ctas - 1;  // places of cut items
     if (e == cudaSuccess && x.stream && x.ctas > 1)
-        e = launch_pdl(cross_join_kernel<D>, dim3(x.ctas - 1, (x.part_rows + kJoinRows - 1) / kJoinRows),
-                       dim3(kJoinRows * D / 8), 0, s, x);
+        e = x.ctas >= 6 * items ? join<D, 4>(x, items, s) : join<D, 1>(x, items, s);
     return static_cast<int>(e);
 }
 
