@@ -721,7 +721,7 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     a.part_rows = a.tiles > 1 ? 2 * kBM : round_up(rows < kBM ? rows : kBM, 32);
     const long long items = static_cast<long long>(B_kv) * H_kv * a.n_pairs;
     a.join_rows = a.tiles > 1 ? 2 * kBM : rows < kBM ? rows : kBM;
-    a.stream = items < 8 * kMaxCtas;
+    a.stream = items < 8 * kMaxCtas && N_kv > kBN;  // an item of one block cannot be cut
     a.by_item = items < kMaxCtas;
     const long long units = items * ((N_kv + kBN - 1) / kBN);
     a.ctas = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);

@@ -387,6 +387,9 @@ def test_backward_of_pieces_and_of_many_items(d):
     lengths = [700, 10, 300, 0, 650, 129]
     q, k, v, do, _, _, grads, scale = step(6, 6, 16, 8, 200, 700, d, lengths, seed=4)
     check_backward(q, k, v, lengths, do, grads, scale, kv_batches=[1, 3, 5])
+    lengths = [int(x) for x in np.random.default_rng(d).integers(0, 200, 70)]
+    q, k, v, do, _, _, grads, scale = step(70, 70, 2, 1, 140, 200, d, lengths, seed=6)
+    check_backward(q, k, v, lengths, do, grads, scale, kv_batches=range(0, 70, 9))
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
