@@ -594,13 +594,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ml[args.part_rows + to] = l;
             } else if (busy) {
                 const float f = row_factor(l);
-                const long long at = place(seg, tile);
-                if (!solo && args.nb == 1)
-                    store_boxes<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, col, f, seg.rows[tile].r0 + wq * 32,
-                                   seg.rows[tile].b * args.H_kv + seg.h, args.R);
-                else
+                if (!solo && args.nb == 1) {
+                    const TileRows T = seg.rows[tile];
+                    const int bh = T.b * args.H_kv + seg.h;
+                    store_boxes<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, col, f, T.r0 + wq * 32, bh, args.R);
+                    if (row < T.rows && args.lse != nullptr)
+                        args.lse[static_cast<size_t>(bh) * args.R + (T.r0 + row)] = row_lse(m_ref, l);
+                } else {
+                    const long long at = place(seg, tile);
                     store_weighted<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
-                if (at >= 0 && args.lse != nullptr) args.lse[at] = row_lse(m_ref, l);
+                    if (at >= 0 && args.lse != nullptr) args.lse[at] = row_lse(m_ref, l);
+                }
             }
             if (solo) {
                 tc_fence_before();
