@@ -29,6 +29,7 @@ struct CrossArgs {
     int nb, tiles_b, tiles, n_pairs, part_rows;
     int stream;            // 0: whole items; 1: equal runs of key blocks, items cut where they end
     int by_item, join_rows;
+    int cluster;           // CTAs of a cluster that share one item, each with its own run of the keys; 0: as `stream`
     int ctas;
     float c_log2;          // scale * log2(e), not 0
     DevCtl ctl;
@@ -132,8 +133,7 @@ __device__ __forceinline__ size_t global_row(const CrossArgs& a, const TileRows&
     return (static_cast<size_t>(t.b + over) * a.H_kv + h) * a.R + (t.r0 + row - over * a.R);
 }
 
-// A run of key blocks of an item: what the kernel's roles read of it.  The blocks of tiles of all segments,
-// both tiles' in turn or a lone tile's one after the other, go to the two softmax warpgroups alternately.
+// A run of key blocks of an item: what the kernel's roles read of it.
 struct __align__(16) Segment {
     int n;       // its blocks; 0: none follows
     int k0;      // the first
@@ -142,16 +142,24 @@ struct __align__(16) Segment {
     int bh_kv, h;
     TileRows rows[2];
     __device__ __forceinline__ bool solo() const { return flags & 1; }        // one tile
-    // the warpgroup that takes the first tile, or a lone tile's first block
-    __device__ __forceinline__ int first() const { return flags >> 1 & 1; }
     __device__ __forceinline__ bool whole() const { return flags & 4; }       // all blocks of the item
     __device__ __forceinline__ int slot() const { return k0 > 0 ? 0 : 1; }    // of the CTA's two parts
 };
 
+// An item's place in a segment.
+__device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int batch, int item) {
+    s.h = item / a.n_pairs;
+    const int pair = item - s.h * a.n_pairs;
+    const bool solo = 2 * pair + 1 >= a.tiles;
+    s.bh_kv = batch * a.H_kv + s.h;
+    s.rows[0] = tile_rows(a, batch, 2 * pair);
+    if (!solo) s.rows[1] = tile_rows(a, batch, 2 * pair + 1);
+    s.flags = solo ? 1 : 0;
+}
+
 // This CTA's segments, one after the other.
 struct Walk {
     int b, item, kb, blocks, len;
-    int turn = 0;  // blocks of tiles so far, modulo 2
     long long left;
     __device__ __forceinline__ Walk(const CrossArgs& a, const Units& units) {
         const long long u = units.first(blockIdx.x);
@@ -192,14 +200,8 @@ struct Walk {
             s.n = cross_blocks(s.len);
             behind = 0;
         }
-        s.h = at / a.n_pairs;
-        const int pair = at - s.h * a.n_pairs;
-        const bool solo = 2 * pair + 1 >= a.tiles;
-        s.bh_kv = batch * a.H_kv + s.h;
-        s.rows[0] = tile_rows(a, batch, 2 * pair);
-        if (!solo) s.rows[1] = tile_rows(a, batch, 2 * pair + 1);
-        s.flags = (solo ? 1 : 0) | turn << 1 | (s.k0 == 0 && behind == 0 ? 4 : 0);
-        if (solo) turn ^= s.n & 1;
+        place_item(a, s, batch, at);
+        if (s.k0 == 0 && behind == 0) s.flags |= 4;
         return true;
     }
 };

@@ -157,6 +157,79 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap& tm_o, uint32_t bo
     }
 }
 
+// A row's state over some of its keys: reference maximum, sum, eight columns of the unnormalised O.
+struct JoinState {
+    float m, l, x[8];
+    // this and another state over other keys
+    __device__ __forceinline__ void add(float mk, float lk, const float (&y)[8]) {
+        const float top = fmaxf(m, mk);
+        // of a part whose keys' scores are all -inf nothing; a NaN in l stays
+        const float keep = m == -INFINITY && l == 0.f ? 0.f : ex2_approx(m == top ? 0.f : m - top);
+        const float w = mk == -INFINITY && lk == 0.f ? 0.f : ex2_approx(mk == top ? 0.f : mk - top);
+        m = top;
+        l = fmaf(w, lk, keep * l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(w, y[e], keep * x[e]);
+    }
+};
+// Blocks of an item's run for CTA r of its cluster: up to this.
+__device__ __forceinline__ int cluster_run(int blocks, int r, int size) {
+    return static_cast<int>(static_cast<long long>(blocks) * r / size);
+}
+__device__ __forceinline__ void cluster_sync() {  // what any thread of the cluster wrote before is visible after
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The parts of an item on a cluster's CTAs, joined by the threads t = 0 .. 255 of each, a share of the rows a CTA:
+// eight columns of a row a thread, four parts' loads in flight.
+template <int D>
+__device__ __forceinline__ void cluster_join(const CrossArgs& args, int t) {
+    const int size = args.cluster, rank = static_cast<int>(blockIdx.x) % size, item = static_cast<int>(blockIdx.x) / size;
+    const int per = args.H_kv * args.n_pairs, batch = item / per, at_item = item - batch * per;
+    const int h = at_item / args.n_pairs, pair = at_item - h * args.n_pairs;
+    const int blocks = cross_blocks(cross_length(args, batch));
+    const int share = (args.join_rows + size - 1) / size;
+    const int first = rank * share, end = min(args.join_rows, first + share);
+    for (int x = t; x < share * (D / 8); x += 256) {
+        // a warp takes 8 rows x 32 columns where there are so many rows
+        const int vec = x / share, at = first + x % share;
+        if (at >= end) continue;
+        const int tile = 2 * pair + at / kPartTile, row = at % kPartTile;
+        if (tile >= args.tiles) continue;
+        const TileRows T = tile_rows(args, batch, tile);
+        if (row >= T.rows) continue;
+        const size_t size_floats = part_floats(D, args.part_rows), ml = static_cast<size_t>(args.part_rows) * D + at;
+        const size_t o_at = static_cast<size_t>(2 * vec) * args.part_rows + at;
+        JoinState s = {-INFINITY, 0.f, {}};
+        for (int r0 = 0; r0 < size; r0 += 4) {
+            float mk[4], lk[4];
+            float4 y[4], z[4];
+            bool there[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + i;
+                there[i] = r < size && cluster_run(blocks, r, size) < cluster_run(blocks, r + 1, size);
+                const float* src = args.part + static_cast<size_t>(item * size + (there[i] ? r : 0)) * size_floats;
+                mk[i] = __ldcg(src + ml);
+                lk[i] = __ldcg(src + ml + args.part_rows);
+                y[i] = __ldcg(reinterpret_cast<const float4*>(src) + o_at);
+                z[i] = __ldcg(reinterpret_cast<const float4*>(src) + o_at + args.part_rows);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float c[8] = {y[i].x, y[i].y, y[i].z, y[i].w, z[i].x, z[i].y, z[i].z, z[i].w};
+                if (there[i]) s.add(mk[i], lk[i], c);
+            }
+        }
+        const size_t out = global_row(args, T, h, row);
+        const float f = row_factor(s.l);
+        reinterpret_cast<uint4*>(args.o)[out * (D / 8) + vec] =
+            make_uint4(pack_bf16x2(s.x[0] * f, s.x[1] * f), pack_bf16x2(s.x[2] * f, s.x[3] * f),
+                       pack_bf16x2(s.x[4] * f, s.x[5] * f), pack_bf16x2(s.x[6] * f, s.x[7] * f));
+        if (vec == 0 && args.lse != nullptr) args.lse[out] = row_lse(s.m, s.l);
+    }
+}
+
 // Persistent.  A warp of its own works out the CTA's segments (some hundred instructions each, which
 // took the other roles 1400 to 2000 cycles) and hands them to the others through a ring in shared memory.
 // Every barrier counts its phases across segments: q_* per tile, kv_* per bundle, s_full and p_full per block
@@ -229,6 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<120>();
         if (warp == 3) {
             // ============================================================ segments
+            if (args.cluster > 0) {
+                Segment s;
+                const int size = args.cluster, rank = static_cast<int>(blockIdx.x) % size;
+                const int item = static_cast<int>(blockIdx.x) / size, per = args.H_kv * args.n_pairs;
+                const int batch = item / per;
+                s.len = cross_length(args, batch);
+                const int blocks = cross_blocks(s.len);
+                s.k0 = cluster_run(blocks, rank, size);
+                s.n = cluster_run(blocks, rank + 1, size) - s.k0;
+                place_item(args, s, batch, item - batch * per);
+                if (lane == 0) {
+                    segments[0] = s;
+                    mbar_arrive(smem_u32(&bars.seg_full[0]));
+                    segments[1].n = 0;
+                    mbar_arrive(smem_u32(&bars.seg_full[1]));
+                }
+            } else {
             const Units units(args);
             Walk walk(args, units);
             // An item that this CTA begins and leaves cut, and its last CTA, for the join.
@@ -275,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (an item's place is written by the CTA that begins it, a CTA's by itself)
             if (lane == 0 && args.stream && args.ctas > 1 && (cut.x >= 0 || !args.by_item)) args.cut[cut_at] = cut;
+            }
         } else if (warp == 0) {
             // ============================================================ TMA producer
             if (lane == 0) {
@@ -578,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // first P V (which overwrites O_t) comes after these loads
             const uint32_t col = lane_base + colO, col1 = lane_base + C::kColO + D;
             if (busy && !seg.whole()) {
-                float* part = args.part + (static_cast<int>(blockIdx.x) * 2 + seg.slot()) * part_floats(D, args.part_rows);
+                const int slot = args.cluster > 0 ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * 2 + seg.slot();
+                float* part = args.part + slot * part_floats(D, args.part_rows);
                 const int to = row + (solo ? 0 : t * kPartTile);
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
@@ -619,6 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     tc_fence_before();
+    if (args.cluster > 0) {  // every thread gets here, also from a wait that ran out
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 4) cluster_join<D>(args, static_cast<int>(threadIdx.x) - 128);
+    }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
@@ -635,20 +732,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kTogether = 4;
 template <int GROUPS>
 constexpr int kJoinRows = GROUPS == 1 ? 16 : 8;
-struct JoinState {
-    float m, l, x[8];
-    // this and another state over other keys
-    __device__ __forceinline__ void add(float mk, float lk, const float (&y)[8]) {
-        const float top = fmaxf(m, mk);
-        // of a part whose keys' scores are all -inf nothing; a NaN in l stays
-        const float keep = m == -INFINITY && l == 0.f ? 0.f : ex2_approx(m == top ? 0.f : m - top);
-        const float w = mk == -INFINITY && lk == 0.f ? 0.f : ex2_approx(mk == top ? 0.f : mk - top);
-        m = top;
-        l = fmaf(w, lk, keep * l);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaf(w, y[e], keep * x[e]);
-    }
-};
 template <int D, int GROUPS>
 __global__ void __launch_bounds__(GROUPS == 1 ? 2 * D : GROUPS * D) cross_join_kernel(const CrossArgs args) {
     constexpr int kCols = D / 32, kWarpRows = kJoinRows<GROUPS> / 8;
@@ -760,6 +843,66 @@ cudaError_t join(const CrossArgs& x, int places, cudaStream_t s) {
                       dim3(GROUPS == 1 ? 2 * D : GROUPS * D), 0, s, x);
 }
 
+// Few items take a cluster each, whose CTAs meet at its barrier, which spares the launch of the join (one token
+// of two requests, 32 items on clusters of four, 11.0 -> 10.0 us): the largest clusters of which the device holds
+// as many at once as there are items (36 of four, 15 of eight).  Those leave some SMs out, so not where that costs
+// more blocks a CTA than the join is worth.  Sizes that are no powers of two and those beyond eight were
+// slower than their numbers of blocks say (8 items of 7 blocks: four 8.3 us, seven 9.2, the join's launch 9.0;
+// 1 item of 32: sixteen 13.6, the launch 11.3).  0: none.
+constexpr int kMaxCluster = 8, kJoinBlocks = 3;  // blocks of keys in the time of a join
+template <int D>
+cudaError_t cluster_size(const CrossArgs& a, int dev, int* size) {
+    static std::atomic<int> known[64][kMaxCluster + 1];  // clusters of a size, + 1; 0: not asked
+    *size = 0;
+    const long long items = static_cast<long long>(a.B_kv) * a.H_kv * a.n_pairs;
+    const int blocks = (a.N_kv + kBN - 1) / kBN;
+    if (!a.stream || items * 2 > kMaxCtas || dev >= 64) return cudaSuccess;
+    for (int s = kMaxCluster; s > 1; s /= 2) {
+        if (s > blocks || items * s > kMaxCtas) continue;
+        if ((blocks + s - 1) / s > items * blocks / kMaxCtas + kJoinBlocks) return cudaSuccess;
+        int n = known[dev][s].load();
+        if (n == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(s);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = Cfg<D>::kSmemAlloc;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim = {static_cast<unsigned>(s), 1, 1};
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, cross_fwd_kernel<D>, &cfg) != cudaSuccess) {
+                cudaGetLastError();  // no such cluster: not the caller's error
+                n = 0;
+            }
+            known[dev][s].store(++n);
+        }
+        if (n > items) {
+            *size = s;
+            return cudaSuccess;
+        }
+    }
+    return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch_clusters(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                            const CrossArgs& x, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(x.B_kv * x.H_kv * x.n_pairs * x.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmemAlloc;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(x.cluster), 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, cross_fwd_kernel<D>, tq, tk, tv, to, x);
+}
+
 template <int D>
 int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a, cudaStream_t s) {
     const int BH_kv = a.B_kv * a.H_kv;
@@ -778,6 +921,9 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
     if (e != cudaSuccess) return static_cast<int>(e);
     CrossArgs x = a;
     if (x.ctas > sms) x.ctas = sms;
+    e = cluster_size<D>(a, dev, &x.cluster);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (x.cluster > 0) return static_cast<int>(launch_clusters<D>(tq, tk, tv, to, x, s));
     e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, to, x);
     const int items = x.by_item ? x.B_kv * x.H_kv * x.n_pairs : x.ctas - 1;  // places of cut items
     if (e == cudaSuccess && x.stream && x.ctas > 1)

@@ -155,6 +155,17 @@ def test_forward_of_many_items():
     check_forward(q[:5], k[:5], v[:5], lengths[:5], o[:5], lse[:5], 0.125, batches=range(1, 5))
 
 
+@pytest.mark.parametrize("B,H,N_q,N_kv", [(1, 8, 1, 1000), (1, 15, 130, 1100), (1, 16, 1, 700), (2, 16, 2, 600), (3, 12, 300, 300),
+                                          (1, 40, 1, 400), (1, 76, 1, 256), (1, 77, 1, 256)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_of_few_items(B, H, N_q, N_kv, d):
+    # an item on the CTAs of a cluster, which has more of them than the shortest sequences have blocks
+    q, k, v, _ = inputs(B, B, H, H, N_q, N_kv, d, seed=H)
+    for lengths in ([N_kv] * B, [130, 1, 0][:B], [N_kv // 2 + 3, N_kv - 1, 257][:B]):
+        o, lse = forward(q, k, v, lengths, scale_for(d))
+        check_forward(q, k, v, lengths, o, lse, scale_for(d))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
 @pytest.mark.parametrize("N_q", [1, 200])
 def test_forward_scales(scale, N_q):
