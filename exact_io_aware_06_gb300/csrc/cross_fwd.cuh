@@ -27,9 +27,10 @@ struct CrossArgs {
     float* part;           // two parts a CTA: [d / 4][part_rows][4] O, then m and l of part_rows each
     int R, share, H_kv, B_kv, N_kv;
     int nb, tiles_b, tiles, n_pairs, part_rows;
+    int per;               // items of a batch, H_kv n_pairs
     int stream;            // 0: whole items; 1: equal runs of key blocks, items cut where they end
     int by_item, join_rows;
-    int cluster;           // CTAs of a cluster that share one item, each with its own run of the keys; 0: as `stream`
+    int cluster;           // 2^cluster CTAs share one item, each with its own run of the keys; 0: as `stream`
     int ctas;
     float c_log2;          // scale * log2(e), not 0
     DevCtl ctl;
@@ -54,60 +55,68 @@ __device__ __forceinline__ long long quotient(long long n, long long d) {
 // The key blocks of all items ("units"), item by item, batch by batch, in equal runs for the CTAs.  By a whole
 // warp, 32 batches at a time.
 struct UnitPlace {
-    int b, item, kb;  // K/V batch, item of the batch, key block
+    int b, item, kb, len;  // K/V batch, item of the batch, key block; the batch's keys
 };
 struct Units {
+    int len, upto;          // of batch `lane`: keys; blocks of an item in batches 0 .. lane
     long long total, each;  // every CTA has `each`, the first `more` one more; those behind the last none
     int more;
+    // batches b0 + lane
+    __device__ __forceinline__ void scan(const CrossArgs& a, int b0) {
+        const int lane = threadIdx.x % 32, b = b0 + lane;
+        len = b < a.B_kv ? cross_length(a, b) : 0;
+        upto = b < a.B_kv ? cross_blocks(len) : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += x;
+        }
+    }
     __device__ __forceinline__ explicit Units(const CrossArgs& a) {
-        const long long items = static_cast<long long>(a.H_kv) * a.n_pairs;
+        const long long items = a.per;
         if (!a.lengths) {
             total = items * a.B_kv * cross_blocks(a.N_kv);
         } else {
             long long n = 0;
-            for (int b = threadIdx.x % 32; b < a.B_kv; b += 32) n += cross_blocks(cross_length(a, b));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+            for (int b0 = (a.B_kv - 1) & ~31; b0 >= 0; b0 -= 32) {  // the first 32 last, which place() begins with
+                scan(a, b0);
+                n += __shfl_sync(0xffffffffu, upto, 31);
+            }
             total = n * items;
         }
         each = quotient(total, a.ctas);
         more = static_cast<int>(total - each * a.ctas);
     }
     __device__ __forceinline__ long long first(int cta) const { return each * cta + min(cta, more); }
-};
-__device__ __forceinline__ UnitPlace unit_place(const CrossArgs& a, long long u) {
-    const long long items = static_cast<long long>(a.H_kv) * a.n_pairs;
-    UnitPlace p;
-    int n;
-    if (!a.lengths) {
-        n = cross_blocks(a.N_kv);
-        p.b = static_cast<int>(quotient(u, items * n));
-        u -= p.b * items * n;
-    } else {
-        const int lane = threadIdx.x % 32;
-        for (int b0 = 0;; b0 += 32) {
-            const int mine = b0 + lane < a.B_kv ? cross_blocks(cross_length(a, b0 + lane)) : 0;
-            int upto = mine;  // blocks of batches b0 .. b0 + lane
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += x;
+    __device__ __forceinline__ UnitPlace place(const CrossArgs& a, long long u) {
+        const long long items = a.per;
+        UnitPlace p;
+        int n;
+        if (!a.lengths) {
+            p.len = a.N_kv;
+            n = cross_blocks(p.len);
+            p.b = static_cast<int>(quotient(u, items * n));
+            u -= p.b * items * n;
+        } else {
+            for (int b0 = 0;; scan(a, b0)) {
+                const unsigned behind = __ballot_sync(0xffffffffu, u < upto * items);
+                if (behind || b0 + 32 >= a.B_kv) {
+                    const int l = behind ? __ffs(behind) - 1 : 31;
+                    p.b = b0 + l;
+                    p.len = __shfl_sync(0xffffffffu, len, l);
+                    n = cross_blocks(p.len);
+                    u -= (__shfl_sync(0xffffffffu, upto, l) - n) * items;
+                    break;
+                }
+                u -= __shfl_sync(0xffffffffu, upto, 31) * items;
+                b0 += 32;
             }
-            const unsigned behind = __ballot_sync(0xffffffffu, u < upto * items);
-            if (behind || b0 + 32 >= a.B_kv) {
-                const int l = behind ? __ffs(behind) - 1 : 31;
-                n = max(1, __shfl_sync(0xffffffffu, mine, l));
-                u -= (__shfl_sync(0xffffffffu, upto, l) - __shfl_sync(0xffffffffu, mine, l)) * items;
-                p.b = b0 + l;
-                break;
-            }
-            u -= __shfl_sync(0xffffffffu, upto, 31) * items;
         }
+        p.item = static_cast<int>(quotient(u, n));
+        p.kb = static_cast<int>(u - static_cast<long long>(p.item) * n);
+        return p;
     }
-    p.item = static_cast<int>(quotient(u, n));
-    p.kb = static_cast<int>(u - static_cast<long long>(p.item) * n);
-    return p;
-}
+};
 
 // Where a tile's rows come from: its first batch and, for nb = 1, its first row there; rows in use.
 struct TileRows {
@@ -120,7 +129,7 @@ __device__ __forceinline__ TileRows tile_rows(const CrossArgs& a, int kv_batch, 
         t.rows = min(a.nb, a.share - t.b) * a.R;
         t.r0 = 0;
     } else {
-        t.b = tile / a.tiles_b;
+        t.b = a.share == 1 ? 0 : tile / a.tiles_b;
         t.r0 = (tile - t.b * a.tiles_b) * kBM;
         t.rows = min(kBM, a.R - t.r0);
     }
@@ -135,20 +144,21 @@ __device__ __forceinline__ size_t global_row(const CrossArgs& a, const TileRows&
 
 // A run of key blocks of an item: what the kernel's roles read of it.
 struct __align__(16) Segment {
-    int n;       // its blocks; 0: none follows
+    int n;       // its blocks; 0: nothing to do for this CTA
     int k0;      // the first
     int len;     // the sequence's keys
-    int flags;
+    int flags;   // 1: of one tile; 2: the CTA's last; 4: all blocks of the item
     int bh_kv, h;
     TileRows rows[2];
-    __device__ __forceinline__ bool solo() const { return flags & 1; }        // one tile
-    __device__ __forceinline__ bool whole() const { return flags & 4; }       // all blocks of the item
-    __device__ __forceinline__ int slot() const { return k0 > 0 ? 0 : 1; }    // of the CTA's two parts
+    __device__ __forceinline__ bool solo() const { return flags & 1; }
+    __device__ __forceinline__ bool last() const { return flags & 2; }
+    __device__ __forceinline__ bool whole() const { return flags & 4; }
+    __device__ __forceinline__ int slot() const { return k0 > 0 ? 0 : 1; }  // of the CTA's two parts
 };
 
 // An item's place in a segment.
 __device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int batch, int item) {
-    s.h = item / a.n_pairs;
+    s.h = a.n_pairs == 1 ? item : item / a.n_pairs;
     const int pair = item - s.h * a.n_pairs;
     const bool solo = 2 * pair + 1 >= a.tiles;
     s.bh_kv = batch * a.H_kv + s.h;
@@ -161,48 +171,29 @@ __device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int b
 struct Walk {
     int b, item, kb, blocks, len;
     long long left;
-    __device__ __forceinline__ Walk(const CrossArgs& a, const Units& units) {
+    __device__ __forceinline__ Walk(const CrossArgs& a, Units& units) {
         const long long u = units.first(blockIdx.x);
-        left = a.stream ? units.first(blockIdx.x + 1) - u : 0;  // blocks, or rounds
+        left = units.first(blockIdx.x + 1) - u;
         if (left > 0) {
-            const UnitPlace p = unit_place(a, u);
-            b = p.b, item = p.item, kb = p.kb;
-            len = cross_length(a, b);
+            const UnitPlace p = units.place(a, u);
+            b = p.b, item = p.item, kb = p.kb, len = p.len;
             blocks = cross_blocks(len);
         }
     }
-    // Whether there is one more; `at` its item of the batch, `behind` the item's blocks after it.
-    __device__ __forceinline__ bool next(const CrossArgs& a, Segment& s, int& batch, int& at, int& behind) {
-        const int per = a.H_kv * a.n_pairs;
-        s.n = 0;
-        if (a.stream) {
-            if (left <= 0) return false;
-            batch = b, at = item, s.k0 = kb, s.len = len;
-            s.n = static_cast<int>(left < blocks - kb ? left : blocks - kb);
-            behind = blocks - kb - s.n;
-            left -= s.n;
-            kb = 0;
-            if (++item == per && left > 0) {
-                item = 0;
-                len = cross_length(a, ++b);
-                blocks = cross_blocks(len);
-            }
-        } else {
-            // whole items in alternating order
-            const long long G = gridDim.x;
-            const long long x = left * G + ((left & 1) ? G - 1 - blockIdx.x : blockIdx.x);
-            if (x >= static_cast<long long>(a.B_kv) * per) return false;
-            ++left;
-            batch = static_cast<int>(quotient(x, per));
-            at = static_cast<int>(x - static_cast<long long>(batch) * per);
-            s.len = cross_length(a, batch);
-            s.k0 = 0;
-            s.n = cross_blocks(s.len);
-            behind = 0;
+    // The next one; `batch` and `at`, its item of the batch; the item's blocks `behind` it.
+    __device__ __forceinline__ void next(const CrossArgs& a, Segment& s, int& batch, int& at, int& behind) {
+        batch = b, at = item, s.k0 = kb, s.len = len;
+        s.n = static_cast<int>(left < blocks - kb ? left : blocks - kb);
+        behind = blocks - kb - s.n;
+        left -= s.n;
+        kb = 0;
+        if (++item == a.per && left > 0) {
+            item = 0;
+            len = cross_length(a, ++b);
+            blocks = cross_blocks(len);
         }
         place_item(a, s, batch, at);
-        if (s.k0 == 0 && behind == 0) s.flags |= 4;
-        return true;
+        s.flags |= (left <= 0 ? 2 : 0) | (s.k0 == 0 && behind == 0 ? 4 : 0);
     }
 };
 

@@ -4,7 +4,21 @@
 //     O = softmax(scale Q K^T over the keys j < len_b) V,  lse = m + ln l,
 // by the online softmax of the plain forward (fwd_sm103.cu): a running reference maximum, sum and
 // unnormalised output a row, lazily rescaled.  Optionally merged with (o_own, lse_own), the same queries'
-// attention to other keys: lse = ln(e^lse + e^lse_own), O weighted by e^(lse_x - lse).
+// attention to other keys: lse = ln(e^lse + e^lse_own), O weighted by e^(lse_x - lse).  That state is the one that
+// the rows begin with (m = lse_own log2 e, l = 1, O = o_own), which costs a load of o_own and no pass of its own.
+//
+// What bounds it, and the split taken for it:
+//   * Many rows on many keys: the tensor pipe.  Two query tiles a CTA in ping-pong share every K and V block, as
+//     in the plain forward: 3,050 cycles for a pair of blocks at d = 128 (2,048 of the pipe), 1,640 TFLOP/s at
+//     16 x 16384 x 16384.
+//   * Many rows on few keys (2 x 16384 video tokens on 77 to 512): an item's end, 3,800 cycles of its softmax
+//     warpgroups (O's last product, its way out, the next scores), beside 6,000 for four blocks.  O leaves in boxes
+//     by TMA, so that the warps go on while it is stored: 101 -> 95 us, floor 42.
+//   * Few rows on many keys: HBM, at the rate that 152 SMs can have loads in flight.  The key blocks of all items
+//     are cut into equal runs (64 ragged single tokens: 185 us, 91% of the copy rate), whose float32 parts a
+//     join adds up in a fixed order.
+//   * Few rows on few keys: latency, of which the join's launch is the largest piece that can be spared: clusters
+//     (one token of 16 heads on 1500 keys: 9.6 us, 10.7 with the join).
 #include <type_traits>
 
 #include "cross_fwd.cuh"
@@ -77,7 +91,7 @@ template <int D>
 __device__ __forceinline__ void store_weighted(uint32_t first, float w0, uint32_t second, float w1, bool two, void* o,
                                                long long at) {
     const int lane = threadIdx.x % 32, q = lane % 4;
-#pragma unroll
+#pragma unroll 1  // a warp comes here once or twice: fetching instructions is what takes its time
     for (int m = 0; m < 2; ++m) {
         float f0[2], f1[2];
         long long to[2];
@@ -88,7 +102,7 @@ __device__ __forceinline__ void store_weighted(uint32_t first, float w0, uint32_
             f1[h] = two ? __shfl_sync(0xffffffffu, w1, from) : 0.f;
             to[h] = __shfl_sync(0xffffffffu, at, from);
         }
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
             const uint32_t part = (static_cast<uint32_t>(16 * m) << 16) + 64 * c;
             uint32_t x[32], w[2][8];
@@ -173,9 +187,7 @@ struct JoinState {
     }
 };
 // Blocks of an item's run for CTA r of its cluster: up to this.
-__device__ __forceinline__ int cluster_run(int blocks, int r, int size) {
-    return static_cast<int>(static_cast<long long>(blocks) * r / size);
-}
+__device__ __forceinline__ int cluster_run(int blocks, int r, int log2_size) { return blocks * r >> log2_size; }
 __device__ __forceinline__ void cluster_sync() {  // what any thread of the cluster wrote before is visible after
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -184,8 +196,8 @@ __device__ __forceinline__ void cluster_sync() {  // what any thread of the clus
 // eight columns of a row a thread, four parts' loads in flight.
 template <int D>
 __device__ __forceinline__ void cluster_join(const CrossArgs& args, int t) {
-    const int size = args.cluster, rank = static_cast<int>(blockIdx.x) % size, item = static_cast<int>(blockIdx.x) / size;
-    const int per = args.H_kv * args.n_pairs, batch = item / per, at_item = item - batch * per;
+    const int size = 1 << args.cluster, rank = static_cast<int>(blockIdx.x) & (size - 1);
+    const int item = static_cast<int>(blockIdx.x) >> args.cluster, batch = item / args.per, at_item = item - batch * args.per;
     const int h = at_item / args.n_pairs, pair = at_item - h * args.n_pairs;
     const int blocks = cross_blocks(cross_length(args, batch));
     const int share = (args.join_rows + size - 1) / size;
@@ -208,7 +220,7 @@ __device__ __forceinline__ void cluster_join(const CrossArgs& args, int t) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = r0 + i;
-                there[i] = r < size && cluster_run(blocks, r, size) < cluster_run(blocks, r + 1, size);
+                there[i] = r < size && cluster_run(blocks, r, args.cluster) < cluster_run(blocks, r + 1, args.cluster);
                 const float* src = args.part + static_cast<size_t>(item * size + (there[i] ? r : 0)) * size_floats;
                 mk[i] = __ldcg(src + ml);
                 lk[i] = __ldcg(src + ml + args.part_rows);
@@ -302,69 +314,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<120>();
         if (warp == 3) {
             // ============================================================ segments
-            if (args.cluster > 0) {
-                Segment s;
-                const int size = args.cluster, rank = static_cast<int>(blockIdx.x) % size;
-                const int item = static_cast<int>(blockIdx.x) / size, per = args.H_kv * args.n_pairs;
-                const int batch = item / per;
-                s.len = cross_length(args, batch);
-                const int blocks = cross_blocks(s.len);
-                s.k0 = cluster_run(blocks, rank, size);
-                s.n = cluster_run(blocks, rank + 1, size) - s.k0;
-                place_item(args, s, batch, item - batch * per);
-                if (lane == 0) {
-                    segments[0] = s;
-                    mbar_arrive(smem_u32(&bars.seg_full[0]));
-                    segments[1].n = 0;
-                    mbar_arrive(smem_u32(&bars.seg_full[1]));
-                }
-            } else {
-            const Units units(args);
-            Walk walk(args, units);
-            // An item that this CTA begins and leaves cut, and its last CTA, for the join.
-            int4 cut = make_int4(-1, 0, 0, static_cast<int>(blockIdx.x));
-            int cut_at = static_cast<int>(blockIdx.x), behind_it = 0;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                Segment s;
-                int batch, item, behind;
-                const bool more = walk.next(args, s, batch, item, behind);
+            // Hands over the i-th; waits until the ring has room for it.
+            auto publish = [&](int i, const Segment& s) -> bool {
                 const int u = i % kSegments;
                 if (i >= kSegments) {
-                    ok = mbar_wait(smem_u32(&bars.seg_empty[u]), ((i / kSegments) & 1) ^ 1, lim, &abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    const bool free = mbar_wait(smem_u32(&bars.seg_empty[u]), ((i / kSegments) & 1) ^ 1, lim, &abort_flag);
+                    if (!__all_sync(0xffffffffu, free)) {
+                        if (lane == 0) record_timeout(args.ctl, &abort_flag);
+                        return false;
+                    }
                 }
                 if (lane == 0) {
                     segments[u] = s;
                     mbar_arrive(smem_u32(&bars.seg_full[u]));
                 }
-                if (!more) break;
-                if (s.k0 > 0 || !args.stream || args.ctas == 1) continue;
-                const int place = batch * args.H_kv * args.n_pairs + item;
-                if (behind > 0) {
-                    cut = make_int4(0, batch, item, cut.w);
-                    behind_it = behind;
-                    if (args.by_item) cut_at = place;
-                } else if (args.by_item && lane == 0) {
-                    args.cut[place] = make_int4(-1, 0, 0, 0);
+                return true;
+            };
+            Segment s;
+            if (args.cluster > 0) {
+                const int rank = static_cast<int>(blockIdx.x) & ((1 << args.cluster) - 1);
+                const int item = static_cast<int>(blockIdx.x) >> args.cluster, batch = item / args.per;
+                s.len = cross_length(args, batch);
+                const int blocks = cross_blocks(s.len);
+                s.k0 = cluster_run(blocks, rank, args.cluster);
+                s.n = cluster_run(blocks, rank + 1, args.cluster) - s.k0;
+                place_item(args, s, batch, item - batch * args.per);
+                s.flags |= 2;
+                publish(0, s);
+            } else if (!args.stream) {
+                // whole items in alternating order
+                const long long G = gridDim.x, all = static_cast<long long>(args.B_kv) * args.per;
+                auto item_of = [&](long long i) { return i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x); };
+                long long x = item_of(0);
+                for (int i = 0;; ++i) {
+                    const int batch = static_cast<int>(quotient(x, args.per));
+                    s.len = cross_length(args, batch);
+                    s.k0 = 0;
+                    s.n = cross_blocks(s.len);
+                    place_item(args, s, batch, static_cast<int>(x - static_cast<long long>(batch) * args.per));
+                    x = item_of(i + 1);
+                    s.flags |= 4 | (x >= all ? 2 : 0);
+                    if (!publish(i, s) || s.last()) break;
                 }
-            }
-            if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
-            if (cut.x == 0) {
-                const long long end = units.first(blockIdx.x + 1) + behind_it;  // behind the item's last unit
-                cut.x = static_cast<int>(blockIdx.x);
-                for (;; cut.x += 32) {
-                    const int cta = cut.x + 1 + lane;
-                    const unsigned in = __ballot_sync(0xffffffffu, cta < args.ctas && units.first(cta) < end);
-                    if (in != 0xffffffffu) {
-                        cut.x += __popc(in);
-                        break;
+            } else {
+                Units units(args);
+                Walk walk(args, units);
+                // An item that this CTA begins and leaves cut, and its last CTA, for the join.
+                int4 cut = make_int4(-1, 0, 0, static_cast<int>(blockIdx.x));
+                int cut_at = static_cast<int>(blockIdx.x), behind_it = 0;
+                if (walk.left <= 0) {
+                    s.n = 0;
+                    s.flags = 2;
+                    publish(0, s);
+                }
+                for (int i = 0; walk.left > 0; ++i) {
+                    int batch, item, behind;
+                    walk.next(args, s, batch, item, behind);
+                    if (!publish(i, s)) break;
+                    if (s.k0 > 0 || args.ctas == 1) continue;
+                    const int place = batch * args.per + item;
+                    if (behind > 0) {
+                        cut = make_int4(0, batch, item, cut.w);
+                        behind_it = behind;
+                        if (args.by_item) cut_at = place;
+                    } else if (args.by_item && lane == 0) {
+                        args.cut[place] = make_int4(-1, 0, 0, 0);
                     }
                 }
-            }
-            // (an item's place is written by the CTA that begins it, a CTA's by itself)
-            if (lane == 0 && args.stream && args.ctas > 1 && (cut.x >= 0 || !args.by_item)) args.cut[cut_at] = cut;
+                if (cut.x == 0) {
+                    const long long end = units.first(blockIdx.x + 1) + behind_it;  // behind the item's last unit
+                    cut.x = static_cast<int>(blockIdx.x);
+                    for (;; cut.x += 32) {
+                        const int cta = cut.x + 1 + lane;
+                        const unsigned in = __ballot_sync(0xffffffffu, cta < args.ctas && units.first(cta) < end);
+                        if (in != 0xffffffffu) {
+                            cut.x += __popc(in);
+                            break;
+                        }
+                    }
+                }
+                // (an item's place is written by the CTA that begins it, a CTA's by itself)
+                if (lane == 0 && args.ctas > 1 && (cut.x >= 0 || !args.by_item)) args.cut[cut_at] = cut;
             }
         } else if (warp == 0) {
             // ============================================================ TMA producer
@@ -411,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             (s.k0 + n - 1) * kBN, s.bh_kv);
                         if (n == 0 && !s.solo()) ok = load_q(1);
                     }
+                    if (s.last()) break;
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
                 // the newest load of every slot has landed before exit
@@ -485,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = segment_there(x);
                     if (!ok) break;
                     const int n = segments[x % kSegments].n;
-                    const bool solo = segments[x % kSegments].solo();
+                    const bool solo = segments[x % kSegments].solo(), last = segments[x % kSegments].last();
                     begun = args.o_own != nullptr && segments[x % kSegments].k0 == 0;
                     segment_taken(x);
                     if (n == 0) break;
@@ -534,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         c1 += n;
                     }
                     gb += n + 1;
+                    if (last) break;
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
                 mma_commit(smem_u32(&bars.drain));
@@ -650,8 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     ++ns;
                     if (!ok) break;
+                    const bool last = seg.last();
                     __syncwarp();
                     if (lane == 0) segment_taken(x);
+                    if (last) break;
                     continue;
                 }
                 ok = mbar_wait(smem_u32(&bars.merge_ml), ns & 1, lim, &abort_flag);
@@ -702,8 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.merge_done));
             }
+            const bool last = seg.last();
             __syncwarp();
             if (lane == 0) segment_taken(x);
+            if (last) break;
         }
         if (!ok && lane == 0) record_timeout(args.ctl, &abort_flag);
         // the stores complete before the CTA's shared memory goes away
@@ -804,9 +840,10 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     a.tiles_b = (a.R + kBM - 1) / kBM;
     a.tiles = a.nb > 1 ? (a.share + a.nb - 1) / a.nb : a.share * a.tiles_b;
     a.n_pairs = (a.tiles + 1) / 2;
+    a.per = H_kv * a.n_pairs;
     const int rows = a.nb > 1 ? a.nb * a.R : a.R;  // of a lone tile
     a.part_rows = a.tiles > 1 ? 2 * kBM : round_up(rows < kBM ? rows : kBM, 32);
-    const long long items = static_cast<long long>(B_kv) * H_kv * a.n_pairs;
+    const long long items = static_cast<long long>(B_kv) * a.per;
     a.join_rows = a.tiles > 1 ? 2 * kBM : rows < kBM ? rows : kBM;
     a.stream = items < 8 * kMaxCtas && N_kv > kBN;  // an item of one block cannot be cut
     a.by_item = items < kMaxCtas;
@@ -851,10 +888,10 @@ cudaError_t join(const CrossArgs& x, int places, cudaStream_t s) {
 // 1 item of 32: sixteen 13.6, the launch 11.3).  0: none.
 constexpr int kMaxCluster = 8, kJoinBlocks = 3;  // blocks of keys in the time of a join
 template <int D>
-cudaError_t cluster_size(const CrossArgs& a, int dev, int* size) {
+cudaError_t cluster_size(const CrossArgs& a, int dev, int* log2_size) {
     static std::atomic<int> known[64][kMaxCluster + 1];  // clusters of a size, + 1; 0: not asked
-    *size = 0;
-    const long long items = static_cast<long long>(a.B_kv) * a.H_kv * a.n_pairs;
+    *log2_size = 0;
+    const long long items = static_cast<long long>(a.B_kv) * a.per;
     const int blocks = (a.N_kv + kBN - 1) / kBN;
     if (!a.stream || items * 2 > kMaxCtas || dev >= 64) return cudaSuccess;
     for (int s = kMaxCluster; s > 1; s /= 2) {
@@ -878,7 +915,7 @@ cudaError_t cluster_size(const CrossArgs& a, int dev, int* size) {
             known[dev][s].store(++n);
         }
         if (n > items) {
-            *size = s;
+            *log2_size = s == 8 ? 3 : s / 2;
             return cudaSuccess;
         }
     }
@@ -889,13 +926,13 @@ template <int D>
 cudaError_t launch_clusters(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                             const CrossArgs& x, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(x.B_kv * x.H_kv * x.n_pairs * x.cluster);
+    cfg.gridDim = dim3(x.B_kv * x.per << x.cluster);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Cfg<D>::kSmemAlloc;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {static_cast<unsigned>(x.cluster), 1, 1};
+    attr[0].val.clusterDim = {1u << x.cluster, 1, 1};
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
@@ -925,7 +962,7 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
     if (e != cudaSuccess) return static_cast<int>(e);
     if (x.cluster > 0) return static_cast<int>(launch_clusters<D>(tq, tk, tv, to, x, s));
     e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, to, x);
-    const int items = x.by_item ? x.B_kv * x.H_kv * x.n_pairs : x.ctas - 1;  // places of cut items
+    const int items = x.by_item ? x.B_kv * x.per : x.ctas - 1;  // places of cut items
     if (e == cudaSuccess && x.stream && x.ctas > 1)
         e = x.ctas >= 6 * items ? join<D, 4>(x, items, s) : join<D, 1>(x, items, s);
     return static_cast<int>(e);
