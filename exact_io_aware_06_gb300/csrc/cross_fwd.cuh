@@ -46,21 +46,15 @@ __device__ __forceinline__ int cross_length(const CrossArgs& a, int b) {
 // A sequence without keys has one block, all of it hidden: its rows get O = 0, lse = -inf from it.
 __device__ __forceinline__ int cross_blocks(int len) { return len > 0 ? (len + kBN - 1) / kBN : 1; }
 
-// n / d; 64-bit division takes some hundred cycles, a 32-bit one a quarter.
-__device__ __forceinline__ long long quotient(long long n, long long d) {
-    if ((n | d) >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
-    return n / d;
-}
-
 // The key blocks of all items ("units"), item by item, batch by batch, in equal runs for the CTAs.  By a whole
-// warp, 32 batches at a time.
+// warp, 32 batches at a time.  Work of fewer than 8 * 152 items of up to 2^17 blocks is dealt so: 32 bits hold all
+// of their units.
 struct UnitPlace {
     int b, item, kb, len;  // K/V batch, item of the batch, key block; the batch's keys
 };
 struct Units {
-    int len, upto;          // of batch `lane`: keys; blocks of an item in batches 0 .. lane
-    long long total, each;  // every CTA has `each`, the first `more` one more; those behind the last none
-    int more;
+    int len, upto;         // of batch `lane`: keys; blocks of an item in batches 0 .. lane
+    int each, more;        // every CTA has `each`, the first `more` one more
     // batches b0 + lane
     __device__ __forceinline__ void scan(const CrossArgs& a, int b0) {
         const int lane = threadIdx.x % 32, b = b0 + lane;
@@ -73,47 +67,45 @@ struct Units {
         }
     }
     __device__ __forceinline__ explicit Units(const CrossArgs& a) {
-        const long long items = a.per;
+        uint32_t total = 0;
         if (!a.lengths) {
-            total = items * a.B_kv * cross_blocks(a.N_kv);
+            total = a.B_kv * cross_blocks(a.N_kv);
         } else {
-            long long n = 0;
             for (int b0 = (a.B_kv - 1) & ~31; b0 >= 0; b0 -= 32) {  // the first 32 last, which place() begins with
                 scan(a, b0);
-                n += __shfl_sync(0xffffffffu, upto, 31);
+                total += __shfl_sync(0xffffffffu, upto, 31);
             }
-            total = n * items;
         }
-        each = quotient(total, a.ctas);
-        more = static_cast<int>(total - each * a.ctas);
+        total *= a.per;
+        each = total / static_cast<uint32_t>(a.ctas);
+        more = total - each * a.ctas;
     }
-    __device__ __forceinline__ long long first(int cta) const { return each * cta + min(cta, more); }
-    __device__ __forceinline__ UnitPlace place(const CrossArgs& a, long long u) {
-        const long long items = a.per;
+    __device__ __forceinline__ int first(int cta) const { return each * cta + min(cta, more); }
+    __device__ __forceinline__ UnitPlace place(const CrossArgs& a, uint32_t u) {
         UnitPlace p;
-        int n;
+        uint32_t n;
         if (!a.lengths) {
             p.len = a.N_kv;
             n = cross_blocks(p.len);
-            p.b = static_cast<int>(quotient(u, items * n));
-            u -= p.b * items * n;
+            p.b = u / (a.per * n);
+            u -= p.b * a.per * n;
         } else {
             for (int b0 = 0;; scan(a, b0)) {
-                const unsigned behind = __ballot_sync(0xffffffffu, u < upto * items);
+                const unsigned behind = __ballot_sync(0xffffffffu, u < static_cast<uint32_t>(upto * a.per));
                 if (behind || b0 + 32 >= a.B_kv) {
                     const int l = behind ? __ffs(behind) - 1 : 31;
                     p.b = b0 + l;
                     p.len = __shfl_sync(0xffffffffu, len, l);
                     n = cross_blocks(p.len);
-                    u -= (__shfl_sync(0xffffffffu, upto, l) - n) * items;
+                    u -= (__shfl_sync(0xffffffffu, upto, l) - n) * a.per;
                     break;
                 }
-                u -= __shfl_sync(0xffffffffu, upto, 31) * items;
+                u -= __shfl_sync(0xffffffffu, upto, 31) * a.per;
                 b0 += 32;
             }
         }
-        p.item = static_cast<int>(quotient(u, n));
-        p.kb = static_cast<int>(u - static_cast<long long>(p.item) * n);
+        p.item = u / n;
+        p.kb = u - p.item * n;
         return p;
     }
 };
@@ -129,7 +121,7 @@ __device__ __forceinline__ TileRows tile_rows(const CrossArgs& a, int kv_batch, 
         t.rows = min(a.nb, a.share - t.b) * a.R;
         t.r0 = 0;
     } else {
-        t.b = a.share == 1 ? 0 : tile / a.tiles_b;
+        t.b = a.share == 1 ? 0 : static_cast<uint32_t>(tile) / static_cast<uint32_t>(a.tiles_b);
         t.r0 = (tile - t.b * a.tiles_b) * kBM;
         t.rows = min(kBM, a.R - t.r0);
     }
@@ -158,7 +150,7 @@ struct __align__(16) Segment {
 
 // An item's place in a segment.
 __device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int batch, int item) {
-    s.h = a.n_pairs == 1 ? item : item / a.n_pairs;
+    s.h = a.n_pairs == 1 ? item : static_cast<uint32_t>(item) / static_cast<uint32_t>(a.n_pairs);
     const int pair = item - s.h * a.n_pairs;
     const bool solo = 2 * pair + 1 >= a.tiles;
     s.bh_kv = batch * a.H_kv + s.h;
@@ -169,10 +161,9 @@ __device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int b
 
 // This CTA's segments, one after the other.
 struct Walk {
-    int b, item, kb, blocks, len;
-    long long left;
+    int b, item, kb, blocks, len, left;
     __device__ __forceinline__ Walk(const CrossArgs& a, Units& units) {
-        const long long u = units.first(blockIdx.x);
+        const int u = units.first(blockIdx.x);
         left = units.first(blockIdx.x + 1) - u;
         if (left > 0) {
             const UnitPlace p = units.place(a, u);
@@ -183,7 +174,7 @@ struct Walk {
     // The next one; `batch` and `at`, its item of the batch; the item's blocks `behind` it.
     __device__ __forceinline__ void next(const CrossArgs& a, Segment& s, int& batch, int& at, int& behind) {
         batch = b, at = item, s.k0 = kb, s.len = len;
-        s.n = static_cast<int>(left < blocks - kb ? left : blocks - kb);
+        s.n = min(left, blocks - kb);
         behind = blocks - kb - s.n;
         left -= s.n;
         kb = 0;

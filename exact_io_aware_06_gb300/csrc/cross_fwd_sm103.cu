@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             Segment s;
             if (args.cluster > 0) {
                 const int rank = static_cast<int>(blockIdx.x) & ((1 << args.cluster) - 1);
-                const int item = static_cast<int>(blockIdx.x) >> args.cluster, batch = item / args.per;
+                const int item = static_cast<int>(blockIdx.x) >> args.cluster;
+                const int batch = args.B_kv == 1 ? 0 : static_cast<uint32_t>(item) / static_cast<uint32_t>(args.per);
                 s.len = cross_length(args, batch);
                 const int blocks = cross_blocks(s.len);
                 s.k0 = cluster_run(blocks, rank, args.cluster);
@@ -343,15 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 publish(0, s);
             } else if (!args.stream) {
                 // whole items in alternating order
-                const long long G = gridDim.x, all = static_cast<long long>(args.B_kv) * args.per;
-                auto item_of = [&](long long i) { return i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x); };
-                long long x = item_of(0);
+                const uint32_t G = gridDim.x, per = args.per, all = args.B_kv * per;  // (up to 2^30 + 2^24)
+                auto item_of = [&](uint32_t i) { return i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x); };
+                uint32_t x = item_of(0);
                 for (int i = 0;; ++i) {
-                    const int batch = static_cast<int>(quotient(x, args.per));
+                    const int batch = x / per;
                     s.len = cross_length(args, batch);
                     s.k0 = 0;
                     s.n = cross_blocks(s.len);
-                    place_item(args, s, batch, static_cast<int>(x - static_cast<long long>(batch) * args.per));
+                    place_item(args, s, batch, x - batch * per);
                     x = item_of(i + 1);
                     s.flags |= 4 | (x >= all ? 2 : 0);
                     if (!publish(i, s) || s.last()) break;
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (cut.x == 0) {
-                    const long long end = units.first(blockIdx.x + 1) + behind_it;  // behind the item's last unit
+                    const int end = units.first(blockIdx.x + 1) + behind_it;  // behind the item's last unit
                     cut.x = static_cast<int>(blockIdx.x);
                     for (;; cut.x += 32) {
                         const int cta = cut.x + 1 + lane;
