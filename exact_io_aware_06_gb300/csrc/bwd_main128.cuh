@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    griddep_wait();               // delta and lse come from the kernel before this one
+    griddep_launch_dependents();  // and so may a kernel that needs nothing else start
 
     if (warp == 0) {
         // ================================================================ Q / dO producer

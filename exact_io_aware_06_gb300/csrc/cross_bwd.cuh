@@ -78,6 +78,6 @@ cudaError_t launch_bwd_cross_main64(const CUtensorMap& q, const CUtensorMap& k, 
                                     cudaStream_t s);
 // dQ of all `heads` = B * H_kv heads of R rows.
 int launch_bwd_cross_dq(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a, int d,
-                        cudaStream_t s);
+                        int main_ctas, cudaStream_t s);
 
 }  // namespace fa

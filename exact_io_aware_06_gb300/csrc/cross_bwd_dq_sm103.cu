@@ -32,13 +32,17 @@ static __device__ __forceinline__ bool hidden_rows(const CrossBwdArgs& a, const 
     r1 = min(kBlk, a.N_kv - block * kBlk);
     return r0 < r1;
 }
+// This kernel starts when every CTA of the dK/dV kernel has seen the rows' values ready; it needs nothing of that
+// kernel, but what comes after it may.
 template <int D>
-static __device__ __forceinline__ void idle_warp(const CrossBwdArgs&, std::integral_constant<int, D>, int, int) {}
+static __device__ __forceinline__ void idle_warp(const CrossBwdArgs&, std::integral_constant<int, D>, int, int) {
+    griddep_wait();
+}
 
 namespace {
 
 template <int D>
-int launch_impl(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a,
+int launch_impl(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a, int main_ctas,
                 cudaStream_t s) {
     const int heads = a.BH_kv * a.share, n_items = heads * a.n_q;
     CUtensorMap tq, tk, tv, tdo;
@@ -54,16 +58,19 @@ int launch_impl(const void* q, const void* k, const void* v, const void* dO, voi
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return static_cast<int>(e);
-    bwd_dq_kernel<D, CrossBwdArgs>
-        <<<n_items < sms ? n_items : sms, kThreads, Cfg<D>::kSmemAlloc, s>>>(tq, tk, tv, tdo, a, dq, n_items);
+    const int grid = n_items < sms ? n_items : sms;
+    if (main_ctas + grid <= sms)
+        return static_cast<int>(launch_pdl(bwd_dq_kernel<D, CrossBwdArgs>, dim3(grid), dim3(kThreads), Cfg<D>::kSmemAlloc, s,
+                                           tq, tk, tv, tdo, a, dq, n_items));
+    bwd_dq_kernel<D, CrossBwdArgs><<<grid, kThreads, Cfg<D>::kSmemAlloc, s>>>(tq, tk, tv, tdo, a, dq, n_items);
     return static_cast<int>(cudaGetLastError());
 }
 
 }  // namespace
 
 int launch_bwd_cross_dq(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a, int d,
-                        cudaStream_t s) {
-    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, s) : launch_impl<128>(q, k, v, dO, dq, a, s);
+                        int main_ctas, cudaStream_t s) {
+    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, main_ctas, s) : launch_impl<128>(q, k, v, dO, dq, a, main_ctas, s);
 }
 
 }  // namespace fa

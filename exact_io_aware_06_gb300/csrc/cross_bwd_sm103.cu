@@ -236,14 +236,13 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
         static std::atomic<uint64_t> smem_done;
         e = allow_smem(bwd_main_kernel<CrossBwdArgs>, kSmemAlloc, smem_done);
         if (e != cudaSuccess) return static_cast<int>(e);
-        bwd_main_kernel<CrossBwdArgs><<<grid, kThreads, kSmemAlloc, s>>>(tq, tk, tv, tdo, a);
-        e = cudaGetLastError();
+        e = launch_pdl(bwd_main_kernel<CrossBwdArgs>, dim3(grid), dim3(kThreads), kSmemAlloc, s, tq, tk, tv, tdo, a);
     }
-    if (e == cudaSuccess && a.pieces > 1)
-        e = launch_pdl(d == 64 ? cross_bwd_join_kernel<64> : cross_bwd_join_kernel<128>,
-                       dim3(a.BH_kv * a.n_k, 2 * kJoinSplit), dim3(256), 0, s, a);
     if (e != cudaSuccess) return static_cast<int>(e);
-    return launch_bwd_cross_dq(q, k, v, dO, dq, a, d, s);
+    rc = launch_bwd_cross_dq(q, k, v, dO, dq, a, d, grid, s);
+    if (rc != 0 || a.pieces == 1) return rc;
+    return static_cast<int>(launch_pdl(d == 64 ? cross_bwd_join_kernel<64> : cross_bwd_join_kernel<128>,
+                                       dim3(a.BH_kv * a.n_k, 2 * kJoinSplit), dim3(256), 0, s, a));
 }
 
 }  // namespace fa
