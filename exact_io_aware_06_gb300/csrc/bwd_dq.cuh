@@ -21,7 +21,8 @@
 //
 // For an argument type A the overloads are, besides those of bwd_tile.cuh,
 //     q_item_at(a, x)      an item: heads bh and bh_kv of Q's and K's tensors, query block qb, its n_kv key blocks
-//                          block(j), and shorty: the first is that of up to 32 sinks
+//                          block(j), shorty: the first is that of up to 32 sinks; with kParts it may have none, and
+//                          part is the place of its float32 part of dQ in a.part_q, or -1 if it is all there is
 //     key_range(a, I, row, key0, ..)   the keys, counted from key0, that a query row sees
 //     hidden_rows(a, I, block, ..)     rows of a key block that hold no key but perhaps something else
 //     idle_warp(a, d, t, n)   what warp 3 of every CTA does, thread t of n
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const Args args, void* const dq, const int n_items) {
     using C = Cfg<D>;
     constexpr int kTile = C::kTile, kOffQ = C::kOffQ, kOffDO = C::kOffDO, kOffK = C::kOffK, kOffV = C::kOffV;
+    constexpr bool kParts = decltype(q_item_at(args, 0))::kParts;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) DqBars bars;
     __shared__ uint32_t tmem_slot;
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                     const auto I = q_item_at(args, x);
+                    if (kParts && I.n_kv == 0) continue;
                     if (n > 0 && !mbar_wait(smem_u32(&bars.q_free), (n - 1) & 1, lim, &abort_flag)) {
                         ok = false;
                         break;
@@ -212,10 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 int g = 0, item = 0;
                 bool ok = true;
-                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k), ++item) {
+                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                     const auto I = q_item_at(args, x);
                     for (int j = 0; j < I.n_kv && ok; ++j, ++g)
                         ok = issue_sp(g, item, j == 0, j + 1 == I.n_kv, I.shorty && j == 0 ? kIdescShort : kIdescSS);
+                    item += kParts && I.n_kv == 0 ? 0 : 1;
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
                 mma_commit(smem_u32(&bars.drain));
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t k_mn = sdesc_sw128_lo(sb + kOffK, 16384);
                 int g = 0, item = 0;
                 bool ok = true;
-                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k), ++item) {
+                for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
                     const auto I = q_item_at(args, x);
                     for (int j = 0; j < I.n_kv; ++j, ++g) {
                         const int sk = g % kKStages;
@@ -255,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_commit(smem_u32(&bars.k_empty[sk]));  // S of this pair read K before dS was made
                         if (j + 1 == I.n_kv) mma_commit(smem_u32(&bars.all_done));
                     }
+                    item += kParts && I.n_kv == 0 ? 0 : 1;
                 }
                 if (!ok) record_timeout(args.ctl, &abort_flag);
                 mma_commit(smem_u32(&bars.drain2));
@@ -401,12 +406,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         bool ok = true;
         int item = 0;
-        for (int k = 0, x = item_x(0); x < n_items; x = item_x(++k), ++item) {
+        for (int k = 0, x = item_x(0); x < n_items; x = item_x(++k)) {
             const auto I = q_item_at(args, x);
-            ok = mbar_wait(smem_u32(&bars.all_done), item & 1, lim, &abort_flag);
+            if (kParts && I.n_kv == 0) continue;
+            ok = mbar_wait(smem_u32(&bars.all_done), item++ & 1, lim, &abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
+            if constexpr (kParts) {
+                if (I.part >= 0) {
+                    const int row = wq * 32 + lane;
+                    write_part_row<D>(args.part_q, I.part, row, I.qb * kBlk + row < N, lb + kColDQ);
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&bars.dq_read));
+                    continue;
+                }
+            }
             RowsOut<D> rows;
             rows.load(lb + kColDQ, args.scale);
             tc_fence_before();

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t col = half ? kColDK : kColDV;
             if (I.slot >= 0) {
-                write_part_row<kD>(args.part, part_of(args, I), half, key_in_blk, lb + col);
+                write_part_row<kD>(args.part, 2 * part_of(args, I) + half, key_in_blk, key < N, lb + col);
             } else {
                 RowsOut<kD> rows;
                 rows.load(lb + col, half ? args.scale : 1.0f);

@@ -385,8 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++kc;
             tc_fence_after();
             if (I.slot >= 0) {
-                write_part_row<kD>(args.part, part_of(args, I), 0, wq * 32 + lane, lb + kColDV);
-                write_part_row<kD>(args.part, part_of(args, I), 1, wq * 32 + lane, lb + kColDK);
+                const int row = wq * 32 + lane;
+                const bool there = I.kvb * kBlk + row < N;
+                write_part_row<kD>(args.part, 2 * part_of(args, I), row, there, lb + kColDV);
+                write_part_row<kD>(args.part, 2 * part_of(args, I) + 1, row, there, lb + kColDK);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.acc_read));
                 continue;

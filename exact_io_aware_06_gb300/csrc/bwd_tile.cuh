@@ -5,7 +5,7 @@
 //     item_count(a), item_at(a, x)       dK/dV: an Item
 //     walk_of(a, I)                      its query blocks one after the other: head, blk, next()
 //     query_range(a, I, key, q0, ..)     which queries from q0 on a key meets
-//     key_rows(a), part_of(a, I)         rows of a head of dK and dV; an item's part
+//     key_rows(a), part_of(a, I)         rows of a head of dK and dV; an item's parts of dV (twice that) and dK (+ 1)
 //     hides(a)                           whether hidden keys may hold anything, an infinity or a NaN
 #pragma once
 
@@ -135,18 +135,18 @@ struct RowsOut {
     }
 };
 
-// This thread's key row of dV (which = 0) or dK, unscaled, from TMEM to its place in the
-// workspace, where four columns of all rows lie side by side: a warp's store is 512 bytes in a run.
-// Rows past N are zeros and fill their places too.
+// This thread's row of an accumulator, unscaled, from TMEM to its place in the workspace (`there`: if it is one of
+// the tensor's), where four columns of all rows lie side by side: a warp's store is 512 bytes in a run.
 template <int D>
-__device__ __forceinline__ void write_part_row(float* parts, size_t part, int which, int row, uint32_t taddr) {
-    uint4* dst = reinterpret_cast<uint4*>(parts) + (2 * part + which) * (kBlk * D / 4) + row;
+__device__ __forceinline__ void write_part_row(float* parts, size_t part, int row, bool there, uint32_t taddr) {
+    uint4* dst = reinterpret_cast<uint4*>(parts) + part * (kBlk * D / 4) + row;
 #pragma unroll
     for (int h = 0; h < D / 32; ++h) {
         uint32_t r[32];
         tmem_ld32(taddr + 32 * h, r);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) dst[(8 * h + x) * kBlk] = make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
+        for (int x = 0; x < 8; ++x)
+            if (there) dst[(8 * h + x) * kBlk] = make_uint4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
     }
 }
 

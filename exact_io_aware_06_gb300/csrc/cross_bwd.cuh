@@ -4,7 +4,7 @@
 // As in the forward the G N_q rows of the query heads that share a K/V head in one batch are the R rows of
 // one longer head.  A key block meets all of their 128-row blocks, those of every batch that shares
 // the keys one after the other; where there are fewer key blocks than SMs these are dealt in pieces,
-// whose float32 dK and dV are added in order afterwards.
+// whose float32 dK and dV are added in order afterwards.  So are the key blocks of a query block for dQ.
 #pragma once
 
 #include "bwd_tile.cuh"
@@ -20,16 +20,22 @@ struct CrossBwdArgs {
     const int* lengths;     // [B_kv] or null
     int N, Np;              // R and that in whole blocks
     int N_kv, n_q, n_k;     // keys; blocks of queries and of keys
+    float* part_q;          // with pieces_q > 1: dQ [B H_kv][n_q][pieces_q][d / 4][128][4] float32
     int share, H_kv, BH_kv;
     int per, pieces;        // query blocks of a piece, over the batches that share
+    int per_q, pieces_q;    // key blocks of a piece of dQ
     float c_log2;           // scale * log2(e), not 0
     float scale;
     DevCtl ctl;
 };
+struct CrossPieceArgs : CrossBwdArgs {};  // for dQ in pieces
 
 static __device__ __forceinline__ int key_count(const CrossBwdArgs& a, int kv_batch) {
     return a.lengths ? min(max(__ldg(a.lengths + kv_batch), 0), a.N_kv) : a.N_kv;
 }
+
+// A sequence without keys has one block, all of it hidden: its queries' gradients are zeros from it.
+static __device__ __forceinline__ int key_blocks(int len) { return max(1, (len + kBlk - 1) / kBlk); }
 
 struct CrossItem {
     int bh, kvb, i0, n_it;

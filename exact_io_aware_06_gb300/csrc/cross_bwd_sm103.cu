@@ -6,7 +6,7 @@
 //     dS = P o (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,
 // dK and dV summed over the query heads and the batches that share a K/V head.  Kernels on one stream:
 // prep (delta, padded -lse log2 e; zeros for dK and dV of key blocks without keys), dK/dV per 128-key block
-// (bwd_main128.cuh, bwd_main64.cuh), the join of its pieces where it has any, dQ (bwd_dq.cuh).  Nothing is
+// (bwd_main128.cuh, bwd_main64.cuh), dQ (bwd_dq.cuh), the join of their pieces where there are any.  Nothing is
 // summed by atomics: the same bits every time.
 #include "bwd_main128.cuh"
 #include "cross_bwd.cuh"
@@ -112,35 +112,52 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const PrepArgs a) {
     }
 }
 
-// dV (blockIdx.y even) and dK of the key blocks that were dealt in pieces: the parts added in order, dK times
-// scale, rounded once.  A warp takes 8 rows x 32 columns, whole lines of the parts and 64-byte runs of
-// the result.
-constexpr int kJoinSplit = 4;  // CTAs of a block's dV or dK
+// What was dealt in pieces: the float32 parts added in order, times a factor, rounded once.  blockIdx.x: dV and dK
+// of every key block, then dQ of every query block.  A warp takes 8 rows x 32 columns, whole lines of the parts
+// and 64-byte runs of the result.
+constexpr int kJoinSplit = 4;  // CTAs of a block
 template <int D>
-__global__ void __launch_bounds__(256) cross_bwd_join_kernel(const CrossBwdArgs a) {
+__global__ void __launch_bounds__(256) cross_bwd_join_kernel(const CrossBwdArgs a, void* const dq, const int key_places) {
     griddep_wait();
     constexpr int kCols = D / 32, kTiles = kCols * (kBlk / 8);
-    const int bh = static_cast<int>(blockIdx.x) / a.n_k, kvb = static_cast<int>(blockIdx.x) - bh * a.n_k;
-    if (kvb * kBlk >= key_count(a, bh / a.H_kv)) return;  // zeros already
-    const int which = blockIdx.y % 2, lane = threadIdx.x % 32;
-    for (int tile = blockIdx.y / 2 * 8 + threadIdx.x / 32; tile < kTiles; tile += kJoinSplit * 8) {
+    const int lane = threadIdx.x % 32;
+    const float4* src;
+    uint4* out;  // of the block's first row
+    int rows, n;
+    float f = a.scale;
+    if (static_cast<int>(blockIdx.x) < key_places) {
+        const int place = static_cast<int>(blockIdx.x) / 2, which = blockIdx.x % 2;
+        const int bh = place / a.n_k, row0 = (place - bh * a.n_k) * kBlk;
+        if (row0 >= key_count(a, bh / a.H_kv)) return;  // zeros already
+        src = reinterpret_cast<const float4*>(a.part) + (static_cast<size_t>(place) * a.pieces * 2 + which) * (kBlk * D / 4);
+        out = static_cast<uint4*>(which ? a.dk : a.dv) + (static_cast<size_t>(bh) * a.N_kv + row0) * (D / 8);
+        rows = a.N_kv - row0;
+        n = a.pieces;
+        if (which == 0) f = 1.f;
+    } else {
+        const int place = static_cast<int>(blockIdx.x) - key_places, bh = place / a.n_q, row0 = (place - bh * a.n_q) * kBlk;
+        const int blocks = key_blocks(key_count(a, bh / a.H_kv / a.share));
+        if (blocks <= a.per_q) return;  // one piece, which wrote the result
+        src = reinterpret_cast<const float4*>(a.part_q) + static_cast<size_t>(place) * a.pieces_q * (kBlk * D / 4);
+        out = static_cast<uint4*>(dq) + (static_cast<size_t>(bh) * a.N + row0) * (D / 8);
+        rows = a.N - row0;
+        n = (blocks + a.per_q - 1) / a.per_q;
+    }
+    const int step = (static_cast<int>(blockIdx.x) < key_places ? 2 : 1) * (kBlk * D / 4);
+    for (int tile = blockIdx.y * 8 + threadIdx.x / 32; tile < kTiles; tile += kJoinSplit * 8) {
         const int row = tile / kCols * 8 + lane % 8, vec = tile % kCols * 4 + lane / 8;
-        const int key = kvb * kBlk + row;
-        if (key >= a.N_kv) continue;
-        const float4* src = reinterpret_cast<const float4*>(a.part) +
-                            (static_cast<size_t>(blockIdx.x) * a.pieces * 2 + which) * (kBlk * D / 4) + 2 * vec * kBlk + row;
+        if (row >= rows) continue;
+        const float4* p = src + 2 * vec * kBlk + row;
         float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
 #pragma unroll 4
-        for (int i = 0; i < a.pieces; ++i) {
-            const float4 y = src[0], z = src[kBlk];
+        for (int i = 0; i < n; ++i) {
+            const float4 y = p[0], z = p[kBlk];
             u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
             w.x += z.x, w.y += z.y, w.z += z.z, w.w += z.w;
-            src += 2 * (kBlk * D / 4);
+            p += step;
         }
-        const float f = which ? a.scale : 1.f;
-        static_cast<uint4*>(which ? a.dk : a.dv)[(static_cast<size_t>(bh) * a.N_kv + key) * (D / 8) + vec] =
-            make_uint4(pack_bf16x2(u.x * f, u.y * f), pack_bf16x2(u.z * f, u.w * f), pack_bf16x2(w.x * f, w.y * f),
-                       pack_bf16x2(w.z * f, w.w * f));
+        out[row * (D / 8) + vec] = make_uint4(pack_bf16x2(u.x * f, u.y * f), pack_bf16x2(u.z * f, u.w * f),
+                                              pack_bf16x2(w.x * f, w.y * f), pack_bf16x2(w.z * f, w.w * f));
     }
 }
 
@@ -149,12 +166,31 @@ size_t rows_bytes(const CrossBwdArgs& a) { return 2 * static_cast<size_t>(a.BH_k
 size_t part_bytes(const CrossBwdArgs& a, int d) {
     return a.pieces > 1 ? static_cast<size_t>(a.BH_kv) * a.n_k * a.pieces * 2 * kBlk * d * sizeof(float) : 0;
 }
+size_t part_q_bytes(const CrossBwdArgs& a, int d) {
+    return a.pieces_q > 1 ? static_cast<size_t>(a.BH_kv) * a.share * a.n_q * a.pieces_q * kBlk * d * sizeof(float) : 0;
+}
 
-// Sizes, and in how many pieces a key block's query blocks are dealt: the number that gives the busiest of
-// 152 CTAs the least to do, counted in pairs of blocks, with 1.5 more an item for its start and end, and
-// for the parts' way to memory and back 0.07 a part (of 128 KB at d = 128, about 0.1 us of all SMs, a pair
-// being 1.3) and 3 for the launch of the join.  152 SMs, whatever the current device: the workspace's size
-// and the order of the sums follow from the sizes alone.
+// `blocks` blocks that meet `all` others each: in how many pieces these are dealt.  The number that gives the
+// busiest of 152 CTAs the least to do, counted in pairs of blocks, with `edge` more an item for its start and end,
+// `part` a part for its way to memory and back, and `join` for the launch of the join.
+// 152 SMs, whatever the current device: the workspace's size and the order of the sums follow from the sizes
+// alone.
+void pieces_of(long long blocks, long long all, double edge, double part, double join, int* per_piece, int* pieces) {
+    double least = 0;
+    for (int p = 1; p <= 64 && p <= all && (p == 1 || blocks < 304); ++p) {
+        const long long per = (all + p - 1) / p, n = (all + per - 1) / per;
+        const double cost = static_cast<double>((blocks * n + 151) / 152) * (per + edge) +
+                            (n > 1 ? join + part * blocks * n : 0);
+        if (p == 1 || cost < least) {
+            least = cost;
+            *per_piece = static_cast<int>(per);
+            *pieces = static_cast<int>(n);
+        }
+    }
+}
+// Sizes and pieces.  At d = 128 a pair of blocks takes 1.3 us for dK and dV, whose parts of 128 KB take about 0.1 us
+// of all SMs, less where a block has fewer keys than rows; for dQ 0.9 us, and a part half of that; the join 4 us
+// unless there is one already.
 CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     CrossBwdArgs a = {};
     a.N = H / H_kv * N_q;
@@ -165,17 +201,11 @@ CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     a.share = B / B_kv;
     a.H_kv = H_kv;
     a.BH_kv = B_kv * H_kv;
-    const long long blocks = static_cast<long long>(a.BH_kv) * a.n_k, all = static_cast<long long>(a.share) * a.n_q;
-    double least = 0;
-    for (int pieces = 1; pieces <= 64 && pieces <= all && (pieces == 1 || blocks < 304); ++pieces) {
-        const long long per = (all + pieces - 1) / pieces, n = (all + per - 1) / per;
-        const double cost = static_cast<double>((blocks * n + 151) / 152) * (per + 1.5) + (n > 1 ? 3 + 0.07 * blocks * n : 0);
-        if (pieces == 1 || cost < least) {
-            least = cost;
-            a.per = static_cast<int>(per);
-            a.pieces = static_cast<int>(n);
-        }
-    }
+    auto filled = [](int n) { return n < kBlk ? static_cast<double>(n) / kBlk : 1.0; };
+    pieces_of(static_cast<long long>(a.BH_kv) * a.n_k, static_cast<long long>(a.share) * a.n_q, 1.5, 0.07 * filled(N_kv),
+              3, &a.per, &a.pieces);
+    pieces_of(static_cast<long long>(a.BH_kv) * a.share * a.n_q, a.n_k, 2, 0.05 * filled(a.N), a.pieces > 1 ? 0 : 5,
+              &a.per_q, &a.pieces_q);
     return a;
 }
 
@@ -183,7 +213,7 @@ CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
 
 size_t bwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     const CrossBwdArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv);
-    return rows_bytes(a) + part_bytes(a, d);
+    return rows_bytes(a) + part_bytes(a, d) + part_q_bytes(a, d);
 }
 
 int launch_bwd_cross(const void* q, const void* k, const void* v, const int* lengths, const void* o, const float* lse,
@@ -198,6 +228,7 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
     a.ws_delta = pa.ws_delta;
     a.ws_lse2 = pa.ws_lse2;
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes(a));
+    a.part_q = a.part + part_bytes(a, d) / sizeof(float);
     a.dk = dk;
     a.dv = dv;
     a.lengths = lengths;
@@ -240,9 +271,11 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
     }
     if (e != cudaSuccess) return static_cast<int>(e);
     rc = launch_bwd_cross_dq(q, k, v, dO, dq, a, d, grid, s);
-    if (rc != 0 || a.pieces == 1) return rc;
+    const int key_places = a.pieces > 1 ? 2 * a.BH_kv * a.n_k : 0;
+    const int places = key_places + (a.pieces_q > 1 ? heads * a.n_q : 0);
+    if (rc != 0 || places == 0) return rc;
     return static_cast<int>(launch_pdl(d == 64 ? cross_bwd_join_kernel<64> : cross_bwd_join_kernel<128>,
-                                       dim3(a.BH_kv * a.n_k, 2 * kJoinSplit), dim3(256), 0, s, a));
+                                       dim3(places, kJoinSplit), dim3(256), 0, s, a, dq, key_places));
 }
 
 }  // namespace fa

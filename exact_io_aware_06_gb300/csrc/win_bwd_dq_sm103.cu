@@ -6,6 +6,7 @@
 namespace fa {
 
 struct WinQItem {
+    static constexpr bool kParts = false;
     int bh, bh_kv, qb, lo, n_sink, n_kv;
     bool shorty;  // the first block is that of up to 32 sinks, in front of the window
     __device__ __forceinline__ int block(int j) const { return j < n_sink ? j : lo + j - n_sink; }

@@ -403,6 +403,19 @@ def test_backward_of_pieces_and_of_many_items(d):
     check_backward(q, k, v, lengths, do, grads, scale, kv_batches=range(0, 70, 9))
 
 
+@pytest.mark.parametrize("B,B_kv,H,H_kv,N_q,N_kv,lengths", [(4, 4, 2, 1, 40, 4100, [4100, 130, 0, 1000]), (1, 1, 1, 1, 1, 3000, [2999]),
+                                                            (6, 2, 3, 1, 70, 2600, [257, 2600]), (1, 1, 2, 2, 300, 2000, None)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_of_few_queries_on_many_keys(B, B_kv, H, H_kv, N_q, N_kv, lengths, d):
+    # the keys of a query block are dealt in pieces, of which a short sequence has one, two or none
+    rows = B * H_kv * (-(-H // H_kv * N_q // 128) * 128)
+    assert fa.fa_bwd_cross_workspace_size(B, B_kv, H, H_kv, N_q, N_kv, d) >= 2 * rows * 4 + 2 * rows * d * 4
+    q, k, v, do, o, lse, grads, scale = step(B, B_kv, H, H_kv, N_q, N_kv, d, lengths, seed=7)
+    check_backward(q, k, v, lengths, do, grads, scale)
+    for a, b in zip(grads, backward(q, k, v, lengths, o, lse, do, scale)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
 def test_backward_scales(scale):
     q, k, v, do, _, _, grads, scale = step(1, 1, 2, 2, 200, 300, 64, [270], seed=3, scale=scale)
