@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 2 * D : GROUPS * D) cross_join_k
 }
 
 // How a call's rows are tiled and its work dealt, from its sizes alone.
-CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
+CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     CrossArgs a = {};
     a.R = H / H_kv * N_q;
     a.share = B / B_kv;
@@ -846,9 +846,18 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     a.part_rows = a.tiles > 1 ? 2 * kBM : round_up(rows < kBM ? rows : kBM, 32);
     const long long items = static_cast<long long>(B_kv) * a.per;
     a.join_rows = a.tiles > 1 ? 2 * kBM : rows < kBM ? rows : kBM;
-    a.stream = items < 8 * kMaxCtas && N_kv > kBN;  // an item of one block cannot be cut
+    // Whole items, or key blocks in equal runs?  In blocks of the busiest CTA, an item's end counting 1.25, the
+    // join's launch 2.5 and what leaves a cut item as float32 and comes back 0.022 for 256 rows at d = 128.
+    // With a CTA or less an item the longest sequence would set the pace, and a batch's mean is taken for 3/4 of
+    // it.  Measured, whole / cut: 138 items of 4 blocks 12.4 / 24.1 us, 512 of 4 37 / 50, 160 of 16 55 / 47,
+    // 63 of up to 17 27.8 / 21.8.
+    const double blocks = (N_kv + kBN - 1) / kBN, even = items * blocks / kMaxCtas;
+    const double whole = ((items + kMaxCtas - 1) / kMaxCtas) * (blocks + 1.25);
+    const double parts = (items < kMaxCtas ? kMaxCtas + items : 2 * kMaxCtas) * a.part_rows / 256.0 * d / 128.0;
+    const double cut = even * (items <= kMaxCtas ? 0.75 : 1.0) + (items / double{kMaxCtas} + 1) * 1.25 + 2.5 + 0.022 * parts;
+    a.stream = N_kv > kBN && items < 8 * kMaxCtas && cut < whole;
     a.by_item = items < kMaxCtas;
-    const long long units = items * ((N_kv + kBN - 1) / kBN);
+    const long long units = a.stream ? items * ((N_kv + kBN - 1) / kBN) : items;
     a.ctas = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);
     return a;
 }
@@ -972,14 +981,14 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
 }  // namespace
 
 size_t fwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
-    const CrossArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv);
+    const CrossArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv, d);
     return a.stream && a.ctas > 1 ? kCutBytes + 2 * a.ctas * part_floats(d, a.part_rows) * sizeof(float) : 0;
 }
 
 int launch_fwd_cross(const void* q, const void* k, const void* v, const int* lengths, const void* o_own,
                      const float* lse_own, void* o, float* lse, void* workspace, int B, int B_kv, int H, int H_kv, int N_q,
                      int N_kv, int d, float c_log2, DevCtl ctl, cudaStream_t s) {
-    CrossArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv);
+    CrossArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv, d);
     a.lengths = lengths;
     a.o = o;
     a.lse = lse;
