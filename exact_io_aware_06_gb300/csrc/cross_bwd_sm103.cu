@@ -189,9 +189,9 @@ void pieces_of(long long blocks, long long all, double edge, double part, double
     }
 }
 // Sizes and pieces.  At d = 128 a pair of blocks takes 1.3 us for dK and dV, whose parts of 128 KB take about 0.1 us
-// of all SMs, less where a block has fewer keys than rows; for dQ 0.9 us, and a part half of that; the join 4 us
-// unless there is one already.
-CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
+// of all SMs, less at d = 64 and where a block has fewer keys than rows; for dQ 0.9 us, and a part half of that;
+// the join 4 us unless there is one already.
+CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     CrossBwdArgs a = {};
     a.N = H / H_kv * N_q;
     a.Np = round_up(a.N, kBlk);
@@ -201,7 +201,7 @@ CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
     a.share = B / B_kv;
     a.H_kv = H_kv;
     a.BH_kv = B_kv * H_kv;
-    auto filled = [](int n) { return n < kBlk ? static_cast<double>(n) / kBlk : 1.0; };
+    auto filled = [&](int rows) { return (rows < kBlk ? rows : kBlk) * d / (128.0 * kBlk); };  // of a part of 64 KB
     pieces_of(static_cast<long long>(a.BH_kv) * a.n_k, static_cast<long long>(a.share) * a.n_q, 1.5, 0.07 * filled(N_kv),
               3, &a.per, &a.pieces);
     pieces_of(static_cast<long long>(a.BH_kv) * a.share * a.n_q, a.n_k, 2, 0.05 * filled(a.N), a.pieces > 1 ? 0 : 5,
@@ -212,7 +212,7 @@ CrossBwdArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv) {
 }  // namespace
 
 size_t bwd_cross_workspace_bytes(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
-    const CrossBwdArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv);
+    const CrossBwdArgs a = deal(B, B_kv, H, H_kv, N_q, N_kv, d);
     return rows_bytes(a) + part_bytes(a, d) + part_q_bytes(a, d);
 }
 
@@ -221,7 +221,7 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
                      int N_q, int N_kv, int d, float scale, DevCtl ctl, cudaStream_t s) {
     PrepArgs pa;
     CrossBwdArgs& a = pa.b;
-    a = deal(B, B_kv, H, H_kv, N_q, N_kv);
+    a = deal(B, B_kv, H, H_kv, N_q, N_kv, d);
     const int heads = a.BH_kv * a.share;
     pa.ws_delta = static_cast<float*>(workspace);
     pa.ws_lse2 = pa.ws_delta + static_cast<size_t>(heads) * a.Np;
