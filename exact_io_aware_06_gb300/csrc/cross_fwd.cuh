@@ -29,6 +29,7 @@ struct CrossArgs {
     int nb, tiles_b, tiles, n_pairs, part_rows;
     int per;               // items of a batch, H_kv n_pairs
     int stream;            // 0: whole items; 1: equal runs of key blocks, items cut where they end
+    int edge;              // an item's start and end in blocks, for these runs
     int by_item, join_rows;
     int cluster;           // 2^cluster CTAs share one item, each with its own run of the keys; 0: as `stream`
     int ctas;
@@ -46,20 +47,21 @@ __device__ __forceinline__ int cross_length(const CrossArgs& a, int b) {
 // A sequence without keys has one block, all of it hidden: its rows get O = 0, lse = -inf from it.
 __device__ __forceinline__ int cross_blocks(int len) { return len > 0 ? (len + kBN - 1) / kBN : 1; }
 
-// The key blocks of all items ("units"), item by item, batch by batch, in equal runs for the CTAs.  By a whole
-// warp, 32 batches at a time.  Work of fewer than 8 * 152 items of up to 2^17 blocks is dealt so: 32 bits hold all
-// of their units.
+// The key blocks of all items and `edge` for each item's start and end ("units", the edge in front), item by item,
+// batch by batch, in equal runs for the CTAs.  By a whole warp, 32 batches at a time.  Work of fewer than 8 * 152
+// items of up to 2^17 blocks is dealt so: 32 bits hold all of their units.
+__device__ __forceinline__ int cross_units(const CrossArgs& a, int len) { return cross_blocks(len) + a.edge; }
 struct UnitPlace {
-    int b, item, kb, len;  // K/V batch, item of the batch, key block; the batch's keys
+    int b, item, at, len;  // K/V batch, item of the batch, unit of the item; the batch's keys
 };
 struct Units {
-    int len, upto;         // of batch `lane`: keys; blocks of an item in batches 0 .. lane
+    int len, upto;         // of batch `lane`: keys; units of an item in batches 0 .. lane
     int each, more;        // every CTA has `each`, the first `more` one more
     // batches b0 + lane
     __device__ __forceinline__ void scan(const CrossArgs& a, int b0) {
         const int lane = threadIdx.x % 32, b = b0 + lane;
         len = b < a.B_kv ? cross_length(a, b) : 0;
-        upto = b < a.B_kv ? cross_blocks(len) : 0;
+        upto = b < a.B_kv ? cross_units(a, len) : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, upto, off);
@@ -69,7 +71,7 @@ struct Units {
     __device__ __forceinline__ explicit Units(const CrossArgs& a) {
         uint32_t total = 0;
         if (!a.lengths) {
-            total = a.B_kv * cross_blocks(a.N_kv);
+            total = a.B_kv * cross_units(a, a.N_kv);
         } else {
             for (int b0 = (a.B_kv - 1) & ~31; b0 >= 0; b0 -= 32) {  // the first 32 last, which place() begins with
                 scan(a, b0);
@@ -86,7 +88,7 @@ struct Units {
         uint32_t n;
         if (!a.lengths) {
             p.len = a.N_kv;
-            n = cross_blocks(p.len);
+            n = cross_units(a, p.len);
             p.b = u / (a.per * n);
             u -= p.b * a.per * n;
         } else {
@@ -96,7 +98,7 @@ struct Units {
                     const int l = behind ? __ffs(behind) - 1 : 31;
                     p.b = b0 + l;
                     p.len = __shfl_sync(0xffffffffu, len, l);
-                    n = cross_blocks(p.len);
+                    n = cross_units(a, p.len);
                     u -= (__shfl_sync(0xffffffffu, upto, l) - n) * a.per;
                     break;
                 }
@@ -105,7 +107,7 @@ struct Units {
             }
         }
         p.item = u / n;
-        p.kb = u - p.item * n;
+        p.at = u - p.item * n;
         return p;
     }
 };
@@ -161,14 +163,17 @@ __device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int b
 
 // This CTA's segments, one after the other.
 struct Walk {
-    int b, item, kb, blocks, len, left;
+    int b, item, kb, blocks, len;
+    int left;  // units behind the edge of the item
     __device__ __forceinline__ Walk(const CrossArgs& a, Units& units) {
         const int u = units.first(blockIdx.x);
         left = units.first(blockIdx.x + 1) - u;
         if (left > 0) {
             const UnitPlace p = units.place(a, u);
-            b = p.b, item = p.item, kb = p.kb, len = p.len;
+            b = p.b, item = p.item, len = p.len;
             blocks = cross_blocks(len);
+            kb = max(0, p.at - a.edge);
+            left -= max(0, a.edge - p.at);
         }
     }
     // The next one; `batch` and `at`, its item of the batch; the item's blocks `behind` it.
@@ -176,7 +181,7 @@ struct Walk {
         batch = b, at = item, s.k0 = kb, s.len = len;
         s.n = min(left, blocks - kb);
         behind = blocks - kb - s.n;
-        left -= s.n;
+        left -= s.n + a.edge;
         kb = 0;
         if (++item == a.per && left > 0) {
             item = 0;

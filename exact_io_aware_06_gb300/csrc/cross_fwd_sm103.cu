@@ -859,6 +859,9 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     a.by_item = items < kMaxCtas;
     const long long units = a.stream ? items * ((N_kv + kBN - 1) / kBN) : items;
     a.ctas = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);
+    // Of packed tiles O leaves more slowly.  Counting blocks alone, some CTAs got many short sequences and few blocks:
+    // 8 short and 8 long items 78 -> 36 us, 64 ragged single tokens 185 -> 175; edges of 1 and 4 were slower.
+    a.edge = units <= kMaxCtas ? 0 : a.part_rows == 2 * kBM && a.nb == 1 ? 2 : 3;
     return a;
 }
 
@@ -893,7 +896,7 @@ cudaError_t join(const CrossArgs& x, int places, cudaStream_t s) {
 // Few items take a cluster each, whose CTAs meet at its barrier, which spares the launch of the join (one token
 // of two requests, 32 items on clusters of four, 11.0 -> 10.0 us): the largest clusters of which the device holds
 // as many at once as there are items (36 of four, 15 of eight).  Those leave some SMs out, so not where that costs
-// more blocks a CTA than the join is worth.  Sizes that are no powers of two and those beyond eight were
+// more blocks a CTA than the join is worth (a ragged batch's mean again taken for 3/4).  Sizes that are no powers of two and those beyond eight were
 // slower than their numbers of blocks say (8 items of 7 blocks: four 8.3 us, seven 9.2, the join's launch 9.0;
 // 1 item of 32: sixteen 13.6, the launch 11.3).  0: none.
 constexpr int kMaxCluster = 8, kJoinBlocks = 3;  // blocks of keys in the time of a join
@@ -906,7 +909,7 @@ cudaError_t cluster_size(const CrossArgs& a, int dev, int* log2_size) {
     if (!a.stream || items * 2 > kMaxCtas || dev >= 64) return cudaSuccess;
     for (int s = kMaxCluster; s > 1; s /= 2) {
         if (s > blocks || items * s > kMaxCtas) continue;
-        if ((blocks + s - 1) / s > items * blocks / kMaxCtas + kJoinBlocks) return cudaSuccess;
+        if ((blocks + s - 1) / s > 0.75 * items * blocks / kMaxCtas + kJoinBlocks) return cudaSuccess;
         int n = known[dev][s].load();
         if (n == 0) {
             cudaLaunchConfig_t cfg = {};
