@@ -281,23 +281,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t hide = args.c_log2 >= 0.f ? 0xff800000u : 0x7f800000u;  // -inf after the multiply by c
         bool ok = true;
         int g = 0;
-        // an item's row values, loaded one item ahead; padded rows exist up to Np
+        // an item's row values, loaded one item ahead; padded rows exist up to Np.  From L2: where this kernel starts
+        // beside the one before it, it has waited for none, and its SM's L1 may hold an earlier call's
         auto row_at = [&](int x) {
             const auto I = q_item_at(args, x);
             return static_cast<size_t>(I.bh) * Np + I.qb * kBlk + row;
         };
         float next_nl = 0.f, next_nd = 0.f;
         if (item_x(0) < n_items) {
-            next_nl = args.ws_lse2[row_at(item_x(0))];
-            next_nd = args.ws_delta[row_at(item_x(0))];
+            next_nl = __ldcg(args.ws_lse2 + row_at(item_x(0)));
+            next_nd = __ldcg(args.ws_delta + row_at(item_x(0)));
         }
         for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
             const auto I = q_item_at(args, x);
             const int qrow = I.qb * kBlk + row;
             const float nl = next_nl, nd = next_nd;
             if (item_x(k + 1) < n_items) {
-                next_nl = args.ws_lse2[row_at(item_x(k + 1))];
-                next_nd = args.ws_delta[row_at(item_x(k + 1))];
+                next_nl = __ldcg(args.ws_lse2 + row_at(item_x(k + 1)));
+                next_nd = __ldcg(args.ws_delta + row_at(item_x(k + 1)));
             }
             const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
             for (int j = 0; j < I.n_kv; ++j, ++g) {

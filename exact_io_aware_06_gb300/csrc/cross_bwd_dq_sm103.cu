@@ -17,7 +17,7 @@ static __device__ __forceinline__ CrossQItem q_item_at(const CrossBwdArgs& a, in
     I.qb = x - I.bh * a.n_q;
     const int b = I.bh / a.H_kv, kv_batch = b / a.share;
     I.bh_kv = kv_batch * a.H_kv + I.bh - b * a.H_kv;
-    I.len = key_count(a, kv_batch);
+    I.len = a.lengths ? min(max(__ldcg(a.lengths + kv_batch), 0), a.N_kv) : a.N_kv;  // (from L2, as the rows' values)
     I.n_kv = key_blocks(I.len);
     return I;
 }
@@ -46,8 +46,8 @@ static __device__ __forceinline__ bool hidden_rows(const CrossBwdArgs& a, const 
     r1 = min(kBlk, a.N_kv - block * kBlk);
     return r0 < r1;
 }
-// This kernel starts when every CTA of the dK/dV kernel has seen the rows' values ready; it needs nothing of that
-// kernel, but what comes after it may.
+// This kernel may start when every CTA of the dK/dV kernel has waited for the rows' values (and all that came
+// before them); it needs nothing of that kernel, but what comes after it may.
 template <int D>
 static __device__ __forceinline__ void idle_warp(const CrossBwdArgs&, std::integral_constant<int, D>, int, int) {
     griddep_wait();
@@ -55,40 +55,34 @@ static __device__ __forceinline__ void idle_warp(const CrossBwdArgs&, std::integ
 
 namespace {
 
+// Programmatically where each item has a CTA of its own, which takes over an SM as soon as the dK/dV kernel leaves
+// it (a step of 6 x 107 queries on 5392 keys 107 -> 106 us, 1646 on 4268 101 -> 96), or both kernels' CTAs fit at
+// once (8 x 8 on 16: 23 -> 19).  With several items a CTA the order in which SMs get free undoes the deal, and it
+// costs up to 10%.
 template <int D, class Args>
-int launch_impl(const void* q, const void* k, const void* v, const void* dO, void* dq, const Args& a, int main_ctas,
-                cudaStream_t s) {
-    const int heads = a.BH_kv * a.share, n_items = heads * a.n_q * a.pieces_q;
-    CUtensorMap tq, tk, tv, tdo;
-    const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    int rc = make_map_3d(&tq, q, dt, 2, D, a.N, heads, 64, kBlk);
-    if (rc == 0) rc = make_map_3d(&tk, k, dt, 2, D, a.N_kv, a.BH_kv, 64, kBlk);
-    if (rc == 0) rc = make_map_3d(&tv, v, dt, 2, D, a.N_kv, a.BH_kv, 64, kBlk);
-    if (rc == 0) rc = make_map_3d(&tdo, dO, dt, 2, D, a.N, heads, 64, kBlk);
-    if (rc != 0) return rc;
+cudaError_t launch_impl(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, void* dq,
+                        const Args& a, int main_ctas, int sms, cudaStream_t s) {
     static std::atomic<uint64_t> smem_done;
-    cudaError_t e = allow_smem(bwd_dq_kernel<D, Args>, Cfg<D>::kSmemAlloc, smem_done);
-    int dev = 0, sms = 152;
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return static_cast<int>(e);
-    const int grid = n_items < sms ? n_items : sms;
+    const cudaError_t e = allow_smem(bwd_dq_kernel<D, Args>, Cfg<D>::kSmemAlloc, smem_done);
+    if (e != cudaSuccess) return e;
+    const int n_items = a.BH_kv * a.share * a.n_q * a.pieces_q, grid = n_items < sms ? n_items : sms;
     if (n_items <= sms || main_ctas + grid <= sms)
-        return static_cast<int>(launch_pdl(bwd_dq_kernel<D, Args>, dim3(grid), dim3(kThreads), Cfg<D>::kSmemAlloc, s,
-                                           tq, tk, tv, tdo, a, dq, n_items));
-    bwd_dq_kernel<D, Args><<<grid, kThreads, Cfg<D>::kSmemAlloc, s>>>(tq, tk, tv, tdo, a, dq, n_items);
-    return static_cast<int>(cudaGetLastError());
+        return launch_pdl(bwd_dq_kernel<D, Args>, dim3(grid), dim3(kThreads), Cfg<D>::kSmemAlloc, s, q, k, v, dO, a, dq, n_items);
+    bwd_dq_kernel<D, Args><<<grid, kThreads, Cfg<D>::kSmemAlloc, s>>>(q, k, v, dO, a, dq, n_items);
+    return cudaGetLastError();
+}
+template <class Args>
+cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, void* dq,
+                     const Args& a, int d, int main_ctas, int sms, cudaStream_t s) {
+    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, main_ctas, sms, s) : launch_impl<128>(q, k, v, dO, dq, a, main_ctas, sms, s);
 }
 
 }  // namespace
 
-int launch_bwd_cross_dq(const void* q, const void* k, const void* v, const void* dO, void* dq, const CrossBwdArgs& a, int d,
-                        int main_ctas, cudaStream_t s) {
-    if (a.pieces_q > 1) {
-        const CrossPieceArgs p = {a};
-        return d == 64 ? launch_impl<64>(q, k, v, dO, dq, p, main_ctas, s) : launch_impl<128>(q, k, v, dO, dq, p, main_ctas, s);
-    }
-    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, main_ctas, s) : launch_impl<128>(q, k, v, dO, dq, a, main_ctas, s);
+cudaError_t launch_bwd_cross_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
+                                void* dq, const CrossBwdArgs& a, int d, int main_ctas, int sms, cudaStream_t s) {
+    if (a.pieces_q == 1) return launch_d(q, k, v, dO, dq, a, d, main_ctas, sms, s);
+    return launch_d(q, k, v, dO, dq, CrossPieceArgs{a}, d, main_ctas, sms, s);
 }
 
 }  // namespace fa
