@@ -763,7 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Items that were cut: the parts of the one in place blockIdx.x of the table, some of its rows at a time
 // (blockIdx.y), in a fixed order.  A warp takes 8 rows x 32 columns (128-byte runs of the parts, 64-byte runs of
 // the result) of every GROUPS-th part, kTogether parts' loads in flight; the groups' states meet in shared
-// memory.  Items of many parts take four groups (16 items of 9 parts each 7.0 -> 3.5 us, 8 of 19 13.7 -> 8.8);
+// memory.  Items of many parts take four groups (16 items of 9 parts each 7.0 -> 3.5 us, 8 of 19 13.7 -> 8.8; a lone
+// tile's rows from four parts on, 27 of 48 rows 14.8 -> 13.3 with the attention);
 // where there are two to four parts four groups are idle and in the way (64 items 8 -> 34 us), and the reads
 // of 128 KB a part at d = 128 count.
 constexpr int kTogether = 4;
@@ -977,7 +978,7 @@ int launch_impl(const void* q, const void* k, const void* v, const CrossArgs& a,
     e = launch_pdl(cross_fwd_kernel<D>, dim3(x.ctas), dim3(kThreads), Cfg<D>::kSmemAlloc, s, tq, tk, tv, to, x);
     const int items = x.by_item ? x.B_kv * x.per : x.ctas - 1;  // places of cut items
     if (e == cudaSuccess && x.stream && x.ctas > 1)
-        e = x.ctas >= 6 * items ? join<D, 4>(x, items, s) : join<D, 1>(x, items, s);
+        e = x.ctas >= (x.join_rows > kBM ? 6 : 4) * items ? join<D, 4>(x, items, s) : join<D, 1>(x, items, s);
     return static_cast<int>(e);
 }
 
