@@ -54,6 +54,7 @@ int norm_rope_args(NormRopeArgs* a, const void* qkv, const float* qw, const floa
     a->weight[1] = kw;
     a->pos = pos;
     a->axes = 1;
+    a->any_order = false;
     a->heads[0] = H;
     a->heads[1] = a->heads[2] = H_kv;
     a->N = N;
@@ -132,6 +133,7 @@ int norm_rope_axes(NormRopeArgs* a, const int* axis, int n_axes) {
     if (n_axes < 1 || n_axes > kMaxRopeAxes) return FA_ERR_INVALID_ARG;
     if (a->rot > 0 && (axis == nullptr || a->pos == nullptr)) return FA_ERR_INVALID_ARG;
     a->axes = n_axes;
+    a->any_order = true;  // (fa_qk_norm_rope_bwd keeps its own)
     for (int p = 0; p < a->rot / 2; ++p) {
         if (axis[p] < 0 || axis[p] >= n_axes) return FA_ERR_INVALID_ARG;
         a->axis[p] = static_cast<uint8_t>(axis[p]);

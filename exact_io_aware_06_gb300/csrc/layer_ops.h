@@ -61,6 +61,7 @@ struct NormRopeArgs {
     RopeFreq freq;
     int axes;               // of positions
     uint8_t axis[64];       // of each pair, where axes > 1
+    bool any_order;         // backward: the order in which a token's heads add to the weights' gradients may follow the sizes
 };
 
 // d in {64, 128}; rot a multiple of 16, at most d.

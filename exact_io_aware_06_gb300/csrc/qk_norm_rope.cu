@@ -345,6 +345,219 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
+// Many tokens of few heads: a token a group of D / 8 lanes, all of whose heads it works through, pass by pass, so
+// that no lane is idle where heads do not fill a pass of one token, no batch ends with Q's or K's heads, and the
+// work for a token (its place, position, cosines and sines, four pairs a lane) is shared by 32 / (D / 8) of them.
+struct Rows {
+    int all, per;         // heads of a token, Q's, K's and V's; passes of a batch
+    uint32_t groups;      // of 32 / (D / 8) tokens
+    Div by_n;
+};
+// The lane's four pairs, and its place: a batch of passes of its token.
+template <int D, int AXES>
+struct LanePairs {
+    uint64_t f[4];
+    int axis[AXES == 2 ? 4 : 1];
+    bool turned;
+    __device__ __forceinline__ LanePairs(const NormRopeArgs& a, int j) {
+        turned = j < a.rot / 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = turned ? a.freq.f[4 * j + i] : 0;
+            if constexpr (AXES == 2) axis[i] = turned ? a.axis[4 * j + i] : 0;
+        }
+    }
+    __device__ __forceinline__ void angles(const int (&pos)[AXES == 2 ? 4 : 1], float2 (&c)[2], float2 (&s)[2]) const {
+        float cs[4], sn[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // as token_angles
+            const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos[AXES == 2 ? i : 0])) * f[i];
+            sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            c[k] = make_float2(cs[2 * k], cs[2 * k + 1]);
+            s[k] = make_float2(sn[2 * k], sn[2 * k + 1]);
+        }
+    }
+};
+template <int AXES>
+struct RowPlace {
+    uint32_t g, tk, b;
+    int n, p, count;
+    int pos[AXES == 2 ? 4 : 1];
+    bool there;
+};
+template <int D, int AXES>
+__device__ __forceinline__ void row_place(const NormRopeArgs& a, const Rows& r, const LanePairs<D, AXES>& pairs, uint32_t g,
+                                          int grp, RowPlace<AXES>& p) {
+    constexpr int kTokens = 32 / (D / 8);
+    p.g = g;
+    p.p = 0;
+    p.count = min(r.per, r.all);
+    p.tk = g * kTokens + grp;
+    p.there = g < r.groups && p.tk < a.tokens;
+    if (!p.there) p.tk = 0;
+    p.b = r.by_n.of(p.tk);
+    p.n = static_cast<int>(p.tk - p.b * r.by_n.d);
+    if constexpr (AXES == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p.pos[i] = pairs.turned ? __ldg(a.pos + (static_cast<size_t>(pairs.axis[i]) * a.tokens + p.tk)) : 0;
+    } else {
+        p.pos[0] = a.pos ? __ldg(a.pos + p.tk) : p.n;
+    }
+}
+template <int D, int AXES>
+__device__ __forceinline__ RowPlace<AXES> row_after(const NormRopeArgs& a, const Rows& r, const LanePairs<D, AXES>& pairs,
+                                                    const RowPlace<AXES>& at, uint32_t step, int grp) {
+    RowPlace<AXES> p = at;
+    if (at.p + at.count >= r.all) {
+        row_place(a, r, pairs, at.g + step, grp, p);
+    } else {
+        p.p += at.count;
+        p.count = min(r.per, r.all - p.p);
+    }
+    return p;
+}
+// The lane's weights of Q (seg = 0) or K.
+template <int D, bool INTER>
+__device__ __forceinline__ void lane_weights(const float (&w)[2][D], int seg, int ea, int eb, float2 (&wf)[2], float2 (&ws)[2]) {
+    const float4 wa = *reinterpret_cast<const float4*>(&w[seg][ea]);
+    const float4 wb = *reinterpret_cast<const float4*>(&w[seg][eb]);
+    wf[0] = INTER ? make_float2(wa.x, wa.z) : make_float2(wa.x, wa.y);
+    wf[1] = INTER ? make_float2(wb.x, wb.z) : make_float2(wa.z, wa.w);
+    ws[0] = INTER ? make_float2(wa.y, wa.w) : make_float2(wb.x, wb.y);
+    ws[1] = INTER ? make_float2(wb.y, wb.w) : make_float2(wb.z, wb.w);
+}
+// Where head p of a token (b, n) lies among the tensors [B][heads][N][D] of Q, K and V.
+__device__ __forceinline__ size_t head_row(const NormRopeArgs& a, int seg, int p, uint32_t b, int n) {
+    const int heads = seg == 0 ? a.heads[0] : a.heads[1];
+    const int h = seg == 0 ? p : seg == 1 ? p - a.heads[0] : p - a.heads[0] - a.heads[1];
+    return (static_cast<size_t>(b) * heads + h) * a.N + n;
+}
+
+template <int D, bool F32, bool INTER, int AXES>
+__global__ void __launch_bounds__(kThreads, 4)
+    qk_norm_rope_rows_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Rows rows) {
+    constexpr int kLanes = D / 8, kElem = F32 ? 4 : 2, kAhead = F32 ? 2 : 8;
+    __shared__ __align__(16) float w[2][D];
+    const int lane = threadIdx.x % 32, grp = lane / kLanes;
+    int ea, eb;
+    lane_groups<D, INTER>(a.rot, lane % kLanes, ea, eb);
+    const int gap = (eb - ea) * kElem;
+    const LanePairs<D, AXES> pairs(a, lane % kLanes);
+    griddep_wait();
+    griddep_launch_dependents();
+    auto load = [&](const RowPlace<AXES>& at, Raw<F32>(&raw)[kAhead]) {
+        const char* src = static_cast<const char*>(a.qkv) + ((static_cast<size_t>(at.tk) * rows.all + at.p) * D + ea) * kElem;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            raw[u] = load8<F32>(src + u * D * kElem, src + gap + u * D * kElem, u < at.count && at.there);
+    };
+    RowPlace<AXES> at;
+    row_place(a, rows, pairs, blockIdx.x * kWarps + threadIdx.x / 32, grp, at);
+    Raw<F32> raw[kAhead];
+    load(at, raw);
+    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+        const float* src = x < D ? a.weight[0] : a.weight[1];
+        w[x / D][x % D] = src ? src[x % D] : 1.f;
+    }
+    __syncthreads();
+
+    float2 c[2], s[2];
+    while (at.g < rows.groups) {
+        const RowPlace<AXES> next = row_after(a, rows, pairs, at, gridDim.x * kWarps, grp);
+        Raw<F32> ahead[kAhead];
+        load(next, ahead);
+        if (at.p == 0) pairs.angles(at.pos, c, s);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (u >= at.count) break;
+            const int p = at.p + u, seg = (p >= a.heads[0]) + (p >= a.heads[0] + a.heads[1]);
+            if (seg < 2) {
+                float2 wf[2], ws[2];
+                lane_weights<D, INTER>(w, seg, ea, eb, wf, ws);
+                const Quad x = unpack<F32, INTER>(raw[u]);
+                const float2 r = both(rsqrtf(fmaf(row_sum<kLanes>(dot(x, x)), 1.f / D, a.eps)));
+                Quad y;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    y.first[k] = mul2(r, fma2(x.first[k], mul2(c[k], wf[k]), mul2(x.second[k], neg2(mul2(s[k], ws[k])))));
+                    y.second[k] = mul2(r, fma2(x.second[k], mul2(c[k], ws[k]), mul2(x.first[k], mul2(s[k], wf[k]))));
+                }
+                raw[u] = pack<F32, INTER>(y);
+            }
+            char* dst = static_cast<char*>(seg == 0 ? a.out[0] : seg == 1 ? a.out[1] : a.out[2]) +
+                        (head_row(a, seg, p, at.b, at.n) * D + ea) * kElem;
+            if (at.there) store8<F32>(dst, dst + gap, raw[u]);
+        }
+        at = next;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
+    }
+}
+
+// Gradient of a row x (`there`, or zeros) from its output's; seg = 0 (Q) or 1 (K), whose sums of dw it adds to.
+template <int LANES>
+__device__ __forceinline__ Quad row_gradient(const Quad& x, const Quad& dy, const float2 (&c)[2], const float2 (&s)[2],
+                                             const float2 (&wf)[2], const float2 (&ws)[2], float eps, bool there, int seg,
+                                             Quad (&dw)[2]) {
+    constexpr int D = 8 * LANES;
+    Quad g, wg;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // turned back: the opposite angle
+        g.first[k] = fma2(dy.first[k], c[k], mul2(dy.second[k], s[k]));
+        g.second[k] = fma2(dy.second[k], c[k], neg2(mul2(dy.first[k], s[k])));
+        wg.first[k] = mul2(g.first[k], wf[k]);
+        wg.second[k] = mul2(g.second[k], ws[k]);
+    }
+    const float sq = fmaf(row_sum<LANES>(dot(x, x)), 1.f / D, eps);
+    // rows of heads past the end are zeros: with a finite r (for eps = 0 too) they add nothing
+    const float r = there ? rsqrtf(sq) : 0.f;
+    const float m = row_sum<LANES>(dot(wg, x)) * (1.f / D) * r * r;
+    const float2 r2 = both(r), m2 = both(-m);
+    Quad dx;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float2 gf = mul2(g.first[k], r2), gs = mul2(g.second[k], r2);
+        if (seg == 0) {
+            dw[0].first[k] = fma2(gf, x.first[k], dw[0].first[k]);
+            dw[0].second[k] = fma2(gs, x.second[k], dw[0].second[k]);
+        } else {
+            dw[1].first[k] = fma2(gf, x.first[k], dw[1].first[k]);
+            dw[1].second[k] = fma2(gs, x.second[k], dw[1].second[k]);
+        }
+        dx.first[k] = mul2(r2, fma2(m2, x.first[k], wg.first[k]));
+        dx.second[k] = mul2(r2, fma2(m2, x.second[k], wg.second[k]));
+    }
+    return dx;
+}
+// The block's sums of dw: over the lanes that hold the same elements of other rows, then over its warps in order.
+template <int D, bool INTER>
+__device__ __forceinline__ void block_sums(const Quad (&dw)[2], float (&sums)[kWarps][2][D], int ea, int eb, float* part) {
+    constexpr int kLanes = D / 8;
+    const int warp = threadIdx.x / 32, grp = threadIdx.x % 32 / kLanes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Raw<true> v = pack<true, INTER>(dw[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float t = __uint_as_float(v.u[e]);
+#pragma unroll
+            for (int off = kLanes; off < 32; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+            if (grp == 0) sums[warp][i][(e < 4 ? ea : eb - 4) + e] = t;
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) v += sums[k][x / D][x % D];
+        part[static_cast<size_t>(blockIdx.x) * 2 * D + x] = v;
+    }
+}
+
 // Gradient.  Each lane keeps its eight elements' sums of dw over all of the warp's rows; the
 // block's warps are then added in order and written as one partial row per block, and
 // dweight_sum_kernel adds the blocks in order: no atomics, the same bits every time.
@@ -423,33 +636,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             const bool there = h + u * kHeads < heads;
             if (at.seg < 2) {
                 const Quad x = unpack<F32, INTER>(rx[u]), dy = unpack<F32, INTER>(rg[u]);
-                Quad g, wg;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {  // turned back: the opposite angle
-                    g.first[k] = fma2(dy.first[k], c[k], mul2(dy.second[k], s[k]));
-                    g.second[k] = fma2(dy.second[k], c[k], neg2(mul2(dy.first[k], s[k])));
-                    wg.first[k] = mul2(g.first[k], wf[k]);
-                    wg.second[k] = mul2(g.second[k], ws[k]);
-                }
-                const float sq = fmaf(row_sum<kLanes>(dot(x, x)), 1.f / D, a.eps);
-                // rows of heads past the end are zeros: with a finite r (for eps = 0 too) they add nothing
-                const float r = there ? rsqrtf(sq) : 0.f;
-                const float m = row_sum<kLanes>(dot(wg, x)) * (1.f / D) * r * r;
-                const float2 r2 = both(r), m2 = both(-m);
-                Quad dx;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 gf = mul2(g.first[k], r2), gs = mul2(g.second[k], r2);
-                    if (at.seg == 0) {
-                        dw[0].first[k] = fma2(gf, x.first[k], dw[0].first[k]);
-                        dw[0].second[k] = fma2(gs, x.second[k], dw[0].second[k]);
-                    } else {
-                        dw[1].first[k] = fma2(gf, x.first[k], dw[1].first[k]);
-                        dw[1].second[k] = fma2(gs, x.second[k], dw[1].second[k]);
-                    }
-                    dx.first[k] = mul2(r2, fma2(m2, x.first[k], wg.first[k]));
-                    dx.second[k] = mul2(r2, fma2(m2, x.second[k], wg.second[k]));
-                }
+                const Quad dx = row_gradient<kLanes>(x, dy, c, s, wf, ws, a.eps, there, at.seg, dw);
                 rg[u] = pack<F32, INTER>(dx);
             }
             if (there) store8<F32>(dst + u * kPass, dst + gap + u * kPass, rg[u]);
@@ -462,25 +649,77 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
     }
     if (a.part == nullptr) return;
-    // lanes that hold the same elements of other heads, then the block's warps
+    block_sums<D, INTER>(dw, sums, ea, eb, a.part);
+}
+
+template <int D, bool F32, bool INTER, int AXES>
+__global__ void __launch_bounds__(kThreads, 3)
+    qk_norm_rope_rows_bwd_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Rows rows) {
+    constexpr int kLanes = D / 8, kElem = F32 ? 4 : 2, kAhead = F32 ? 2 : 4;
+    __shared__ __align__(16) float w[2][D];
+    __shared__ float sums[kWarps][2][D];
+    const int lane = threadIdx.x % 32, grp = lane / kLanes;
+    int ea, eb;
+    lane_groups<D, INTER>(a.rot, lane % kLanes, ea, eb);
+    const int gap = (eb - ea) * kElem;
+    const LanePairs<D, AXES> pairs(a, lane % kLanes);
+    griddep_wait();
+    griddep_launch_dependents();
+    auto load = [&](const RowPlace<AXES>& at, Raw<F32>(&rx)[kAhead], Raw<F32>(&rg)[kAhead]) {
+        const char* src = static_cast<const char*>(a.qkv) + ((static_cast<size_t>(at.tk) * rows.all + at.p) * D + ea) * kElem;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const Raw<true> v = pack<true, INTER>(dw[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float t = __uint_as_float(v.u[e]);
-#pragma unroll
-            for (int off = kLanes; off < 32; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-            if (grp == 0) sums[warp][i][(e < 4 ? ea : eb - 4) + e] = t;
+        for (int u = 0; u < kAhead; ++u) {
+            const int p = at.p + u, seg = (p >= a.heads[0]) + (p >= a.heads[0] + a.heads[1]);
+            const bool valid = u < at.count && at.there;
+            const char* grad = static_cast<const char*>(seg == 0 ? a.grad[0] : seg == 1 ? a.grad[1] : a.grad[2]) +
+                               (head_row(a, seg, p, at.b, at.n) * D + ea) * kElem;
+            rx[u] = load8<F32>(src + u * D * kElem, src + gap + u * D * kElem, valid && seg < 2);
+            rg[u] = load8<F32>(grad, grad + gap, valid);
         }
+    };
+    RowPlace<AXES> at;
+    row_place(a, rows, pairs, blockIdx.x * kWarps + threadIdx.x / 32, grp, at);
+    Raw<F32> rx[kAhead], rg[kAhead];
+    load(at, rx, rg);
+    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+        const float* src = x < D ? a.weight[0] : a.weight[1];
+        w[x / D][x % D] = src ? src[x % D] : 1.f;
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
-        float v = 0.f;
+
+    float2 c[2], s[2];
+    Quad dw[2];
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) v += sums[k][x / D][x % D];
-        a.part[static_cast<size_t>(blockIdx.x) * 2 * D + x] = v;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) dw[i].first[k] = dw[i].second[k] = make_float2(0.f, 0.f);
+    while (at.g < rows.groups) {
+        const RowPlace<AXES> next = row_after(a, rows, pairs, at, gridDim.x * kWarps, grp);
+        Raw<F32> nx[kAhead], ng[kAhead];
+        load(next, nx, ng);
+        if (at.p == 0) pairs.angles(at.pos, c, s);
+        char* dst = static_cast<char*>(a.dqkv) + ((static_cast<size_t>(at.tk) * rows.all + at.p) * D + ea) * kElem;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (u >= at.count) break;
+            const int p = at.p + u, seg = (p >= a.heads[0]) + (p >= a.heads[0] + a.heads[1]);
+            if (seg < 2) {
+                float2 wf[2], ws[2];
+                lane_weights<D, INTER>(w, seg, ea, eb, wf, ws);
+                const Quad x = unpack<F32, INTER>(rx[u]), dy = unpack<F32, INTER>(rg[u]);
+                rg[u] = pack<F32, INTER>(row_gradient<kLanes>(x, dy, c, s, wf, ws, a.eps, at.there, seg, dw));
+            }
+            if (at.there) store8<F32>(dst + u * D * kElem, dst + gap + u * D * kElem, rg[u]);
+        }
+        at = next;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            rx[u] = nx[u];
+            rg[u] = ng[u];
+        }
     }
+    if (a.part == nullptr) return;
+    block_sums<D, INTER>(dw, sums, ea, eb, a.part);
 }
 
 // Sum of `rows` partial rows of 2 D values: a block owns 8 columns, 32 threads each, which have 16
@@ -523,7 +762,7 @@ __global__ void __launch_bounds__(256)
 // 69).  That is all of a token's passes where there are many tokens, and one pass a warp for one
 // token of 40 heads.  Against filling 32 warps an SM, d = 128, H 32 / 8: 512 tokens 5.4 us for 7.1,
 // 2000 tokens 11.6 for 13.9, their gradient 19.7 for 20.7, that of 500 tokens 7.6 for 9.2.
-Split split_passes(const NormRopeArgs& a, int d, long long warps) {
+Split split_passes(const NormRopeArgs& a, int d, long long warps, long long* cost_of) {
     const int per_pass = 256 / d;  // heads of one pass
     Split sp;
     sp.first[0] = 0;
@@ -542,10 +781,24 @@ Split split_passes(const NormRopeArgs& a, int d, long long warps) {
         chunks += chunks < 4 ? 1 : chunks / 2;
         if (chunks > all || chunks > 63) chunks = all;
     }
+    *cost_of = least;
     sp.chunks = (all + sp.per - 1) / sp.per;
     sp.by_tokens = make_div(a.tokens);
     sp.by_n = make_div(a.N);
     return sp;
+}
+
+// The rows kernels' work, in passes of the busiest warp as above.
+Rows split_rows(const NormRopeArgs& a, int d, int ahead, long long warps, long long* cost_of) {
+    const uint32_t together = 256 / d;
+    Rows r;
+    r.all = a.heads[0] + 2 * a.heads[1];
+    const int batches = (r.all + ahead - 1) / ahead;
+    r.per = (r.all + batches - 1) / batches;
+    r.groups = a.tokens / together + (a.tokens % together != 0);
+    r.by_n = make_div(a.N);
+    *cost_of = (r.groups + warps - 1) / warps * (r.all + 4);
+    return r;
 }
 
 // CTAs of a kernel that are resident together on the current device, asked once per device.
@@ -566,32 +819,46 @@ cudaError_t resident_ctas(K kernel, std::atomic<int> (&known)[64], int* sms, int
     return cudaSuccess;
 }
 
+int grid_of(long long warps, int cap) {
+    const long long blocks = (warps + kWarps - 1) / kWarps;
+    return static_cast<int>(blocks < cap ? blocks : cap);
+}
+
 template <int D, bool F32, bool INTER, int AXES>
 cudaError_t launch_fwd(const NormRopeArgs& a, cudaStream_t s) {
-    static std::atomic<int> known[64];
-    int sms = 0, cap = 0;
-    const cudaError_t e = resident_ctas(qk_norm_rope_kernel<D, F32, INTER, AXES>, known, &sms, &cap);
+    static std::atomic<int> known[64], known_rows[64];
+    int sms = 0, cap = 0, cap_rows = 0;
+    cudaError_t e = resident_ctas(qk_norm_rope_kernel<D, F32, INTER, AXES>, known, &sms, &cap);
+    if (e == cudaSuccess) e = resident_ctas(qk_norm_rope_rows_kernel<D, F32, INTER, AXES>, known_rows, &sms, &cap_rows);
     if (e != cudaSuccess) return e;
-    const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps);
-    const long long blocks = (static_cast<long long>(a.tokens) * sp.chunks + kWarps - 1) / kWarps;
-    return launch_pdl(qk_norm_rope_kernel<D, F32, INTER, AXES>, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
-                      dim3(kThreads), 0, s, a, sp);
+    long long cost = 0, cost_rows = 0;
+    const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps, &cost);
+    const Rows rows = split_rows(a, D, F32 ? 2 : 8, static_cast<long long>(cap_rows) * kWarps, &cost_rows);
+    if (cost_rows < cost)
+        return launch_pdl(qk_norm_rope_rows_kernel<D, F32, INTER, AXES>, dim3(grid_of(rows.groups, cap_rows)), dim3(kThreads),
+                          0, s, a, rows);
+    return launch_pdl(qk_norm_rope_kernel<D, F32, INTER, AXES>,
+                      dim3(grid_of(static_cast<long long>(a.tokens) * sp.chunks, cap)), dim3(kThreads), 0, s, a, sp);
 }
 
 template <int D, bool F32, bool INTER, int AXES>
 cudaError_t launch_bwd(NormRopeArgs a, float* const (&dweight)[2], cudaStream_t s) {
-    static std::atomic<int> known[64];
-    int sms = 0, cap = 0;
-    const cudaError_t e = resident_ctas(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, known, &sms, &cap);
+    static std::atomic<int> known[64], known_rows[64];
+    int sms = 0, cap = 0, cap_rows = 0;
+    cudaError_t e = resident_ctas(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, known, &sms, &cap);
+    if (e == cudaSuccess) e = resident_ctas(qk_norm_rope_rows_bwd_kernel<D, F32, INTER, AXES>, known_rows, &sms, &cap_rows);
     if (e != cudaSuccess) return e;
-    const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps);
-    const bool want = dweight[0] != nullptr || dweight[1] != nullptr;
+    long long cost = 0, cost_rows = 0;
+    const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps, &cost);
+    const Rows rows = split_rows(a, D, F32 ? 2 : 4, static_cast<long long>(cap_rows) * kWarps, &cost_rows);
+    const bool want = dweight[0] != nullptr || dweight[1] != nullptr, by_rows = a.any_order && cost_rows < cost;
     if (!want) a.part = nullptr;
-    const long long blocks = (static_cast<long long>(a.tokens) * sp.chunks + kWarps - 1) / kWarps;
+    if (by_rows) cap = cap_rows;
     if (cap > kBwdMaxBlocks) cap = kBwdMaxBlocks;
-    const int grid = static_cast<int>(blocks < cap ? blocks : cap);
-    const cudaError_t e2 = launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, dim3(grid), dim3(kThreads), 0, s, a, sp);
-    if (e2 != cudaSuccess || !want) return e2;
+    const int grid = grid_of(by_rows ? rows.groups : static_cast<long long>(a.tokens) * sp.chunks, cap);
+    e = by_rows ? launch_pdl(qk_norm_rope_rows_bwd_kernel<D, F32, INTER, AXES>, dim3(grid), dim3(kThreads), 0, s, a, rows)
+                : launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, dim3(grid), dim3(kThreads), 0, s, a, sp);
+    if (e != cudaSuccess || !want) return e;
     return launch_pdl(dweight_sum_kernel<D>, dim3(2 * D / 8), dim3(256), 0, s, a.part, grid, dweight[0],
                       dweight[1]);
 }
