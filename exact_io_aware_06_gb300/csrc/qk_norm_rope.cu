@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 // that no lane is idle where heads do not fill a pass of one token, no batch ends with Q's or K's heads, and the
 // work for a token (its place, position, cosines and sines, four pairs a lane) is shared by 32 / (D / 8) of them.
 struct Rows {
-    int all, per;         // heads of a token, Q's, K's and V's; passes of a batch
-    uint32_t groups;      // of 32 / (D / 8) tokens
-    Div by_n;
+    int all, per, batch;      // heads of a token, Q's, K's and V's; passes of an item; of a batch of loads
+    uint32_t groups, items;   // of 32 / (D / 8) tokens; all groups' first passes, then their next ones
+    Div by_groups, by_n;
 };
 // The lane's four pairs, and its place: a batch of passes of its token.
 template <int D, int AXES>
@@ -383,20 +383,23 @@ struct LanePairs {
 };
 template <int AXES>
 struct RowPlace {
-    uint32_t g, tk, b;
-    int n, p, count;
+    uint32_t it, tk, b;
+    int n, p, p1, count;
     int pos[AXES == 2 ? 4 : 1];
-    bool there;
+    bool there, fresh;
 };
 template <int D, int AXES>
-__device__ __forceinline__ void row_place(const NormRopeArgs& a, const Rows& r, const LanePairs<D, AXES>& pairs, uint32_t g,
+__device__ __forceinline__ void row_place(const NormRopeArgs& a, const Rows& r, const LanePairs<D, AXES>& pairs, uint32_t it,
                                           int grp, RowPlace<AXES>& p) {
     constexpr int kTokens = 32 / (D / 8);
-    p.g = g;
-    p.p = 0;
-    p.count = min(r.per, r.all);
-    p.tk = g * kTokens + grp;
-    p.there = g < r.groups && p.tk < a.tokens;
+    const uint32_t chunk = r.by_groups.of(min(it, r.items - 1));
+    p.it = it;
+    p.p = static_cast<int>(chunk) * r.per;
+    p.p1 = min(p.p + r.per, r.all);
+    p.count = min(r.batch, p.p1 - p.p);
+    p.tk = (it - chunk * r.groups) * kTokens + grp;
+    p.fresh = true;
+    p.there = it < r.items && p.tk < a.tokens;
     if (!p.there) p.tk = 0;
     p.b = r.by_n.of(p.tk);
     p.n = static_cast<int>(p.tk - p.b * r.by_n.d);
@@ -412,11 +415,12 @@ template <int D, int AXES>
 __device__ __forceinline__ RowPlace<AXES> row_after(const NormRopeArgs& a, const Rows& r, const LanePairs<D, AXES>& pairs,
                                                     const RowPlace<AXES>& at, uint32_t step, int grp) {
     RowPlace<AXES> p = at;
-    if (at.p + at.count >= r.all) {
-        row_place(a, r, pairs, at.g + step, grp, p);
+    if (at.p + at.count >= at.p1) {
+        row_place(a, r, pairs, at.it + step, grp, p);
     } else {
         p.p += at.count;
-        p.count = min(r.per, r.all - p.p);
+        p.count = min(r.batch, at.p1 - p.p);
+        p.fresh = false;
     }
     return p;
 }
@@ -466,11 +470,11 @@ __global__ void __launch_bounds__(kThreads, 4)
     __syncthreads();
 
     float2 c[2], s[2];
-    while (at.g < rows.groups) {
+    while (at.it < rows.items) {
         const RowPlace<AXES> next = row_after(a, rows, pairs, at, gridDim.x * kWarps, grp);
         Raw<F32> ahead[kAhead];
         load(next, ahead);
-        if (at.p == 0) pairs.angles(at.pos, c, s);
+        if (at.fresh) pairs.angles(at.pos, c, s);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (u >= at.count) break;
@@ -693,11 +697,11 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) dw[i].first[k] = dw[i].second[k] = make_float2(0.f, 0.f);
-    while (at.g < rows.groups) {
+    while (at.it < rows.items) {
         const RowPlace<AXES> next = row_after(a, rows, pairs, at, gridDim.x * kWarps, grp);
         Raw<F32> nx[kAhead], ng[kAhead];
         load(next, nx, ng);
-        if (at.p == 0) pairs.angles(at.pos, c, s);
+        if (at.fresh) pairs.angles(at.pos, c, s);
         char* dst = static_cast<char*>(a.dqkv) + ((static_cast<size_t>(at.tk) * rows.all + at.p) * D + ea) * kElem;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -762,42 +766,49 @@ __global__ void __launch_bounds__(256)
 // 69).  That is all of a token's passes where there are many tokens, and one pass a warp for one
 // token of 40 heads.  Against filling 32 warps an SM, d = 128, H 32 / 8: 512 tokens 5.4 us for 7.1,
 // 2000 tokens 11.6 for 13.9, their gradient 19.7 for 20.7, that of 500 tokens 7.6 for 9.2.
-Split split_passes(const NormRopeArgs& a, int d, long long warps, long long* cost_of) {
-    const int per_pass = 256 / d;  // heads of one pass
-    Split sp;
-    sp.first[0] = 0;
-    for (int i = 0; i < 3; ++i) sp.first[i + 1] = sp.first[i] + (a.heads[i] + per_pass - 1) / per_pass;
-    const int all = sp.first[3];
+int least_per(long long tokens, int all, long long warps, int edge, long long* cost_of) {
     long long least = -1;
+    int least_of = all;
     for (int chunks = 1;;) {  // 1, 2, 3, 4, 6, 9, ... 63, all
         const int per = (all + chunks - 1) / chunks;
-        const long long runs = static_cast<long long>(a.tokens) * ((all + per - 1) / per);
-        const long long cost = (runs + warps - 1) / warps * (per + 3);
+        const long long runs = tokens * ((all + per - 1) / per);
+        const long long cost = (runs + warps - 1) / warps * (per + edge);
         if (least < 0 || cost < least) {
             least = cost;
-            sp.per = per;
+            least_of = per;
         }
         if (chunks >= all) break;
         chunks += chunks < 4 ? 1 : chunks / 2;
         if (chunks > all || chunks > 63) chunks = all;
     }
     *cost_of = least;
+    return least_of;
+}
+Split split_passes(const NormRopeArgs& a, int d, long long warps, long long* cost_of) {
+    const int per_pass = 256 / d;  // heads of one pass
+    Split sp;
+    sp.first[0] = 0;
+    for (int i = 0; i < 3; ++i) sp.first[i + 1] = sp.first[i] + (a.heads[i] + per_pass - 1) / per_pass;
+    const int all = sp.first[3];
+    sp.per = least_per(a.tokens, all, warps, 3, cost_of);
     sp.chunks = (all + sp.per - 1) / sp.per;
     sp.by_tokens = make_div(a.tokens);
     sp.by_n = make_div(a.N);
     return sp;
 }
 
-// The rows kernels' work, in passes of the busiest warp as above.
+// The rows kernels' work, in the same way.
 Rows split_rows(const NormRopeArgs& a, int d, int ahead, long long warps, long long* cost_of) {
     const uint32_t together = 256 / d;
     Rows r;
     r.all = a.heads[0] + 2 * a.heads[1];
-    const int batches = (r.all + ahead - 1) / ahead;
-    r.per = (r.all + batches - 1) / batches;
     r.groups = a.tokens / together + (a.tokens % together != 0);
+    r.per = least_per(r.groups, r.all, warps, 4, cost_of);
+    const int batches = (r.per + ahead - 1) / ahead;
+    r.batch = (r.per + batches - 1) / batches;
+    r.items = r.groups * ((r.all + r.per - 1) / r.per);
+    r.by_groups = make_div(r.groups);
     r.by_n = make_div(a.N);
-    *cost_of = (r.groups + warps - 1) / warps * (r.all + 4);
     return r;
 }
 
@@ -835,7 +846,7 @@ cudaError_t launch_fwd(const NormRopeArgs& a, cudaStream_t s) {
     const Split sp = split_passes(a, D, static_cast<long long>(cap) * kWarps, &cost);
     const Rows rows = split_rows(a, D, F32 ? 2 : 8, static_cast<long long>(cap_rows) * kWarps, &cost_rows);
     if (cost_rows < cost)
-        return launch_pdl(qk_norm_rope_rows_kernel<D, F32, INTER, AXES>, dim3(grid_of(rows.groups, cap_rows)), dim3(kThreads),
+        return launch_pdl(qk_norm_rope_rows_kernel<D, F32, INTER, AXES>, dim3(grid_of(rows.items, cap_rows)), dim3(kThreads),
                           0, s, a, rows);
     return launch_pdl(qk_norm_rope_kernel<D, F32, INTER, AXES>,
                       dim3(grid_of(static_cast<long long>(a.tokens) * sp.chunks, cap)), dim3(kThreads), 0, s, a, sp);
@@ -855,7 +866,7 @@ cudaError_t launch_bwd(NormRopeArgs a, float* const (&dweight)[2], cudaStream_t 
     if (!want) a.part = nullptr;
     if (by_rows) cap = cap_rows;
     if (cap > kBwdMaxBlocks) cap = kBwdMaxBlocks;
-    const int grid = grid_of(by_rows ? rows.groups : static_cast<long long>(a.tokens) * sp.chunks, cap);
+    const int grid = grid_of(by_rows ? rows.items : static_cast<long long>(a.tokens) * sp.chunks, cap);
     e = by_rows ? launch_pdl(qk_norm_rope_rows_bwd_kernel<D, F32, INTER, AXES>, dim3(grid), dim3(kThreads), 0, s, a, rows)
                 : launch_pdl(qk_norm_rope_bwd_kernel<D, F32, INTER, AXES>, dim3(grid), dim3(kThreads), 0, s, a, sp);
     if (e != cudaSuccess || !want) return e;
