@@ -792,6 +792,8 @@ Split split_passes(const NormRopeArgs& a, int d, long long warps, long long* cos
     const int all = sp.first[3];
     sp.per = least_per(a.tokens, all, warps, 3, cost_of);
     sp.chunks = (all + sp.per - 1) / sp.per;
+    // against the rows kernels: batches of one pass for K and for V cost their latency once more
+    if (sp.first[2] - sp.first[1] == 1) *cost_of += 2 * ((static_cast<long long>(a.tokens) * sp.chunks + warps - 1) / warps);
     sp.by_tokens = make_div(a.tokens);
     sp.by_n = make_div(a.N);
     return sp;

@@ -358,7 +358,8 @@ int fa_qk_norm_rope_axes(const void* qkv, const float* q_weight, const float* k_
                          int interleaved, float eps, int dtype, void* stream);
 
 /*
- * Gradient of fa_qk_norm_rope_axes, as fa_qk_norm_rope_bwd, whose workspace size holds here too.
+ * Gradient of fa_qk_norm_rope_axes, as fa_qk_norm_rope_bwd, whose workspace size holds here too.  The same
+ * bits every time; against fa_qk_norm_rope_bwd's the weights' gradients may add up in another order.
  */
 int fa_qk_norm_rope_axes_bwd(const void* qkv, const float* q_weight, const float* k_weight,
                              const int* positions, const double* inv_freq, const int* axis,

@@ -109,8 +109,29 @@ def test_equal_axes_give_the_single_axis_bit_for_bit(axes, interleaved):
     dqkv2, dw2 = torch.empty_like(dqkv), [torch.empty_like(x) for x in dw]
     ws = torch.empty(fa.fa_qk_norm_rope_bwd_workspace_size(B, H, H_kv, N, d), dtype=torch.uint8, device="cuda")
     fa.fa_qk_norm_rope_bwd(qkv, qw, kw, one[0], f, *up, dqkv2, *dw2, ws, 1e-6, interleaved)
-    for a, b in zip([*out, dqkv, *dw], [*out2, dqkv2, *dw2]):
+    # (the weights' gradients, sums over all heads and tokens in an order of each call's own, are checked by run_both)
+    for a, b in zip([*out, dqkv], [*out2, dqkv2]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,N,H,H_kv,d,sections", [(3, 3335, 1, 1, 64, [16, 48]), (2, 5001, 3, 1, 128, [128]), (1, 9999, 7, 2, 64, [32]),
+                                                   (5, 601, 8, 8, 128, [32, 48, 16])])
+def test_many_tokens_of_few_heads(B, N, H, H_kv, d, sections, interleaved, dtype):
+    # where the tokens do not fill the last group of lanes, and a group holds tokens of two batches
+    qkv, qw, kw, up, out, dqkv, dw = run_both(B, N, H, H_kv, d, dtype, sections, interleaved)
+    pos, (f, axis) = grid_positions(len(sections), B, N), fa.rope_axes(sections)
+    for again in range(2):
+        dqkv2, dw2 = torch.empty_like(dqkv), [torch.empty_like(x) for x in dw]
+        ws = torch.full((fa.fa_qk_norm_rope_bwd_workspace_size(B, H, H_kv, N, d),), 255, dtype=torch.uint8, device="cuda")
+        fa.fa_qk_norm_rope_axes_bwd(qkv, qw, kw, pos, f, axis, *up, dqkv2, *dw2, ws, 1e-6, interleaved)
+        for a, b in zip([dqkv, *dw], [dqkv2, *dw2]):
+            assert torch.equal(a, b)
+    # the same rows as in another call of one batch (another place in the group)
+    out2 = nr.outputs(1, N, H, H_kv, d, qkv.dtype)
+    fa.fa_qk_norm_rope_axes(qkv[-1:], qw, kw, pos[:, -1:].clone(), f, axis, *out2, 1e-6, interleaved)
+    assert all(torch.equal(a[-1:], b) for a, b in zip(out, out2))
 
 
 def test_without_rotation():
