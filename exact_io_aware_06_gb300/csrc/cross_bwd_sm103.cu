@@ -114,13 +114,14 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const PrepArgs a) {
 
 // What was dealt in pieces: the float32 parts added in order, times a factor, rounded once.  blockIdx.x: dV and dK
 // of every key block, then dQ of every query block.  A warp takes 8 rows x 32 columns, whole lines of the parts
-// and 64-byte runs of the result.
-constexpr int kJoinSplit = 4;  // CTAs of a block
-template <int D>
+// and 64-byte runs of the result, of every WARPS-th part; the warps' sums meet in shared memory.  Few blocks of
+// many parts need more than a warp a tile: 2 blocks of 53 33 -> 7 us, 6 of 25 at d = 128 31 -> 8.
+template <int D, int WARPS>
 __global__ void __launch_bounds__(256) cross_bwd_join_kernel(const CrossBwdArgs a, void* const dq, const int key_places) {
-    griddep_wait();
     constexpr int kCols = D / 32, kTiles = kCols * (kBlk / 8);
-    const int lane = threadIdx.x % 32;
+    __shared__ float4 sums[WARPS > 1 ? 8 : 1][2][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, first = warp % WARPS;
+    griddep_wait();
     const float4* src;
     uint4* out;  // of the block's first row
     int rows, n;
@@ -144,21 +145,42 @@ __global__ void __launch_bounds__(256) cross_bwd_join_kernel(const CrossBwdArgs 
         n = (blocks + a.per_q - 1) / a.per_q;
     }
     const int step = (static_cast<int>(blockIdx.x) < key_places ? 2 : 1) * (kBlk * D / 4);
-    for (int tile = blockIdx.y * 8 + threadIdx.x / 32; tile < kTiles; tile += kJoinSplit * 8) {
-        const int row = tile / kCols * 8 + lane % 8, vec = tile % kCols * 4 + lane / 8;
-        if (row >= rows) continue;
-        const float4* p = src + 2 * vec * kBlk + row;
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
+    const int tile = blockIdx.y * (8 / WARPS) + warp / WARPS;
+    const int row = tile / kCols * 8 + lane % 8, vec = tile % kCols * 4 + lane / 8;
+    static_assert(kTiles % (8 / WARPS) == 0, "whole CTAs");
+    const float4* p = src + 2 * vec * kBlk + row + static_cast<size_t>(first) * step;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
+    if (row < rows) {
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
+        for (int i = first; i < n; i += WARPS) {
             const float4 y = p[0], z = p[kBlk];
             u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
             w.x += z.x, w.y += z.y, w.z += z.z, w.w += z.w;
-            p += step;
+            p += static_cast<size_t>(WARPS) * step;
         }
+    }
+    if constexpr (WARPS > 1) {
+        sums[warp][0][lane] = u;
+        sums[warp][1][lane] = w;
+        __syncthreads();
+        if (first > 0) return;
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) {
+            const float4 y = sums[warp + i][0][lane], z = sums[warp + i][1][lane];
+            u.x += y.x, u.y += y.y, u.z += y.z, u.w += y.w;
+            w.x += z.x, w.y += z.y, w.z += z.z, w.w += z.w;
+        }
+    }
+    if (row < rows)
         out[row * (D / 8) + vec] = make_uint4(pack_bf16x2(u.x * f, u.y * f), pack_bf16x2(u.z * f, u.w * f),
                                               pack_bf16x2(w.x * f, w.y * f), pack_bf16x2(w.z * f, w.w * f));
-    }
+}
+template <int D>
+cudaError_t join(const CrossBwdArgs& a, void* dq, int key_places, int places, cudaStream_t s) {
+    constexpr int kTiles = D / 32 * (kBlk / 8);
+    const int most = a.pieces > a.pieces_q ? a.pieces : a.pieces_q;
+    if (most >= 8) return launch_pdl(cross_bwd_join_kernel<D, 8>, dim3(places, kTiles), dim3(256), 0, s, a, dq, key_places);
+    return launch_pdl(cross_bwd_join_kernel<D, 1>, dim3(places, kTiles / 8), dim3(256), 0, s, a, dq, key_places);
 }
 
 // delta and lse rows in bytes; the parts follow
@@ -256,8 +278,11 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
     if (rc == 0 && d == 64) rc = make_map_3d(&tdk, dk, dt, 2, d, N_kv, a.BH_kv, 64, 32);
     if (rc == 0 && d == 64) rc = make_map_3d(&tdv, dv, dt, 2, d, N_kv, a.BH_kv, 64, 32);
     if (rc != 0) return rc;
+    // CTAs for the rows, or for the key blocks that may have to be zeroed (few rows on long ragged sequences)
+    const int for_rows = grid_for(static_cast<size_t>(heads) * (a.Np / 16), 8, sms * 8);
+    const int for_keys = lengths ? grid_for(static_cast<size_t>(a.BH_kv) * a.n_k, 1, sms * 4) : 0;
     e = launch_pdl(d == 64 ? cross_bwd_prep_kernel<64> : cross_bwd_prep_kernel<128>,
-                   dim3(grid_for(static_cast<size_t>(heads) * (a.Np / 16), 8, sms * 8)), dim3(256), 0, s, pa);
+                   dim3(for_rows > for_keys ? for_rows : for_keys), dim3(256), 0, s, pa);
     if (e != cudaSuccess) return static_cast<int>(e);
     const int n_items = a.BH_kv * a.n_k * a.pieces;
     const int grid = n_items < sms ? n_items : sms;
@@ -273,8 +298,7 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
     const int key_places = a.pieces > 1 ? 2 * a.BH_kv * a.n_k : 0;
     const int places = key_places + (a.pieces_q > 1 ? heads * a.n_q : 0);
     if (e != cudaSuccess || places == 0) return static_cast<int>(e);
-    return static_cast<int>(launch_pdl(d == 64 ? cross_bwd_join_kernel<64> : cross_bwd_join_kernel<128>,
-                                       dim3(places, kJoinSplit), dim3(256), 0, s, a, dq, key_places));
+    return static_cast<int>(d == 64 ? join<64>(a, dq, key_places, places, s) : join<128>(a, dq, key_places, places, s));
 }
 
 }  // namespace fa
