@@ -13,12 +13,13 @@
 //     16 x 16384 x 16384.
 //   * Many rows on few keys (2 x 16384 video tokens on 77 to 512): an item's end, 3,800 cycles of its softmax
 //     warpgroups (O's last product, its way out, the next scores), beside 6,000 for four blocks.  O leaves in boxes
-//     by TMA, so that the warps go on while it is stored: 101 -> 95 us, floor 42.
+//     by TMA, so that the warps go on while it is stored: 101 -> 95 us, 92 now, floor 42.
 //   * Few rows on many keys: HBM, at the rate that 152 SMs can have loads in flight.  The key blocks of all items
-//     are cut into equal runs (64 ragged single tokens: 185 us, 91% of the copy rate), whose float32 parts a
-//     join adds up in a fixed order.
-//   * Few rows on few keys: latency, of which the join's launch is the largest piece that can be spared: clusters
-//     (one token of 16 heads on 1500 keys: 9.6 us, 10.7 with the join).
+//     are cut into equal runs (64 ragged single tokens on 500-8192 keys: 175 us, 96% of the copy rate), whose
+//     float32 parts a join adds up in a fixed order.
+//   * Few rows on few keys: latency: 8.2 us for one token of 16 heads on 1500 keys, of which the start takes 0.3,
+//     the segments 0.7, the first loads 0.7 to 1.5, a block 1, joining in a cluster 1.  Much of each is instructions
+//     fetched for the first time.
 #include <type_traits>
 
 #include "cross_fwd.cuh"
