@@ -664,6 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             gj += i;
             gb += n + 1;
+            // a whole item's lse, while its last P V runs
+            const bool by_box = !solo && args.nb == 1 && seg.whole();
+            if (by_box && args.lse != nullptr && row < seg.rows[tile].rows) {
+                const TileRows T = seg.rows[tile];
+                args.lse[static_cast<size_t>(T.b * args.H_kv + seg.h) * args.R + (T.r0 + row)] = row_lse(m_ref, l);
+            }
             if (ok && i > 0) {
                 ok = mbar_wait(smem_u32(&bars.o_done[t]), kd & 1, lim, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -722,12 +728,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ml[args.part_rows + to] = l;
             } else if (busy) {
                 const float f = row_factor(l);
-                if (!solo && args.nb == 1) {
+                if (by_box) {
                     const TileRows T = seg.rows[tile];
-                    const int bh = T.b * args.H_kv + seg.h;
-                    store_boxes<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, col, f, T.r0 + wq * 32, bh, args.R);
-                    if (row < T.rows && args.lse != nullptr)
-                        args.lse[static_cast<size_t>(bh) * args.R + (T.r0 + row)] = row_lse(m_ref, l);
+                    store_boxes<D>(tm_o, smem_base + C::kOffO + (warp - 4) * 4096, col, f, T.r0 + wq * 32,
+                                   T.b * args.H_kv + seg.h, args.R);
                 } else {
                     const long long at = place(seg, tile);
                     store_weighted<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
