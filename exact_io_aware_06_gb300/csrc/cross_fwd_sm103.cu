@@ -58,7 +58,7 @@ struct Bars {
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     uint64_t q_full[2], q_free[2];  // of a tile's Q: landed; read by its last S
     uint64_t kv_full[STAGES], kv_empty[STAGES];
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
     uint64_t merge_ml, merge_done;  // one tile: warpgroup 1's state is in shared memory; its O was read
     uint64_t drain;
 };
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars.q_full[t]), 1);
             mbar_init(smem_u32(&bars.q_free[t]), 1);
             mbar_init(smem_u32(&bars.s_full[t]), 1);
+            mbar_init(smem_u32(&bars.p_half[t]), 128);
             mbar_init(smem_u32(&bars.p_full[t]), 128);
             mbar_init(smem_u32(&bars.o_done[t]), 1);
         }
@@ -473,16 +474,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mma_commit(smem_u32(&bars.s_full[t]));
                 };
-                auto issue_pv = [&](int t, int u, bool acc) {
+                // O_t += P_t V, each half of the keys as soon as its P is there
+                auto issue_pv = [&](int t, int u, bool acc, uint32_t par) -> bool {
                     const uint32_t vl = v_lo + u * (C::kTileBytes >> 4);
                     const uint32_t colO = tmem + C::kColO + D * t, colP = tmem + C::kColS + 128 * t;
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk) {
+                        if (kk % (kBN / 32) == 0) {
+                            if (!mbar_wait(smem_u32(kk == 0 ? &bars.p_half[t] : &bars.p_full[t]), par, lim, &abort_flag)) return false;
+                            tc_fence_after();
+                        }
                         if (kk == 0)
                             mma_ts_w<false, -1>(colO, colP, vl, kDescHi, C::kIdescO, acc ? 1u : 0u);
                         else
                             mma_ts_w<false, 1>(colO, colP + kk * 8, vl + ((kk * 16 * 128) >> 4), kDescHi, C::kIdescO);
                     }
+                    return true;
                 };
                 int gb = 0, kq0 = 0, kq1 = 0;
                 int c0 = 0, c1 = 0;    // blocks of warpgroup 0 / 1 before the segment
@@ -493,17 +500,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     constexpr bool more = decltype(more_c)::value, last2 = decltype(last2_c)::value;
                     const int u = g1 % kStages;
                     if (!mbar_wait(smem_u32(&bars.kv_full[u]), (g1 / kStages) & 1, lim, &abort_flag)) return false;
-                    if (!mbar_wait(smem_u32(&bars.p_full[0]), p0, lim, &abort_flag)) return false;
-                    tc_fence_after();
-                    issue_pv(0, u, j > 0 || begun);
+                    if (!issue_pv(0, u, j > 0 || begun, p0)) return false;
                     if constexpr (more)
                         issue_s(0, 0, u);
                     else
                         mma_commit(smem_u32(&bars.o_done[0]));
                     if constexpr (last2) mma_commit(smem_u32(&bars.q_free[0]));
-                    if (!mbar_wait(smem_u32(&bars.p_full[1]), p1, lim, &abort_flag)) return false;
-                    tc_fence_after();
-                    issue_pv(1, u, j > 0 || begun);
+                    if (!issue_pv(1, u, j > 0 || begun, p1)) return false;
                     if constexpr (more)
                         issue_s(1, 1, u);
                     else
@@ -549,10 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (i == n - 1) mma_commit(smem_u32(&bars.q_free[0]));
                             }
                             const int j = i - 1, t = j & 1;
-                            ok = mbar_wait(smem_u32(&bars.p_full[t]), ((t ? c1 : c0) + j / 2) & 1, lim, &abort_flag);
+                            ok = issue_pv(t, u, j >= 2 || (j == 0 && begun), ((t ? c1 : c0) + j / 2) & 1);
                             if (!ok) break;
-                            tc_fence_after();
-                            issue_pv(t, u, j >= 2 || (j == 0 && begun));
                             if (j + 2 >= n) mma_commit(smem_u32(&bars.o_done[t]));  // the warpgroup's last
                             mma_commit(smem_u32(&bars.kv_empty[u]));
                         }
@@ -658,7 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (busy)
                     softmax_block<D, kBN>(lane_base, colS, colS, colO, c, c_pos, mask_bits, valid - 1, -1, 0, i == 0 && !begun,
-                                          m_ref, l, [] {}, [] { return true; });
+                                          m_ref, l, [] {}, [] { return true; }, [&] {
+                                              tc_fence_before();
+                                              mbar_arrive(smem_u32(&bars.p_half[t]));
+                                          });
+                else
+                    mbar_arrive(smem_u32(&bars.p_half[t]));
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.p_full[t]));
             }

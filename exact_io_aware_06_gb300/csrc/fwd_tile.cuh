@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -50,6 +51,20 @@ __device__ __forceinline__ void ld32_at(uint32_t taddr, uint32_t (&r)[NC]) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float max3f(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -94,11 +109,13 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 // One key block for one row: NC raw scores (columns colS ..) to P (columns colP ..), the reference
 // maximum, the sum and, where the reference moves, O.  `taken` is called once the scores are in
 // registers; `free` before P and O are written, true when P V of the tile's last block is done.
-// Returns false when `free` did.
-template <int D, int NC, class Taken, class Free>
+// Returns false when `free` did.  With `half` O is rescaled first, and it is called once the first 64 columns of
+// P are in TMEM, so that P V can begin.
+struct NoHalf {};
+template <int D, int NC, class Taken, class Free, class Half = NoHalf>
 __device__ __forceinline__ bool softmax_block(uint32_t lane_base, uint32_t colS, uint32_t colP, uint32_t colO, float c,
                                               bool c_pos, uint32_t mask_bits, int hi, int lo, int sink, bool first,
-                                              float& m_ref, float& l, Taken taken, Free free) {
+                                              float& m_ref, float& l, Taken taken, Free free, Half half = {}) {
     uint32_t r[NC];
     ld32_at<0>(lane_base + colS, r);
     if constexpr (NC == 128) {
@@ -130,6 +147,19 @@ __device__ __forceinline__ bool softmax_block(uint32_t lane_base, uint32_t colS,
         m_ref = mt;
         l *= alpha;
     }
+    constexpr bool kHalf = !std::is_same<Half, NoHalf>::value;
+    if constexpr (kHalf) {
+        if (!first && __any_sync(0xffffffffu, bump)) {  // (with the scores in registers: few columns at a time)
+#pragma unroll 1
+            for (int q = 0; q < D; q += 8) {
+                uint32_t ov[8];
+                tmem_ld8(lane_base + colO + q, ov);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                tmem_st8(lane_base + colO + q, ov);
+            }
+        }
+    }
     const float ref = (m_ref == -INFINITY) ? 0.f : m_ref;
     const float2 c2 = make_float2(c, c), nref2 = make_float2(-ref, -ref);
     float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
@@ -153,8 +183,14 @@ __device__ __forceinline__ bool softmax_block(uint32_t lane_base, uint32_t colS,
             tmem_st16(lane_base + colP, pk);
         else
             tmem_st32(lane_base + colP + 32 * h, pk);
+        if constexpr (kHalf) {
+            if (h == 0) {
+                tmem_st_wait();
+                half();
+            }
+        }
     }
-    if (!first && __any_sync(0xffffffffu, bump)) {
+    if (!kHalf && !first && __any_sync(0xffffffffu, bump)) {
 #pragma unroll
         for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t ov[32];
