@@ -773,17 +773,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Items that were cut: the parts of the one in place blockIdx.x of the table, some of its rows at a time
 // (blockIdx.y), in a fixed order.  A warp takes 8 rows x 32 columns (128-byte runs of the parts, 64-byte runs of
-// the result) of every GROUPS-th part, kTogether parts' loads in flight; the groups' states meet in shared
+// the result) of every GROUPS-th part; the groups' states meet in shared
 // memory.  Items of many parts take four groups (16 items of 9 parts each 7.0 -> 3.5 us, 8 of 19 13.7 -> 8.8; a lone
 // tile's rows from four parts on, 27 of 48 rows 14.8 -> 13.3 with the attention);
 // where there are two to four parts four groups are idle and in the way (64 items 8 -> 34 us), and the reads
 // of 128 KB a part at d = 128 count.
-constexpr int kTogether = 4;
+// Parts in flight: four in four groups take 73 registers, one CTA an SM instead of two (64 requests on 16384 keys
+// 30.6 us, three 28.0).
+template <int GROUPS>
+constexpr int kTogetherOf = GROUPS == 1 ? 2 : 3;
 template <int GROUPS>
 constexpr int kJoinRows = GROUPS == 1 ? 16 : 8;
 template <int D, int GROUPS>
 __global__ void __launch_bounds__(GROUPS == 1 ? 2 * D : GROUPS * D) cross_join_kernel(const CrossArgs args) {
-    constexpr int kCols = D / 32, kWarpRows = kJoinRows<GROUPS> / 8;
+    constexpr int kCols = D / 32, kWarpRows = kJoinRows<GROUPS> / 8, kTogether = kTogetherOf<GROUPS>;
     __shared__ JoinState states[GROUPS > 1 ? GROUPS - 1 : 1][GROUPS > 1 ? kCols * 32 : 1];
     griddep_wait();
     griddep_launch_dependents();
@@ -810,11 +813,12 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 2 * D : GROUPS * D) cross_join_k
             const int k = k0 + GROUPS * i;
             const bool there = k <= cut.x;
             // the item's first part is its CTA's second slot, the others are their CTAs' first
-            const float* src = args.part + static_cast<size_t>(there ? 2 * k + (k == c) : 2 * c + 1) * size;
+            const float* src = args.part + static_cast<size_t>(2 * k + (k == c)) * size;
+            const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
             mk[i] = there ? src[ml] : -INFINITY;
             lk[i] = there ? src[ml + args.part_rows] : 0.f;
-            y[i] = reinterpret_cast<const float4*>(src)[o_at];
-            z[i] = reinterpret_cast<const float4*>(src)[o_at + args.part_rows];
+            y[i] = there ? reinterpret_cast<const float4*>(src)[o_at] : none;
+            z[i] = there ? reinterpret_cast<const float4*>(src)[o_at + args.part_rows] : none;
         }
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
