@@ -112,6 +112,21 @@ struct Units {
     }
 };
 
+// Of up to 32 batches the one that comes in this lane's place if those of most blocks go first; by a whole warp.
+__device__ __forceinline__ int batch_order(const CrossArgs& a) {
+    const int lane = threadIdx.x % 32, blocks = lane < a.B_kv ? cross_blocks(cross_length(a, lane)) : 0;
+    const int first = __shfl_sync(0xffffffffu, blocks, 0);
+    if (__all_sync(0xffffffffu, lane >= a.B_kv || blocks == first)) return lane;
+    int rank = 0, batch = 0;
+    for (int j = 0; j < a.B_kv; ++j) {
+        const int other = __shfl_sync(0xffffffffu, blocks, j);
+        rank += other > blocks || (other == blocks && j < lane) ? 1 : 0;
+    }
+    for (int j = 0; j < a.B_kv; ++j)
+        if (__shfl_sync(0xffffffffu, rank, j) == lane) batch = j;
+    return batch;
+}
+
 // Where a tile's rows come from: its first batch and, for nb = 1, its first row there; rows in use.
 struct TileRows {
     int b, r0, rows;

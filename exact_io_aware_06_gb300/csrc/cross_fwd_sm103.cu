@@ -345,16 +345,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s.flags |= 2;
                 publish(0, s);
             } else if (!args.stream) {
-                // whole items in alternating order
+                // Whole items in alternating order, of up to 32 sequences the longest first (4 x 2048 queries on
+                // 300-1000 keys 45.7 -> 39.5 us, 8 x 512 on 100-512 19.0 -> 16.7).
+                int order = lane;  // lane r: the batch of rank r
+                if (args.lengths != nullptr && args.B_kv <= 32 && gridDim.x < args.B_kv * args.per) order = batch_order(args);
                 const uint32_t G = gridDim.x, per = args.per, all = args.B_kv * per;  // (up to 2^30 + 2^24)
                 auto item_of = [&](uint32_t i) { return i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x); };
                 uint32_t x = item_of(0);
                 for (int i = 0;; ++i) {
-                    const int batch = x / per;
+                    const int place = x / per, batch = args.B_kv <= 32 ? __shfl_sync(0xffffffffu, order, place) : place;
                     s.len = cross_length(args, batch);
                     s.k0 = 0;
                     s.n = cross_blocks(s.len);
-                    place_item(args, s, batch, x - batch * per);
+                    place_item(args, s, batch, x - place * per);
                     x = item_of(i + 1);
                     s.flags |= 4 | (x >= all ? 2 : 0);
                     if (!publish(i, s) || s.last()) break;

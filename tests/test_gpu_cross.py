@@ -166,6 +166,19 @@ def test_forward_of_few_items(B, H, N_q, N_kv, d):
         check_forward(q, k, v, lengths, o, lse, scale_for(d))
 
 
+@pytest.mark.parametrize("B,H,N_q,N_kv", [(5, 40, 130, 300), (32, 8, 129, 200), (33, 8, 129, 200), (2, 80, 256, 128)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_of_many_items_of_ragged_sequences(B, H, N_q, N_kv, d):
+    # whole items, more than CTAs: of up to 32 sequences the longest first, some of the same length, some empty
+    lengths = [(37 * b * b + 11 * b) % (N_kv + 1) if b % 7 else N_kv * (b % 2) for b in range(B)]
+    assert fa.fa_fwd_cross_workspace_size(B, B, H, H, N_q, N_kv, d) == 0
+    q, k, v, _ = inputs(B, B, H, H, N_q, N_kv, d, seed=B)
+    for b, n in enumerate(lengths):
+        k[b, :, n:], v[b, :, n:] = float("nan"), float("inf")
+    o, lse = forward(q, k, v, lengths, scale_for(d))
+    check_forward(q, k, v, lengths, o, lse, scale_for(d), batches=range(0, B, max(1, B // 5)))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
 @pytest.mark.parametrize("N_q", [1, 200])
 def test_forward_scales(scale, N_q):
