@@ -23,7 +23,6 @@
 #include <type_traits>
 
 #include "cross_fwd.cuh"
-#include "rows_out.cuh"
 #include "tma_host.h"
 
 namespace fa {
@@ -85,57 +84,27 @@ __device__ __forceinline__ void weighted32(uint32_t first, float w0, uint32_t se
     }
 }
 
-// A warp's 32 rows of O as bf16 from TMEM to global memory in runs of 64 bytes of 8 rows (one row a lane makes
-// every store touch 32 lines, and the SM's next TMEM loads wait behind them).  Lane r has row r's weights of
-// the accumulator(s) and its place (`at`, rows; -1: not stored).
+// A warp's rows of O as bf16 from TMEM to global memory, each lane its own: row `at` of o (-1: none), the weights of
+// the accumulator(s) its own.  For tiles that are packed or alone, which a warp stores once or twice: the time is
+// that of fetching the instructions.  (Through lanes that exchange their columns for runs of 64 bytes 64 single
+// tokens of 16 heads took 25.7 us instead of 23.7, of 32 heads 27.0 instead of 24.4; a lone tile of 128 rows 31.3
+// instead of 32.4.)
 template <int D>
-__device__ __forceinline__ void store_weighted(uint32_t first, float w0, uint32_t second, float w1, bool two, void* o,
-                                               long long at) {
-    const int lane = threadIdx.x % 32, q = lane % 4;
-#pragma unroll 1  // a warp comes here once or twice: fetching instructions is what takes its time
-    for (int m = 0; m < 2; ++m) {
-        float f0[2], f1[2];
-        long long to[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // rows 16 m + 8 h + lane / 4
-            const int from = 16 * m + 8 * h + lane / 4;
-            f0[h] = __shfl_sync(0xffffffffu, w0, from);
-            f1[h] = two ? __shfl_sync(0xffffffffu, w1, from) : 0.f;
-            to[h] = __shfl_sync(0xffffffffu, at, from);
-        }
+__device__ __forceinline__ void store_lanes(uint32_t first, float w0, uint32_t second, float w1, bool two, void* o, long long at) {
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-            const uint32_t part = (static_cast<uint32_t>(16 * m) << 16) + 64 * c;
-            uint32_t x[32], w[2][8];
-            tmem_ld_rows16(first + part, x);
-            if (two) {
-                uint32_t y[32];
-                tmem_ld_rows16(second + part, y);
+    for (int c = 0; c < D / 32; ++c) {
+        float x[32];
+        weighted32(first + 32 * c, w0, second + 32 * c, w1, two, x);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(o) + at * D) + 4 * c;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f1[e / 2 % 2], __uint_as_float(x[e]) * f0[e / 2 % 2]));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float f = two ? 1.f : f0[h];
-                    w[h][j] = pack_bf16x2(__uint_as_float(x[4 * j + 2 * h]) * f, __uint_as_float(x[4 * j + 2 * h + 1]) * f);
-                }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(o) + to[h] * D) + 8 * c + q;
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    transpose4(w[h][j], w[h][j + 1], w[h][j + 2], w[h][j + 3], q);  // columns 64 c + 8 (j + q) ..
-                    if (to[h] >= 0) dst[j] = make_uint4(w[h][j], w[h][j + 1], w[h][j + 2], w[h][j + 3]);
-                }
-            }
-        }
+        for (int g = 0; g < 4; ++g)
+            if (at >= 0)
+                dst[g] = make_uint4(pack_bf16x2(x[8 * g], x[8 * g + 1]), pack_bf16x2(x[8 * g + 2], x[8 * g + 3]),
+                                    pack_bf16x2(x[8 * g + 4], x[8 * g + 5]), pack_bf16x2(x[8 * g + 6], x[8 * g + 7]));
     }
 }
 
-// The same for whole tiles of one batch, by TMA: 32 columns a box, two boxes in turn, so that one is filled
+// O of whole tiles of one batch, by TMA: 32 columns a box, two boxes in turn, so that one is filled
 // while the other is stored, and the warp goes on with its next block while the last ones leave.  16-byte
 // granule g of row r lies at g ^ (r / 2 % 4).
 template <int D>
@@ -743,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    T.b * args.H_kv + seg.h, args.R);
                 } else {
                     const long long at = place(seg, tile);
-                    store_weighted<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
+                    store_lanes<D>(col, w0 * f, col1, w1 * f, two, args.o, at);
                     if (at >= 0 && args.lse != nullptr) args.lse[at] = row_lse(m_ref, l);
                 }
             }
