@@ -33,12 +33,19 @@ struct CrossArgs {
     int by_item, join_rows;
     int cluster;           // 2^cluster CTAs share one item, each with its own run of the keys; 0: as `stream`
     int ctas;
+    int few;               // no tiles
     float c_log2;          // scale * log2(e), not 0
     DevCtl ctl;
 };
 
+constexpr int kFewShort = 128;  // keys, up to which cross_few_sm103.cu has no loads ahead
+cudaError_t launch_cross_few(const CrossArgs& a, int d, const void* q, const void* k, const void* v, cudaStream_t s);
+
 namespace {
 
+__device__ __forceinline__ void cluster_sync() {  // what any thread of the cluster wrote before is visible after
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 constexpr int kPartTile = kBM;  // rows of a part's second tile start here
 
 __device__ __forceinline__ int cross_length(const CrossArgs& a, int b) {

@@ -158,9 +158,6 @@ struct JoinState {
 };
 // Blocks of an item's run for CTA r of its cluster: up to this.
 __device__ __forceinline__ int cluster_run(int blocks, int r, int log2_size) { return blocks * r >> log2_size; }
-__device__ __forceinline__ void cluster_sync() {  // what any thread of the cluster wrote before is visible after
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // The parts of an item on a cluster's CTAs, joined by the threads t = 0 .. 255 of each, a share of the rows a CTA:
 // eight columns of a row a thread, four parts' loads in flight.
@@ -844,6 +841,18 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     const double parts = (items < kMaxCtas ? kMaxCtas + items : 2 * kMaxCtas) * a.part_rows / 256.0 * d / 128.0;
     const double cut = even * (items <= kMaxCtas ? 0.75 : 1.0) + (items / double{kMaxCtas} + 1) * 1.25 + 2.5 + 0.022 * parts;
     a.stream = N_kv > kBN && items < 8 * kMaxCtas && cut < whole;
+    // A few rows: no tiles (cross_few_sm103.cu), and clusters of up to eight CTAs, for four an SM.  One row at any
+    // length, two at d = 64 (at d = 128 64 requests on 500-4096 keys 110 us, tiles 101), four on up to 128 keys (on 300
+    // 31 us, tiles 22), unless the CTAs are few and have long to read (4 heads on 16000 keys 27 us, tiles 17).
+    const int few_rows = a.R * a.share;
+    int cluster = 0;
+    while (cluster < 3 && items << cluster < 4 * kMaxCtas && N_kv >> cluster > 256) ++cluster;
+    a.few = few_rows <= 4 && (N_kv <= kFewShort || (few_rows * d <= 128 && ((N_kv >> cluster) * d <= 1 << 17 ||
+                                                                           items << cluster >= 2 * kMaxCtas)));
+    if (a.few) {
+        a.cluster = cluster;
+        a.stream = 0;
+    }
     a.by_item = items < kMaxCtas;
     const long long units = a.stream ? items * ((N_kv + kBN - 1) / kBN) : items;
     a.ctas = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);
@@ -990,6 +999,7 @@ int launch_fwd_cross(const void* q, const void* k, const void* v, const int* len
     // a scale of 0 makes all scores 0; the mask multiplies -inf by c, which has to stay -inf
     a.c_log2 = c_log2 == 0.f ? 1e-30f : c_log2;
     a.ctl = ctl;
+    if (a.few) return static_cast<int>(launch_cross_few(a, d, q, k, v, s));
     return d == 64 ? launch_impl<64>(q, k, v, a, s) : launch_impl<128>(q, k, v, a, s);
 }
 

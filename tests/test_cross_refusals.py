@@ -99,8 +99,10 @@ def test_cross_backward_refusals(L, change, status):
 
 def test_cross_workspaces(L):
     size = fa.fa_fwd_cross_workspace_size
-    # one row of one head over 12 blocks of keys: 152 places of cut items, and twelve CTAs with two parts of 32 rows
-    assert size(1, 1, 1, 1, 1, 1500, 64) == 152 * 16 + 12 * 2 * 32 * (64 + 2) * 4
+    # five rows of a K/V head over 12 blocks of keys: 152 places of cut items, and twelve CTAs with two parts of 32 rows
+    assert size(1, 1, 5, 1, 1, 1500, 64) == 152 * 16 + 12 * 2 * 32 * (64 + 2) * 4
+    # one row: none
+    assert size(1, 1, 1, 1, 1, 1500, 64) == 0
     # more items than the work is cut for: none
     assert size(8, 8, 16, 16, 2400, 100, 64) == 0
     for bad in ((0, 1, 1, 1, 1, 1, 64), (3, 2, 1, 1, 1, 1, 64), (1, 1, 3, 2, 1, 1, 64), (1, 1, 1, 1, 1, 1, 80), (1, 1, 1, 1, 1 << 40, 1, 64)):

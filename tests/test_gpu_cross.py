@@ -179,6 +179,24 @@ def test_forward_of_many_items_of_ragged_sequences(B, H, N_q, N_kv, d):
     check_forward(q, k, v, lengths, o, lse, scale_for(d), batches=range(0, B, max(1, B // 5)))
 
 
+@pytest.mark.parametrize("B,B_kv,H,H_kv,N_q", [(3, 3, 2, 2, 1), (3, 3, 4, 2, 1), (3, 3, 2, 2, 2), (3, 3, 3, 1, 1), (3, 3, 2, 2, 4),
+                                                (6, 3, 2, 2, 1), (12, 3, 1, 1, 1), (6, 3, 2, 1, 1), (60, 60, 16, 16, 1)])
+@pytest.mark.parametrize("N_kv", [1, 40, 128, 129, 700, 3000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_of_few_rows(B, B_kv, H, H_kv, N_q, N_kv, d):
+    # of one batch, of heads that share keys, of batches that share keys; CTAs of a cluster without keys
+    q, k, v, _ = inputs(B, B_kv, H, H_kv, N_q, N_kv, d, seed=N_kv)
+    for lengths in (None, ([N_kv, 0, (N_kv + 1) // 2] * 20)[:B_kv], ([7, N_kv - 1, N_kv + 9] * 20)[:B_kv]):
+        if lengths is not None:
+            for b, n in enumerate(lengths):
+                k[b, :, n:], v[b, :, n:] = float("inf"), float("nan")
+        o, lse = forward(q, k, v, lengths, scale_for(d))
+        check_forward(q, k, v, lengths, o, lse, scale_for(d), batches=range(0, B, max(1, B // 9)))
+        again = forward(q, k, v, lengths, scale_for(d))
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+        k, v = (torch.nan_to_num(x, nan=0.5, posinf=-0.5) for x in (k, v))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
 @pytest.mark.parametrize("N_q", [1, 200])
 def test_forward_scales(scale, N_q):
@@ -233,7 +251,7 @@ def test_forward_without_workspace_where_none_is_needed():
 
 def test_forward_large_offsets():
     # queries and keys beyond 2^31 bytes from the base, of whole items and of cut ones
-    for B, H, N_q, N_kv in ((70, 8, 16384, 64), (70, 8, 1, 16384)):
+    for B, H, N_q, N_kv in ((70, 8, 16384, 64), (70, 8, 1, 16384), (70, 8, 5, 16384)):
         q = torch.zeros((B, H, N_q, 128), dtype=torch.bfloat16, device="cuda")
         k = torch.zeros((B, H, N_kv, 128), dtype=torch.bfloat16, device="cuda")
         v = torch.zeros_like(k)
@@ -531,7 +549,8 @@ def own_attention(q, seed):
 
 
 @pytest.mark.parametrize("B,B_kv,H,H_kv,N_q,N_kv", [(8, 1, 8, 2, 1, 1500), (6, 2, 4, 4, 3, 300), (64, 1, 4, 1, 1, 130),
-                                                    (4, 1, 2, 2, 300, 200), (2, 2, 3, 1, 1, 77), (16, 1, 16, 16, 1024, 130)])
+                                                    (4, 1, 2, 2, 300, 200), (2, 2, 3, 1, 1, 77), (16, 1, 16, 16, 1024, 130),
+                                                    (2, 2, 2, 2, 1, 1500), (4, 2, 3, 3, 1, 333)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_prefix(B, B_kv, H, H_kv, N_q, N_kv, d, in_place):
