@@ -2,10 +2,11 @@
 //
 // With up to four rows to a K/V head in a batch a tile of 128 is nearly empty, and what a call costs is a tile's way
 // through the tensor core: 2.9 us for every two blocks of keys, where their bytes take 1.  Here the keys stream through
-// registers: D / 8 lanes hold a key's 16 bytes each, multiply them with each row's part of q, and add up p V in the
-// same places; a lane group keeps a running maximum and sum of its own.  The states of a warp's groups, of a CTA's
-// eight warps and of the up to eight CTAs of a cluster that share a K/V head are joined in a fixed order.  Everything
-// is float32 up to the result.
+// registers: D / 8 lanes hold a key's 16 bytes of V each and add up p V for every row.  Up to two rows take their
+// scores in the same way, from K's 16 bytes, and a lane group keeps a running maximum and sum of its own; more take
+// the scores of 16 keys from small matrix products (64 x 32 / 8 heads on 100 keys at d = 128 14.2 -> 11.1 us).  The
+// states of a warp's groups, of a CTA's eight warps and of the up to eight CTAs of a cluster that share a K/V head are
+// joined in a fixed order.  Sums, statistics, P and O are float32 up to the result.
 //
 // Bound by HBM on long sequences, as long as a warp's next 16 keys are in flight while it works on these (64 x 16
 // heads on 1500-4096 keys, d = 64: 112 us, 6.5 TB/s; without 130; by tiles 129), by the loads' latency on short ones,
@@ -19,6 +20,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTogether = 4;  // keys of a lane group in flight
+constexpr int kShort = 128;   // keys, up to which there are no loads ahead
 
 // A state over some of the keys, of one row and some columns: reference maximum (log2 units) and sum.
 __device__ __forceinline__ float state_weight(float m, float l, float top) {
@@ -31,6 +33,14 @@ __device__ __forceinline__ float shared_of(uint32_t addr, int rank) {  // of a C
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
     return x;
+}
+
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 template <int D, int R, bool AHEAD, int CTAS>
@@ -46,95 +56,180 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) cross_few_kernel(const Cros
     const int len = cross_length(a, batch);
     const int lo = static_cast<int>(static_cast<long long>(len) * rank >> a.cluster);
     const int hi = static_cast<int>(static_cast<long long>(len) * (rank + 1) >> a.cluster);
-    float2 qf[R][4], acc[R][4];
+    float2 acc[R][4];
     float m[R], l[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const uint4 x = r < T.rows ? q[global_row(a, T, h, r) * kLanes + j] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            qf[r][e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-            acc[r][e] = make_float2(0.f, 0.f);
-        }
+        for (int e = 0; e < 4; ++e) acc[r][e] = make_float2(0.f, 0.f);
         m[r] = -INFINITY;
         l[r] = 0.f;
     }
-    const size_t first = static_cast<size_t>(item) * a.N_kv * kLanes + j;
-    constexpr int kStep = kWarps * kKeys * kTogether;
-    struct Keys {
-        uint4 k[kTogether], v[kTogether];
-    };
-    auto load = [&](int key0) {
-        Keys x;
-#pragma unroll
-        for (int u = 0; u < kTogether; ++u) {
-            const int key = key0 + u * kKeys;
-            const size_t at = first + static_cast<size_t>(key) * kLanes;
-            x.k[u] = key < hi ? __ldcs(k + at) : make_uint4(0, 0, 0, 0);
-            x.v[u] = key < hi ? __ldcs(v + at) : make_uint4(0, 0, 0, 0);
-        }
-        return x;
-    };
-    int key0 = lo + warp * (kKeys * kTogether) + grp;
-    Keys now, ahead;
-    if (AHEAD) now = load(key0);
-    for (; key0 - grp < hi; key0 += kStep) {
-        if (AHEAD)
-            ahead = load(key0 + kStep);
-        else
-            now = load(key0);
-        const uint4(&kr)[kTogether] = now.k;
-        const uint4(&vr)[kTogether] = now.v;
-        float s[R][kTogether];
-#pragma unroll
-        for (int u = 0; u < kTogether; ++u) {
-            const uint32_t w[4] = {kr[u].x, kr[u].y, kr[u].z, kr[u].w};
-            float2 x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float2 t = __ffma2_rn(qf[r][3], x[3], __ffma2_rn(qf[r][2], x[2], __ffma2_rn(qf[r][1], x[1], __fmul2_rn(qf[r][0], x[0]))));
-                s[r][u] = t.x + t.y;
-            }
-        }
-#pragma unroll
-        for (int off = 1; off < kLanes; off <<= 1)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int u = 0; u < kTogether; ++u) s[r][u] += __shfl_xor_sync(0xffffffffu, s[r][u], off);
+    const size_t first = static_cast<size_t>(item) * a.N_kv * kLanes;
+    if constexpr (R <= 2) {
+        float2 qf[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float top = m[r];
+            const uint4 x = r < T.rows ? q[global_row(a, T, h, r) * kLanes + j] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qf[r][e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+        }
+        constexpr int kStep = kWarps * kKeys * kTogether;
+        struct Keys {
+            uint4 k[kTogether], v[kTogether];
+        };
+        auto load = [&](int key0) {
+            Keys x;
 #pragma unroll
             for (int u = 0; u < kTogether; ++u) {
-                s[r][u] = key0 + u * kKeys < hi ? s[r][u] * a.c_log2 : -INFINITY;
-                top = fmaxf(top, s[r][u]);
+                const int key = key0 + u * kKeys;
+                const size_t at = first + static_cast<size_t>(key) * kLanes + j;
+                x.k[u] = key < hi ? __ldcs(k + at) : make_uint4(0, 0, 0, 0);
+                x.v[u] = key < hi ? __ldcs(v + at) : make_uint4(0, 0, 0, 0);
             }
-            const float ref = top == -INFINITY ? 0.f : top, keep = ex2_approx(m[r] - ref);
-            m[r] = top;
-            l[r] *= keep;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[r][e] = __fmul2_rn(acc[r][e], make_float2(keep, keep));
+            return x;
+        };
+        int key0 = lo + warp * (kKeys * kTogether) + grp;
+        Keys now, ahead;
+        if (AHEAD) now = load(key0);
+        for (; key0 - grp < hi; key0 += kStep) {
+            if (AHEAD)
+                ahead = load(key0 + kStep);
+            else
+                now = load(key0);
+            const uint4(&kr)[kTogether] = now.k;
+            const uint4(&vr)[kTogether] = now.v;
+            float s[R][kTogether];
 #pragma unroll
             for (int u = 0; u < kTogether; ++u) {
-                s[r][u] = ex2_approx(s[r][u] - ref);
-                l[r] += s[r][u];
+                const uint32_t w[4] = {kr[u].x, kr[u].y, kr[u].z, kr[u].w};
+                float2 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float2 t = __ffma2_rn(qf[r][3], x[3], __ffma2_rn(qf[r][2], x[2], __ffma2_rn(qf[r][1], x[1], __fmul2_rn(qf[r][0], x[0]))));
+                    s[r][u] = t.x + t.y;
+                }
+            }
+#pragma unroll
+            for (int off = 1; off < kLanes; off <<= 1)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int u = 0; u < kTogether; ++u) s[r][u] += __shfl_xor_sync(0xffffffffu, s[r][u], off);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float top = m[r];
+#pragma unroll
+                for (int u = 0; u < kTogether; ++u) {
+                    s[r][u] = key0 + u * kKeys < hi ? s[r][u] * a.c_log2 : -INFINITY;
+                    top = fmaxf(top, s[r][u]);
+                }
+                const float ref = top == -INFINITY ? 0.f : top, keep = ex2_approx(m[r] - ref);
+                m[r] = top;
+                l[r] *= keep;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][e] = __fmul2_rn(acc[r][e], make_float2(keep, keep));
+#pragma unroll
+                for (int u = 0; u < kTogether; ++u) {
+                    s[r][u] = ex2_approx(s[r][u] - ref);
+                    l[r] += s[r][u];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kTogether; ++u) {
+                const uint32_t w[4] = {vr[u].x, vr[u].y, vr[u].z, vr[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r][e] = __ffma2_rn(make_float2(s[r][u], s[r][u]), x, acc[r][e]);
+                }
+            }
+            if (AHEAD) now = ahead;
+        }
+    } else {
+        // Scores of 16 keys and eight rows by matrix fragments straight from memory: the order of d in a product is
+        // free, so that a lane's 16 neighbouring bytes serve two products.  Lane (g, t) has the scores of keys g and
+        // g + 8 with rows 2 t and 2 t + 1; the lanes that hold V's columns fetch their key's from there.
+        constexpr int kC = D / 32, kLoads = 16 / kKeys, kStep = 16 * kWarps;
+        const int g = lane / 4, t = lane % 4;
+        uint4 qb[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            qb[c] = g < T.rows ? q[global_row(a, T, h, g) * kLanes + 4 * c + t] : make_uint4(0, 0, 0, 0);
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};  // of rows 2 t, 2 t + 1
+        for (int key0 = lo + 16 * warp; key0 < hi; key0 += kStep) {
+            uint4 kr[2][kC], vr[kLoads];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const int key = key0 + g + 8 * i;
+                    kr[i][c] = key < hi ? __ldcs(k + first + static_cast<size_t>(key) * kLanes + 4 * c + t) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int key = key0 + u * kKeys + grp;
+                vr[u] = key < hi ? __ldcs(v + first + static_cast<size_t>(key) * kLanes + j) : make_uint4(0, 0, 0, 0);
+            }
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                mma_16x8(s, kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y, qb[c].x, qb[c].y);
+                mma_16x8(s, kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w, qb[c].z, qb[c].w);
+            }
+            float keep[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[i] = key0 + g < hi ? s[i] * a.c_log2 : -INFINITY;
+                s[2 + i] = key0 + g + 8 < hi ? s[2 + i] * a.c_log2 : -INFINITY;
+                float mx = fmaxf(s[i], s[2 + i]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                mx = fmaxf(mx, top[i]);
+                const float ref = mx == -INFINITY ? 0.f : mx;
+                keep[i] = ex2_approx(top[i] - ref);
+                top[i] = mx;
+                s[i] = ex2_approx(s[i] - ref);
+                s[2 + i] = ex2_approx(s[2 + i] - ref);
+                sum[i] = fmaf(sum[i], keep[i], s[i] + s[2 + i]);
+            }
+            if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float f = __shfl_sync(0xffffffffu, keep[r % 2], r / 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][e] = __fmul2_rn(acc[r][e], make_float2(f, f));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const uint32_t w[4] = {vr[u].x, vr[u].y, vr[u].z, vr[u].w};
+                float2 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+                const int from = (u * kKeys + grp) % 8 * 4;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float p = __shfl_sync(0xffffffffu, s[u * kKeys / 8 * 2 + r % 2], from + r / 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][e] = __ffma2_rn(make_float2(p, p), x[e], acc[r][e]);
+                }
             }
         }
 #pragma unroll
-        for (int u = 0; u < kTogether; ++u) {
-            const uint32_t w[4] = {vr[u].x, vr[u].y, vr[u].z, vr[u].w};
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+            for (int off = 4; off < 32; off <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
 #pragma unroll
-                for (int r = 0; r < R; ++r) acc[r][e] = __ffma2_rn(make_float2(s[r][u], s[r][u]), x, acc[r][e]);
-            }
+        for (int r = 0; r < R; ++r) {  // the warp's sum once, in its first group
+            m[r] = __shfl_sync(0xffffffffu, top[r % 2], r / 2);
+            const float x = __shfl_sync(0xffffffffu, sum[r % 2], r / 2);
+            l[r] = grp == 0 ? x : 0.f;
         }
-        if (AHEAD) now = ahead;
     }
     // the warp's groups
 #pragma unroll
@@ -168,7 +263,8 @@ __global__ void __launch_bounds__(32 * kWarps, CTAS) cross_few_kernel(const Cros
     // (lse may be written to where this is read)
     if (a.o_own != nullptr && threadIdx.x < T.rows) own_lse[threadIdx.x] = a.lse_own[global_row(a, T, h, threadIdx.x)];
     __syncthreads();
-    // A column of a row over `n` states, and their maximum and sum.
+    // A column of a row over `n` states, and their maximum and sum.  (Every thread works out the weights; a stage
+    // of its own for them made one token 4.7 -> 5.4 us.)
     auto join = [&](int n, int r, int col, auto state, float& top, float& sum) {
         top = -INFINITY;
         for (int i = 0; i < n; ++i) top = fmaxf(top, state(i, r, D));
@@ -244,14 +340,14 @@ cudaError_t launch(const CrossArgs& a, const void* q, const void* k, const void*
 
 cudaError_t launch_cross_few(const CrossArgs& a, int d, const void* q, const void* k, const void* v, cudaStream_t s) {
     const int rows = a.R * a.share;
-    if (a.N_kv > kFewShort) {
+    if (rows > 2 || rows * d > 128) return d == 64 ? launch<64, 4, false, 2>(a, q, k, v, s) : launch<128, 4, false, 2>(a, q, k, v, s);
+    if (a.N_kv > kShort) {
         const bool many = (static_cast<long long>(a.B_kv * a.H_kv) << a.cluster) > 2 * 152;
         if (rows == 2) return launch<64, 2, true, 2>(a, q, k, v, s);
         if (d == 64) return many ? launch<64, 1, true, 3>(a, q, k, v, s) : launch<64, 1, true, 2>(a, q, k, v, s);
         return many ? launch<128, 1, true, 3>(a, q, k, v, s) : launch<128, 1, true, 2>(a, q, k, v, s);
     }
-    if (rows > 2) return d == 64 ? launch<64, 4, false, 2>(a, q, k, v, s) : launch<128, 4, false, 2>(a, q, k, v, s);
-    if (rows == 2) return d == 64 ? launch<64, 2, false, 3>(a, q, k, v, s) : launch<128, 2, false, 3>(a, q, k, v, s);
+    if (rows == 2) return launch<64, 2, false, 3>(a, q, k, v, s);
     return d == 64 ? launch<64, 1, false, 4>(a, q, k, v, s) : launch<128, 1, false, 4>(a, q, k, v, s);
 }
 

@@ -38,7 +38,7 @@ struct CrossArgs {
     DevCtl ctl;
 };
 
-constexpr int kFewShort = 128;  // keys, up to which cross_few_sm103.cu has no loads ahead
+// Attention of up to four rows a K/V head and batch (all of share R), on 2^cluster CTAs each.
 cudaError_t launch_cross_few(const CrossArgs& a, int d, const void* q, const void* k, const void* v, cudaStream_t s);
 
 namespace {

@@ -841,14 +841,15 @@ CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
     const double parts = (items < kMaxCtas ? kMaxCtas + items : 2 * kMaxCtas) * a.part_rows / 256.0 * d / 128.0;
     const double cut = even * (items <= kMaxCtas ? 0.75 : 1.0) + (items / double{kMaxCtas} + 1) * 1.25 + 2.5 + 0.022 * parts;
     a.stream = N_kv > kBN && items < 8 * kMaxCtas && cut < whole;
-    // A few rows: no tiles (cross_few_sm103.cu), and clusters of up to eight CTAs, for four an SM.  One row at any
-    // length, two at d = 64 (at d = 128 64 requests on 500-4096 keys 110 us, tiles 101), four on up to 128 keys (on 300
-    // 31 us, tiles 22), unless the CTAs are few and have long to read (4 heads on 16000 keys 27 us, tiles 17).
+    // A few rows: no tiles (cross_few_sm103.cu), and clusters of up to eight CTAs to fill the SMs.  One row, or two at
+    // d = 64, at any length, unless the CTAs are few and have long to read (4 heads on 16000 keys 27 us, tiles 17); up
+    // to four on short sequences (64 x 32 / 8 heads at d = 128 on 500 keys 27 us, tiles 30; on 500-8192 193, tiles 175).
     const int few_rows = a.R * a.share;
     int cluster = 0;
-    while (cluster < 3 && items << cluster < 4 * kMaxCtas && N_kv >> cluster > 256) ++cluster;
-    a.few = few_rows <= 4 && (N_kv <= kFewShort || (few_rows * d <= 128 && ((N_kv >> cluster) * d <= 1 << 17 ||
-                                                                           items << cluster >= 2 * kMaxCtas)));
+    const bool narrow = few_rows * d <= 128;
+    while (cluster < 3 && items << cluster < (narrow ? 4 : 2) * kMaxCtas && N_kv >> cluster > 256) ++cluster;
+    a.few = few_rows <= 4 && (narrow ? (N_kv >> cluster) * d <= 1 << 17 || items << cluster >= 2 * kMaxCtas
+                                     : N_kv <= 640);
     if (a.few) {
         a.cluster = cluster;
         a.stream = 0;
