@@ -272,10 +272,11 @@ def test_rows_behind_the_queries_are_left_alone():
     assert (o[3] == 7).all() and (lse[3] == 7).all()
 
 
-def test_two_calls_at_once():
+@pytest.mark.parametrize("N_q", [1, 9, 300])
+def test_two_calls_at_once(N_q):
     calls, streams = [], [torch.cuda.Stream() for _ in range(2)]
     for i in range(2):
-        q, k, v, _ = inputs(4, 4, 8, 8, 1, 3000, 64, seed=20 + i)
+        q, k, v, _ = inputs(4, 4, 8, 8, N_q, 3000, 64, seed=20 + i)
         ws = space(fa.fa_fwd_cross_workspace_size(*sizes(q, k)))
         calls.append((q, k, v, torch.empty_like(q), torch.empty(q.shape[:3], device="cuda"), ws))
     torch.cuda.synchronize()
@@ -297,8 +298,9 @@ def captured(call):
     return graph
 
 
-def test_captured_call_follows_the_lengths():
-    q, k, v, _ = inputs(4, 4, 8, 2, 1, 2000, 128, seed=15)
+@pytest.mark.parametrize("H_kv,N_q", [(2, 1), (8, 1), (8, 260)])
+def test_captured_call_follows_the_lengths(H_kv, N_q):
+    q, k, v, _ = inputs(4, 4, 8, H_kv, N_q, 2000, 128, seed=15)
     lengths = on_device([5, 5, 5, 5])
     o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
     ws = space(fa.fa_fwd_cross_workspace_size(*sizes(q, k)))
@@ -489,24 +491,27 @@ def test_backward_repeats_bit_for_bit(d):
         assert torch.equal(a, b)
 
 
-def test_captured_step_follows_the_lengths():
-    q, k, v, do = inputs(4, 2, 4, 2, 150, 300, 64, seed=15)
+@pytest.mark.parametrize("B,N_q,N_kv,d", [(4, 150, 300, 64), (2, 40, 4000, 64), (2, 40, 4000, 128), (4, 3, 20, 128)])
+def test_captured_step_follows_the_lengths(B, N_q, N_kv, d):
+    # also where dQ, in pieces, runs beside dK and dV on rows' values that the replay before wrote in the same place
+    q, k, v, do = inputs(B, 2, 4, 2, N_q, N_kv, d, seed=15)
     lengths = on_device([5, 5])
     o, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
     dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
     ws = space(max(fa.fa_fwd_cross_workspace_size(*sizes(q, k)), fa.fa_bwd_cross_workspace_size(*sizes(q, k))))
 
     def call():
-        fa.fa_fwd_cross(q, k, v, lengths, o, lse, ws, 0.125)
-        fa.fa_bwd_cross(q, k, v, lengths, o, lse, do, dq, dk, dv, ws, 0.125)
+        fa.fa_fwd_cross(q, k, v, lengths, o, lse, ws, scale_for(d))
+        fa.fa_bwd_cross(q, k, v, lengths, o, lse, do, dq, dk, dv, ws, scale_for(d))
 
     graph = captured(call)
-    for new in ([300, 17], [0, 129], [128, 300]):
+    for new in ([N_kv, 17], [0, N_kv // 2 - 21], [N_kv - 7, N_kv]):
+        q.copy_(q.flip(2)), do.copy_(do.roll(1, 2))
         lengths.copy_(torch.tensor(new, dtype=torch.int32))
         graph.replay()
         check_status()
-        check_forward(q, k, v, new, o, lse, 0.125)
-        check_backward(q, k, v, new, do, (dq, dk, dv), 0.125)
+        check_forward(q, k, v, new, o, lse, scale_for(d))
+        check_backward(q, k, v, new, do, (dq, dk, dv), scale_for(d))
 
 
 def test_backward_large_offsets():
