@@ -82,8 +82,8 @@ static __device__ __forceinline__ constexpr bool hides(const CrossBwdArgs&) { re
 cudaError_t launch_bwd_cross_main64(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
                                     const CUtensorMap& dk, const CUtensorMap& dv, const CrossBwdArgs& a, int grid,
                                     cudaStream_t s);
-// dQ of all B * H_kv heads of R rows, on `sms` SMs, after (or beside) the main_ctas CTAs of dK and dV.
+// dQ of all B * H_kv heads of R rows, on `sms` SMs, after (or beside) dK and dV.
 cudaError_t launch_bwd_cross_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
-                                void* dq, const CrossBwdArgs& a, int d, int main_ctas, int sms, cudaStream_t s);
+                                void* dq, const CrossBwdArgs& a, int d, int sms, cudaStream_t s);
 
 }  // namespace fa

@@ -55,34 +55,34 @@ static __device__ __forceinline__ void idle_warp(const CrossBwdArgs&, std::integ
 
 namespace {
 
-// Programmatically where each item has a CTA of its own, which takes over an SM as soon as the dK/dV kernel leaves
-// it (a step of 6 x 107 queries on 5392 keys 107 -> 106 us, 1646 on 4268 101 -> 96), or both kernels' CTAs fit at
-// once (8 x 8 on 16: 23 -> 19).  With several items a CTA the order in which SMs get free undoes the deal, and it
-// costs up to 10%.
+// Up to two items an SM have a CTA each, launched programmatically, which takes over an SM as soon as the dK/dV kernel
+// leaves it or at once (a step of 2 x 900 queries on 2000 keys 90 -> 83 us, 12 x 82 on 272-2179 112 -> 105, 8 x 8 on 16
+// 23 -> 19).  With several items a CTA the order in which SMs get free undoes the deal, which costs up to 10%; with
+// three CTAs an SM their starts do (1681 on 21 41.7 -> 45.3).
 template <int D, class Args>
 cudaError_t launch_impl(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, void* dq,
-                        const Args& a, int main_ctas, int sms, cudaStream_t s) {
+                        const Args& a, int sms, cudaStream_t s) {
     static std::atomic<uint64_t> smem_done;
     const cudaError_t e = allow_smem(bwd_dq_kernel<D, Args>, Cfg<D>::kSmemAlloc, smem_done);
     if (e != cudaSuccess) return e;
-    const int n_items = a.BH_kv * a.share * a.n_q * a.pieces_q, grid = n_items < sms ? n_items : sms;
-    if (n_items <= sms || main_ctas + grid <= sms)
+    const int n_items = a.BH_kv * a.share * a.n_q * a.pieces_q, grid = n_items <= 2 * sms ? n_items : sms;
+    if (n_items <= 2 * sms)
         return launch_pdl(bwd_dq_kernel<D, Args>, dim3(grid), dim3(kThreads), Cfg<D>::kSmemAlloc, s, q, k, v, dO, a, dq, n_items);
     bwd_dq_kernel<D, Args><<<grid, kThreads, Cfg<D>::kSmemAlloc, s>>>(q, k, v, dO, a, dq, n_items);
     return cudaGetLastError();
 }
 template <class Args>
 cudaError_t launch_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, void* dq,
-                     const Args& a, int d, int main_ctas, int sms, cudaStream_t s) {
-    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, main_ctas, sms, s) : launch_impl<128>(q, k, v, dO, dq, a, main_ctas, sms, s);
+                     const Args& a, int d, int sms, cudaStream_t s) {
+    return d == 64 ? launch_impl<64>(q, k, v, dO, dq, a, sms, s) : launch_impl<128>(q, k, v, dO, dq, a, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_bwd_cross_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
-                                void* dq, const CrossBwdArgs& a, int d, int main_ctas, int sms, cudaStream_t s) {
-    if (a.pieces_q == 1) return launch_d(q, k, v, dO, dq, a, d, main_ctas, sms, s);
-    return launch_d(q, k, v, dO, dq, CrossPieceArgs{a}, d, main_ctas, sms, s);
+                                void* dq, const CrossBwdArgs& a, int d, int sms, cudaStream_t s) {
+    if (a.pieces_q == 1) return launch_d(q, k, v, dO, dq, a, d, sms, s);
+    return launch_d(q, k, v, dO, dq, CrossPieceArgs{a}, d, sms, s);
 }
 
 }  // namespace fa

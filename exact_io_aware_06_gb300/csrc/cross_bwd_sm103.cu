@@ -298,7 +298,7 @@ int launch_bwd_cross(const void* q, const void* k, const void* v, const int* len
         if (e != cudaSuccess) return static_cast<int>(e);
         e = launch_pdl(bwd_main_kernel<CrossBwdArgs>, dim3(grid), dim3(kThreads), kSmemAlloc, s, tq, tk, tv, tdo, a);
     }
-    if (e == cudaSuccess) e = launch_bwd_cross_dq(tq, tk, tv, tdo, dq, a, d, grid, sms, s);
+    if (e == cudaSuccess) e = launch_bwd_cross_dq(tq, tk, tv, tdo, dq, a, d, sms, s);
     const int key_places = a.pieces > 1 ? 2 * a.BH_kv * a.n_k : 0;
     const int places = key_places + (a.pieces_q > 1 ? heads * a.n_q : 0);
     if (e != cudaSuccess || places == 0) return static_cast<int>(e);
