@@ -199,13 +199,16 @@ def fa_bwd_window(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, window, n_s
 def _cross(q, k, v, kv_lengths, o, lse, workspace, device):
     """Pointers of q, k, v, lengths, o, lse; of the workspace, and its bytes; B, B_kv, H, H_kv, N_q, N_kv, d."""
     B, H, N_q, d = rows = _sizes("q", q)
-    B_kv, H_kv, N_kv, _ = _sizes("k", k)
-    kv_rows = (B_kv, H_kv, N_kv, d)
-    return ((_dense("q", q, _BF16, rows, device), _dense("k", k, _BF16, kv_rows, device),
-             _dense("v", v, _BF16, kv_rows, device),
+    B_kv, H_kv, N_kv, d_kv = kv_rows = _sizes("k", k)
+    # at once what _dense checks one by one (0.5 us of a call's 8)
+    if not (q.dtype is k.dtype is v.dtype is o.dtype is _BF16 and d_kv == d and v.shape == kv_rows and o.shape == rows
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous()
+            and q.get_device() == k.get_device() == v.get_device() == o.get_device() == device):
+        for what, t, shape in (("q", q, rows), ("k", k, (B_kv, H_kv, N_kv, d)), ("v", v, (B_kv, H_kv, N_kv, d)), ("o", o, rows)):
+            _dense(what, t, _BF16, shape, device)
+    return ((q.data_ptr(), k.data_ptr(), v.data_ptr(),
              None if kv_lengths is None else _dense("kv_lengths", kv_lengths, _I32, (B_kv,), device),
-             _dense("o", o, _BF16, rows, device),
-             None if lse is None else _dense("lse", lse, _F32, (B, H, N_q), device)),
+             o.data_ptr(), None if lse is None else _dense("lse", lse, _F32, (B, H, N_q), device)),
             (None, 0) if workspace is None else _space(workspace, device), (B, B_kv, H, H_kv, N_q, N_kv, d))
 
 
