@@ -50,6 +50,11 @@ struct Cfg {
 };
 static_assert(Cfg<128>::kSmemAlloc + 2000 <= 232448, "smem");
 
+// Columns of S and P that a block with `valid` keys takes: a sequence's end of up to 32 or 64 keys has its own softmax
+// (6 x 2629 queries of 16 heads on 4 keys 26.6 -> 19.2 us, 2 x 16384 on 50 62.4 -> 52.1; one for 64 alone 22.3 and
+// 51.7; asked for before the usual one 2 x 8192 on 2048 keys take 177.8 us instead of 175.4).
+__device__ __forceinline__ int columns_of(int valid) { return valid <= 32 ? 32 : valid <= 64 ? 64 : kBN; }
+
 constexpr int kSegments = 8;   // ring of segments
 constexpr int kReaders = 10;   // the loading thread, the MMA thread, 8 softmax warps
 template <int STAGES>
@@ -444,11 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(smem_u32(&bars.s_full[t]));
                 };
                 // O_t += P_t V, each half of the keys as soon as its P is there
-                auto issue_pv = [&](int t, int u, bool acc, uint32_t par) -> bool {
+                auto issue_pv = [&](int t, int u, bool acc, uint32_t par, auto steps) -> bool {  // of 16 keys
                     const uint32_t vl = v_lo + u * (C::kTileBytes >> 4);
                     const uint32_t colO = tmem + C::kColO + D * t, colP = tmem + C::kColS + 128 * t;
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk) {
+                        if (kk >= steps) break;
                         if (kk % (kBN / 32) == 0) {
                             if (!mbar_wait(smem_u32(kk == 0 ? &bars.p_half[t] : &bars.p_full[t]), par, lim, &abort_flag)) return false;
                             tc_fence_after();
@@ -465,17 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true, begun;  // O begins with the own attention's
                 // Block j of two tiles: P_t V_j, then the next block's scores, tile by tile; the last two
                 // blocks run outside the loop, which keeps its body free of branches.
-                auto block = [&](int j, int g1, uint32_t p0, uint32_t p1, auto more_c, auto last2_c) -> bool {
+                auto block = [&](int j, int g1, uint32_t p0, uint32_t p1, auto more_c, auto last2_c, auto steps) -> bool {
                     constexpr bool more = decltype(more_c)::value, last2 = decltype(last2_c)::value;
                     const int u = g1 % kStages;
                     if (!mbar_wait(smem_u32(&bars.kv_full[u]), (g1 / kStages) & 1, lim, &abort_flag)) return false;
-                    if (!issue_pv(0, u, j > 0 || begun, p0)) return false;
+                    if (!issue_pv(0, u, j > 0 || begun, p0, steps)) return false;
                     if constexpr (more)
                         issue_s(0, 0, u);
                     else
                         mma_commit(smem_u32(&bars.o_done[0]));
                     if constexpr (last2) mma_commit(smem_u32(&bars.q_free[0]));
-                    if (!issue_pv(1, u, j > 0 || begun, p1)) return false;
+                    if (!issue_pv(1, u, j > 0 || begun, p1, steps)) return false;
                     if constexpr (more)
                         issue_s(1, 1, u);
                     else
@@ -486,12 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 using T = std::true_type;
                 using F = std::false_type;
+                using All = std::integral_constant<int, kBN / 16>;
                 for (int x = 0; ok; ++x) {
                     ok = segment_there(x);
                     if (!ok) break;
                     const int n = segments[x % kSegments].n;
                     const bool solo = segments[x % kSegments].solo(), last = segments[x % kSegments].last();
                     begun = args.o_own != nullptr && segments[x % kSegments].k0 == 0;
+                    const int steps = columns_of(segments[x % kSegments].len - (segments[x % kSegments].k0 + n - 1) * kBN) / 16;
                     segment_taken(x);
                     if (n == 0) break;
                     ok = mbar_wait(smem_u32(&bars.q_full[0]), kq0++ & 1, lim, &abort_flag);
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (i == n - 1) mma_commit(smem_u32(&bars.q_free[0]));
                             }
                             const int j = i - 1, t = j & 1;
-                            ok = issue_pv(t, u, j >= 2 || (j == 0 && begun), ((t ? c1 : c0) + j / 2) & 1);
+                            ok = issue_pv(t, u, j >= 2 || (j == 0 && begun), ((t ? c1 : c0) + j / 2) & 1, i < n ? kBN / 16 : steps);
                             if (!ok) break;
                             if (j + 2 >= n) mma_commit(smem_u32(&bars.o_done[t]));  // the warpgroup's last
                             mma_commit(smem_u32(&bars.kv_empty[u]));
@@ -530,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         c1 += n / 2;
                     } else {
                         int j = 0;
-                        for (; j + 2 < n && ok; ++j) ok = block(j, gb + j + 1, (c0 + j) & 1, (c1 + j) & 1, T{}, F{});
-                        if (ok && n >= 2) ok = block(n - 2, gb + n - 1, (c0 + n - 2) & 1, (c1 + n - 2) & 1, T{}, T{});
-                        if (ok) ok = block(n - 1, gb + n, (c0 + n - 1) & 1, (c1 + n - 1) & 1, F{}, F{});
+                        for (; j + 2 < n && ok; ++j) ok = block(j, gb + j + 1, (c0 + j) & 1, (c1 + j) & 1, T{}, F{}, All{});
+                        if (ok && n >= 2) ok = block(n - 2, gb + n - 1, (c0 + n - 2) & 1, (c1 + n - 2) & 1, T{}, T{}, All{});
+                        if (ok) ok = block(n - 1, gb + n, (c0 + n - 1) & 1, (c1 + n - 1) & 1, F{}, F{}, steps);
                         c0 += n;
                         c1 += n;
                     }
@@ -626,14 +634,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          : "memory");
                     fence_proxy_async_smem();
                 }
-                if (busy)
-                    softmax_block<D, kBN>(lane_base, colS, colS, colO, c, c_pos, mask_bits, valid - 1, -1, 0, i == 0 && !begun,
-                                          m_ref, l, [] {}, [] { return true; }, [&] {
-                                              tc_fence_before();
-                                              mbar_arrive(smem_u32(&bars.p_half[t]));
-                                          });
-                else
+                auto softmax = [&](auto columns) {
+                    softmax_block<D, decltype(columns)::value>(lane_base, colS, colS, colO, c, c_pos, mask_bits, valid - 1, -1, 0,
+                                                               i == 0 && !begun, m_ref, l, [] {}, [] { return true; }, [&] {
+                                                                   tc_fence_before();
+                                                                   mbar_arrive(smem_u32(&bars.p_half[t]));
+                                                               });
+                };
+                if (!busy)
                     mbar_arrive(smem_u32(&bars.p_half[t]));
+                else if (__builtin_expect(valid > 64, 1))
+                    softmax(std::integral_constant<int, kBN>{});
+                else if (valid > 32)
+                    softmax(std::integral_constant<int, 64>{});
+                else
+                    softmax(std::integral_constant<int, 32>{});
                 tc_fence_before();
                 mbar_arrive(smem_u32(&bars.p_full[t]));
             }

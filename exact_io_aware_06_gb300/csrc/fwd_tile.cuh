@@ -118,8 +118,8 @@ __device__ __forceinline__ bool softmax_block(uint32_t lane_base, uint32_t colS,
                                               float& m_ref, float& l, Taken taken, Free free, Half half = {}) {
     uint32_t r[NC];
     ld32_at<0>(lane_base + colS, r);
+    if constexpr (NC >= 64) ld32_at<32>(lane_base + colS + 32, r);
     if constexpr (NC == 128) {
-        ld32_at<32>(lane_base + colS + 32, r);
         ld32_at<64>(lane_base + colS + 64, r);
         ld32_at<96>(lane_base + colS + 96, r);
     }
