@@ -197,6 +197,22 @@ def test_forward_of_few_rows(B, B_kv, H, H_kv, N_q, N_kv, d):
         k, v = (torch.nan_to_num(x, nan=0.5, posinf=-0.5) for x in (k, v))
 
 
+@pytest.mark.parametrize("N_q,H,H_kv", [(7, 2, 2), (200, 2, 1), (130, 24, 24)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_ends_of_few_keys(N_q, H, H_kv, d):
+    # the last block's keys around 32 and 64, behind none, one and two whole blocks; of lone tiles and of pairs, cut or not
+    lengths = [31, 32, 33, 63, 64, 65, 1, 159, 160, 161, 191, 192, 193, 257, 288, 289, 320, 321]
+    q, k, v, _ = inputs(18, 18, H, H_kv, N_q, 330, d, seed=18)
+    for b, n in enumerate(lengths):
+        k[b, :, n:], v[b, :, n:] = float("-inf"), float("nan")
+    o, lse = forward(q, k, v, lengths, scale_for(d))
+    check_forward(q, k, v, lengths, o, lse, scale_for(d), batches=range(18) if H < 24 else range(0, 18, 2))
+    for n in (32, 64, 65, 160, 192):  # and of all the keys there are
+        x, y = k[-1:, :, :n].contiguous(), v[-1:, :, :n].contiguous()
+        o, lse = forward(q[-1:], x, y, None, -0.2)
+        check_forward(q[-1:], x, y, None, o, lse, -0.2)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
 @pytest.mark.parametrize("N_q", [1, 200])
 def test_forward_scales(scale, N_q):
