@@ -21,7 +21,7 @@
 //
 // For an argument type A the overloads are, besides those of bwd_tile.cuh,
 //     q_item_at(a, x)      an item: heads bh and bh_kv of Q's and K's tensors, query block qb, its n_kv key blocks
-//                          block(j), shorty: the first is that of up to 32 sinks; with kParts it may have none, and
+//                          block(j), shorty: the first has up to 32 keys (sinks); with kParts it may have none, and
 //                          part is the place of its float32 part of dQ in a.part_q, or -1 if it is all there is
 //     key_range(a, I, row, key0, ..)   the keys, counted from key0, that a query row sees
 //     hidden_rows(a, I, block, ..)     rows of a key block that hold no key but perhaps something else
@@ -52,7 +52,7 @@ static_assert(Cfg<128>::kSmemAlloc + 1024 <= 232448, "smem");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescSS = idesc_bf16(128, 128, false, false);  // S, dP
-constexpr uint32_t kIdescShort = idesc_bf16(128, 32, false, false);  // of up to 32 sinks
+constexpr uint32_t kIdescShort = idesc_bf16(128, 32, false, false);  // of up to 32 keys
 
 struct DqBars {
     uint64_t q_full, q_free;

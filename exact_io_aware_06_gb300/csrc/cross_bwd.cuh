@@ -29,6 +29,7 @@ struct CrossBwdArgs {
     DevCtl ctl;
 };
 struct CrossPieceArgs : CrossBwdArgs {};  // for dQ in pieces
+struct CrossShortArgs : CrossBwdArgs {};  // for dQ of up to 32 keys
 
 static __device__ __forceinline__ int key_count(const CrossBwdArgs& a, int kv_batch) {
     return a.lengths ? min(max(__ldg(a.lengths + kv_batch), 0), a.N_kv) : a.N_kv;
