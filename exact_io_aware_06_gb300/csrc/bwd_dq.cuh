@@ -23,6 +23,7 @@
 //     q_item_at(a, x)      an item: heads bh and bh_kv of Q's and K's tensors, query block qb, its n_kv key blocks
 //                          block(j), shorty: the first has up to 32 keys (sinks); with kParts it may have none, and
 //                          part is the place of its float32 part of dQ in a.part_q, or -1 if it is all there is
+//     row_value(a, p)      -lse log2 e or -delta of a row
 //     key_range(a, I, row, key0, ..)   the keys, counted from key0, that a query row sees
 //     hidden_rows(a, I, block, ..)     rows of a key block that hold no key but perhaps something else
 //     idle_warp(a, d, t, n)   what warp 3 of every CTA does, thread t of n
@@ -281,24 +282,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t hide = args.c_log2 >= 0.f ? 0xff800000u : 0x7f800000u;  // -inf after the multiply by c
         bool ok = true;
         int g = 0;
-        // an item's row values, loaded one item ahead; padded rows exist up to Np.  From L2: where this kernel starts
-        // beside the one before it, it has waited for none, and its SM's L1 may hold an earlier call's
+        // an item's row values, loaded one item ahead; padded rows exist up to Np
         auto row_at = [&](int x) {
             const auto I = q_item_at(args, x);
             return static_cast<size_t>(I.bh) * Np + I.qb * kBlk + row;
         };
         float next_nl = 0.f, next_nd = 0.f;
         if (item_x(0) < n_items) {
-            next_nl = __ldcg(args.ws_lse2 + row_at(item_x(0)));
-            next_nd = __ldcg(args.ws_delta + row_at(item_x(0)));
+            next_nl = row_value(args, args.ws_lse2 + row_at(item_x(0)));
+            next_nd = row_value(args, args.ws_delta + row_at(item_x(0)));
         }
         for (int k = 0, x = item_x(0); x < n_items && ok; x = item_x(++k)) {
             const auto I = q_item_at(args, x);
             const int qrow = I.qb * kBlk + row;
             const float nl = next_nl, nd = next_nd;
             if (item_x(k + 1) < n_items) {
-                next_nl = __ldcg(args.ws_lse2 + row_at(item_x(k + 1)));
-                next_nd = __ldcg(args.ws_delta + row_at(item_x(k + 1)));
+                next_nl = row_value(args, args.ws_lse2 + row_at(item_x(k + 1)));
+                next_nd = row_value(args, args.ws_delta + row_at(item_x(k + 1)));
             }
             const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
             for (int j = 0; j < I.n_kv; ++j, ++g) {

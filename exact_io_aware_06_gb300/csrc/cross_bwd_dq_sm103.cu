@@ -43,6 +43,9 @@ struct CrossQShort : CrossQItem {
 static __device__ __forceinline__ CrossQShort q_item_at(const CrossShortArgs& a, int x) {
     return {q_item_at(static_cast<const CrossBwdArgs&>(a), x)};
 }
+// From L2: where this kernel starts beside the one before it, it has waited for none, and its SM's L1 may hold an
+// earlier call's.
+static __device__ __forceinline__ float row_value(const CrossBwdArgs&, const float* p) { return __ldcg(p); }
 static __device__ __forceinline__ void key_range(const CrossBwdArgs&, const CrossQItem& I, int, int key0, int& first,
                                                  int& last, int& sink) {
     first = -1;

@@ -25,6 +25,7 @@ static __device__ __forceinline__ WinQItem q_item_at(const WinBwdArgs& args, int
     I.shorty = I.n_sink > 0 && args.split.sinks <= 32;
     return I;
 }
+static __device__ __forceinline__ float row_value(const WinBwdArgs&, const float* p) { return *p; }
 static __device__ __forceinline__ void key_range(const WinBwdArgs& args, const WinQItem&, int row, int key0, int& first, int& last,
                                           int& sink) {
     last = row - key0;
