@@ -1,42 +1,12 @@
-// cross_fwd.cuh -- attention to another sequence's keys: its arguments, how the work is dealt, and the
-// rows of a query tile.
-//
-// No query has a place among the keys, so all rows that meet the same K/V head are alike: the G N_q
-// rows of a group of heads lie side by side in q [B][H_kv][G N_q][d] (R = G N_q), and where R is small and
-// batches share their keys, several batches' rows fill one tile.  Single tokens, beams over one
-// encoder's states and a shared prefix are then the same tiles as a long text's.
+// cross_fwd.cuh -- attention to another sequence's keys: what the kernels of the forward share.
 #pragma once
 
+#include "cross_deal.cuh"
 #include "fwd_tile.cuh"
 #include "layer_ops.h"
 #include "ptx.cuh"
 
 namespace fa {
-
-// A K/V head's query rows in tiles of 128: nb whole batches of R rows each, or (nb = 1) runs of 128 rows
-// of one batch.  Two tiles are an item, as in the plain forward: K_j and V_j are loaded once for both.
-struct CrossArgs {
-    const int* lengths;    // [B_kv] or null
-    void* o;               // [B][H_kv][R][d] bf16
-    float* lse;            // [B][H_kv][R] or null
-    const void* o_own;     // as o, merged into it; null: none
-    const float* lse_own;
-    // Items that were cut, each by the CTA that begins it: last CTA (-1: none), batch, item, first CTA; in the
-    // item's place (by_item) or the CTA's, whichever are fewer.
-    int4* cut;
-    float* part;           // two parts a CTA: [d / 4][part_rows][4] O, then m and l of part_rows each
-    int R, share, H_kv, B_kv, N_kv;
-    int nb, tiles_b, tiles, n_pairs, part_rows;
-    int per;               // items of a batch, H_kv n_pairs
-    int stream;            // 0: whole items; 1: equal runs of key blocks, items cut where they end
-    int edge;              // an item's start and end in blocks, for these runs
-    int by_item, join_rows;
-    int cluster;           // 2^cluster CTAs share one item, each with its own run of the keys; 0: as `stream`
-    int ctas;
-    int few;               // no tiles
-    float c_log2;          // scale * log2(e), not 0
-    DevCtl ctl;
-};
 
 // Attention of up to four rows a K/V head and batch (all of share R), on 2^cluster CTAs each.
 cudaError_t launch_cross_few(const CrossArgs& a, int d, const void* q, const void* k, const void* v, cudaStream_t s);
@@ -47,173 +17,6 @@ __device__ __forceinline__ void cluster_sync() {  // what any thread of the clus
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 constexpr int kPartTile = kBM;  // rows of a part's second tile start here
-
-__device__ __forceinline__ int cross_length(const CrossArgs& a, int b) {
-    return a.lengths ? min(max(__ldg(a.lengths + b), 0), a.N_kv) : a.N_kv;
-}
-// A sequence without keys has one block, all of it hidden: its rows get O = 0, lse = -inf from it.
-__device__ __forceinline__ int cross_blocks(int len) { return len > 0 ? (len + kBN - 1) / kBN : 1; }
-
-// The key blocks of all items and `edge` for each item's start and end ("units", the edge in front), item by item,
-// batch by batch, in equal runs for the CTAs.  By a whole warp, 32 batches at a time.  Work of fewer than 8 * 152
-// items of up to 2^17 blocks is dealt so: 32 bits hold all of their units.
-__device__ __forceinline__ int cross_units(const CrossArgs& a, int len) { return cross_blocks(len) + a.edge; }
-struct UnitPlace {
-    int b, item, at, len;  // K/V batch, item of the batch, unit of the item; the batch's keys
-};
-struct Units {
-    int len, upto;         // of batch `lane`: keys; units of an item in batches 0 .. lane
-    int each, more;        // every CTA has `each`, the first `more` one more
-    // batches b0 + lane
-    __device__ __forceinline__ void scan(const CrossArgs& a, int b0) {
-        const int lane = threadIdx.x % 32, b = b0 + lane;
-        len = b < a.B_kv ? cross_length(a, b) : 0;
-        upto = b < a.B_kv ? cross_units(a, len) : 0;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += x;
-        }
-    }
-    __device__ __forceinline__ explicit Units(const CrossArgs& a) {
-        uint32_t total = 0;
-        if (!a.lengths) {
-            total = a.B_kv * cross_units(a, a.N_kv);
-        } else {
-            for (int b0 = (a.B_kv - 1) & ~31; b0 >= 0; b0 -= 32) {  // the first 32 last, which place() begins with
-                scan(a, b0);
-                total += __shfl_sync(0xffffffffu, upto, 31);
-            }
-        }
-        total *= a.per;
-        each = total / static_cast<uint32_t>(a.ctas);
-        more = total - each * a.ctas;
-    }
-    __device__ __forceinline__ int first(int cta) const { return each * cta + min(cta, more); }
-    __device__ __forceinline__ UnitPlace place(const CrossArgs& a, uint32_t u) {
-        UnitPlace p;
-        uint32_t n;
-        if (!a.lengths) {
-            p.len = a.N_kv;
-            n = cross_units(a, p.len);
-            p.b = u / (a.per * n);
-            u -= p.b * a.per * n;
-        } else {
-            for (int b0 = 0;; scan(a, b0)) {
-                const unsigned behind = __ballot_sync(0xffffffffu, u < static_cast<uint32_t>(upto * a.per));
-                if (behind || b0 + 32 >= a.B_kv) {
-                    const int l = behind ? __ffs(behind) - 1 : 31;
-                    p.b = b0 + l;
-                    p.len = __shfl_sync(0xffffffffu, len, l);
-                    n = cross_units(a, p.len);
-                    u -= (__shfl_sync(0xffffffffu, upto, l) - n) * a.per;
-                    break;
-                }
-                u -= __shfl_sync(0xffffffffu, upto, 31) * a.per;
-                b0 += 32;
-            }
-        }
-        p.item = u / n;
-        p.at = u - p.item * n;
-        return p;
-    }
-};
-
-// Of up to 32 batches the one that comes in this lane's place if those of most blocks go first; by a whole warp.
-__device__ __forceinline__ int batch_order(const CrossArgs& a) {
-    const int lane = threadIdx.x % 32, blocks = lane < a.B_kv ? cross_blocks(cross_length(a, lane)) : 0;
-    const int first = __shfl_sync(0xffffffffu, blocks, 0);
-    if (__all_sync(0xffffffffu, lane >= a.B_kv || blocks == first)) return lane;
-    int rank = 0, batch = 0;
-    for (int j = 0; j < a.B_kv; ++j) {
-        const int other = __shfl_sync(0xffffffffu, blocks, j);
-        rank += other > blocks || (other == blocks && j < lane) ? 1 : 0;
-    }
-    for (int j = 0; j < a.B_kv; ++j)
-        if (__shfl_sync(0xffffffffu, rank, j) == lane) batch = j;
-    return batch;
-}
-
-// Where a tile's rows come from: its first batch and, for nb = 1, its first row there; rows in use.
-struct TileRows {
-    int b, r0, rows;
-};
-__device__ __forceinline__ TileRows tile_rows(const CrossArgs& a, int kv_batch, int tile) {
-    TileRows t;
-    if (a.nb > 1) {
-        t.b = tile * a.nb;
-        t.rows = min(a.nb, a.share - t.b) * a.R;
-        t.r0 = 0;
-    } else {
-        t.b = a.share == 1 ? 0 : static_cast<uint32_t>(tile) / static_cast<uint32_t>(a.tiles_b);
-        t.r0 = (tile - t.b * a.tiles_b) * kBM;
-        t.rows = min(kBM, a.R - t.r0);
-    }
-    t.b += kv_batch * a.share;
-    return t;
-}
-// Row `row` of the tile, among the rows [B][H_kv][R].
-__device__ __forceinline__ size_t global_row(const CrossArgs& a, const TileRows& t, int h, int row) {
-    const int over = a.nb > 1 ? row / a.R : 0;
-    return (static_cast<size_t>(t.b + over) * a.H_kv + h) * a.R + (t.r0 + row - over * a.R);
-}
-
-// A run of key blocks of an item: what the kernel's roles read of it.
-struct __align__(16) Segment {
-    int n;       // its blocks; 0: nothing to do for this CTA
-    int k0;      // the first
-    int len;     // the sequence's keys
-    int flags;   // 1: of one tile; 2: the CTA's last; 4: all blocks of the item
-    int bh_kv, h;
-    TileRows rows[2];
-    __device__ __forceinline__ bool solo() const { return flags & 1; }
-    __device__ __forceinline__ bool last() const { return flags & 2; }
-    __device__ __forceinline__ bool whole() const { return flags & 4; }
-    __device__ __forceinline__ int slot() const { return k0 > 0 ? 0 : 1; }  // of the CTA's two parts
-};
-
-// An item's place in a segment.
-__device__ __forceinline__ void place_item(const CrossArgs& a, Segment& s, int batch, int item) {
-    s.h = a.n_pairs == 1 ? item : static_cast<uint32_t>(item) / static_cast<uint32_t>(a.n_pairs);
-    const int pair = item - s.h * a.n_pairs;
-    const bool solo = 2 * pair + 1 >= a.tiles;
-    s.bh_kv = batch * a.H_kv + s.h;
-    s.rows[0] = tile_rows(a, batch, 2 * pair);
-    if (!solo) s.rows[1] = tile_rows(a, batch, 2 * pair + 1);
-    s.flags = solo ? 1 : 0;
-}
-
-// This CTA's segments, one after the other.
-struct Walk {
-    int b, item, kb, blocks, len;
-    int left;  // units behind the edge of the item
-    __device__ __forceinline__ Walk(const CrossArgs& a, Units& units) {
-        const int u = units.first(blockIdx.x);
-        left = units.first(blockIdx.x + 1) - u;
-        if (left > 0) {
-            const UnitPlace p = units.place(a, u);
-            b = p.b, item = p.item, len = p.len;
-            blocks = cross_blocks(len);
-            kb = max(0, p.at - a.edge);
-            left -= max(0, a.edge - p.at);
-        }
-    }
-    // The next one; `batch` and `at`, its item of the batch; the item's blocks `behind` it.
-    __device__ __forceinline__ void next(const CrossArgs& a, Segment& s, int& batch, int& at, int& behind) {
-        batch = b, at = item, s.k0 = kb, s.len = len;
-        s.n = min(left, blocks - kb);
-        behind = blocks - kb - s.n;
-        left -= s.n + a.edge;
-        kb = 0;
-        if (++item == a.per && left > 0) {
-            item = 0;
-            len = cross_length(a, ++b);
-            blocks = cross_blocks(len);
-        }
-        place_item(a, s, batch, at);
-        s.flags |= (left <= 0 ? 2 : 0) | (s.k0 == 0 && behind == 0 ? 4 : 0);
-    }
-};
 
 // A row's end from its state (reference maximum m in log2 units, sum l): the factor of O, and lse.
 __device__ __forceinline__ float row_factor(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }

@@ -29,7 +29,6 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMaxCtas = 152;
 constexpr size_t kCutBytes = kMaxCtas * sizeof(int4);
 
 template <int D>
@@ -334,44 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!publish(i, s) || s.last()) break;
                 }
             } else {
-                Units units(args);
-                Walk walk(args, units);
-                // An item that this CTA begins and leaves cut, and its last CTA, for the join.
-                int4 cut = make_int4(-1, 0, 0, static_cast<int>(blockIdx.x));
-                int cut_at = static_cast<int>(blockIdx.x), behind_it = 0;
-                if (walk.left <= 0) {
-                    s.n = 0;
-                    s.flags = 2;
-                    publish(0, s);
-                }
-                for (int i = 0; walk.left > 0; ++i) {
-                    int batch, item, behind;
-                    walk.next(args, s, batch, item, behind);
-                    if (!publish(i, s)) break;
-                    if (s.k0 > 0 || args.ctas == 1) continue;
-                    const int place = batch * args.per + item;
-                    if (behind > 0) {
-                        cut = make_int4(0, batch, item, cut.w);
-                        behind_it = behind;
-                        if (args.by_item) cut_at = place;
-                    } else if (args.by_item && lane == 0) {
-                        args.cut[place] = make_int4(-1, 0, 0, 0);
-                    }
-                }
-                if (cut.x == 0) {
-                    const int end = units.first(blockIdx.x + 1) + behind_it;  // behind the item's last unit
-                    cut.x = static_cast<int>(blockIdx.x);
-                    for (;; cut.x += 32) {
-                        const int cta = cut.x + 1 + lane;
-                        const unsigned in = __ballot_sync(0xffffffffu, cta < args.ctas && units.first(cta) < end);
-                        if (in != 0xffffffffu) {
-                            cut.x += __popc(in);
-                            break;
-                        }
-                    }
-                }
-                // (an item's place is written by the CTA that begins it, a CTA's by itself)
-                if (lane == 0 && args.ctas > 1 && (cut.x >= 0 || !args.by_item)) args.cut[cut_at] = cut;
+                deal_runs(args, s, publish);
             }
         } else if (warp == 0) {
             // ============================================================ TMA producer
@@ -826,56 +788,6 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 2 * D : GROUPS * D) cross_join_k
     reinterpret_cast<uint4*>(args.o)[out * (D / 8) + vec] =
         make_uint4(pack_bf16x2(s.x[0], s.x[1]), pack_bf16x2(s.x[2], s.x[3]), pack_bf16x2(s.x[4], s.x[5]), pack_bf16x2(s.x[6], s.x[7]));
     if (vec == 0 && args.lse != nullptr) args.lse[out] = row_lse(s.m, s.l);
-}
-
-// How a call's rows are tiled and its work dealt, from its sizes alone.
-CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d) {
-    CrossArgs a = {};
-    a.R = H / H_kv * N_q;
-    a.share = B / B_kv;
-    a.H_kv = H_kv;
-    a.B_kv = B_kv;
-    a.N_kv = N_kv;
-    a.nb = 1;
-    if (a.R <= kBM / 2 && a.share > 1) a.nb = a.share < kBM / a.R ? a.share : kBM / a.R;
-    a.tiles_b = (a.R + kBM - 1) / kBM;
-    a.tiles = a.nb > 1 ? (a.share + a.nb - 1) / a.nb : a.share * a.tiles_b;
-    a.n_pairs = (a.tiles + 1) / 2;
-    a.per = H_kv * a.n_pairs;
-    const int rows = a.nb > 1 ? a.nb * a.R : a.R;  // of a lone tile
-    a.part_rows = a.tiles > 1 ? 2 * kBM : round_up(rows < kBM ? rows : kBM, 32);
-    const long long items = static_cast<long long>(B_kv) * a.per;
-    a.join_rows = a.tiles > 1 ? 2 * kBM : rows < kBM ? rows : kBM;
-    // Whole items, or key blocks in equal runs?  In blocks of the busiest CTA, an item's end counting 1.25, the
-    // join's launch 2.5 and what leaves a cut item as float32 and comes back 0.022 for 256 rows at d = 128.
-    // With a CTA or less an item the longest sequence would set the pace, and a batch's mean is taken for 3/4 of
-    // it.  Measured, whole / cut: 138 items of 4 blocks 12.4 / 24.1 us, 512 of 4 37 / 50, 160 of 16 55 / 47,
-    // 63 of up to 17 27.8 / 21.8.
-    const double blocks = (N_kv + kBN - 1) / kBN, even = items * blocks / kMaxCtas;
-    const double whole = ((items + kMaxCtas - 1) / kMaxCtas) * (blocks + 1.25);
-    const double parts = (items < kMaxCtas ? kMaxCtas + items : 2 * kMaxCtas) * a.part_rows / 256.0 * d / 128.0;
-    const double cut = even * (items <= kMaxCtas ? 0.75 : 1.0) + (items / double{kMaxCtas} + 1) * 1.25 + 2.5 + 0.022 * parts;
-    a.stream = N_kv > kBN && items < 8 * kMaxCtas && cut < whole;
-    // A few rows: no tiles (cross_few_sm103.cu), and clusters of up to eight CTAs to fill the SMs.  One row, or two at
-    // d = 64, at any length, unless the CTAs are few and have long to read (4 heads on 16000 keys 27 us, tiles 17); up
-    // to four on short sequences (64 x 32 / 8 heads at d = 128 on 500 keys 27 us, tiles 30; on 500-8192 193, tiles 175).
-    const int few_rows = a.R * a.share;
-    int cluster = 0;
-    const bool narrow = few_rows * d <= 128;
-    while (cluster < 3 && items << cluster < (narrow ? 4 : 2) * kMaxCtas && N_kv >> cluster > 256) ++cluster;
-    a.few = few_rows <= 4 && (narrow ? (N_kv >> cluster) * d <= 1 << 17 || items << cluster >= 2 * kMaxCtas
-                                     : N_kv <= 640);
-    if (a.few) {
-        a.cluster = cluster;
-        a.stream = 0;
-    }
-    a.by_item = items < kMaxCtas;
-    const long long units = a.stream ? items * ((N_kv + kBN - 1) / kBN) : items;
-    a.ctas = static_cast<int>(units < kMaxCtas ? units : kMaxCtas);
-    // Of packed tiles O leaves more slowly.  Counting blocks alone, some CTAs got many short sequences and few blocks:
-    // 8 short and 8 long items 78 -> 36 us, 64 ragged single tokens 185 -> 175; edges of 1 and 4 were slower.
-    a.edge = units <= kMaxCtas ? 0 : a.part_rows == 2 * kBM && a.nb == 1 ? 2 : 3;
-    return a;
 }
 
 // q as [B][H_kv][R][d] in boxes of `rows` rows of nb batches, 64 columns, or o in boxes of a warp's 32 rows, 32

@@ -5,14 +5,13 @@
 #include <cmath>
 #include <type_traits>
 
+#include "fwd_sizes.h"
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kBM = 128;       // query rows per tile
-constexpr int kBN = 128;       // keys per block
 constexpr float kTau = 8.0f;   // lazy-rescale threshold, log2 units
 
 __device__ __forceinline__ void record_timeout(const DevCtl& ctl, volatile int* abort_flag) {
