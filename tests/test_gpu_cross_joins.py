@@ -36,3 +36,69 @@ def test_a_wait_that_runs_out_where_items_are_cut(B, H, H_kv, N_q, N_kv, d, leng
     for _ in range(3):
         ws.fill_(255)
         until_a_wait_runs_out(lambda: fa.fa_fwd_cross(q, k, v, n, *out, ws, scale_for(d)), out, ref)
+
+
+# B, B_kv, H, H_kv, N_q, N_kv, lengths; d: with rows of several batches to a tile, of one batch in two tiles and more, of
+# lone tiles; a table place per item (fewer than 152 items) and per CTA
+JOINED = [(64, 1, 8, 2, 1, 16384, [16384]), (64, 1, 8, 2, 1, 16384, [10101]), (64, 1, 8, 2, 1, 16384, None),
+          (64, 2, 8, 2, 1, 16384, [15000, 300]), (40, 20, 8, 8, 5, 2048, [2048, 0, 1000, 1999, 1] * 4),
+          (20, 20, 8, 8, 5, 2048, [2047, 1, 0, 1500, 129] * 4), (2, 2, 2, 2, 300, 5000, [4999, 0]), (3, 1, 2, 1, 200, 5000, [4097])]
+SHAPES = ("B,B_kv,H,H_kv,N_q,N_kv,lengths", JOINED)
+
+
+def own_attention(q, seed):
+    """What the queries' own tokens gave; every fifth row has none."""
+    g = torch.Generator().manual_seed(seed)
+    o = (0.3 * torch.randn(q.shape, generator=g)).to(torch.bfloat16).cuda()
+    lse = (6 * torch.randn(q.shape[:3], generator=g)).cuda()
+    lse.view(-1)[::5] = -float("inf")
+    o.view(-1, q.shape[-1])[::5] = float("nan")
+    return o, lse
+
+
+def poisoned(k, v, lengths):
+    for b, n in enumerate(lengths or []):
+        k[b, :, n:], v[b, :, n:] = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize(*SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_of_cut_items(B, B_kv, H, H_kv, N_q, N_kv, lengths, d):
+    q, k, v, _ = inputs(B, B_kv, H, H_kv, N_q, N_kv, d, seed=N_q)
+    poisoned(k, v, lengths)
+    ws = space(fa.fa_fwd_cross_workspace_size(*sizes(q, k)))
+    o, lse = forward(q, k, v, lengths, scale_for(d), ws)
+    assert cut_items(ws) > 0
+    check_forward(q, k, v, lengths, o, lse, scale_for(d), batches=range(0, B, max(1, B // 8)))
+
+
+@pytest.mark.parametrize(*SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_prefix_of_cut_items(B, B_kv, H, H_kv, N_q, N_kv, lengths, d, in_place):
+    # the own attention belongs to the part that has the first block; in place it is written over by the join
+    q, k, v, _ = inputs(B, B_kv, H, H_kv, N_q, N_kv, d, seed=N_q)
+    poisoned(k, v, lengths)
+    own = own_attention(q, 3)
+    keep = [t.clone() for t in own]
+    o, lse = own if in_place else (torch.full_like(q, float("nan")), torch.full(q.shape[:3], float("nan"), device="cuda"))
+    ws = space(fa.fa_fwd_prefix_workspace_size(*sizes(q, k)))
+    fa.fa_fwd_prefix(q, k, v, on_device(lengths), *own, o, lse, ws, scale_for(d))
+    check_status()
+    assert cut_items(ws) > 0
+    check_forward(q, k, v, lengths, o, lse, scale_for(d), own=keep, batches=range(0, B, max(1, B // 8)))
+
+
+def test_empty_prefix_whose_items_might_be_cut():
+    q, k, v, _ = inputs(64, 1, 8, 2, 1, 16384, 128)
+    poisoned(k, v, [0])
+    o_own, lse_own = own_attention(q, 4)
+    o, lse = torch.full_like(q, float("nan")), torch.full_like(lse_own, float("nan"))
+    ws = space(fa.fa_fwd_prefix_workspace_size(*sizes(q, k)))
+    assert ws.numel() > 152 * 16
+    fa.fa_fwd_prefix(q, k, v, on_device([0]), o_own, lse_own, o, lse, ws, scale_for(128))
+    check_status()
+    none = torch.isinf(lse_own)
+    assert (o[none] == 0).all() and torch.equal(o[~none], o_own[~none]) and (lse[none] == -float("inf")).all()
+    # lse passes through base 2: two roundings of 2^-24
+    assert torch.allclose(lse[~none], lse_own[~none], rtol=2.0 ** -22, atol=0)
