@@ -287,7 +287,7 @@ inline CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d
     // A few rows: no tiles (cross_few_sm103.cu), and clusters of up to eight CTAs to fill the SMs.  One row, or two at
     // d = 64, at any length, unless the CTAs are few and have long to read (4 heads on 16000 keys 27 us, tiles 17); up
     // to four on short sequences (64 x 32 / 8 heads at d = 128 on 500 keys 27 us, tiles 30; on 500-8192 193, tiles 175).
-    const int few_rows = a.R * a.share;
+    const long long few_rows = static_cast<long long>(a.R) * a.share;
     int cluster = 0;
     const bool narrow = few_rows * d <= 128;
     while (cluster < 3 && items << cluster < (narrow ? 4 : 2) * kMaxCtas && N_kv >> cluster > 256) ++cluster;

@@ -145,3 +145,15 @@ def test_cases_reach_the_ring(deal):
     # that a CTA has more segments than the ring holds (8), so that a wait for room can run out
     most = {case: np.bincount(deal(*CASES[case])[1][:, 0]).max() for case in CASES}
     assert most["long then short"] > 16 and most["many empty"] > 8, most
+
+
+@pytest.mark.parametrize("B,N_q", [(1 << 16, 1 << 16), (1 << 15, 1 << 16), ((1 << 16) + 1, 1 << 16), (1 << 12, 1 << 20), (3, 1 << 23), (1 << 8, 1 << 23)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_are_not_taken_for_few(deal, B, N_q, d):
+    # the rows that share a K/V head, counted over the batches that do: beyond an int
+    assert not deal((B, 1, 1, 1, N_q, 300, d), None)[2]["few"]
+
+
+def test_few_rows(deal):
+    assert deal((1, 1, 8, 8, 1, 300, 64), None)[2]["few"] and deal((4, 1, 1, 1, 1, 300, 128), None)[2]["few"]
+    assert not deal((5, 1, 1, 1, 1, 300, 64), None)[2]["few"]
