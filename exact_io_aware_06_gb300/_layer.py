@@ -123,11 +123,11 @@ def fa_qk_norm_rope_bwd(qkv, q_weight, k_weight, positions, inv_freq, dq, dk, dv
 
 def _axes(positions, inv_freq, axis):
     """Number of axes of positions [axes, B, N], and the host pointer of axis, one entry a pair."""
-    if positions is None and inv_freq is None:  # nothing is turned
+    n = 0 if inv_freq is None else inv_freq.numel()
+    if positions is None and n == 0:  # nothing is turned
         return 1, None
     if positions is None or positions.dim() != 3:
         raise ValueError("positions: [axes, B, N] expected")
-    n = 0 if inv_freq is None else inv_freq.numel()
     if n and (axis is None or axis.dtype is not _I32 or axis.is_cuda or not axis.is_contiguous() or axis.numel() != n):
         raise ValueError(f"axis: a contiguous int32 tensor of {n} entries on the host (rope_axes)")
     return positions.shape[0], axis.data_ptr() if n else None
