@@ -458,7 +458,8 @@ size_t fa_bwd_cross_workspace_size(int B, int B_kv, int H, int H_kv, int N_q, in
  * batches that share it, whose rows fill tiles together.
  *
  *   o_own, lse_own : as o and lse, read; a row with lse_own = -inf has no keys of its own, and its o_own is
- *                    not used.  o may be o_own and lse may be lse_own (in place); they must not
+ *                    not used.  Finite lse_own are of up to 2^127 in magnitude; the lowest float is
+ *                    taken as -inf.  o may be o_own and lse may be lse_own (in place); they must not
  *                    overlap otherwise.
  *   lse            : may be NULL.   Other arguments and errors as fa_fwd_cross.
  */

@@ -97,3 +97,27 @@ def test_large_offsets():
         check_status()
         check_forward(q1, k1, v1, None, o[-1:, -1:], lse[-1:, -1:], scale_for(128), own=own1)
         assert (o[0] == 0).all()
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_rows_whose_own_lse_is_the_lowest_float_have_no_keys(way):
+    # as with -inf, and between them own attention that weighs next to nothing or all there is
+    p = Prefix(*way, 128, seed=7)
+    o, lse = p.own
+    lse.view(-1)[::5] = torch.finfo(torch.float32).min
+    lse.view(-1)[1::5], lse.view(-1)[2::5] = -2.0 ** 127, 2.0 ** 100
+    p()
+    check_status()
+    low, high = lse <= -2.0 ** 127, lse == 2.0 ** 100
+    own, here = p.own, torch.zeros_like(low)
+    for b, n in enumerate(p.lengths):
+        share = len(p.q) // len(p.lengths)
+        here[b * share:(b + 1) * share] = n > 0
+    out, out_lse = p.o.clone(), p.lse.clone()
+    lse[low] = -float("inf")  # the prefix alone
+    p()
+    check_status()
+    assert torch.equal(out[low & here], p.o[low & here]) and torch.equal(out_lse[low & here], p.lse[low & here])
+    none = (own[0] != own[0]).any(-1) & ~here  # of neither
+    assert none.sum() == 0 or (out[none] == 0).all() and (out_lse[none] == -float("inf")).all()
+    assert torch.equal(out[high], o[high]) and torch.allclose(out_lse[high], lse[high], rtol=2.0 ** -22, atol=0)
