@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 // P^T of this thread's key and a run of 32 NW queries from their raw scores, in their place, and as
-// bf16 pairs for dV.  The key's queries are q_first .. q_end - 1, counted from the first of the run;
+// bf16 pairs for dV (the type of dO, the product's other operand).  The key's queries are q_first .. q_end - 1, counted from the first of the run;
 // nl: -lse log2(e) of the queries.
 template <int NW>
 __device__ __forceinline__ void probabilities(uint32_t (&r)[NW][32], int q_first, int q_end, uint32_t hide, float2 c2,
@@ -77,7 +77,8 @@ __device__ __forceinline__ void probabilities(uint32_t (&r)[NW][32], int q_first
         rr[3] = __float_as_uint(p3);
     }
 }
-// dS^T = P^T o (dP^T - delta) of 32 queries as bf16 pairs; nd: -delta.
+// dS^T = P^T o (dP^T - delta) of 32 queries as bf16 pairs (the type of Q, the other operand of dK's product: a step's error
+// relative to 64 bits 2.4e-3, of which the gradients' own rounding is 1.7e-3); P before its rounding; nd: -delta.
 __device__ __forceinline__ void score_gradients(const uint32_t (&p)[32], const uint32_t (&dp)[32], const float4* nd,
                                                 uint32_t (&w)[16]) {
 #pragma unroll

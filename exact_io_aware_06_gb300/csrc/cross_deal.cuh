@@ -278,7 +278,9 @@ inline CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d
     // join's launch 2.5 and what leaves a cut item as float32 and comes back 0.022 for 256 rows at d = 128.
     // With a CTA or less an item the longest sequence would set the pace, and a batch's mean is taken for 3/4 of
     // it.  Measured, whole / cut: 138 items of 4 blocks 12.4 / 24.1 us, 512 of 4 37 / 50, 160 of 16 55 / 47,
-    // 63 of up to 17 27.8 / 21.8.
+    // 63 of up to 17 27.8 / 21.8.  Lone tiles of four rows, bound by HBM (tokens of 32 / 8 heads at d = 128 on 1500 keys):
+    // 24 requests 36.2 / 33.0 us, 32 37.9 / 41.7, 40 52.2 / 47.9, 64 70.5 / 69.0; 32 on 3000 keys 67.3 / 68.7, the only
+    // one of these where the slower is taken.
     const double blocks = (N_kv + kBN - 1) / kBN, even = items * blocks / kMaxCtas;
     const double whole = ((items + kMaxCtas - 1) / kMaxCtas) * (blocks + 1.25);
     const double parts = (items < kMaxCtas ? kMaxCtas + items : 2 * kMaxCtas) * a.part_rows / 256.0 * d / 128.0;
@@ -287,6 +289,9 @@ inline CrossArgs deal(int B, int B_kv, int H, int H_kv, int N_q, int N_kv, int d
     // A few rows: no tiles (cross_few_sm103.cu), and clusters of up to eight CTAs to fill the SMs.  One row, or two at
     // d = 64, at any length, unless the CTAs are few and have long to read (4 heads on 16000 keys 27 us, tiles 17); up
     // to four on short sequences (64 x 32 / 8 heads at d = 128 on 500 keys 27 us, tiles 30; on 500-8192 193, tiles 175).
+    // Four rows without tiles / with them (tokens of 32 / 8 heads at d = 128): 1 request on 700 keys 6.5 / 7.9 us, on 1500
+    // 7.5 / 8.6, on 4000 12.3 / 11.2, on 16000 30 / 21; 4 on 700 7.5 / 9.0, on 1500 11.0 / 11.3; 8 on 1500 20.8 / 15.1, on
+    // 16000 90 / 86: beyond 640 keys the tiles lose up to 1.4 us to few requests and win as much as a quarter elsewhere.
     const long long few_rows = static_cast<long long>(a.R) * a.share;
     int cluster = 0;
     const bool narrow = few_rows * d <= 128;

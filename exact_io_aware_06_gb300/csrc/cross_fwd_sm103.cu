@@ -11,15 +11,16 @@
 //   * Many rows on many keys: the tensor pipe.  Two query tiles a CTA in ping-pong share every K and V block, as
 //     in the plain forward: 3,050 cycles for a pair of blocks at d = 128 (2,048 of the pipe), 1,640 TFLOP/s at
 //     16 x 16384 x 16384.
-//   * Many rows on few keys (2 x 16384 video tokens on 77 to 512): an item's end, 3,800 cycles of its softmax
-//     warpgroups (O's last product, its way out, the next scores), beside 6,000 for four blocks.  O leaves in boxes
-//     by TMA, so that the warps go on while it is stored: 101 -> 95 us, 92 now, floor 42.
+//   * Many rows on few keys (2 x 16384 video tokens on 77 to 512, one to four blocks): an item's end, 3,600 cycles of
+//     its softmax warpgroups (O's last product, its way out, the next scores), beside 3,050 for each block of keys.  O
+//     leaves in boxes by TMA, so that the warps go on while it is stored: 101 -> 95 us by that step, 88 now, floor 42.
 //   * Few rows on many keys: HBM, at the rate that 152 SMs can have loads in flight.  The key blocks of all items
 //     are cut into equal runs (64 ragged single tokens on 500-8192 keys: 175 us, 96% of the copy rate), whose
 //     float32 parts a join adds up in a fixed order.
-//   * Few rows on few keys: latency: 8.2 us for one token of 16 heads on 1500 keys, of which the start takes 0.3,
-//     the segments 0.7, the first loads 0.7 to 1.5, a block 1, joining in a cluster 1.  Much of each is instructions
-//     fetched for the first time.
+//   * Few rows on few keys: latency: 7.3 us for 10 x 3 tokens of 12 / 4 heads on 500 to 777 keys, 8.6 for one token of
+//     32 / 8 heads on 1500.  Of 8.2 us (one token of 16 heads on 1500 keys, which takes no tiles any more) the start
+//     took 0.3, the segments 0.7, the first loads 0.7 to 1.5, a block 1, joining in a cluster 1.  Much of each is
+//     instructions fetched for the first time.
 #include <type_traits>
 
 #include "cross_fwd.cuh"
@@ -90,9 +91,9 @@ __device__ __forceinline__ void weighted32(uint32_t first, float w0, uint32_t se
 
 // A warp's rows of O as bf16 from TMEM to global memory, each lane its own: row `at` of o (-1: none), the weights of
 // the accumulator(s) its own.  For tiles that are packed or alone, which a warp stores once or twice: the time is
-// that of fetching the instructions.  (Through lanes that exchange their columns for runs of 64 bytes 64 single
-// tokens of 16 heads took 25.7 us instead of 23.7, of 32 heads 27.0 instead of 24.4; a lone tile of 128 rows 31.3
-// instead of 32.4.)
+// that of fetching the instructions.  (Through lanes that exchange their columns for runs of 64 bytes 64 tokens of
+// 16 heads took 25.7 us instead of 23.7, of 32 / 8 heads 27.0 instead of 24.4, both on keys so few that they take no
+// tiles any more; a lone tile of 128 rows 31.3 instead of 32.4.)
 template <int D>
 __device__ __forceinline__ void store_lanes(uint32_t first, float w0, uint32_t second, float w1, bool two, void* o, long long at) {
 #pragma unroll 1
@@ -818,8 +819,10 @@ cudaError_t join(const CrossArgs& x, int places, cudaStream_t s) {
                       dim3(GROUPS == 1 ? 2 * D : GROUPS * D), 0, s, x);
 }
 
-// Few items take a cluster each, whose CTAs meet at its barrier, which spares the launch of the join (one token
-// of two requests, 32 items on clusters of four, 11.0 -> 10.0 us): the largest clusters of which the device holds
+// Few items take a cluster each, whose CTAs meet at its barrier, which spares the launch of the join (one token of 32 / 8
+// heads on 1500 keys, 8 items on clusters of eight, 9.25 -> 8.6 us; 8 queries of 16 heads there 10.3 -> 8.55, of 36 on 700,
+// clusters of four, 10.6 -> 8.2; 10 x 3 tokens on two prompts 8.2 -> 7.8; but 15 x 130 queries on 1100 keys 13.0 -> 14.4,
+// where 15 clusters of eight leave 32 SMs out): the largest clusters of which the device holds
 // as many at once as there are items (36 of four, 15 of eight).  Those leave some SMs out, so not where that costs
 // more blocks a CTA than the join is worth (a ragged batch's mean again taken for 3/4).  Sizes that are no powers of two and those beyond eight were
 // slower than their numbers of blocks say (8 items of 7 blocks: four 8.3 us, seven 9.2, the join's launch 9.0;
